@@ -3,65 +3,11 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "fg_abi_util.h"
 #include "fg_common.cuh"
 #include "fg_internal.h"
 
 namespace {
-
-using fg::cdiv;
-
-constexpr size_t kAlign = 256;
-constexpr int kMaxIdSet = 4096;
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-int ratio_count(float r, int n) { return (int)ceil((double)r * (double)n); }
-
-fg_status check_params(const fg_params* p) {
-  if (!p) return FG_EINVAL;
-  if (p->B < 1 || p->L < 1 || p->H < 1 || p->n < 1) return FG_EINVAL;
-  const long long G = (long long)p->B * p->L * p->H;
-  if (G > 0x7fffffffLL || (long long)G * p->n > (1LL << 40)) return FG_EINVAL;
-  if (p->d != 64 && p->d != 128) return FG_EDTYPE;
-  if (p->dtype != FG_BF16 && p->dtype != FG_FP32) return FG_EDTYPE;
-  if (!(p->T > 0.f && p->T <= 1.f)) return FG_EINVAL;
-  if (!(p->r_l >= 0.f && p->r_l <= 1.f) || !(p->r_f >= 0.f && p->r_f <= 1.f)) return FG_EINVAL;
-  if (!(p->scale >= 0.f) || isinf(p->scale)) return FG_EINVAL;
-  if (p->Hkv < 0 || (p->Hkv > 0 && p->H % p->Hkv != 0)) return FG_EINVAL;
-  const int R = p->Hkv > 0 ? p->H / p->Hkv : 1;
-  if (R != 1 && R != 2 && R != 4 && R != 8) return FG_EDTYPE;
-  return FG_OK;
-}
-
-fg::ProfileDims dims(const fg_params* p) {
-  fg::ProfileDims pd;
-  pd.B = p->B;
-  pd.HL = p->L * p->H;
-  pd.G = p->B * pd.HL;
-  pd.H = p->H;
-  pd.Hkv = p->Hkv > 0 ? p->Hkv : p->H;
-  pd.R = p->H / pd.Hkv;
-  pd.HLkv = p->L * pd.Hkv;
-  pd.Gkv = p->B * pd.HLkv;
-  pd.n = p->n;
-  pd.d = p->d;
-  pd.dtype = p->dtype;
-  pd.w = ratio_count(p->r_l, p->n);
-  pd.k = ratio_count(p->r_f, p->n);
-  pd.T = p->T;
-  const float s = p->scale > 0.f ? p->scale : (float)(1.0 / sqrt((double)p->d));
-  pd.sl2 = s * fg::kLog2e;
-  return pd;
-}
-
-fg_status check_ids(const int32_t* set, int32_t cnt) {
-  if (cnt < 0 || cnt > kMaxIdSet) return FG_EINVAL;
-  if (cnt > 0 && !set) return FG_EINVAL;
-  return FG_OK;
-}
-
-fg_status cuda_status(cudaError_t e) { return e == cudaSuccess ? FG_OK : FG_ECUDA; }
 
 size_t elem_bytes(const fg_params* p) { return p->dtype == FG_BF16 ? 2 : 4; }
 
@@ -69,8 +15,6 @@ size_t elem_bytes(const fg_params* p) { return p->dtype == FG_BF16 ? 2 : 4; }
 size_t plan_desc_bytes(int Gkv) { return align_up((size_t)Gkv * sizeof(fg_head_desc)); }
 size_t plan_cinfo_bytes(int Gkv) { return align_up((size_t)Gkv * sizeof(int2)); }
 size_t plan_work_offset(int Gkv) { return plan_desc_bytes(Gkv) + plan_cinfo_bytes(Gkv) + kAlign; }
-int kv_count(const fg_params* p) { return p->B * p->L * (p->Hkv > 0 ? p->Hkv : p->H); }
-int group_size(const fg_params* p) { return p->Hkv > 0 ? p->H / p->Hkv : 1; }
 size_t plan_max_work(const fg_params* p, int32_t max_new) {
   const size_t Gkv = (size_t)kv_count(p);
   const int w = ratio_count(p->r_l, p->n);

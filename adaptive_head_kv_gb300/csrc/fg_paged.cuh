@@ -1,0 +1,293 @@
+// Paged 8-bit caches: the layout, the e4m3 coding of rows and the position
+// rotation, shared by the kernels that fill, extend and read them.
+//
+// A page holds kPageRows rows of one cache; every kBlockRows rows share one
+// power-of-two exponent for K and one for V, so that a row's value is
+// code * 2^exponent.  Powers of two make the coding exact to reproduce (the
+// scaling itself never rounds) and let a block's exponent grow when a larger
+// row arrives: e4m3 keeps its fraction bits, only codes that fall among the
+// subnormals are rounded again (absolute error <= 2^-10 of the code range's
+// unit, i.e. 2^-18.8 of the block's largest value).
+#pragma once
+
+#include "fg_common.cuh"
+#include "fg_internal.h"
+
+namespace fg {
+
+constexpr int kPageRows = FG_PAGE_ROWS;
+constexpr int kBlockRows = FG_BLOCK_ROWS;
+constexpr int kPageBlocks = kPageRows / kBlockRows;
+// Rows of a decode work item: whole pages.
+constexpr int kQ8RowsPerWork = 256;
+constexpr int kQ8RowsPerWorkWide = 512;
+constexpr int kExpMin = -100;  // exponent of a block without finite non-zero values
+
+// Bits of |x| as an unsigned integer, 0 for infinities and NaN: the order of
+// finite magnitudes is the order of these integers.
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+  const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
+  return b < 0x7f800000u ? b : 0u;
+}
+
+// Least e >= kExpMin with amax <= 448 * 2^e (448 = 1.75 * 2^8, the largest
+// e4m3 value), from the bits of amax.
+__device__ __forceinline__ int block_exponent(uint32_t amax_bits) {
+  const int e = (int)(amax_bits >> 23) - 127 - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return max(e, kExpMin);
+}
+
+// 2^e for a normal result (-126 <= e <= 127).
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
+
+// e4m3 codes of a (low byte) and b, nearest even; magnitudes past 448 and
+// infinities become 448, NaN stays NaN.
+__device__ __forceinline__ uint32_t code2(float a, float b) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) {
+  return code2(a, b) | (code2(c, d) << 16);
+}
+
+// Two e4m3 codes (bits 0-15 of w) as f16x2; exact.
+__device__ __forceinline__ uint32_t decode2(uint32_t w) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)w));
+  return r;
+}
+
+// Four codes times the f16x2 factor f (two equal powers of two <= 1), rounded
+// again.  The f16 product of a 4-bit fraction is exact above 2^-24, far below
+// the code's last place, so only the final conversion rounds.
+__device__ __forceinline__ uint32_t recode4(uint32_t w, uint32_t f) {
+  uint32_t lo = decode2(w), hi = decode2(w >> 16);
+  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(f));
+  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(f));
+  unsigned short a, b;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(lo));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b) : "r"(hi));
+  return (uint32_t)a | ((uint32_t)b << 16);
+}
+
+// f16x2 of 2^-k, k >= 1.  From k = 19 on every code (at most 448 = 2^8.8)
+// falls below half of the smallest one (2^-10) and becomes zero, so larger k
+// may stand for 24, the last one f16 holds.
+__device__ __forceinline__ uint32_t half2_pow2_neg(int k) {
+  k = min(k, 24);
+  const uint32_t h = k <= 14 ? (uint32_t)(15 - k) << 10 : 1u << (24 - k);
+  return h | (h << 16);
+}
+
+// cos and sin of 2 pi * pos * turns / 2^64.  The product keeps the fraction
+// of the turn exactly (modulo one turn, at any position), so nothing of the
+// angle is lost at far positions; the fraction's top 32 bits, as a signed
+// number of half turns in [-1, 1), are within 2^-25 of it after rounding.
+__device__ __forceinline__ void rope_cos_sin(uint32_t pos, unsigned long long turns, float& c,
+                                             float& s) {
+  const int frac = (int)((unsigned long long)pos * turns >> 32);
+  sincospif((float)frac * 4.656612873077393e-10f, &s, &c);
+}
+
+// Streaming 16-byte load of memory that the kernel also writes (not the
+// read-only path).
+__device__ __forceinline__ uint4 ld16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+struct RopeArgs {
+  const unsigned long long* turns;  // [rot / 2]
+  int rot;                          // 0: no rotation
+  int style;                        // FG_ROPE_*
+};
+
+struct PagedArgs {
+  uint8_t* kp;
+  uint8_t* vp;
+  int8_t* exps;
+  int32_t* pos;
+  int32_t* table;
+  const fg_paged_desc* caches;
+  const int32_t* rows;
+  int32_t* rows_out;
+  int32_t* next_page;
+  const int2* ranges;  // [Gkv] (first work item, items) of each cache
+  const int2* work;    // [n_work] (cache, item of the cache)
+  int n_pages, table_len, n_work, rpw;
+  int32_t* dev_err;
+};
+
+// Bits of dev_err.
+constexpr int kErrCapacity = 1, kErrInvalid = 4;
+
+// Page of entry `i` of a segment with `entries` entries from `first`; -1 when
+// the entry does not exist or holds no page of the pool.
+__device__ __forceinline__ int page_at(const PagedArgs& a, int first, int entries, int i) {
+  if (i < 0 || i >= entries || first < 0 || first > a.table_len - 1 - i) return -1;
+  const int page = a.table[first + i];
+  return page >= 0 && page < a.n_pages ? page : -1;
+}
+
+// ------------------------------------------------- rows held by one warp
+// A row of D values over the 32 lanes: lane l has values l * PER ..
+
+// Rotates a row (all lanes call).  angle(i) gives (cos, sin) of pair i.
+template <int PER, typename Angle>
+__device__ __forceinline__ void rotate_row(float (&x)[PER], int rot, int style, Angle angle) {
+  const int lane = threadIdx.x & 31, e0 = lane * PER;
+  if (style == FG_ROPE_INTERLEAVED) {
+    if (e0 < rot) {
+#pragma unroll
+      for (int k = 0; k < PER; k += 2) {
+        const float2 cs = angle((e0 + k) / 2);
+        const float u = x[k], v = x[k + 1];
+        x[k] = u * cs.x - v * cs.y;
+        x[k + 1] = v * cs.x + u * cs.y;
+      }
+    }
+  } else {
+    const int h = rot / 2;  // a multiple of 8: pairs of lanes hold pairs of values
+    const bool first = e0 < h;
+    const int other = e0 >= rot ? lane : first ? lane + h / PER : lane - h / PER;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const float y = __shfl_sync(0xffffffffu, x[k], other);
+      if (e0 < rot) {
+        const float2 cs = angle(e0 + k - (first ? 0 : h));
+        x[k] = first ? x[k] * cs.x - y * cs.y : x[k] * cs.x + y * cs.y;
+      }
+    }
+  }
+}
+
+// The warp's values of one row of bf16 or fp32.
+template <int PER>
+__device__ __forceinline__ void load_row(const __nv_bfloat16* p, float (&x)[PER]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < PER; k += 2) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p + lane * PER + k);
+    x[k] = bf16_lo(w);
+    x[k + 1] = bf16_hi(w);
+  }
+}
+template <int PER>
+__device__ __forceinline__ void load_row(const float* p, float (&x)[PER]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < PER; k += 2) {
+    const float2 w = *reinterpret_cast<const float2*>(p + lane * PER + k);
+    x[k] = w.x;
+    x[k + 1] = w.y;
+  }
+}
+
+// Puts NR new rows into a block (all lanes call): row i of x goes to row
+// first + i where bit i of mask is set.  The block's exponent grows when they
+// need it, and then its other codes are rounded again; fresh: the block
+// starts with these rows.
+template <int D, int NR>
+__device__ __forceinline__ void put_rows(const float (&x)[NR][D / 32], uint32_t mask, int first,
+                                         bool fresh, uint8_t* codes, int8_t* exp_at) {
+  constexpr int PER = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int had = fresh ? -128 : *exp_at;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < NR; ++i)
+    if (mask >> i & 1) {
+#pragma unroll
+      for (int k = 0; k < PER; ++k) top = max(top, finite_bits(x[i][k]));
+    }
+  top = __reduce_max_sync(0xffffffffu, top);
+  const int now = max(had, block_exponent(top));
+  if (!fresh && now > had) {
+    const uint32_t f = half2_pow2_neg(now - had);
+#pragma unroll
+    for (int i = 0; i < kBlockRows * D / 512; ++i) {
+      uint4* p = reinterpret_cast<uint4*>(codes) + i * 32 + lane;
+      uint4 v = *p;
+      v.x = recode4(v.x, f);
+      v.y = recode4(v.y, f);
+      v.z = recode4(v.z, f);
+      v.w = recode4(v.w, f);
+      *p = v;
+    }
+  }
+  __syncwarp();  // the exponent has been read, the old codes are in place
+  const float inv = pow2f(-now);
+#pragma unroll
+  for (int i = 0; i < NR; ++i)
+    if (mask >> i & 1) {
+      uint8_t* p = codes + (size_t)(first + i) * D + lane * PER;
+      if constexpr (PER == 4)
+        *reinterpret_cast<uint32_t*>(p) =
+            code4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
+      else
+        *reinterpret_cast<unsigned short*>(p) =
+            (unsigned short)code2(x[i][0] * inv, x[i][1] * inv);
+    }
+  if (lane == 0) *exp_at = (int8_t)now;
+}
+
+struct AppendArgs {
+  const void* k_new;
+  const void* v_new;
+  const int32_t* ids;
+  const int32_t* n_new;  // null: m tokens of every sequence
+  const int32_t* pos;
+  const int32_t* special;
+  int ns;
+  const int32_t* punct;
+  int np;
+  int m;
+  RopeArgs rope;
+  // workspace
+  int32_t* lists;   // [B, 2, m]: indices of the special / special or punctuation tokens
+  int32_t* old;     // [Gkv, 2]: rows before the call, rows stored
+  float2* angles;   // [B, m, rot / 2]: (cos, sin)
+};
+
+struct PagedDecodeArgs {
+  const void* q;
+  const void* k_new;  // null: no token is appended
+  const void* v_new;
+  const int32_t* ids;
+  const int32_t* pos;
+  const int32_t* special;
+  int ns;
+  const int32_t* punct;
+  int np;
+  RopeArgs rope;
+  void* out;
+  float* part_ml;
+  float* part_acc;
+};
+
+cudaError_t launch_rope(const ProfileDims& pd, const void* Q, const void* K, const int32_t* pos,
+                        const RopeArgs& rope, void* Qo, void* Ko, cudaStream_t s);
+// Layout of the caches after the prompt: descriptors, row counts and page
+// table from cinfo (policy, never-evicted rows); totals = {pages, worst-case
+// pages, table entries}.
+cudaError_t launch_paged_plan(int Gkv, int w, int reserve, const int2* cinfo, fg_paged_desc* caches,
+                              int32_t* rows, int32_t* table, int32_t* next_page,
+                              long long* totals, cudaStream_t s);
+// Decode work list of the current row counts; totals[3] = items, totals[4] =
+// rows per item.
+cudaError_t launch_paged_schedule(int Gkv, const fg_paged_desc* caches, const int32_t* rows,
+                                  int table_len, int max_work, int sms, int2* ranges, int2* work,
+                                  long long* totals, cudaStream_t s);
+cudaError_t launch_compact_q8(const ProfileDims& pd, const void* K, const void* V,
+                              const uint8_t* keep, const PagedArgs& a, cudaStream_t s);
+cudaError_t launch_append_q8(const ProfileDims& pd, const PagedArgs& a, const AppendArgs& n,
+                             cudaStream_t s);
+cudaError_t launch_decode_q8(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
+                             cudaStream_t s);
+
+}  // namespace fg

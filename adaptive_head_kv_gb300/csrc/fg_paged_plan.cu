@@ -1,0 +1,309 @@
+// Paged 8-bit caches: layout of the prompt's caches, the decode work list and
+// the coding of the kept prompt rows (Model Tells You What to Discard, Method:
+// K_C, V_C = f(K, V, C), with rows of 8 bits in pages).
+#include "fg_paged.cuh"
+
+namespace fg {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+// One CTA: exclusive scans over the caches of their prompt pages and table
+// entries.  A cache's entries hold room for `reserve` more rows; the first
+// page of a cache is left in its first entry for the fill kernel.
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(
+    const int2* __restrict__ cinfo, int G, int w, int reserve, fg_paged_desc* __restrict__ caches,
+    int32_t* __restrict__ rows, int32_t* __restrict__ table, int32_t* __restrict__ next_page,
+    long long* __restrict__ totals) {
+  __shared__ long long scr[33];
+  long long page_base = 0, entry_base = 0;
+  for (int base = 0; base < G; base += blockDim.x) {
+    const int c = base + threadIdx.x;
+    long long pages = 0, entries = 0;
+    int policy = 0, n_static = 0, wg = 0, seg = 0, ring = 0;
+    if (c < G) {
+      policy = cinfo[c].x;
+      n_static = cinfo[c].y;
+      wg = policy == FG_POLICY_SPFL ? w : 0;
+      seg = max(1, cdiv(n_static + reserve, kPageRows));
+      ring = cdiv(wg, kPageRows);
+      pages = cdiv(n_static, kPageRows) + ring;
+      entries = seg + ring;
+    }
+    long long ptot, etot;
+    const long long p0 = page_base + block_exclusive_scan(pages, scr, &ptot);
+    const long long e0 = entry_base + block_exclusive_scan(entries, scr, &etot);
+    if (c < G) {
+      fg_paged_desc d;
+      d.policy = policy;
+      d.w = wg;
+      d.first_page = (int)e0;
+      d.max_pages = seg;
+      d.ring_page = (int)e0 + seg;
+      d.ring_pages = ring;
+      caches[c] = d;
+      rows[c] = n_static;
+      table[e0] = (int)p0;
+    }
+    page_base += ptot;
+    entry_base += etot;
+  }
+  if (threadIdx.x == 0) {
+    *next_page = (int)page_base;
+    totals[0] = page_base;
+    totals[1] = entry_base;  // every entry filled
+    totals[2] = entry_base;
+  }
+}
+
+// One warp per cache: its prompt pages in order, -1 where it may grow.
+__global__ void __launch_bounds__(256) paged_fill_kernel(const fg_paged_desc* __restrict__ caches,
+                                                         const int32_t* __restrict__ rows, int G,
+                                                         int32_t* __restrict__ table) {
+  const int c = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (c >= G) return;
+  const fg_paged_desc d = caches[c];
+  const int now = cdiv(rows[c], kPageRows);
+  const int page = table[d.first_page];
+  __syncwarp();  // every lane has read the first entry before it is overwritten
+  for (int i = lane; i < d.max_pages; i += 32) table[d.first_page + i] = i < now ? page + i : -1;
+  for (int i = lane; i < d.ring_pages; i += 32) table[d.ring_page + i] = page + now + i;
+}
+
+// Decode items of a cache at `rpw` rows per item: its never-evicted segment
+// (at least one) and its ring.  Descriptors the plan did not write may say
+// anything: what lies past the table is not counted.
+__device__ __forceinline__ int cache_items(const fg_paged_desc& d, int rows, int table_len,
+                                           int rpw) {
+  const long long cap = (long long)min(max(d.max_pages, 0), table_len) * kPageRows;
+  const long long ring = (long long)min(max(d.ring_pages, 0), table_len) * kPageRows;
+  const long long seg = max(0LL, min((long long)rows, cap)), w = max(0LL, min((long long)d.w, ring));
+  return (int)(max(1LL, (seg + rpw - 1) / rpw) + (w + rpw - 1) / rpw);
+}
+
+// One CTA: items of every cache at the chosen item size, and their offsets.
+__global__ void __launch_bounds__(kPlanThreads) paged_schedule_kernel(
+    const fg_paged_desc* __restrict__ caches, const int32_t* __restrict__ rows, int G,
+    int table_len, int wide_at, int2* __restrict__ ranges, long long* __restrict__ totals) {
+  __shared__ long long scr[33];
+  long long small = 0;
+  for (int base = 0; base < G; base += blockDim.x) {
+    const int c = base + threadIdx.x;
+    long long items = 0, tot;
+    if (c < G) items = cache_items(caches[c], rows[c], table_len, kQ8RowsPerWork);
+    block_exclusive_scan(items, scr, &tot);
+    small += tot;
+  }
+  const int rpw = small >= wide_at ? kQ8RowsPerWorkWide : kQ8RowsPerWork;
+  long long item_base = 0;
+  for (int base = 0; base < G; base += blockDim.x) {
+    const int c = base + threadIdx.x;
+    long long items = 0, tot;
+    if (c < G) items = cache_items(caches[c], rows[c], table_len, rpw);
+    const long long at = item_base + block_exclusive_scan(items, scr, &tot);
+    if (c < G) ranges[c] = make_int2((int)min(at, 0x7fffffffLL), (int)items);
+    item_base += tot;
+  }
+  if (threadIdx.x == 0) {
+    totals[3] = item_base;
+    totals[4] = rpw;
+  }
+}
+
+__global__ void __launch_bounds__(256) paged_worklist_kernel(const int2* __restrict__ ranges, int G,
+                                                             int max_work, int2* __restrict__ work) {
+  const int c = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (c >= G) return;
+  const int2 r = ranges[c];
+  const int end = (int)min((long long)r.x + r.y, (long long)max_work);
+  for (int i = r.x + lane; i < end && i >= r.x; i += 32) work[i] = make_int2(c, i - r.x);
+}
+
+// ---------------------------------------------------------------------------
+// Coding the kept rows.  One CTA per (cache, kChunkRows rows of its
+// never-evicted segment or of its ring).  A segment's CTA first finds the
+// positions of its rows: a scan of the keep codes, in which each thread counts
+// its positions' never-evicted codes.  Then each warp takes blocks of 16 rows:
+// the rows' K and V in registers (one pass over the data), the block's largest
+// magnitudes, the exponents, the codes.  Bound by HBM: 2 * eb + 2 bytes a
+// value.
+constexpr int kCodeThreads = 256;
+constexpr int kCodeWarps = kCodeThreads / 32;
+constexpr int kChunkRows = 512;
+constexpr int kScanPer = 16;  // positions per thread and scan step
+
+// Codes a block of 16 rows: src[i] is the prompt position of row i, or -1.
+template <typename T, int D>
+__device__ __forceinline__ void code_block(const T* __restrict__ X, const int* src, uint8_t* dst,
+                                           int8_t* exp_dst) {
+  constexpr int E = Vec16<T>::kElems;
+  constexpr int LPR = D / E;              // lanes per row
+  constexpr int RPI = 32 / LPR;           // rows per load
+  constexpr int NI = kBlockRows / RPI;
+  const int lane = threadIdx.x & 31;
+  const int sub = lane / LPR, gl = lane % LPR;
+  uint4 x[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int j = src[i * RPI + sub];
+    x[i] = j >= 0 ? ldg_stream(X + (size_t)j * D + gl * E) : make_uint4(0, 0, 0, 0);
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    float f[E];
+    unpack16(x[i], f, (const T*)nullptr);
+#pragma unroll
+    for (int e = 0; e < E; ++e) top = max(top, finite_bits(f[e]));
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  const int e = block_exponent(top);
+  const float inv = pow2f(-e);
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int r = i * RPI + sub;
+    float f[E];
+    unpack16(x[i], f, (const T*)nullptr);
+    uint32_t w[E / 4];
+#pragma unroll
+    for (int k = 0; k < E / 4; ++k)
+      w[k] = code4(f[4 * k] * inv, f[4 * k + 1] * inv, f[4 * k + 2] * inv, f[4 * k + 3] * inv);
+    if (src[r] >= 0) {
+      uint8_t* p = dst + (size_t)r * D + gl * E;
+      if constexpr (E == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(p) = w[0];
+    }
+  }
+  if (lane == 0) *exp_dst = (int8_t)e;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kCodeThreads) compact_q8_kernel(
+    const T* __restrict__ K, const T* __restrict__ V, const uint8_t* __restrict__ keep, int n,
+    int H, int R, int seg_chunks, int chunks, const PagedArgs a) {
+  __shared__ int src[kChunkRows];
+  __shared__ int scr[33];
+  const int c = blockIdx.x / chunks;
+  int chunk = blockIdx.x % chunks;
+  const fg_paged_desc d = a.caches[c];
+  const bool ring = chunk >= seg_chunks;
+  if (ring) chunk -= seg_chunks;
+  const int lo = chunk * kChunkRows;
+  const int total = ring ? d.w : (int)min((long long)a.rows[c], (long long)d.max_pages * kPageRows);
+  if (!ring && chunk == 0 && threadIdx.x == 0 && a.rows[c] > total)
+    atomicOr(a.dev_err, kErrInvalid);
+  if (lo >= total) return;
+  const int hi = min(lo + kChunkRows, total);
+  const int Hkv = H / R;
+  const size_t g0 = (size_t)(c / Hkv) * H + (size_t)(c % Hkv) * R;  // first query head
+  for (int i = threadIdx.x; i < kChunkRows; i += kCodeThreads) src[i] = -1;
+  __syncthreads();
+  if (!ring) {
+    // static bits of kScanPer positions of a thread (any member keeps them so)
+    int seen = 0;  // never-evicted rows before the step
+    for (int base = 0; base < n && seen < hi; base += kCodeThreads * kScanPer) {
+      const int j0 = base + threadIdx.x * kScanPer;
+      uint32_t bits = 0;
+      for (int m = 0; m < R; ++m) {
+        const uint8_t* row = keep + (g0 + m) * (size_t)n;
+        if (j0 + kScanPer <= n && (reinterpret_cast<uintptr_t>(row + j0) & 15) == 0) {
+          const uint4 v = *reinterpret_cast<const uint4*>(row + j0);
+          const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t s = __vcmpeq4(ws[k], 0x01010101u * FG_KEEP_STATIC) & 0x01010101u;
+            bits |= ((s * 0x01020408u) >> 24) << (4 * k);  // byte i's flag to bit i
+          }
+        } else {
+          for (int k = 0; k < kScanPer; ++k)
+            if (j0 + k < n && row[j0 + k] == FG_KEEP_STATIC) bits |= 1u << k;
+        }
+      }
+      int tot;
+      int rank = seen + block_exclusive_scan(__popc(bits), scr, &tot);
+      while (bits) {
+        const int k = __ffs(bits) - 1;
+        bits &= bits - 1;
+        if (rank >= lo && rank < hi) src[rank - lo] = j0 + k;
+        ++rank;
+      }
+      seen += tot;
+    }
+  } else {
+    // slot s holds the one position of [n - w, n) that is s modulo w
+    for (int s = lo + threadIdx.x; s < hi; s += kCodeThreads) {
+      const int back = (n - 1 - s) % d.w;
+      const int j = n - 1 - (back < 0 ? back + d.w : back);
+      int st = 0, win = 0;
+      for (int m = 0; m < R && j >= 0; ++m) {
+        const int code = keep[(g0 + m) * (size_t)n + j];
+        st |= code == FG_KEEP_STATIC;
+        win |= code == FG_KEEP_WINDOW;
+      }
+      src[s - lo] = win && !st ? j : -1;
+    }
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const T* Kc = K + (size_t)c * n * D;
+  const T* Vc = V + (size_t)c * n * D;
+  for (int b = warp; b * kBlockRows < hi - lo; b += kCodeWarps) {
+    const int row = lo + b * kBlockRows;
+    const int page = ring ? page_at(a, d.ring_page, d.ring_pages, row / kPageRows)
+                          : page_at(a, d.first_page, d.max_pages, row / kPageRows);
+    if (page < 0) {
+      if (lane == 0) atomicOr(a.dev_err, kErrInvalid);
+      continue;
+    }
+    const int r = row % kPageRows;
+    const int* bs = src + b * kBlockRows;
+    if (lane < kBlockRows && row + lane < hi && (ring || bs[lane] >= 0))
+      a.pos[(size_t)page * kPageRows + r + lane] = bs[lane];
+    const size_t off = ((size_t)page * kPageRows + r) * D;
+    int8_t* ex = a.exps + ((size_t)page * kPageBlocks + r / kBlockRows) * 2;
+    code_block<T, D>(Kc, bs, a.kp + off, ex);
+    code_block<T, D>(Vc, bs, a.vp + off, ex + 1);
+  }
+}
+
+template <typename T, int D>
+cudaError_t run_compact_q8(const ProfileDims& pd, const void* K, const void* V,
+                           const uint8_t* keep, const PagedArgs& a, cudaStream_t s) {
+  const int seg = cdiv(pd.n, kChunkRows), chunks = seg + cdiv(pd.w, kChunkRows);
+  const long long grid = (long long)pd.Gkv * chunks;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  compact_q8_kernel<T, D><<<(unsigned)grid, kCodeThreads, 0, s>>>(
+      (const T*)K, (const T*)V, keep, pd.n, pd.H, pd.R, seg, chunks, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_plan(int Gkv, int w, int reserve, const int2* cinfo, fg_paged_desc* caches,
+                              int32_t* rows, int32_t* table, int32_t* next_page,
+                              long long* totals, cudaStream_t s) {
+  paged_plan_kernel<<<1, kPlanThreads, 0, s>>>(cinfo, Gkv, w, reserve, caches, rows, table,
+                                               next_page, totals);
+  paged_fill_kernel<<<cdiv(Gkv, 8), 256, 0, s>>>(caches, rows, Gkv, table);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_schedule(int Gkv, const fg_paged_desc* caches, const int32_t* rows,
+                                  int table_len, int max_work, int sms, int2* ranges, int2* work,
+                                  long long* totals, cudaStream_t s) {
+  paged_schedule_kernel<<<1, kPlanThreads, 0, s>>>(caches, rows, Gkv, table_len, 64 * sms,
+                                                    ranges, totals);
+  paged_worklist_kernel<<<cdiv(Gkv, 8), 256, 0, s>>>(ranges, Gkv, max_work, work);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_compact_q8(const ProfileDims& pd, const void* K, const void* V,
+                              const uint8_t* keep, const PagedArgs& a, cudaStream_t s) {
+  if (pd.dtype == FG_FP32)
+    return pd.d == 64 ? run_compact_q8<float, 64>(pd, K, V, keep, a, s)
+                      : run_compact_q8<float, 128>(pd, K, V, keep, a, s);
+  return pd.d == 64 ? run_compact_q8<__nv_bfloat16, 64>(pd, K, V, keep, a, s)
+                    : run_compact_q8<__nv_bfloat16, 128>(pd, K, V, keep, a, s);
+}
+
+}  // namespace fg

@@ -20,10 +20,13 @@ FG_POLICY_S, FG_POLICY_SP, FG_POLICY_SPF, FG_POLICY_SPFL, FG_POLICY_FULL = range
 POLICY_NAMES = ("special", "special+punct", "special+punct+frequent",
                 "special+punct+frequent+local", "full")
 FG_KEEP_DROP, FG_KEEP_STATIC, FG_KEEP_WINDOW = 0, 1, 2
+FG_ROPE_INTERLEAVED, FG_ROPE_HALF = 0, 1
+FG_PAGE_ROWS, FG_BLOCK_ROWS = 64, 16
 
 # kernels launched by one call of each entry point (counted in the bench)
 LAUNCHES = {"profile": 4, "profile_attn": 5, "profile_with_policy": 5, "plan": 3, "compact": 1,
-            "decode": 2, "decode_acc": 3, "refresh": 1, "refresh_init": 1}
+            "decode": 2, "decode_acc": 3, "refresh": 1, "refresh_init": 1, "rope": 1, "paged_plan": 5,
+            "paged_schedule": 2, "compact_q8": 1, "append_q8": 2, "decode_q8": 2}
 
 EXPORTS = (
     "fastgen_status_string", "fastgen_version", "fastgen_profile_workspace_bytes",
@@ -31,7 +34,10 @@ EXPORTS = (
     "fastgen_decode_workspace_bytes", "fastgen_decode_attn", "fastgen_read_error",
     "fastgen_decode_attn_noalloc", "fastgen_profile_with_policy", "fastgen_profile_attn",
     "fastgen_plan_compact", "fastgen_refresh_state_bytes", "fastgen_refresh_init",
-    "fastgen_decode_attn_refresh", "fastgen_profile_stall_test",
+    "fastgen_decode_attn_refresh", "fastgen_profile_stall_test", "fastgen_rope_table",
+    "fastgen_rope", "fastgen_paged_table_len", "fastgen_paged_sched_bytes", "fastgen_paged_plan",
+    "fastgen_paged_schedule", "fastgen_compact_q8", "fastgen_append_q8_workspace_bytes",
+    "fastgen_append_q8", "fastgen_decode_q8_workspace_bytes", "fastgen_decode_attn_q8",
 )
 
 # size of the library-held scratch array used by fastgen_decode_attn_noalloc
@@ -57,6 +63,33 @@ class PlanInfo(ctypes.Structure):
                 ("rows_per_work", ctypes.c_int32)]
 
 
+class RopeStruct(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("style", ctypes.c_int32)]
+
+
+class PagedDesc(ctypes.Structure):
+    _fields_ = [("policy", ctypes.c_int32), ("w", ctypes.c_int32),
+                ("first_page", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("ring_page", ctypes.c_int32), ("ring_pages", ctypes.c_int32)]
+
+
+class PagedCacheStruct(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("exps", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("caches", ctypes.c_void_p),
+                ("rows", ctypes.c_void_p), ("rows_out", ctypes.c_void_p),
+                ("next_page", ctypes.c_void_p), ("sched", ctypes.c_void_p),
+                ("sched_bytes", ctypes.c_int64), ("n_pages", ctypes.c_int32),
+                ("table_len", ctypes.c_int32), ("n_work", ctypes.c_int32),
+                ("rows_per_work", ctypes.c_int32)]
+
+
+class PagedInfo(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("table_used", ctypes.c_int32)]
+
+
 class FastGenError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -66,6 +99,7 @@ class FastGenError(RuntimeError):
 _lib = None
 _P = ctypes.c_void_p
 _I32, _I64, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_PP, _CP, _RP = (ctypes.POINTER(x) for x in (Params, PagedCacheStruct, RopeStruct))
 _SIGS = {
     "fastgen_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fastgen_version": (_I32, []),
@@ -102,6 +136,19 @@ _SIGS = {
     "fastgen_decode_attn_noalloc": (ctypes.c_int, [ctypes.POINTER(Params), _P,
                                                    ctypes.POINTER(PlanInfo), _P, _P, _P, _P, _P,
                                                    _P, _P, _P, _I32, _P, _I32, _I32, _P, _P, _P]),
+    "fastgen_rope_table": (ctypes.c_int, [_P, _I32, _P]),
+    "fastgen_rope": (ctypes.c_int, [_PP, _P, _P, _P, _RP, _P, _P, _P]),
+    "fastgen_paged_table_len": (_I32, [_PP, _I32]),
+    "fastgen_paged_sched_bytes": (_SZ, [_PP, _I32]),
+    "fastgen_paged_plan": (ctypes.c_int, [_PP, _P, _P, _I32, _CP, ctypes.POINTER(PagedInfo), _P]),
+    "fastgen_paged_schedule": (ctypes.c_int, [_PP, _CP, _P]),
+    "fastgen_compact_q8": (ctypes.c_int, [_PP, _P, _P, _P, _CP, _P, _P]),
+    "fastgen_append_q8_workspace_bytes": (_SZ, [_PP, _I32]),
+    "fastgen_append_q8": (ctypes.c_int, [_PP, _CP, _P, _P, _P, _I32, _P, _P, _I32, _P, _I32, _P,
+                                         _RP, _P, _SZ, _P, _P]),
+    "fastgen_decode_q8_workspace_bytes": (_SZ, [_PP, _CP]),
+    "fastgen_decode_attn_q8": (ctypes.c_int, [_PP, _CP, _P, _P, _P, _P, _P, _I32, _P, _I32, _P,
+                                              _RP, _P, _P, _SZ, _P, _P]),
 }
 
 
@@ -296,3 +343,243 @@ def fastgen_profile_stall_test(params, Q, K, token_ids, special_ids, punct_ids, 
         _count(special_ids), _ptr(punct_ids), _count(punct_ids), _ptr(policy), _ptr(mass),
         _ptr(cost), _ptr(colsum), _ptr(keep), _ptr(kept), _ptr(workspace), _nbytes(workspace),
         _ptr(dev_err), int(stall_pass), _stream(stream)), "fastgen_profile_stall_test")
+
+
+# ---------------------------------------------------------------------------
+# Position rotation and paged 8-bit caches.  These calls take torch tensors
+# and check their types, sizes and device before the library sees them; they
+# run on the tensors' device, on its current stream unless one is given.
+
+
+def _refuse(where: str, what: str) -> None:
+    raise FastGenError(FG_EINVAL, f"{where}: {what}")
+
+
+def _heads(p: Params) -> tuple[int, int]:
+    """Query and key/value head instances of the batch."""
+    layers = p.B * p.L
+    return layers * p.H, layers * (p.Hkv or p.H)
+
+
+def _is(x, where: str, name: str, dtype, count: int, device):
+    """The address of tensor x, which must be contiguous, of that type (or one
+    of those types) and device, with `count` elements."""
+    if x.dtype != dtype and not (isinstance(dtype, tuple) and x.dtype in dtype):
+        _refuse(where, f"{name} has type {x.dtype}")
+    if x.numel() != count:
+        _refuse(where, f"{name} has {x.numel()} elements, not {count}")
+    if x.device != device or not x.is_contiguous():
+        _refuse(where, f"{name} must be contiguous and on {device}")
+    return x.data_ptr()
+
+
+def _ids(x, where: str, name: str, device):
+    return None if x is None else _is(x, where, name, _torch().int32, x.numel(), device)
+
+
+def _torch():
+    import torch
+
+    return torch
+
+
+def _elem(p: Params):
+    torch = _torch()
+    return torch.bfloat16 if p.dtype == FG_BF16 else torch.float32
+
+
+def _run(where: str, device, stream, fn, *args) -> None:
+    """Calls fn(*args, stream) with `device` current."""
+    torch = _torch()
+    if device.type != "cuda":
+        _refuse(where, f"tensors on {device}")
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), where)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)), where)
+
+
+class Rope:
+    """A position rotation: turns [rot_dim / 2] int64 on the device (64-bit
+    fractions of a turn per position, see fastgen_rope_table) and the pairing
+    (FG_ROPE_INTERLEAVED or FG_ROPE_HALF)."""
+
+    def __init__(self, turns, style: int = FG_ROPE_INTERLEAVED):
+        torch = _torch()
+        if turns.dtype != torch.int64 or not turns.is_contiguous():
+            _refuse("Rope", "turns must be a contiguous int64 tensor")
+        self.turns, self.device = turns, turns.device
+        self.c = RopeStruct(turns.data_ptr(), 2 * turns.numel(), style)
+
+    @classmethod
+    def make(cls, rot_dim: int, base: float = 10000.0, style: int = FG_ROPE_INTERLEAVED,
+             device="cuda", inv_freq=None):
+        """inv_freq (radians per position, default base^(-2i/rot_dim))."""
+        if inv_freq is None:
+            inv_freq = [float(base) ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+        return cls(fastgen_rope_table(inv_freq).to(device), style)
+
+
+def _rope(rope, where: str, device):
+    if rope is None:
+        return None
+    if rope.device != device:
+        _refuse(where, f"rope must be on {device}")
+    return rope.c
+
+
+def fastgen_rope_table(inv_freq):
+    """int64 CPU tensor of the turns per position of each frequency."""
+    torch = _torch()
+    f = torch.as_tensor(inv_freq, dtype=torch.float64).contiguous().cpu()
+    out = torch.empty(f.numel(), dtype=torch.int64)
+    _check(lib().fastgen_rope_table(f.data_ptr(), f.numel(), out.data_ptr()), "fastgen_rope_table")
+    return out
+
+
+def fastgen_rope(params, Q, K, pos, rope, Q_out, K_out, stream=None) -> None:
+    """Rotates Q [G, n, d] and K [Gkv, n, d] at pos [B, n] (None: 0 .. n-1)."""
+    w, p = "fastgen_rope", params
+    G, Gkv = _heads(p)
+    dt, size = _elem(p), p.n * p.d
+    if rope is None or (Q is None and K is None):
+        _refuse(w, "no rotation, or nothing to rotate")
+    dev = (K if Q is None else Q).device
+    ptr = [None if x is None else _is(x, w, name, dt, count * size, dev)
+           for x, name, count in ((Q, "Q", G), (K, "K", Gkv), (Q_out, "Q_out", G),
+                                  (K_out, "K_out", Gkv))]
+    at = None if pos is None else _is(pos, w, "pos", _torch().int32, p.B * p.n, dev)
+    _run(w, dev, stream, lib().fastgen_rope, p, ptr[0], ptr[1], at, _rope(rope, w, dev), ptr[2],
+         ptr[3])
+
+
+def fastgen_paged_table_len(params, max_new_tokens: int) -> int:
+    return lib().fastgen_paged_table_len(params, max_new_tokens)
+
+
+def fastgen_paged_sched_bytes(params, table_len: int) -> int:
+    return lib().fastgen_paged_sched_bytes(params, table_len)
+
+
+class PagedCache:
+    """The buffers of one batch of paged 8-bit caches (fg_paged_cache):
+    k_pages, v_pages [n_pages, 64, d] float8_e4m3fn, exps [n_pages, 4, 2] int8, pos
+    [n_pages, 64] int32, page_table int32, caches [Gkv, 6] int32, rows [Gkv]
+    int32, next_page [1] int32, rows_out [Gkv] int32 (default: rows, in
+    place).  The page buffers may be None until set_pages.  Holds the decode
+    work list, which schedule or fastgen_paged_plan fills."""
+
+    def __init__(self, params, k_pages, v_pages, exps, pos, page_table, caches, rows, next_page,
+                 rows_out=None):
+        torch, w = _torch(), "PagedCache"
+        Gkv = _heads(params)[1]
+        dev, i32 = page_table.device, torch.int32
+        self.device, self.d = dev, params.d
+        c = self.c = PagedCacheStruct()
+        c.table_len = page_table.numel()
+        c.page_table = _is(page_table, w, "page_table", i32, page_table.numel(), dev)
+        c.caches = _is(caches, w, "caches", i32, Gkv * 6, dev)
+        c.rows = _is(rows, w, "rows", i32, Gkv, dev)
+        c.next_page = _is(next_page, w, "next_page", i32, 1, dev)
+        c.rows_out = c.rows if rows_out is None else _is(rows_out, w, "rows_out", i32, Gkv, dev)
+        need = fastgen_paged_sched_bytes(params, c.table_len)
+        if need == 0:
+            _refuse(w, "parameters or table length")
+        self.sched = torch.empty(need, dtype=torch.uint8, device=dev)
+        c.sched, c.sched_bytes = self.sched.data_ptr(), need
+        self.page_table, self.caches, self.rows, self.next_page = page_table, caches, rows, next_page
+        self.rows_out = rows if rows_out is None else rows_out
+        self.k_pages = self.v_pages = self.exps = self.pos = None
+        if k_pages is not None:
+            self.set_pages(k_pages, v_pages, exps, pos)
+
+    def set_pages(self, k_pages, v_pages, exps, pos) -> None:
+        torch, w, c = _torch(), "PagedCache", self.c
+        pages, row = exps.numel() // 8, FG_PAGE_ROWS * self.d
+        codes = (torch.float8_e4m3fn, torch.uint8)
+        c.k_pages = _is(k_pages, w, "k_pages", codes, pages * row, self.device)
+        c.v_pages = _is(v_pages, w, "v_pages", codes, pages * row, self.device)
+        c.exps = _is(exps, w, "exps", torch.int8, pages * 8, self.device)
+        c.pos = _is(pos, w, "pos", torch.int32, pages * FG_PAGE_ROWS, self.device)
+        c.n_pages = pages
+        self.k_pages, self.v_pages, self.exps, self.pos = k_pages, v_pages, exps, pos
+
+    def schedule(self, params, stream=None) -> None:
+        fastgen_paged_schedule(params, self, stream)
+
+
+def fastgen_paged_plan(params, policy, keep, max_new_tokens, cache, stream=None) -> PagedInfo:
+    w, torch = "fastgen_paged_plan", _torch()
+    G, dev, info = _heads(params)[0], cache.device, PagedInfo()
+    _run(w, dev, stream, lib().fastgen_paged_plan, params,
+         _is(policy, w, "policy", torch.int8, G, dev),
+         _is(keep, w, "keep", torch.uint8, G * params.n, dev), max_new_tokens, cache.c, info)
+    return info
+
+
+def fastgen_paged_schedule(params, cache, stream=None) -> None:
+    _run("fastgen_paged_schedule", cache.device, stream, lib().fastgen_paged_schedule, params,
+         cache.c)
+
+
+def _of_cache(p, cache, w: str):
+    """The cache's struct, if it belongs to these parameters."""
+    if cache.rows.numel() != _heads(p)[1] or cache.d != p.d:
+        _refuse(w, "the cache was made for other parameters")
+    return cache.c
+
+
+def fastgen_compact_q8(params, K, V, keep, cache, dev_err, stream=None) -> None:
+    w, p, torch = "fastgen_compact_q8", params, _torch()
+    G, Gkv = _heads(p)
+    dev, dt, size = cache.device, _elem(p), Gkv * p.n * p.d
+    _run(w, dev, stream, lib().fastgen_compact_q8, p, _is(K, w, "K", dt, size, dev),
+         _is(V, w, "V", dt, size, dev), _is(keep, w, "keep", torch.uint8, G * p.n, dev),
+         _of_cache(p, cache, w), _is(dev_err, w, "dev_err", torch.int32, 1, dev))
+
+
+def fastgen_append_q8_workspace_bytes(params, m: int) -> int:
+    return lib().fastgen_append_q8_workspace_bytes(params, m)
+
+
+def fastgen_append_q8(params, cache, k_new, v_new, new_ids, n_new, special_ids, punct_ids, pos,
+                      rope, workspace, dev_err, stream=None) -> None:
+    """Appends m tokens: k_new, v_new [Gkv, m, d], new_ids [B, m], n_new [B] or
+    None (m each), pos [B] the first new position of each sequence (< 0: idle)."""
+    w, p, torch = "fastgen_append_q8", params, _torch()
+    Gkv, dev, dt, i32 = _heads(p)[1], cache.device, _elem(p), torch.int32
+    m = new_ids.numel() // p.B
+    _run(w, dev, stream, lib().fastgen_append_q8, p, _of_cache(p, cache, w),
+         _is(k_new, w, "k_new", dt, Gkv * m * p.d, dev),
+         _is(v_new, w, "v_new", dt, Gkv * m * p.d, dev),
+         _is(new_ids, w, "new_ids", i32, p.B * m, dev), m,
+         None if n_new is None else _is(n_new, w, "n_new", i32, p.B, dev),
+         _ids(special_ids, w, "special_ids", dev), _count(special_ids),
+         _ids(punct_ids, w, "punct_ids", dev), _count(punct_ids),
+         _is(pos, w, "pos", i32, p.B, dev), _rope(rope, w, dev),
+         _is(workspace, w, "workspace", torch.uint8, workspace.numel(), dev), workspace.numel(),
+         _is(dev_err, w, "dev_err", i32, 1, dev))
+
+
+def fastgen_decode_q8_workspace_bytes(params, cache) -> int:
+    return lib().fastgen_decode_q8_workspace_bytes(params, cache.c)
+
+
+def fastgen_decode_attn_q8(params, cache, q, k_new, v_new, new_ids, special_ids, punct_ids, pos,
+                           rope, out, workspace, dev_err, stream=None) -> None:
+    """One generation step: q, out [G, d], k_new, v_new [Gkv, d] (None: nothing is
+    appended), new_ids [B], pos [B] int32 on the device (< 0: idle)."""
+    w, p, torch = "fastgen_decode_attn_q8", params, _torch()
+    (G, Gkv), dev, dt, i32 = _heads(p), cache.device, _elem(p), torch.int32
+    new = [None if x is None else _is(x, w, name, dt, Gkv * p.d, dev)
+           for x, name in ((k_new, "k_new"), (v_new, "v_new"))]
+    _run(w, dev, stream, lib().fastgen_decode_attn_q8, p, _of_cache(p, cache, w),
+         _is(q, w, "q", dt, G * p.d, dev), new[0], new[1],
+         None if new_ids is None else _is(new_ids, w, "new_ids", i32, p.B, dev),
+         _ids(special_ids, w, "special_ids", dev), _count(special_ids),
+         _ids(punct_ids, w, "punct_ids", dev), _count(punct_ids),
+         _is(pos, w, "pos", i32, p.B, dev), _rope(rope, w, dev),
+         _is(out, w, "out", dt, G * p.d, dev),
+         _is(workspace, w, "workspace", torch.uint8, workspace.numel(), dev), workspace.numel(),
+         _is(dev_err, w, "dev_err", i32, 1, dev))

@@ -221,6 +221,102 @@ class FastGenSession:
         return (fg.HeadDesc * self.Gkv).from_buffer_copy(raw)
 
 
+class PagedSession(FastGenSession):
+    """A session whose caches are paged 8-bit ones: the same calls, with rows
+    of e4m3 codes in pages that a cache takes when it grows, several tokens
+    at a time (append), and a position per sequence.
+
+    rope (fastgen.Rope): prefill, append and decode then take queries and keys
+    as projected and rotate them at their positions; None: they are taken as
+    they are.  pages: size of the page pool; None gives the worst case (every
+    cache growing by max_new_tokens rows).  A smaller pool that runs out is
+    reported as FG_ECAPACITY by fastgen_read_error(dev_err)."""
+
+    def __init__(self, params: fg.Params, special_ids, punct_ids, max_new_tokens: int,
+                 device="cuda", stream=None, guard=False, rope=None, pages=None):
+        super().__init__(params, special_ids, punct_ids, max_new_tokens, device, stream, guard)
+        self.rope, self.pages = rope, pages
+        Gkv, E, i32 = self.Gkv, self._empty, torch.int32
+        self.cache = fg.PagedCache(
+            params, None, None, None, None,
+            E((fg.fastgen_paged_table_len(params, self.max_new),), i32), E((Gkv, 6), i32),
+            E((Gkv,), i32), E((1,), i32))
+        self.aws = None
+        self._rotated = None
+
+    def rotate(self, Q, K, pos=None, out=None):
+        """Q and K rotated at pos [B, n] (None: 0 .. n-1) into `out` (a pair;
+        None: buffers of the session, reused by the next call)."""
+        if out is None:
+            if self._rotated is None:
+                self._rotated = (torch.empty_like(Q), torch.empty_like(K))
+            out = self._rotated
+        fg.fastgen_rope(self.p, Q, K, pos, self.rope, out[0], out[1], self.stream)
+        return out
+
+    def prefill(self, Q, K, V, token_ids):
+        if self.rope is not None:
+            Q, K = self.rotate(Q, K)
+        super().prefill(Q, K, V, token_ids)
+
+    def prefill_with_policy(self, Q, K, V, token_ids, policy_map):
+        if self.rope is not None:
+            Q, K = self.rotate(Q, K)
+        super().prefill_with_policy(Q, K, V, token_ids, policy_map)
+
+    def compact(self, K, V):
+        """Plans the paged caches of the profiled prompt and codes its kept
+        rows; K as it was profiled (rotated)."""
+        self.info = fg.fastgen_paged_plan(self.p, self.policy, self.keep, self.max_new, self.cache,
+                                          self.stream)
+        want = self.info.max_pages if self.pages is None else max(self.pages, self.info.pages)
+        if self.cache.exps is None or self.cache.c.n_pages < want:
+            rows, d = want * fg.FG_PAGE_ROWS, self.p.d
+            self.cache.set_pages(self._empty((rows, d), torch.uint8),
+                                 self._empty((rows, d), torch.uint8),
+                                 self._empty((want, 8), torch.int8),
+                                 self._empty((rows,), torch.int32))
+        self._size_decode_workspace()
+        fg.fastgen_compact_q8(self.p, K, V, self.keep, self.cache, self.dev_err, self.stream)
+
+    def reschedule(self):
+        """Splits the decode work by the caches' present sizes (worth a call
+        now and then in a long generation; graphs captured before it are void)."""
+        self.cache.schedule(self.p, self.stream)
+        self._size_decode_workspace()
+
+    def _size_decode_workspace(self):
+        need = fg.fastgen_decode_q8_workspace_bytes(self.p, self.cache)
+        if self.dws is None or self.dws.numel() < need:
+            self.dws = self._empty((max(need, 256),), torch.uint8)
+
+    def _positions(self, pos):
+        if isinstance(pos, int):
+            return torch.full((self.p.B,), pos, dtype=torch.int32, device=self.device)
+        return pos
+
+    def append(self, k_new, v_new, new_ids, pos, n_new=None):
+        """Appends m tokens to every cache: k_new, v_new [Gkv, m, d], new_ids
+        [B, m], pos [B] (or an int) the first new position of each sequence (< 0:
+        left out), n_new [B] the tokens of each (None: m)."""
+        m = new_ids.numel() // self.p.B
+        need = fg.fastgen_append_q8_workspace_bytes(self.p, m)
+        if self.aws is None or self.aws.numel() < need:
+            self.aws = self._empty((max(need, 256),), torch.uint8)
+        fg.fastgen_append_q8(self.p, self.cache, k_new, v_new, new_ids, n_new, self.special,
+                             self.punct, self._positions(pos), self.rope, self.aws, self.dev_err,
+                             self.stream)
+
+    def decode(self, q, k_new, v_new, new_ids, pos, out=None):
+        """One generation step at pos [B] (or an int): the tokens appended, then
+        q [G, d] attending; k_new = v_new = None attends only."""
+        out = self.out if out is None else out
+        fg.fastgen_decode_attn_q8(self.p, self.cache, q, k_new, v_new, new_ids, self.special,
+                                  self.punct, self._positions(pos), self.rope, out, self.dws,
+                                  self.dev_err, self.stream)
+        return out
+
+
 POLICY_MAP_FORMAT = "fastgen-head-policy-map"
 
 

@@ -418,10 +418,179 @@ fg_status fastgen_profile_stall_test(const fg_params* p, const void* Q, const vo
                                      size_t workspace_bytes, int32_t* dev_err, int32_t stall_pass,
                                      void* stream);
 
+/* ------------------------------------------------------------------------
+ * Position rotation (rotary embedding) of a prompt's queries and keys.
+ *
+ * With theta_i = pos * inv_freq_i for pair i < rot_dim / 2, a pair (x, y) of
+ * a row becomes (x cos theta - y sin theta, y cos theta + x sin theta); the
+ * dimensions from rot_dim on stay.  FG_ROPE_INTERLEAVED pairs dimensions
+ * (2i, 2i + 1), FG_ROPE_HALF (i, i + rot_dim / 2).  The frequencies are given
+ * as turns per position, 64-bit fractions of a turn: the angle's fraction of
+ * a turn is then exact at every position.
+ *
+ * fastgen_rope_table (HOST, no GPU): turns[i] = inv_freq[i] / (2 pi) modulo
+ *   one turn, times 2^64, rounded; inv_freq in radians per position, finite
+ *   and >= 0, else FG_EINVAL.  The caller copies the table to the device.
+ * fastgen_rope: Q [G, n, d] and K [Gkv, n, d] of dtype, rotated into Q_out and
+ *   K_out (which may be Q and K themselves, but must not overlap them
+ *   otherwise); 32-bit arithmetic, rounded once.  pos [B, n] int32 (>= 0)
+ *   or NULL for positions 0 .. n-1.  Q and Q_out, or K and K_out, may both be
+ *   NULL (that side is left out).
+ * rot_dim: a multiple of 16, at most d.
+ * Errors: FG_EINVAL, FG_EDTYPE as above.
+ * ------------------------------------------------------------------------ */
+enum { FG_ROPE_INTERLEAVED = 0, FG_ROPE_HALF = 1 };
+
+typedef struct {
+  const uint64_t* turns; /* DEVICE [rot_dim / 2] */
+  int32_t rot_dim;
+  int32_t style; /* FG_ROPE_* */
+} fg_rope;
+
+fg_status fastgen_rope_table(const double* inv_freq, int32_t count, uint64_t* turns);
+
+fg_status fastgen_rope(const fg_params* p, const void* Q, const void* K, const int32_t* pos,
+                       const fg_rope* rope, void* Q_out, void* K_out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Paged 8-bit caches: the compressed caches above with rows of e4m3 codes in
+ * pages that a cache takes when it grows.
+ *
+ * A page holds FG_PAGE_ROWS rows of one cache: the codes of K and of V, the
+ * rows' absolute positions, and, for every block of FG_BLOCK_ROWS rows, one
+ * power-of-two exponent of K and one of V; a row's value is code * 2^exponent.
+ * A block's exponent is the least e >= -100 with amax <= 448 * 2^e over its
+ * finite values; infinities are stored as the largest code, NaN as NaN.  When
+ * a row arrives that needs a larger exponent, the block's codes are rounded
+ * again at the new one (a code keeps its fraction bits unless it becomes
+ * subnormal); exponents never shrink, except that a block of the
+ * never-evicted segment whose first row arrives starts afresh.
+ *
+ * Cache c has a never-evicted segment of rows[c] rows, the pages of which are
+ * page_table[first_page ..], and for FG_POLICY_SPFL a ring of w rows in the
+ * pages page_table[ring_page ..]: position p lives at slot p mod w, and a
+ * slot counts at time t while its row's position is in (t - w, t].  An entry
+ * of -1 is a page not taken yet: appending takes page (*next_page)++.  All
+ * buffers belong to the caller, who may also lay out caches, rows and
+ * page_table (pages in any order, entries assigned ahead) itself.
+ *
+ * An entry or a descriptor that names no page of the pool, or a row count past
+ * its segment, is never followed: those rows count as absent and 4 is ORed
+ * into *dev_err (FG_EINVAL from fastgen_read_error).
+ * ------------------------------------------------------------------------ */
+#define FG_PAGE_ROWS 64
+#define FG_BLOCK_ROWS 16
+
+typedef struct {
+  int32_t policy;     /* FG_POLICY_* */
+  int32_t w;          /* ring rows (0 unless policy is FG_POLICY_SPFL) */
+  int32_t first_page; /* first page_table entry of the never-evicted segment */
+  int32_t max_pages;  /* entries of that segment */
+  int32_t ring_page;  /* first page_table entry of the ring */
+  int32_t ring_pages; /* entries of the ring: ceil(w / FG_PAGE_ROWS) */
+} fg_paged_desc;
+
+/* The buffers of one batch of paged caches (a HOST struct of DEVICE pointers). */
+typedef struct {
+  void* k_pages;         /* [n_pages, FG_PAGE_ROWS, d] e4m3, 16-byte aligned */
+  void* v_pages;         /* like k_pages */
+  int8_t* exps;          /* [n_pages, FG_PAGE_ROWS / FG_BLOCK_ROWS, 2] (K, V), 8-byte aligned */
+  int32_t* pos;          /* [n_pages, FG_PAGE_ROWS], 8-byte aligned */
+  int32_t* page_table;   /* [table_len] */
+  fg_paged_desc* caches; /* [Gkv], 8-byte aligned */
+  int32_t* rows;         /* [Gkv] rows of the never-evicted segments */
+  int32_t* rows_out;     /* [Gkv] the counts after a call; may be rows.  Another buffer leaves
+                            rows as it was, so that the same call can be made again. */
+  int32_t* next_page;    /* [1] first page no cache has taken */
+  void* sched;           /* the decode work list, 256-byte aligned */
+  int64_t sched_bytes;
+  int32_t n_pages;
+  int32_t table_len;
+  int32_t n_work;        /* set by fastgen_paged_plan and fastgen_paged_schedule */
+  int32_t rows_per_work; /* likewise */
+} fg_paged_cache;
+
+typedef struct {
+  int32_t pages;       /* pages the prompt takes */
+  int32_t max_pages;   /* pages if every cache grows by max_new_tokens rows */
+  int32_t table_used;  /* page_table entries in use */
+} fg_paged_info;
+
+/* Entries page_table may need for max_new_tokens (0: parameters rejected, or past 2^31 - 1), and
+ * bytes of sched for a table of table_len entries. */
+int32_t fastgen_paged_table_len(const fg_params* p, int32_t max_new_tokens);
+size_t fastgen_paged_sched_bytes(const fg_params* p, int32_t table_len);
+
+/* Layout of the prompt's caches from policy [G] and keep [G, n] (as fastgen_compact_plan; groups
+ * share the union cache): writes caches, rows, page_table (the prompt's pages in order, -1 where a
+ * cache may grow), next_page and the work list.  Needs those buffers, table_len >=
+ * fastgen_paged_table_len and sched_bytes; the page buffers may be NULL until n_pages is known.
+ * *info, cache->n_work and cache->rows_per_work (HOST) are set: SYNCHRONOUS on `stream`.
+ * Errors: FG_EINVAL, FG_EDTYPE, FG_EWORKSPACE for a short table or sched. */
+fg_status fastgen_paged_plan(const fg_params* p, const int8_t* policy, const uint8_t* keep,
+                             int32_t max_new_tokens, fg_paged_cache* cache, fg_paged_info* info,
+                             void* stream);
+
+/* The decode work list of the current rows (needed before the first decode of caches that
+ * fastgen_paged_plan did not lay out, and worth a call now and then in a long generation: the last
+ * item of a segment takes every row appended later).  SYNCHRONOUS on `stream`. */
+fg_status fastgen_paged_schedule(const fg_params* p, fg_paged_cache* cache, void* stream);
+
+/* Gathers and codes the kept prompt rows: K, V [Gkv, n, d] dtype and keep [G, n] as
+ * fastgen_compact.  Writes codes, exponents and positions of the rows in use and -1 as the
+ * position of ring slots without a row; every other byte of a page stays.
+ * Asynchronous.  Errors: FG_EINVAL, FG_EDTYPE; dev_err as above. */
+fg_status fastgen_compact_q8(const fg_params* p, const void* K, const void* V, const uint8_t* keep,
+                             const fg_paged_cache* cache, int32_t* dev_err, void* stream);
+
+/* Appends new tokens' rows to every cache, rotated on the way.
+ *
+ * Sequence b has n_new[b] new tokens (0 .. m; n_new NULL: m) at positions pos[b], pos[b] + 1, ...
+ * with ids new_ids [B, m]; k_new, v_new [Gkv, m, d] dtype.  Each token is placed by its cache's
+ * policy as in fastgen_decode_attn: rows of the never-evicted segment in token order, ring rows at
+ * their slots (of tokens that share a slot the last one).  K rows are rotated at their position in
+ * 32 bits before they are coded (rope NULL: as they are).  A sequence with pos[b] < 0, and tokens
+ * from n_new[b] on, are left out; what belongs to them is not touched.  rows_out gets the new
+ * counts.  When a segment's table or the pool has no page left, the tokens from there on are not
+ * stored and 1 is ORed into *dev_err (FG_ECAPACITY).
+ * m: 1 .. 2^20.  The workspace (256-byte aligned) holds nothing between calls; calls that share
+ * one must not overlap.  Asynchronous.  Errors: FG_EINVAL, FG_EDTYPE, FG_EWORKSPACE. */
+size_t fastgen_append_q8_workspace_bytes(const fg_params* p, int32_t m);
+
+fg_status fastgen_append_q8(const fg_params* p, const fg_paged_cache* cache, const void* k_new,
+                            const void* v_new, const int32_t* new_ids, int32_t m,
+                            const int32_t* n_new, const int32_t* special_ids, int32_t n_special,
+                            const int32_t* punct_ids, int32_t n_punct, const int32_t* pos,
+                            const fg_rope* rope, void* workspace, size_t workspace_bytes,
+                            int32_t* dev_err, void* stream);
+
+/* One generation step over paged caches.
+ *
+ * The token of sequence b at position pos[b] (device, so that a captured step can be replayed; < 0:
+ * the sequence takes no part and its outputs stay as they were) is appended as by
+ * fastgen_append_q8 with m = 1; then every query head attends over its cache,
+ *   out[g] = sum_j softmax_j(s q_g . k_j) v_j   (zeros if empty)
+ * with q [G, d] rotated at pos[b] and the rows as stored.  k_new, v_new NULL: nothing is
+ * appended; pos[b] is then the position of the newest token, and new_ids may be NULL.
+ * bf16 queries enter the products with 11 bits after rotation (rounding at most 2^-12 of each
+ * value; without rotation they are exact), fp32 queries with 22; the softmax weights times their
+ * row's value exponent likewise, and those below 2^-40 of the largest of them count as zero in
+ * the product.  Sums are 32-bit.
+ * Arguments else as fastgen_decode_attn; needs a work list.  Asynchronous.
+ * Errors: FG_EINVAL, FG_EDTYPE, FG_EWORKSPACE; dev_err as above. */
+size_t fastgen_decode_q8_workspace_bytes(const fg_params* p, const fg_paged_cache* cache);
+
+fg_status fastgen_decode_attn_q8(const fg_params* p, const fg_paged_cache* cache, const void* q,
+                                 const void* k_new, const void* v_new, const int32_t* new_ids,
+                                 const int32_t* special_ids, int32_t n_special,
+                                 const int32_t* punct_ids, int32_t n_punct, const int32_t* pos,
+                                 const fg_rope* rope, void* out, void* workspace,
+                                 size_t workspace_bytes, int32_t* dev_err, void* stream);
+
 /* Synchronously reads a device flag written by fastgen_profile,
- * fastgen_profile_with_policy or fastgen_decode_attn and maps it to a status
- * (FG_OK, FG_ECAPACITY, FG_EINVAL for an out-of-range saved policy, or
- * FG_EDEVICE).  Waits on `stream`. */
+ * fastgen_profile_with_policy, fastgen_decode_attn or a paged call and maps it to a status
+ * (FG_OK, FG_ECAPACITY, FG_EINVAL for an out-of-range saved policy or a bad
+ * page, or FG_EDEVICE).  Waits on `stream`. */
 fg_status fastgen_read_error(const int32_t* dev_err, void* stream);
 
 #ifdef __cplusplus
