@@ -56,7 +56,7 @@ fg_status check_pages(const fg_paged_cache* c) {
   if (st != FG_OK) return st;
   if (!c->k_pages || !c->v_pages || !c->exps || !c->pos || c->n_pages < 1) return FG_EINVAL;
   if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16) || !aligned(c->exps, 8) ||
-      !aligned(c->pos, 8))
+      !aligned(c->pos, 16))
     return FG_EINVAL;
   return FG_OK;
 }

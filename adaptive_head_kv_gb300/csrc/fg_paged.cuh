@@ -101,6 +101,26 @@ __device__ __forceinline__ uint4 ld16(const void* p) {
   return v;
 }
 
+// Is `id` one of the `cnt` ids of `set`?  All lanes of a warp call with the
+// same id: each looks at every 32nd entry.
+__device__ __forceinline__ bool warp_id_in(int id, const int32_t* __restrict__ set, int cnt) {
+  bool hit = false;
+  for (int i = threadIdx.x & 31; i < cnt; i += 32) hit |= __ldg(set + i) == id;
+  return __any_sync(0xffffffffu, hit);
+}
+
+// 16-byte global -> shared copy in the background, and its groups.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 struct RopeArgs {
   const unsigned long long* turns;  // [rot / 2]
   int rot;                          // 0: no rotation
@@ -137,31 +157,44 @@ __device__ __forceinline__ int page_at(const PagedArgs& a, int first, int entrie
 // ------------------------------------------------- rows held by one warp
 // A row of D values over the 32 lanes: lane l has values l * PER ..
 
-// Rotates a row (all lanes call).  angle(i) gives (cos, sin) of pair i.
+// (cos, sin) of the pair of each of the lane's values; angle(i) gives pair i's.
 template <int PER, typename Angle>
-__device__ __forceinline__ void rotate_row(float (&x)[PER], int rot, int style, Angle angle) {
+__device__ __forceinline__ void row_angles(float2 (&cs)[PER], int rot, int style, Angle angle) {
+  const int e0 = (threadIdx.x & 31) * PER, h = rot / 2;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) cs[k] = make_float2(1.f, 0.f);
+  if (e0 >= rot) return;
+  if (style == FG_ROPE_INTERLEAVED) {
+#pragma unroll
+    for (int k = 0; k < PER; k += 2) cs[k] = cs[k + 1] = angle((e0 + k) / 2);
+  } else {
+#pragma unroll
+    for (int k = 0; k < PER; ++k) cs[k] = angle(e0 + k - (e0 < h ? 0 : h));
+  }
+}
+
+// Rotates a row by its angles (all lanes call).
+template <int PER>
+__device__ __forceinline__ void rotate_row(float (&x)[PER], const float2 (&cs)[PER], int rot,
+                                           int style) {
   const int lane = threadIdx.x & 31, e0 = lane * PER;
   if (style == FG_ROPE_INTERLEAVED) {
-    if (e0 < rot) {
 #pragma unroll
-      for (int k = 0; k < PER; k += 2) {
-        const float2 cs = angle((e0 + k) / 2);
-        const float u = x[k], v = x[k + 1];
-        x[k] = u * cs.x - v * cs.y;
-        x[k + 1] = v * cs.x + u * cs.y;
+    for (int k = 0; k < PER; k += 2) {
+      const float u = x[k], v = x[k + 1];
+      if (e0 < rot) {
+        x[k] = u * cs[k].x - v * cs[k].y;
+        x[k + 1] = v * cs[k].x + u * cs[k].y;
       }
     }
   } else {
-    const int h = rot / 2;  // a multiple of 8: pairs of lanes hold pairs of values
+    const int h = rot / 2;  // a multiple of 8: the two halves of a pair sit in two lanes
     const bool first = e0 < h;
     const int other = e0 >= rot ? lane : first ? lane + h / PER : lane - h / PER;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const float y = __shfl_sync(0xffffffffu, x[k], other);
-      if (e0 < rot) {
-        const float2 cs = angle(e0 + k - (first ? 0 : h));
-        x[k] = first ? x[k] * cs.x - y * cs.y : x[k] * cs.x + y * cs.y;
-      }
+      if (e0 < rot) x[k] = first ? x[k] * cs[k].x - y * cs[k].y : x[k] * cs[k].x + y * cs[k].y;
     }
   }
 }

@@ -189,8 +189,10 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const PagedArgs a, 
     for (int i = 0; i < kBlockRows; ++i) {
       const int t = __shfl_sync(0xffffffffu, tok, i);
       if (t < 0) continue;
-      const float2* cs = n.angles + ((size_t)b * n.m + t) * pairs;
-      rotate_row<PER>(x[i], n.rope.rot, n.rope.style, [&](int p) { return cs[p]; });
+      const float2* at = n.angles + ((size_t)b * n.m + t) * pairs;
+      float2 cs[PER];
+      row_angles<PER>(cs, n.rope.rot, n.rope.style, [&](int p) { return at[p]; });
+      rotate_row<PER>(x[i], cs, n.rope.rot, n.rope.style);
     }
   }
   put_rows<D, kBlockRows>(x, mask, 0, fresh, (which ? a.vp : a.kp) + ((size_t)page * kPageRows + r) * D,

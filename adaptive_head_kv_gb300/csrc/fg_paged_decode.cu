@@ -5,20 +5,23 @@
 // never-evicted segment (the last one also every row appended later) or of
 // its ring.  A CTA of 4 warps takes an item, warp v its blocks of 16 rows v,
 // v + 4, ...; the CTA whose item holds the new token's row codes it into the
-// page first.  A block's K and V codes go from HBM to registers in 16-byte
-// pieces, each read once, and both products run as warp MMAs in f16, which
-// holds every e4m3 code exactly:
+// page first.  A warp's blocks reach a ring of kStages blocks in shared memory by
+// cp.async (each code is read once, and loads stay in flight without holding
+// registers), and both products run as warp MMAs in f16, which holds every
+// e4m3 code exactly:
 //   S[16 x 16 keys] = Q[16 x d] . K^T    queries in rows 0-7; rows 8-15 hold
 //                                        what f16 loses of fp32 queries
 //   O^T[d x 8]     += V^T[d x 16 keys] . P^T
 // The dimension order inside a product is free as long as both operands agree,
-// so every lane's operand fragments are consecutive bytes of a row and
-// nothing passes through shared memory; S's accumulators are P^T's operand
-// fragment as they stand.  The exponents of a block are two numbers for the
-// whole MMA: K's scales the scores, V's is added to them in base 2, so that
-// the weight carries it and the sum divides it out again.  A weight enters the
-// product in f16, times 2^15: 11 bits (22 in two terms for fp32), and nothing
-// below 2^-40 of the largest weight times 2^exponent.
+// so a lane's operand fragments are 16 consecutive bytes of a row; S's
+// accumulators are P^T's operand fragment as they stand.  The order of the
+// keys is free as well: with 16-byte pieces swizzled by the row, slot_key
+// puts the rows that a load phase touches on different banks.  The exponents
+// of a block are two numbers for the whole MMA: K's scales the scores, V's is
+// added to them in base 2, so that the weight carries it and the sum divides
+// it out again.  A weight enters the product in f16, times 2^15: 11 bits (22
+// in two terms for fp32), and nothing below 2^-40 of the largest weight times
+// 2^exponent.
 //
 // Bound by HBM: 2 d bytes a row.  Unpacking costs one conversion per two
 // codes; scoring on the SIMT lanes would cost four instructions per two
@@ -64,12 +67,22 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ uint2 ld8(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
-               : "=r"(v.x), "=r"(v.y)
-               : "l"(p)
+__device__ __forceinline__ uint4 lds16(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(p)
                : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t p) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ int lds4(uint32_t p) {
+  int v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(p) : "memory");
   return v;
 }
 
@@ -78,17 +91,37 @@ struct Piece;  // a lane's D / 8 codes of a V row
 template <>
 struct Piece<128> {
   uint4 v;
-  __device__ void load(const uint8_t* p) { v = ld16(p); }
+  __device__ void load(uint32_t p) { v = lds16(p); }
   __device__ void zero() { v = make_uint4(0, 0, 0, 0); }
   __device__ uint32_t word(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 };
 template <>
 struct Piece<64> {
   uint2 v;
-  __device__ void load(const uint8_t* p) { v = ld8(p); }
+  __device__ void load(uint32_t p) { v = lds8(p); }
   __device__ void zero() { v = make_uint2(0, 0); }
   __device__ uint32_t word(int i) const { return i == 0 ? v.x : v.y; }
 };
+
+// The ring: per stage a block's K and V codes, its rows' positions and its
+// exponents.  Row r's 16-byte piece c sits at piece c ^ swizzle(r).  A load
+// phase (8 lanes of 16 bytes, 16 of 8) of the K fragments touches all pieces
+// of one half (d = 128) or all pieces (d = 64) of two rows, one of the V
+// fragments two adjacent pieces of four rows; slot_key orders the 8 keys of a
+// tile so that these fall on different banks.
+template <int D>
+struct Ring {
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kV = kBlockRows * D, kPos = 2 * kV, kMeta = kPos + kBlockRows * 4;
+  static constexpr int kStride = kMeta + 64;  // a multiple of 128
+  static constexpr int kWarpBytes = kStages * kStride;
+  __device__ static int swizzle(int r) { return D == 128 ? r & 7 : r & 2; }
+  __device__ static int slot_key(int n) {
+    const int k = n >> 1;
+    return D == 128 ? (n & 1 ? (n + 4) & 7 : n) : (n & 1 ? 4 + (k ^ 1) : k);
+  }
+};
+static_assert(Ring<128>::kStride % 128 == 0 && Ring<64>::kStride % 128 == 0, "bank phase");
 
 __device__ __forceinline__ uint32_t word4(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
@@ -97,64 +130,63 @@ __device__ __forceinline__ uint32_t word4(const uint4& v, int i) {
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
     q8_split_kernel(const PagedArgs a, const PagedDecodeArgs n, int H, int R, int HLkv, float sl2) {
+  using RG = Ring<D>;
   constexpr bool kWide = sizeof(T) == 4;  // fp32: queries and weights in two f16 terms
   constexpr int KI = D / 64;   // 16-byte pieces of a K row per lane
   constexpr int PW = D / 32;   // words of a lane's V piece
   constexpr int MT = D / 16;   // 16-row tiles of O^T
   constexpr int PER = D / 32;
+  extern __shared__ __align__(128) uint8_t ring_smem[];
   __shared__ float sm_m[kWarps][kMaxR], sm_l[kWarps][kMaxR], sm_f[kWarps][kMaxR];
-  __shared__ float sm_acc[kWarps][kMaxR][D];  // first the rotated queries, then the warps' sums
-  __shared__ int sm_put;
+  __shared__ float qs[kMaxR][D];
+  __shared__ int sm_page;
 
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t4 = lane & 3;
   const int2 it = a.work[blockIdx.x];
   const int c = it.x;
   const int b = c / HLkv;
   const fg_paged_desc hd = a.caches[c];
   const int2 range = a.ranges[c];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int t = n.pos[b];
-  if (t < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t4 = lane & 3;
   const int rpw = a.rpw;
   const int nsc = range.y - cdiv(max(hd.w, 0), rpw);  // items of the never-evicted segment
   const bool ring = it.y >= nsc;
+  const int r0 = (ring ? it.y - nsc : it.y) * rpw;
+  const int first = ring ? hd.ring_page : hd.first_page;
+  const int entries = ring ? hd.ring_pages : hd.max_pages;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int t = n.pos[b];
+  const int had = a.rows[c];
+  // pages of the item, 32 at a time: lane l holds page l
+  int page_l = page_at(a, first, entries, r0 / kPageRows + lane);
+  if (t < 0) return;
 
   // rows of the item, and the new token's place
-  const int had = a.rows[c];
   const int old = (int)max(0LL, min((long long)had, (long long)hd.max_pages * kPageRows));
   if (old != had && it.y == 0 && threadIdx.x == 0) atomicOr(a.dev_err, kErrInvalid);
-  int put = -1;  // row (or slot) of the new token if this item holds it
-  int r0, r1, first, entries;
-  bool is_static = false;
-  if (n.k_new) {
-    const int tau = n.ids[b];
-    const bool s = id_in(tau, n.special, n.ns);
-    is_static = joins_static(hd.policy, s, s || id_in(tau, n.punct, n.np));
-  }
+  int r1, put = -1;  // put: row (or slot) of the new token if this item holds it
   if (!ring) {
-    r0 = it.y * rpw;
-    const bool last = it.y == nsc - 1;
-    r1 = last ? old : min(r0 + rpw, old);
-    first = hd.first_page;
-    entries = hd.max_pages;
-    if (is_static && min(old / rpw, nsc - 1) == it.y) put = old;
+    r1 = it.y == nsc - 1 ? old : min(r0 + rpw, old);
+    if (min(old / rpw, nsc - 1) == it.y) put = old;
   } else {
-    r0 = (it.y - nsc) * rpw;
     r1 = min(r0 + rpw, hd.w);
-    first = hd.ring_page;
-    entries = hd.ring_pages;
-    if (n.k_new && !is_static && hd.policy == FG_POLICY_SPFL) {
-      const int slot = t % hd.w;
-      if (slot >= r0 && slot < r1) put = slot;
-    }
+    const int slot = t % hd.w;
+    if (hd.policy == FG_POLICY_SPFL && slot >= r0 && slot < r1) put = slot;
+  }
+  if (n.k_new && put >= 0) {
+    const int tau = n.ids[b];
+    const bool s = warp_id_in(tau, n.special, n.ns);
+    const bool sp = s || warp_id_in(tau, n.punct, n.np);
+    if (joins_static(hd.policy, s, sp) == ring) put = -1;
+  } else {
+    put = -1;
   }
   if (put >= 0) {  // uniform over the CTA
     if (threadIdx.x == 0) {
-      int page = page_at(a, first, entries, put / kPageRows);
+      const int i = put / kPageRows;
+      int page = page_at(a, first, entries, i);
       if (page < 0) {
-        const int i = put / kPageRows;
         int err = kErrInvalid;
         if (!ring && i >= entries) {
           err = kErrCapacity;
@@ -169,20 +201,23 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
         }
         if (page < 0) atomicOr(a.dev_err, err);
       }
-      sm_put = page;
+      sm_page = page;
     }
     __syncthreads();
-    const int page = sm_put;
+    const int page = sm_page;
     if (page >= 0) {
       if (warp < 2) {
         float x[1][PER];
         load_row<PER>((const T*)(warp ? n.v_new : n.k_new) + (size_t)c * D, x[0]);
-        if (warp == 0 && n.rope.rot > 0)
-          rotate_row<PER>(x[0], n.rope.rot, n.rope.style, [&](int p) {
-            float2 cs;
-            rope_cos_sin((unsigned)t, n.rope.turns[p], cs.x, cs.y);
-            return cs;
+        if (warp == 0 && n.rope.rot > 0) {
+          float2 cs[PER];
+          row_angles<PER>(cs, n.rope.rot, n.rope.style, [&](int p) {
+            float2 y;
+            rope_cos_sin((unsigned)t, n.rope.turns[p], y.x, y.y);
+            return y;
           });
+          rotate_row<PER>(x[0], cs, n.rope.rot, n.rope.style);
+        }
         const int r = put % kPageRows, blk = r / kBlockRows;
         put_rows<D, 1>(x, 1u, r % kBlockRows, !ring && r % kBlockRows == 0,
                        (warp ? a.vp : a.kp) + ((size_t)page * kPageRows + blk * kBlockRows) * D,
@@ -192,22 +227,71 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
       if (!ring) r1 = put + 1;
     }
     __syncthreads();  // the row, its exponents and its position are visible to the CTA
+    page_l = page_at(a, first, entries, r0 / kPageRows + lane);
+  }
+
+  // this warp's blocks: warp, warp + 4, ... of the item, i.e. block `warp` of each page
+  static_assert(kPageBlocks == kWarps, "a warp takes one block of every page");
+  const int blocks = r1 > r0 ? cdiv(r1 - r0, kBlockRows) : 0;
+  const int mine = blocks > warp ? cdiv(blocks - warp, kWarps) : 0;
+  const uint32_t stages =
+      (uint32_t)__cvta_generic_to_shared(ring_smem) + (uint32_t)(warp * RG::kWarpBytes);
+  uint32_t exp_l = 0;
+  auto fetch = [&](int group) {  // pages group * 32 + lane of the item, and their exponents
+    const int i = r0 / kPageRows + group * 32 + lane;
+    const bool in = i * kPageRows < r1;
+    if (group > 0) page_l = page_at(a, first, entries, i);
+    if (!in) page_l = -1;
+    else if (page_l < 0) atomicOr(a.dev_err, kErrInvalid);
+    if (page_l >= 0)
+      exp_l = *reinterpret_cast<const volatile unsigned short*>(
+          a.exps + ((size_t)page_l * kPageBlocks + warp) * 2);
+  };
+  constexpr int kNoPage = 1 << 30;
+  auto issue = [&](int j) {
+    if ((j & 31) == 0) fetch(j >> 5);
+    const int pg = __shfl_sync(0xffffffffu, page_l, j & 31);
+    const int ex = (int)__shfl_sync(0xffffffffu, exp_l, j & 31);
+    const uint32_t st = stages + (uint32_t)((j % RG::kStages) * RG::kStride);
+    if (lane == 0)
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + RG::kMeta), "r"(pg < 0 ? kNoPage : ex)
+                   : "memory");
+    if (pg >= 0) {
+      const size_t row = (size_t)pg * kPageRows + warp * kBlockRows;
+      const uint8_t* kb = a.kp + row * D + lane * 16;
+      const uint8_t* vb = a.vp + row * D + lane * 16;
+      constexpr int CPR = D / 16;  // pieces per row
+#pragma unroll
+      for (int i = 0; i < kBlockRows * CPR / 32; ++i) {
+        const int r = i * (32 / CPR) + lane / CPR;
+        const uint32_t dst = st + (uint32_t)(r * D + (((lane % CPR) ^ RG::swizzle(r)) << 4));
+        cp_async16(dst, kb + i * 512);
+        cp_async16(dst + RG::kV, vb + i * 512);
+      }
+      if (ring && lane < 4) cp_async16(st + RG::kPos + lane * 16, a.pos + row + lane * 4);
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < RG::kStages - 1; ++j) {
+    if (j < mine) issue(j);
+    cp_async_commit();
   }
 
   // the group's queries, rotated, in shared memory
-  float(*qs)[D] = sm_acc[0];
   {
     const int Hkv = H / R;
     const size_t g0 = (size_t)(c / Hkv) * H + (size_t)(c % Hkv) * R;
+    float2 cs[PER];
+    if (n.rope.rot > 0 && warp < R)
+      row_angles<PER>(cs, n.rope.rot, n.rope.style, [&](int p) {
+        float2 y;
+        rope_cos_sin((unsigned)t, n.rope.turns[p], y.x, y.y);
+        return y;
+      });
     for (int qi = warp; qi < R; qi += kWarps) {
       float x[PER];
       load_row<PER>((const T*)n.q + (g0 + qi) * D, x);
-      if (n.rope.rot > 0)
-        rotate_row<PER>(x, n.rope.rot, n.rope.style, [&](int p) {
-          float2 cs;
-          rope_cos_sin((unsigned)t, n.rope.turns[p], cs.x, cs.y);
-          return cs;
-        });
+      if (n.rope.rot > 0) rotate_row<PER>(x, cs, n.rope.rot, n.rope.style);
       uint32_t top = 0;
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
@@ -250,92 +334,52 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
 #pragma unroll
       for (int k = 0; k < (kWide ? 4 : 2); ++k) qa[i][k] = 0;
   }
-  __syncthreads();  // the queries' place becomes the warps' sums
 
-  // pages of the item: lane l holds page l (of 32 at a time) and its exponents
-  int page_l = -1;
-  uint2 exp_l = make_uint2(0, 0);
-  auto fetch_pages = [&](int group) {
-    const int i = r0 / kPageRows + group * 32 + lane;
-    const bool in = i * kPageRows < r1;
-    page_l = in ? page_at(a, first, entries, i) : -1;
-    if (in && page_l < 0) atomicOr(a.dev_err, kErrInvalid);
-    if (page_l >= 0)
-      exp_l = ld8(a.exps + (size_t)page_l * kPageBlocks * 2);
-  };
-
-  uint4 k0[KI], k1[KI];  // keys g and g + 8 of the block
-  Piece<D> v[4];         // keys 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9
-  int4 kp;               // their positions (ring)
-  int page = -1, page_next = -1, ek = 0, ev = 0, ek_next = 0, ev_next = 0;
-  const int blocks = r1 > r0 ? cdiv(r1 - r0, kBlockRows) : 0;
-  // page and exponents of block `blk` of the item (all lanes call)
-  auto look = [&](int blk, int& pg, int& e_k, int& e_v) {
-    const int i = blk / kPageBlocks;
-    if ((i & 31) == 0 && blk % kPageBlocks == warp) fetch_pages(i >> 5);
-    pg = __shfl_sync(0xffffffffu, page_l, i & 31);
-    const uint32_t lo = __shfl_sync(0xffffffffu, exp_l.x, i & 31);
-    const uint32_t hi = __shfl_sync(0xffffffffu, exp_l.y, i & 31);
-    const uint32_t w = (blk & 2 ? hi : lo) >> (blk & 1 ? 16 : 0);
-    e_k = (int)(signed char)(w & 0xff);
-    e_v = (int)(signed char)((w >> 8) & 0xff);
-  };
-  auto load_k = [&](int blk, int pg) {
-    if (pg < 0) return;
-    const uint8_t* p = a.kp + ((size_t)pg * kPageRows + (blk % kPageBlocks) * kBlockRows) * D;
+  // this lane's rows of a block and their places in a stage: key kr (and + 8) for the scores,
+  // keys va, vb (and + 8) for the values and the weights
+  const int kr = RG::slot_key(g), va = RG::slot_key(2 * t4), vb = RG::slot_key(2 * t4 + 1);
+  uint32_t k_off[KI];
 #pragma unroll
-    for (int i = 0; i < KI; ++i) {
-      k0[i] = ld16(p + g * D + 64 * i + 16 * t4);
-      k1[i] = ld16(p + (g + 8) * D + 64 * i + 16 * t4);
-    }
-  };
-  auto load_v = [&](int blk, int pg) {
-    if (pg < 0) return;
-    const size_t row = (size_t)pg * kPageRows + (blk % kPageBlocks) * kBlockRows;
-    const uint8_t* p = a.vp + row * D + g * (D / 8);
-    v[0].load(p + (2 * t4) * D);
-    v[1].load(p + (2 * t4 + 1) * D);
-    v[2].load(p + (2 * t4 + 8) * D);
-    v[3].load(p + (2 * t4 + 9) * D);
-    if (ring) {
-      const uint2 x = ld8(a.pos + row + 2 * t4), y = ld8(a.pos + row + 2 * t4 + 8);
-      kp = make_int4((int)x.x, (int)x.y, (int)y.x, (int)y.y);
-    }
-  };
+  for (int i = 0; i < KI; ++i)
+    k_off[i] = (uint32_t)(kr * D + (((t4 + 4 * i) ^ RG::swizzle(kr)) << 4));
+  const int vp = D == 128 ? g : g >> 1, vo = D == 128 ? 0 : (g & 1) * 8;
+  const uint32_t va_off = (uint32_t)(RG::kV + va * D + ((vp ^ RG::swizzle(va)) << 4) + vo);
+  const uint32_t vb_off = (uint32_t)(RG::kV + vb * D + ((vp ^ RG::swizzle(vb)) << 4) + vo);
 
   // lanes without a query keep a maximum that no score passes: weight 0
   float m = g < R ? FG_NEG_INF : 1e30f, l = 0.f;
   float o[MT][4];
 #pragma unroll
   for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-#pragma unroll
-  for (int i = 0; i < KI; ++i) k0[i] = k1[i] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i].zero();
-  kp = make_int4(-1, -1, -1, -1);
 
-  if (warp < blocks) {
-    look(warp, page, ek, ev);
-    load_k(warp, page);
-    load_v(warp, page);
-  }
 #pragma unroll 1
-  for (int blk = warp; blk < blocks; blk += kWarps) {
-    const int nxt = blk + kWarps;
-    if (nxt < blocks) look(nxt, page_next, ek_next, ev_next);
+  for (int j = 0; j < mine; ++j) {
+    cp_async_wait<RG::kStages - 2>();
+    __syncwarp();  // the stage has landed for every lane; the one before it is free
+    if (j + RG::kStages - 1 < mine) issue(j + RG::kStages - 1);
+    cp_async_commit();
+    const uint32_t st = stages + (uint32_t)((j % RG::kStages) * RG::kStride);
+    const int meta = lds4(st + RG::kMeta);
+    const int ek = (int)(signed char)(meta & 0xff), ev = (int)(signed char)((meta >> 8) & 0xff);
     float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < KI; ++i)
+    for (int i = 0; i < KI; ++i) {
+      const uint4 k0 = lds16(st + k_off[i]), k1 = lds16(st + k_off[i] + 8 * D);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const uint32_t x = word4(k0[i], w), y = word4(k1[i], w);
+        const uint32_t x = word4(k0, w), y = word4(k1, w);
         const uint32_t(&q)[kWide ? 4 : 2] = qa[4 * i + w];
         const uint32_t q2 = kWide ? q[kWide ? 2 : 0] : 0u, q3 = kWide ? q[kWide ? 3 : 0] : 0u;
         mma_f16_16816(s0, q[0], q2, q[1], q3, decode2(x), decode2(x >> 16));
         mma_f16_16816(s1, q[0], q2, q[1], q3, decode2(y), decode2(y >> 16));
       }
-    if (nxt < blocks) load_k(nxt, page_next);  // the K registers are free now
-    // scores in base 2, V's exponent added: keys 2 t4, 2 t4 + 1, + 8, + 9 of query g
+    }
+    Piece<D> v[4];  // keys va, vb, va + 8, vb + 8
+    v[0].load(st + va_off);
+    v[1].load(st + vb_off);
+    v[2].load(st + va_off + 8 * D);
+    v[3].load(st + vb_off + 8 * D);
+    // scores in base 2, V's exponent added: those keys and query g
     const int e = max(-126, min(127, ek + eq));
     const float kf = pow2f(e) * sl2, fv = (float)ev;
     float x[4] = {s0[0], s0[1], s1[0], s1[1]};
@@ -345,24 +389,24 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
       x[2] += s1[2] * (1.f / 2048.f);
       x[3] += s1[3] * (1.f / 2048.f);
     }
-    const int row = r0 + blk * kBlockRows + 2 * t4;
-    bool ok[4];
-    ok[0] = row < r1;
-    ok[1] = row + 1 < r1;
-    ok[2] = row + 8 < r1;
-    ok[3] = row + 9 < r1;
-    if (ring) {  // in the window: position in (t - w, t]
-      const unsigned w = (unsigned)hd.w;
-      ok[0] = ok[0] && kp.x >= 0 && (unsigned)t - (unsigned)kp.x < w;
-      ok[1] = ok[1] && kp.y >= 0 && (unsigned)t - (unsigned)kp.y < w;
-      ok[2] = ok[2] && kp.z >= 0 && (unsigned)t - (unsigned)kp.z < w;
-      ok[3] = ok[3] && kp.w >= 0 && (unsigned)t - (unsigned)kp.w < w;
-    }
-    if (page < 0) ok[0] = ok[1] = ok[2] = ok[3] = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = ok[i] ? fmaf(x[i], kf, fv) : FG_NEG_INF;
-      if (!ok[i]) v[i].zero();  // such a row may hold anything, also NaN
+    for (int i = 0; i < 4; ++i) x[i] = fmaf(x[i], kf, fv);
+    const int row = r0 + (warp + j * kWarps) * kBlockRows;
+    if (ring || row + kBlockRows > r1 || meta == kNoPage) {  // uniform: rows may be missing
+      const unsigned w = (unsigned)hd.w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = (i & 1 ? vb : va) + (i & 2 ? 8 : 0);
+        bool ok = row + key < r1 && meta != kNoPage;
+        if (ring) {  // in the window: position in (t - w, t]
+          const int p = lds4(st + RG::kPos + key * 4);
+          ok = ok && p >= 0 && (unsigned)t - (unsigned)p < w;
+        }
+        if (!ok) {
+          x[i] = FG_NEG_INF;
+          v[i].zero();  // such a row may hold anything, also NaN
+        }
+      }
     }
     float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -375,11 +419,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
       const float c0 = __shfl_sync(0xffffffffu, corr, 8 * t4);
       const float c1 = __shfl_sync(0xffffffffu, corr, 8 * t4 + 4);
 #pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        o[j][0] *= c0;
-        o[j][1] *= c1;
-        o[j][2] *= c0;
-        o[j][3] *= c1;
+      for (int i = 0; i < MT; ++i) {
+        o[i][0] *= c0;
+        o[i][1] *= c1;
+        o[i][2] *= c0;
+        o[i][3] *= c1;
       }
     }
     const float base = (m == FG_NEG_INF ? 0.f : m) - kPBits;
@@ -413,15 +457,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
         mma_f16_16816(o[2 * w + 1], h0, h1, h2, h3, r01, r23);
       }
     }
-    if (nxt < blocks) load_v(nxt, page_next);
-    page = page_next;
-    ek = ek_next;
-    ev = ev_next;
   }
+  cp_async_wait<0>();
   l += __shfl_xor_sync(0xffffffffu, l, 1);
   l += __shfl_xor_sync(0xffffffffu, l, 2);
 
   // O^T: rows 16 j + g, + 8 are dimensions (D / 8) g + 2 j, + 1; columns queries 2 t4, 2 t4 + 1
+  __syncthreads();  // every warp is done with its ring: the warps' sums take its place
+  float* sums = reinterpret_cast<float*>(ring_smem);  // [kWarps][R][D]
+  static_assert(kWarps * kMaxR * D * 4 <= kWarps * RG::kWarpBytes, "the sums fit the rings");
   if (t4 == 0 && g < R) {
     sm_m[warp][g] = m;
     sm_l[warp][g] = l;
@@ -431,10 +475,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
     const int qi = 2 * t4 + qc;
     if (qi < R) {
 #pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        sm_acc[warp][qi][(D / 8) * g + 2 * j] = o[j][qc];
-        sm_acc[warp][qi][(D / 8) * g + 2 * j + 1] = o[j][qc + 2];
-      }
+      for (int j = 0; j < MT; ++j)
+        *reinterpret_cast<float2*>(&sums[(warp * R + qi) * D + (D / 8) * g + 2 * j]) =
+            make_float2(o[j][qc], o[j][qc + 2]);
     }
   }
   __syncthreads();
@@ -459,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
     const int qi = x / D, dd = x % D;
     float A = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) A = fmaf(sm_f[w][qi], sm_acc[w][qi][dd], A);
+    for (int w = 0; w < kWarps; ++w) A = fmaf(sm_f[w][qi], sums[(w * R + qi) * D + dd], A);
     n.part_acc[((size_t)blockIdx.x * R + qi) * D + dd] = A;
   }
 }
@@ -480,6 +523,13 @@ __global__ void __launch_bounds__(D) q8_combine_kernel(const PagedArgs a, const 
   if (n.pos[b] < 0) {
     if (bump) a.rows_out[c] = a.rows[c];
     return;
+  }
+  bool stored = false;  // the new token belongs to the never-evicted segment
+  if (n.k_new && qi == 0 && t < 32) {
+    const int tau = n.ids[b];
+    const bool s = warp_id_in(tau, n.special, n.ns);
+    const bool sp = s || warp_id_in(tau, n.punct, n.np);
+    stored = joins_static(hd.policy, s, sp);
   }
   float M = FG_NEG_INF, L = 0.f, acc = 0.f;
   for (int i0 = 0; i0 < range.y; i0 += 8) {
@@ -512,22 +562,21 @@ __global__ void __launch_bounds__(D) q8_combine_kernel(const PagedArgs a, const 
   store_out((T*)n.out + (size_t)gq * D + t, L == 0.f ? 0.f : acc / L);
   if (bump) {
     const int had = a.rows[c];
-    int put = 0;
-    if (n.k_new) {
-      const int tau = n.ids[b];
-      const bool s = id_in(tau, n.special, n.ns);
-      if (joins_static(hd.policy, s, s || id_in(tau, n.punct, n.np)) && had >= 0)
-        put = page_at(a, hd.first_page, hd.max_pages, had / kPageRows) >= 0;
-    }
-    a.rows_out[c] = had + put;
+    const bool put =
+        stored && had >= 0 && page_at(a, hd.first_page, hd.max_pages, had / kPageRows) >= 0;
+    a.rows_out[c] = had + (put ? 1 : 0);
   }
 }
 
 template <typename T, int D>
 cudaError_t run_decode_q8(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
                           cudaStream_t s) {
-  cudaError_t e = launch_pdl(q8_split_kernel<T, D>, a.n_work, kThreads, 0, s, a, n, pd.H, pd.R,
-                             pd.HLkv, pd.sl2);
+  constexpr int smem = kWarps * Ring<D>::kWarpBytes;
+  cudaError_t e = cudaFuncSetAttribute(q8_split_kernel<T, D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess)
+    e = launch_pdl(q8_split_kernel<T, D>, a.n_work, kThreads, smem, s, a, n, pd.H, pd.R, pd.HLkv,
+                   pd.sl2);
   if (e == cudaSuccess)
     e = launch_pdl(q8_combine_kernel<T, D>, pd.G, D, 0, s, a, n, pd.H, pd.R, pd.HLkv);
   return e;

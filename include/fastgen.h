@@ -495,7 +495,7 @@ typedef struct {
   void* k_pages;         /* [n_pages, FG_PAGE_ROWS, d] e4m3, 16-byte aligned */
   void* v_pages;         /* like k_pages */
   int8_t* exps;          /* [n_pages, FG_PAGE_ROWS / FG_BLOCK_ROWS, 2] (K, V), 8-byte aligned */
-  int32_t* pos;          /* [n_pages, FG_PAGE_ROWS], 8-byte aligned */
+  int32_t* pos;          /* [n_pages, FG_PAGE_ROWS], 16-byte aligned */
   int32_t* page_table;   /* [table_len] */
   fg_paged_desc* caches; /* [Gkv], 8-byte aligned */
   int32_t* rows;         /* [Gkv] rows of the never-evicted segments */

@@ -106,7 +106,7 @@ def test_rope_rejects_on_host():
 LAYOUT = [dict(page_table=None), dict(caches=None), dict(rows=None), dict(table_len=0),
           dict(caches=FAKE + 4), dict(page_table=FAKE + 1), dict(rows=FAKE + 2)]
 PAGES = [dict(k_pages=None), dict(v_pages=None), dict(exps=None), dict(pos=None), dict(n_pages=0),
-         dict(k_pages=FAKE + 8), dict(v_pages=FAKE + 8), dict(exps=FAKE + 4), dict(pos=FAKE + 4)]
+         dict(k_pages=FAKE + 8), dict(v_pages=FAKE + 8), dict(exps=FAKE + 4), dict(pos=FAKE + 8)]
 
 
 def test_plan_and_schedule_reject_on_host():
