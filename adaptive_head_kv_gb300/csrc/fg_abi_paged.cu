@@ -3,9 +3,7 @@
 #include "fg_abi_util.h"
 #include "fg_paged.cuh"
 
-static_assert(fg::kPageRows % fg::kBlockRows == 0 && fg::kQ8RowsPerWork % fg::kPageRows == 0 &&
-                  fg::kQ8RowsPerWorkWide % fg::kPageRows == 0,
-              "items are whole pages, pages whole blocks");
+static_assert(fg::kPageRows % fg::kBlockRows == 0, "pages are whole blocks");
 
 namespace {
 
@@ -26,13 +24,31 @@ fg_status check_rope(const fg_rope* r, int d, fg::RopeArgs* out) {
   return FG_OK;
 }
 
-// sched: [totals: 256 bytes][ranges int2 x Gkv][work list]
-size_t sched_ranges_bytes(int Gkv) { return align_up((size_t)Gkv * sizeof(int2)); }
+// sched: [totals: 256 bytes][ranges int4 x Gkv][items][first items of the thread blocks]
+size_t sched_ranges_bytes(int Gkv) { return align_up((size_t)Gkv * sizeof(int4)); }
+size_t sched_items_bytes(long long work) { return align_up((size_t)work * sizeof(fg::PagedItem)); }
 
-// Work items a table of table_len entries can need: every segment and ring
-// rounds up once.
+// Work items a table of table_len entries can need: items of kItemPages
+// pages, one that a cache leaves over, one that the cut of a length adds.
 long long sched_max_work(int Gkv, int32_t table_len) {
-  return (long long)table_len / (fg::kQ8RowsPerWork / fg::kPageRows) + 2LL * Gkv;
+  return (long long)table_len / fg::kItemPages + 2LL * Gkv + 1;
+}
+
+struct Sched {
+  long long* totals;
+  int4* ranges;
+  fg::PagedItem* items;
+  int32_t* cta_first;
+};
+Sched sched_parts(const fg_params* p, const fg_paged_cache* c) {
+  char* s = (char*)c->sched;
+  Sched o;
+  o.totals = (long long*)s;
+  o.ranges = (int4*)(s + kAlign);
+  s += kAlign + sched_ranges_bytes(kv_count(p));
+  o.items = (fg::PagedItem*)s;
+  o.cta_first = (int32_t*)(s + sched_items_bytes(sched_max_work(kv_count(p), c->table_len)));
+  return o;
 }
 
 fg_status check_sched(const fg_params* p, const fg_paged_cache* c) {
@@ -72,13 +88,20 @@ fg::PagedArgs paged_args(const fg_params* p, const fg_paged_cache* c, int32_t* d
   a.rows = c->rows;
   a.rows_out = c->rows_out ? c->rows_out : c->rows;
   a.next_page = c->next_page;
-  char* s = (char*)c->sched;
-  a.ranges = s ? (const int2*)(s + kAlign) : nullptr;
-  a.work = s ? (const int2*)(s + kAlign + sched_ranges_bytes(kv_count(p))) : nullptr;
+  if (c->sched) {
+    const Sched o = sched_parts(p, c);
+    a.ranges = o.ranges;
+    a.items = o.items;
+    a.cta_first = o.cta_first;
+  } else {
+    a.ranges = nullptr;
+    a.items = nullptr;
+    a.cta_first = nullptr;
+  }
   a.n_pages = c->n_pages;
   a.table_len = c->table_len;
   a.n_work = c->n_work;
-  a.rpw = c->rows_per_work;
+  a.n_ctas = c->n_ctas;
   a.dev_err = dev_err;
   return a;
 }
@@ -92,21 +115,18 @@ fg_status schedule(const fg_params* p, fg_paged_cache* c, long long* totals_read
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return FG_ECUDA;
   const int Gkv = kv_count(p);
-  char* base = (char*)c->sched;
-  long long* totals = (long long*)base;
-  int2* ranges = (int2*)(base + kAlign);
-  int2* work = (int2*)(base + kAlign + sched_ranges_bytes(Gkv));
+  const Sched o = sched_parts(p, c);
   const long long most = sched_max_work(Gkv, c->table_len);
   cudaError_t e = fg::launch_paged_schedule(Gkv, c->caches, c->rows, c->table_len, (int)most, sms,
-                                            ranges, work, totals, s);
+                                            o.ranges, o.items, o.cta_first, o.totals, s);
   long long h[5] = {0, 0, 0, 0, 0};
-  if (e == cudaSuccess) e = cudaMemcpyAsync(h, totals, sizeof(h), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(h, o.totals, sizeof(h), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return FG_ECUDA;
-  // descriptors past the table (never laid out by the plan) would need more items than fit
-  if (h[3] < Gkv || h[3] > most) return FG_EINVAL;
+  // descriptors that overlap (never laid out by the plan) would need more items than fit
+  if (h[3] < Gkv || h[3] > most || h[4] < 1 || h[4] > h[3]) return FG_EINVAL;
   c->n_work = (int32_t)h[3];
-  c->rows_per_work = (int32_t)h[4];
+  c->n_ctas = (int32_t)h[4];
   if (totals_read)
     for (int i = 0; i < 3; ++i) totals_read[i] = h[i];
   return FG_OK;
@@ -158,7 +178,8 @@ size_t fastgen_paged_sched_bytes(const fg_params* p, int32_t table_len) {
   const int Gkv = kv_count(p);
   const long long work = sched_max_work(Gkv, table_len);
   if (work > 0x7fffffffLL) return 0;
-  return kAlign + sched_ranges_bytes(Gkv) + (size_t)work * sizeof(int2);
+  return kAlign + sched_ranges_bytes(Gkv) + sched_items_bytes(work) +
+         (size_t)(work + 1) * sizeof(int32_t);
 }
 
 fg_status fastgen_paged_plan(const fg_params* p, const int8_t* policy, const uint8_t* keep,
@@ -175,12 +196,12 @@ fg_status fastgen_paged_plan(const fg_params* p, const int8_t* policy, const uin
   if ((st = check_sched(p, cache)) != FG_OK) return st;
   const fg::ProfileDims pd = dims(p);
   cudaStream_t s = (cudaStream_t)stream;
-  char* base = (char*)cache->sched;
-  int2* cinfo = (int2*)(base + kAlign);  // the ranges' place: read before they are written
+  const Sched o = sched_parts(p, cache);
+  int2* cinfo = (int2*)o.ranges;  // the ranges' place: read before they are written
   cudaError_t e = fg::launch_group(pd, policy, keep, cinfo, s);
   if (e == cudaSuccess)
     e = fg::launch_paged_plan(pd.Gkv, pd.w, max_new_tokens, cinfo, cache->caches, cache->rows,
-                              cache->page_table, cache->next_page, (long long*)base, s);
+                              cache->page_table, cache->next_page, o.totals, s);
   if (e != cudaSuccess) return FG_ECUDA;
   long long totals[3];
   if ((st = schedule(p, cache, totals, s)) != FG_OK) return st == FG_EINVAL ? FG_ECUDA : st;
@@ -284,10 +305,9 @@ fg_status fastgen_decode_attn_q8(const fg_params* p, const fg_paged_cache* cache
       !aligned(v_new, 16) || !aligned(out, 16) || !aligned(new_ids, 4) || !aligned(pos, 4) ||
       !aligned(workspace, kAlign) || !aligned(dev_err, 4))
     return FG_EINVAL;
-  // a work list is there: one item a cache at least, of a size that the schedule gives
+  // a work list is there: one item a cache at least, no thread block without one
   if (cache->n_work < kv_count(p) || cache->n_work > sched_max_work(kv_count(p), cache->table_len) ||
-      (cache->rows_per_work != fg::kQ8RowsPerWork &&
-       cache->rows_per_work != fg::kQ8RowsPerWorkWide))
+      cache->n_ctas < 1 || cache->n_ctas > cache->n_work)
     return FG_EINVAL;
   fg::PagedDecodeArgs n;
   if ((st = check_rope(rope, p->d, &n.rope)) != FG_OK) return st;

@@ -18,9 +18,8 @@ namespace fg {
 constexpr int kPageRows = FG_PAGE_ROWS;
 constexpr int kBlockRows = FG_BLOCK_ROWS;
 constexpr int kPageBlocks = kPageRows / kBlockRows;
-// Rows of a decode work item: whole pages.
-constexpr int kQ8RowsPerWork = 256;
-constexpr int kQ8RowsPerWorkWide = 512;
+// Pages of a decode work item when each item has a thread block of its own.
+constexpr int kItemPages = 4;
 constexpr int kExpMin = -100;  // exponent of a block without finite non-zero values
 
 // Bits of |x| as an unsigned integer, 0 for infinities and NaN: the order of
@@ -127,6 +126,13 @@ struct RopeArgs {
   int style;                        // FG_ROPE_*
 };
 
+// A decode work item: pages [seg0, seg1) of a cache's never-evicted segment
+// and [ring0, ring1) of its ring.  The item with `last` set also takes the
+// segment's pages from seg1 on (rows appended after the schedule).
+struct PagedItem {
+  int cache, last, seg0, seg1, ring0, ring1;
+};
+
 struct PagedArgs {
   uint8_t* kp;
   uint8_t* vp;
@@ -137,14 +143,15 @@ struct PagedArgs {
   const int32_t* rows;
   int32_t* rows_out;
   int32_t* next_page;
-  const int2* ranges;  // [Gkv] (first work item, items) of each cache
-  const int2* work;    // [n_work] (cache, item of the cache)
-  int n_pages, table_len, n_work, rpw;
+  const int4* ranges;      // [Gkv] x, y: first work item and items of each cache
+  const PagedItem* items;  // [n_work]
+  const int32_t* cta_first;  // [n_ctas + 1] first item of each thread block
+  int n_pages, table_len, n_work, n_ctas;
   int32_t* dev_err;
 };
 
 // Bits of dev_err.
-constexpr int kErrCapacity = 1, kErrInvalid = 4;
+constexpr int kErrCapacity = 1, kErrDevice = 2, kErrInvalid = 4;
 
 // Page of entry `i` of a segment with `entries` entries from `first`; -1 when
 // the entry does not exist or holds no page of the pool.
@@ -312,10 +319,11 @@ cudaError_t launch_paged_plan(int Gkv, int w, int reserve, const int2* cinfo, fg
                               int32_t* rows, int32_t* table, int32_t* next_page,
                               long long* totals, cudaStream_t s);
 // Decode work list of the current row counts; totals[3] = items, totals[4] =
-// rows per item.
+// thread blocks.
 cudaError_t launch_paged_schedule(int Gkv, const fg_paged_desc* caches, const int32_t* rows,
-                                  int table_len, int max_work, int sms, int2* ranges, int2* work,
-                                  long long* totals, cudaStream_t s);
+                                  int table_len, int max_work, int sms, int4* ranges,
+                                  PagedItem* items, int32_t* cta_first, long long* totals,
+                                  cudaStream_t s);
 cudaError_t launch_compact_q8(const ProfileDims& pd, const void* K, const void* V,
                               const uint8_t* keep, const PagedArgs& a, cudaStream_t s);
 cudaError_t launch_append_q8(const ProfileDims& pd, const PagedArgs& a, const AppendArgs& n,

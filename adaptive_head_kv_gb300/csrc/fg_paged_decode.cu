@@ -1,14 +1,18 @@
 // One generation step over paged 8-bit caches (Model Tells You What to
 // Discard, Method: head-specific caches, the prompt-time policy reused).
 //
-// Split-K over the work list: an item is up to rpw rows of one cache's
-// never-evicted segment (the last one also every row appended later) or of
-// its ring.  A CTA of 4 warps takes an item, warp v its blocks of 16 rows v,
-// v + 4, ...; the CTA whose item holds the new token's row codes it into the
-// page first.  A warp's blocks reach a ring of kStages blocks in shared memory by
-// cp.async (each code is read once, and loads stay in flight without holding
-// registers), and both products run as warp MMAs in f16, which holds every
-// e4m3 code exactly:
+// Split-K over the work list: an item is a run of pages of one cache (its
+// never-evicted segment, the last item's run growing with the rows appended
+// later, then its ring).  A CTA takes one or more items in turn.  Its last
+// warp streams their pages into a ring of kStages pages in shared memory by
+// cp.async, across the items' borders: while the four other warps work on one
+// item, the next one's descriptors, page numbers and queries are read, so the
+// chain of dependent loads that opens an item (about 2 us) hides behind the
+// pages in the ring.  Each of the four warps takes 16 rows of every page.
+// New tokens' rows are coded by those four warps before they start; the page
+// that holds one is streamed last of its item, once that is done.
+//
+// Both products run as warp MMAs in f16, which holds every e4m3 code exactly:
 //   S[16 x 16 keys] = Q[16 x d] . K^T    queries in rows 0-7; rows 8-15 hold
 //                                        what f16 loses of fp32 queries
 //   O^T[d x 8]     += V^T[d x 16 keys] . P^T
@@ -29,12 +33,13 @@
 #include <type_traits>
 
 #include "fg_paged.cuh"
+#include "fg_sm100.cuh"
 
 namespace fg {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kWarps = 4;  // that compute
+constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kMaxR = 8;
 constexpr float kPBits = 15.f;  // weights are formed times 2^15, near the top of f16's range
 
@@ -80,12 +85,6 @@ __device__ __forceinline__ uint2 lds8(uint32_t p) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ int lds4(uint32_t p) {
-  int v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(p) : "memory");
-  return v;
-}
-
 template <int D>
 struct Piece;  // a lane's D / 8 codes of a V row
 template <>
@@ -103,240 +102,414 @@ struct Piece<64> {
   __device__ uint32_t word(int i) const { return i == 0 ? v.x : v.y; }
 };
 
-// The ring: per stage a block's K and V codes, its rows' positions and its
-// exponents.  Row r's 16-byte piece c sits at piece c ^ swizzle(r).  A load
-// phase (8 lanes of 16 bytes, 16 of 8) of the K fragments touches all pieces
-// of one half (d = 128) or all pieces (d = 64) of two rows, one of the V
-// fragments two adjacent pieces of four rows; slot_key orders the 8 keys of a
-// tile so that these fall on different banks.
-template <int D>
+// What a stage of the ring holds beside the codes: its page's rows and
+// exponents, and the item it belongs to.
+struct StageInfo {
+  int row, end;      // first row (or slot) of the page, end of the item's rows
+  int kind;          // kSeg, kRing, kNone: no page
+  int last;          // the item's last page
+  uint32_t exps[2];  // of the page's four blocks: (K, V) bytes
+  int item, cache;   // item -1: of a sequence that takes no part
+  int alone;         // the cache's only item: its sums are the result
+  int t, w;          // the sequence's position, ring slots
+};
+enum { kSeg, kRing, kNone };
+
+// A stage: a page's K and V codes, its rows' positions, StageInfo, and, in an
+// item's first stage, the group's queries: f16 terms and the exponent each
+// query was divided by.  Row r's 16-byte piece c sits at piece c ^ swizzle(r).
+// A load phase (8 lanes of 16 bytes, 16 of 8) of the K fragments touches all
+// pieces of one half (d = 128) or all pieces (d = 64) of two rows, one of the
+// V fragments two adjacent pieces of four rows; slot_key orders the 8 keys of
+// a tile so that these fall on different banks.
+template <int D, bool kWide>
 struct Ring {
-  static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr int kV = kBlockRows * D, kPos = 2 * kV, kMeta = kPos + kBlockRows * 4;
-  static constexpr int kStride = kMeta + 64;  // a multiple of 128
-  static constexpr int kWarpBytes = kStages * kStride;
+  static constexpr int kStages = D == 128 ? 3 : 5;
+  static constexpr int kV = kPageRows * D, kPos = 2 * kV, kInfo = kPos + kPageRows * 4;
+  static constexpr int kQExp = kInfo + 64, kQ = kQExp + 64;
+  static constexpr int kQTerm = kMaxR * D * 2;  // bytes of one term of the queries
+  static constexpr int kStride = (kQ + (kWide ? 2 : 1) * kQTerm + 127) / 128 * 128;
+  static constexpr int kBytes = kStages * kStride;
   __device__ static int swizzle(int r) { return D == 128 ? r & 7 : r & 2; }
   __device__ static int slot_key(int n) {
     const int k = n >> 1;
     return D == 128 ? (n & 1 ? (n + 4) & 7 : n) : (n & 1 ? 4 + (k ^ 1) : k);
   }
 };
-static_assert(Ring<128>::kStride % 128 == 0 && Ring<64>::kStride % 128 == 0, "bank phase");
+static_assert(sizeof(StageInfo) <= 64 && kMaxR * 4 <= 64, "room in a stage");
+
+// Barrier waits end after a second at most: the CTA then runs on without
+// waiting (every address it forms stays in bounds) and reports FG_EDEVICE.
+struct Bars {
+  uint64_t full[5], empty[5], puts, sync;
+  int stop;
+};
+__device__ __forceinline__ void wait_bar(Bars* s, uint64_t* bar, uint32_t parity, int32_t* err) {
+  if (*(volatile int*)&s->stop) return;
+  if (!sm100::mbar_wait(bar, parity)) {
+    *(volatile int*)&s->stop = 1;
+    atomicOr(err, kErrDevice);
+  }
+}
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_addr(bar))
+               : "memory");
+}
+
+// A small id set over the lanes of a warp, read ahead of its use: lane l holds
+// entry l; entries past 32 are looked up when asked.
+struct LaneSet {
+  const int32_t* set;
+  int cnt, id;
+  __device__ __forceinline__ LaneSet(const int32_t* s, int n) : set(s), cnt(n) {
+    const int lane = threadIdx.x & 31;
+    id = lane < n ? __ldg(s + lane) : 0;
+  }
+  __device__ __forceinline__ bool has(int x) const {  // all lanes call
+    const int lane = threadIdx.x & 31;
+    if (__any_sync(0xffffffffu, lane < cnt && id == x)) return true;
+    return cnt > 32 && warp_id_in(x, set + 32, cnt - 32);
+  }
+};
+
+// Where the step's token goes in a cache, if it falls in an item's pages.
+struct Put {
+  int at;     // row of the segment or slot of the ring, -1: not in this item
+  bool ring;
+};
+// All lanes call; `old`: rows of the segment before the step.
+__device__ __forceinline__ Put item_put(const PagedDecodeArgs& n, const PagedItem& it,
+                                        const fg_paged_desc& hd, const LaneSet& special,
+                                        const LaneSet& punct, int old, int t, int tau) {
+  Put p{-1, false};
+  if (!n.k_new) return p;
+  const int page = old / kPageRows;
+  const bool seg_mine = page >= it.seg0 && (it.last || page < it.seg1);
+  const int slot = hd.policy == FG_POLICY_SPFL && hd.w > 0 ? t % hd.w : -1;
+  const bool ring_mine = slot >= 0 && slot / kPageRows >= it.ring0 && slot / kPageRows < it.ring1;
+  if (!seg_mine && !ring_mine) return p;
+  const bool s = special.has(tau), sp = s || punct.has(tau);
+  p.ring = !joins_static(hd.policy, s, sp);
+  if (p.ring ? ring_mine : seg_mine) p.at = p.ring ? slot : old;
+  return p;
+}
+__device__ __forceinline__ int live_rows(const fg_paged_desc& hd, int rows) {
+  return (int)max(0LL, min((long long)rows, (long long)hd.max_pages * kPageRows));
+}
 
 __device__ __forceinline__ uint32_t word4(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
+// Codes the new token's row of an item into its page (all lanes call).
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
+__device__ __forceinline__ void put_token(const PagedArgs& a, const PagedDecodeArgs& n, int c,
+                                          const fg_paged_desc& hd, const Put& put, int t) {
+  constexpr int PER = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int first = put.ring ? hd.ring_page : hd.first_page;
+  const int entries = put.ring ? hd.ring_pages : hd.max_pages;
+  float xk[1][PER], xv[1][PER];
+  load_row<PER>((const T*)n.k_new + (size_t)c * D, xk[0]);
+  load_row<PER>((const T*)n.v_new + (size_t)c * D, xv[0]);
+  const int i = put.at / kPageRows;
+  int page = page_at(a, first, entries, i);
+  if (page < 0) {
+    if (lane == 0) {
+      int err = kErrInvalid;
+      if (!put.ring && i >= entries) {
+        err = kErrCapacity;
+      } else if (!put.ring && first >= 0 && first <= a.table_len - 1 - i &&
+                 a.table[first + i] < 0) {
+        page = atomicAdd(a.next_page, 1);
+        if (page >= 0 && page < a.n_pages) {
+          a.table[first + i] = page;
+        } else {
+          page = -1;
+          err = kErrCapacity;
+        }
+      }
+      if (page < 0) atomicOr(a.dev_err, err);
+    }
+    page = __shfl_sync(0xffffffffu, page, 0);
+  }
+  if (page < 0) return;
+  if (n.rope.rot > 0) {
+    float2 cs[PER];
+    row_angles<PER>(cs, n.rope.rot, n.rope.style, [&](int p) {
+      float2 y;
+      rope_cos_sin((unsigned)t, n.rope.turns[p], y.x, y.y);
+      return y;
+    });
+    rotate_row<PER>(xk[0], cs, n.rope.rot, n.rope.style);
+  }
+  const int r = put.at % kPageRows, blk = r / kBlockRows;
+  const size_t row = (size_t)page * kPageRows + blk * kBlockRows;
+  const bool fresh = !put.ring && r % kBlockRows == 0;
+  int8_t* ex = a.exps + ((size_t)page * kPageBlocks + blk) * 2;
+  put_rows<D, 1>(xk, 1u, r % kBlockRows, fresh, a.kp + row * D, ex);
+  put_rows<D, 1>(xv, 1u, r % kBlockRows, fresh, a.vp + row * D, ex + 1);
+  if (lane == 0) a.pos[(size_t)page * kPageRows + r] = t;
+}
+
+// The streaming warp.
+template <typename T, int D>
+__device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDecodeArgs& n, int H,
+                                             int R, int HLkv, uint8_t* ring_smem, Bars* bars,
+                                             int wi, int wi_end, PagedItem it, fg_paged_desc hd,
+                                             int items, const LaneSet& special,
+                                             const LaneSet& punct) {
+  constexpr bool kWide = sizeof(T) == 4;
+  using RG = Ring<D, kWide>;
+  constexpr int PER = D / 32, CPR = D / 16;  // values per lane of a row; 16-byte pieces per row
+  const int lane = threadIdx.x & 31;
+  const uint32_t base = sm100::smem_addr(ring_smem);
+  bool puts_done = false;
+  auto wait_puts = [&]() {
+    if (!puts_done) wait_bar(bars, &bars->puts, 0, a.dev_err);
+    puts_done = true;
+  };
+  int stage = 0;
+  bool opened = true;  // hd and items are the first item's
+  for (; wi < wi_end; ++wi) {
+    const int c = it.cache, b = c / HLkv;
+    if (!opened) {
+      hd = a.caches[c];
+      items = a.ranges[c].y;
+    }
+    opened = false;
+    const bool alone = items == 1;
+    const int t = n.pos[b], had = a.rows[c], tau = n.k_new ? n.ids[b] : 0;
+    const PagedItem cur = it;
+    if (wi + 1 < wi_end) it = a.items[wi + 1];  // known by the time this item is through
+    // the group's queries and the angles' turns, on their way while the pages are looked up
+    const size_t g0 = (size_t)(c / (H / R)) * H + (size_t)(c % (H / R)) * R;
+    float x[kMaxR][PER];
+#pragma unroll
+    for (int qi = 0; qi < kMaxR; ++qi)
+      if (qi < R) load_row<PER>((const T*)n.q + (g0 + qi) * D, x[qi]);
+    if (t < 0) {  // the sequence takes no part: one empty stage says so
+      const int slot = stage % RG::kStages;
+      wait_bar(bars, &bars->empty[slot], (stage / RG::kStages & 1) ^ 1, a.dev_err);
+      if (lane == 0) {
+        StageInfo* info = reinterpret_cast<StageInfo*>(ring_smem + slot * RG::kStride + RG::kInfo);
+        info->kind = kNone;
+        info->last = 1;
+        info->item = -1;
+        if (alone) a.rows_out[c] = had;
+      }
+      arrive_after_copies(&bars->full[slot]);
+      sm100::mbar_arrive(&bars->full[slot]);
+      ++stage;
+      continue;
+    }
+    const int old = live_rows(hd, had);
+    if (old != had && cur.last && lane == 0) atomicOr(a.dev_err, kErrInvalid);
+    const Put put = item_put(n, cur, hd, special, punct, old, t, tau);
+    int seg_end = cur.last ? old : (int)min((long long)old, (long long)cur.seg1 * kPageRows);
+    const int ring_end = (int)min((long long)hd.w, (long long)cur.ring1 * kPageRows);
+    auto pages_of = [](int page0, int end) {
+      const int rows = end - page0 * kPageRows;
+      return rows > 0 ? cdiv(rows, kPageRows) : 0;
+    };
+    int n_seg = pages_of(cur.seg0, seg_end);
+    const int n_ring = cur.ring1 > cur.ring0 ? pages_of(cur.ring0, ring_end) : 0;
+    bool grown = false;  // the new row opens a page of its own
+    if (put.at >= 0 && !put.ring) {
+      grown = old % kPageRows == 0;
+      if (grown) ++n_seg;
+    }
+    const int pages = n_seg + n_ring;
+    // the page of the new row goes last
+    const int put_j = put.at < 0 ? -1
+                      : put.ring ? n_seg + put.at / kPageRows - cur.ring0
+                                 : put.at / kPageRows - cur.seg0;
+    auto page_j = [&](int j) {
+      return j < n_seg ? page_at(a, hd.first_page, hd.max_pages, cur.seg0 + j)
+                       : page_at(a, hd.ring_page, hd.ring_pages, cur.ring0 + j - n_seg);
+    };
+    // pages 32 at a time, in streaming order: lane l holds one and its exponents
+    int page_l = -1;
+    uint2 exp_l = make_uint2(0, 0);
+    auto fetch = [&](int group) {
+      int k = group * 32 + lane;
+      page_l = -1;
+      if (k >= pages - (put_j >= 0 ? 1 : 0)) return;  // the new row's page is looked up later
+      if (k == put_j) k = pages - 1;
+      page_l = page_j(k);
+      if (page_l < 0)
+        atomicOr(a.dev_err, kErrInvalid);
+      else
+        exp_l = *reinterpret_cast<const uint2*>(a.exps + (size_t)page_l * kPageBlocks * 2);
+    };
+    fetch(0);
+    // the group's queries into an item's first stage: rotated, divided by the power of two that
+    // brings the largest value to [2^13, 2^14), as f16 (fp32: and what f16 loses, times 2^11)
+    auto put_queries = [&](uint8_t* st) {
+      float2 cs[PER];
+      if (n.rope.rot > 0)
+        row_angles<PER>(cs, n.rope.rot, n.rope.style, [&](int p) {
+          float2 y;
+          rope_cos_sin((unsigned)t, n.rope.turns[p], y.x, y.y);
+          return y;
+        });
+#pragma unroll
+      for (int qi = 0; qi < kMaxR; ++qi) {
+        if (qi >= R) break;
+        if (n.rope.rot > 0) rotate_row<PER>(x[qi], cs, n.rope.rot, n.rope.style);
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) top = max(top, finite_bits(x[qi][k]));
+        top = __reduce_max_sync(0xffffffffu, top);
+        const int eq = max(-110, (int)(top >> 23) - 127 - 13);
+        const float inv = pow2f(-eq);
+#pragma unroll
+        for (int k = 0; k < PER; k += 2) {
+          const float u = x[qi][k] * inv, v = x[qi][k + 1] * inv;
+          const uint32_t hi = pack_f16x2(u, v);
+          uint8_t* q = st + RG::kQ + (qi * D + lane * PER + k) * 2;
+          *reinterpret_cast<uint32_t*>(q) = hi;
+          if constexpr (kWide) {
+            const float2 f = unpack_f16x2(hi);
+            *reinterpret_cast<uint32_t*>(q + RG::kQTerm) =
+                pack_f16x2((u - f.x) * 2048.f, (v - f.y) * 2048.f);
+          }
+        }
+        if (lane == 0) reinterpret_cast<int*>(st + RG::kQExp)[qi] = eq;
+      }
+    };
+    // an item without a page has one empty stage
+    for (int k = 0; k == 0 || k < pages; ++k, ++stage) {
+      const int slot = stage % RG::kStages;
+      if (k > 0 && (k & 31) == 0) fetch(k >> 5);
+      wait_bar(bars, &bars->empty[slot], (stage / RG::kStages & 1) ^ 1, a.dev_err);
+      int page = __shfl_sync(0xffffffffu, page_l, k & 31);
+      uint2 ex = make_uint2(0, 0);
+      const bool with_put = put_j >= 0 && k == pages - 1;
+      int j = k == put_j ? pages - 1 : k;
+      if (with_put) {
+        j = put_j;
+        wait_puts();
+        page = page_j(j);
+        if (page >= 0)
+          ex = __ldcg(reinterpret_cast<const uint2*>(a.exps + (size_t)page * kPageBlocks * 2));
+        if (page < 0 && !grown && lane == 0) atomicOr(a.dev_err, kErrInvalid);
+        if (page >= 0 && !put.ring) seg_end = put.at + 1;
+      }
+      const bool ring = j >= n_seg;
+      const int row = (ring ? cur.ring0 + j - n_seg : cur.seg0 + j) * kPageRows;
+      const int end = ring ? ring_end : seg_end;
+      if (page >= 0 && pages > 0) {
+        const uint32_t st = base + (uint32_t)(slot * RG::kStride);
+        const uint8_t* kb = a.kp + (size_t)page * kPageRows * D + lane * 16;
+        const uint8_t* vb = a.vp + (size_t)page * kPageRows * D + lane * 16;
+        const int blocks = min(kPageBlocks, cdiv(end - row, kBlockRows));  // with rows
+        constexpr int kPer = kBlockRows * CPR / 32;  // pieces per lane of a block
+#pragma unroll
+        for (int i = 0; i < kPageBlocks * kPer; ++i) {
+          if (i / kPer < blocks) {
+            const int r = i * (32 / CPR) + lane / CPR;
+            const uint32_t dst = st + (uint32_t)(r * D + (((lane % CPR) ^ RG::swizzle(r)) << 4));
+            cp_async16(dst, kb + i * 512);
+            cp_async16(dst + RG::kV, vb + i * 512);
+          }
+        }
+        if (ring && lane < kPageRows / 4)
+          cp_async16(st + RG::kPos + lane * 16, a.pos + (size_t)page * kPageRows + lane * 4);
+      }
+      if (k == 0) put_queries(ring_smem + slot * RG::kStride);
+      if (!with_put) {
+        ex.x = __shfl_sync(0xffffffffu, exp_l.x, k & 31);
+        ex.y = __shfl_sync(0xffffffffu, exp_l.y, k & 31);
+      }
+      if (lane == 0) {
+        StageInfo* info = reinterpret_cast<StageInfo*>(ring_smem + slot * RG::kStride + RG::kInfo);
+        info->row = row;
+        info->end = end;
+        info->kind = page < 0 || pages == 0 ? kNone : ring ? kRing : kSeg;
+        info->last = k + 1 >= pages;
+        info->exps[0] = ex.x;
+        info->exps[1] = ex.y;
+        info->item = wi;
+        info->cache = c;
+        info->alone = alone;
+        info->t = t;
+        info->w = hd.w;
+      }
+      arrive_after_copies(&bars->full[slot]);
+      sm100::mbar_arrive(&bars->full[slot]);
+    }
+    if (alone) {  // no other reader of the count is left once the rows are put
+      wait_puts();
+      const bool stored = put.at >= 0 && !put.ring && had >= 0 &&
+                          page_at(a, hd.first_page, hd.max_pages, had / kPageRows) >= 0;
+      if (lane == 0) a.rows_out[c] = had + (stored ? 1 : 0);
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 3)
     q8_split_kernel(const PagedArgs a, const PagedDecodeArgs n, int H, int R, int HLkv, float sl2) {
-  using RG = Ring<D>;
   constexpr bool kWide = sizeof(T) == 4;  // fp32: queries and weights in two f16 terms
+  using RG = Ring<D, kWide>;
   constexpr int KI = D / 64;   // 16-byte pieces of a K row per lane
   constexpr int PW = D / 32;   // words of a lane's V piece
   constexpr int MT = D / 16;   // 16-row tiles of O^T
-  constexpr int PER = D / 32;
   extern __shared__ __align__(128) uint8_t ring_smem[];
-  __shared__ float sm_m[kWarps][kMaxR], sm_l[kWarps][kMaxR], sm_f[kWarps][kMaxR];
-  __shared__ float qs[kMaxR][D];
-  __shared__ int sm_page;
+  __shared__ float sm_ml[2][2][kWarps][kMaxR];
+  __shared__ Bars bars;
+  float* sums = reinterpret_cast<float*>(ring_smem + RG::kBytes);  // [kWarps][R][D]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
-  const int2 it = a.work[blockIdx.x];
-  const int c = it.x;
-  const int b = c / HLkv;
-  const fg_paged_desc hd = a.caches[c];
-  const int2 range = a.ranges[c];
-  const int rpw = a.rpw;
-  const int nsc = range.y - cdiv(max(hd.w, 0), rpw);  // items of the never-evicted segment
-  const bool ring = it.y >= nsc;
-  const int r0 = (ring ? it.y - nsc : it.y) * rpw;
-  const int first = ring ? hd.ring_page : hd.first_page;
-  const int entries = ring ? hd.ring_pages : hd.max_pages;
+  const int wi0 = a.cta_first[blockIdx.x], wi_end = a.cta_first[blockIdx.x + 1];
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < RG::kStages; ++i) {
+      sm100::mbar_init(&bars.full[i], 64);  // every streaming lane: its copies, and its stores
+      sm100::mbar_init(&bars.empty[i], kWarps);
+    }
+    sm100::mbar_init(&bars.puts, kWarps);
+    sm100::mbar_init(&bars.sync, kWarps);
+    bars.stop = 0;
+    sm100::fence_barrier_init();
+  }
+  // what the schedule and the caller have fixed is read before the wait
+  const int own = min(wi0 + (warp == kWarps ? 0 : warp), wi_end - 1);
+  const PagedItem own_item = a.items[own];
+  const fg_paged_desc own_cache = a.caches[own_item.cache];
+  const int own_items = a.ranges[own_item.cache].y;
+  const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
+  __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
-  const int t = n.pos[b];
-  const int had = a.rows[c];
-  // pages of the item, 32 at a time: lane l holds page l
-  int page_l = page_at(a, first, entries, r0 / kPageRows + lane);
-  if (t < 0) return;
-
-  // rows of the item, and the new token's place
-  const int old = (int)max(0LL, min((long long)had, (long long)hd.max_pages * kPageRows));
-  if (old != had && it.y == 0 && threadIdx.x == 0) atomicOr(a.dev_err, kErrInvalid);
-  int r1, put = -1;  // put: row (or slot) of the new token if this item holds it
-  if (!ring) {
-    r1 = it.y == nsc - 1 ? old : min(r0 + rpw, old);
-    if (min(old / rpw, nsc - 1) == it.y) put = old;
-  } else {
-    r1 = min(r0 + rpw, hd.w);
-    const int slot = t % hd.w;
-    if (hd.policy == FG_POLICY_SPFL && slot >= r0 && slot < r1) put = slot;
-  }
-  if (n.k_new && put >= 0) {
-    const int tau = n.ids[b];
-    const bool s = warp_id_in(tau, n.special, n.ns);
-    const bool sp = s || warp_id_in(tau, n.punct, n.np);
-    if (joins_static(hd.policy, s, sp) == ring) put = -1;
-  } else {
-    put = -1;
-  }
-  if (put >= 0) {  // uniform over the CTA
-    if (threadIdx.x == 0) {
-      const int i = put / kPageRows;
-      int page = page_at(a, first, entries, i);
-      if (page < 0) {
-        int err = kErrInvalid;
-        if (!ring && i >= entries) {
-          err = kErrCapacity;
-        } else if (!ring && first >= 0 && first <= a.table_len - 1 - i && a.table[first + i] < 0) {
-          page = atomicAdd(a.next_page, 1);
-          if (page >= 0 && page < a.n_pages) {
-            a.table[first + i] = page;
-          } else {
-            page = -1;
-            err = kErrCapacity;
-          }
-        }
-        if (page < 0) atomicOr(a.dev_err, err);
-      }
-      sm_page = page;
-    }
-    __syncthreads();
-    const int page = sm_page;
-    if (page >= 0) {
-      if (warp < 2) {
-        float x[1][PER];
-        load_row<PER>((const T*)(warp ? n.v_new : n.k_new) + (size_t)c * D, x[0]);
-        if (warp == 0 && n.rope.rot > 0) {
-          float2 cs[PER];
-          row_angles<PER>(cs, n.rope.rot, n.rope.style, [&](int p) {
-            float2 y;
-            rope_cos_sin((unsigned)t, n.rope.turns[p], y.x, y.y);
-            return y;
-          });
-          rotate_row<PER>(x[0], cs, n.rope.rot, n.rope.style);
-        }
-        const int r = put % kPageRows, blk = r / kBlockRows;
-        put_rows<D, 1>(x, 1u, r % kBlockRows, !ring && r % kBlockRows == 0,
-                       (warp ? a.vp : a.kp) + ((size_t)page * kPageRows + blk * kBlockRows) * D,
-                       a.exps + ((size_t)page * kPageBlocks + blk) * 2 + warp);
-        if (warp == 0 && lane == 0) a.pos[(size_t)page * kPageRows + r] = t;
-      }
-      if (!ring) r1 = put + 1;
-    }
-    __syncthreads();  // the row, its exponents and its position are visible to the CTA
-    page_l = page_at(a, first, entries, r0 / kPageRows + lane);
+  if (warp == kWarps) {
+    stream_items<T, D>(a, n, H, R, HLkv, ring_smem, &bars, wi0, wi_end, own_item, own_cache,
+                       own_items, special, punct);
+    return;
   }
 
-  // this warp's blocks: warp, warp + 4, ... of the item, i.e. block `warp` of each page
-  static_assert(kPageBlocks == kWarps, "a warp takes one block of every page");
-  const int blocks = r1 > r0 ? cdiv(r1 - r0, kBlockRows) : 0;
-  const int mine = blocks > warp ? cdiv(blocks - warp, kWarps) : 0;
-  const uint32_t stages =
-      (uint32_t)__cvta_generic_to_shared(ring_smem) + (uint32_t)(warp * RG::kWarpBytes);
-  uint32_t exp_l = 0;
-  auto fetch = [&](int group) {  // pages group * 32 + lane of the item, and their exponents
-    const int i = r0 / kPageRows + group * 32 + lane;
-    const bool in = i * kPageRows < r1;
-    if (group > 0) page_l = page_at(a, first, entries, i);
-    if (!in) page_l = -1;
-    else if (page_l < 0) atomicOr(a.dev_err, kErrInvalid);
-    if (page_l >= 0)
-      exp_l = *reinterpret_cast<const volatile unsigned short*>(
-          a.exps + ((size_t)page_l * kPageBlocks + warp) * 2);
-  };
-  constexpr int kNoPage = 1 << 30;
-  auto issue = [&](int j) {
-    if ((j & 31) == 0) fetch(j >> 5);
-    const int pg = __shfl_sync(0xffffffffu, page_l, j & 31);
-    const int ex = (int)__shfl_sync(0xffffffffu, exp_l, j & 31);
-    const uint32_t st = stages + (uint32_t)((j % RG::kStages) * RG::kStride);
-    if (lane == 0)
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + RG::kMeta), "r"(pg < 0 ? kNoPage : ex)
-                   : "memory");
-    if (pg >= 0) {
-      const size_t row = (size_t)pg * kPageRows + warp * kBlockRows;
-      const uint8_t* kb = a.kp + row * D + lane * 16;
-      const uint8_t* vb = a.vp + row * D + lane * 16;
-      constexpr int CPR = D / 16;  // pieces per row
-#pragma unroll
-      for (int i = 0; i < kBlockRows * CPR / 32; ++i) {
-        const int r = i * (32 / CPR) + lane / CPR;
-        const uint32_t dst = st + (uint32_t)(r * D + (((lane % CPR) ^ RG::swizzle(r)) << 4));
-        cp_async16(dst, kb + i * 512);
-        cp_async16(dst + RG::kV, vb + i * 512);
-      }
-      if (ring && lane < 4) cp_async16(st + RG::kPos + lane * 16, a.pos + row + lane * 4);
+  // the new tokens' rows of this CTA's items
+  if (n.k_new) {
+    for (int wi = wi0 + warp; wi < wi_end; wi += kWarps) {
+      const PagedItem it = wi == own ? own_item : a.items[wi];
+      const int c = it.cache, b = c / HLkv;
+      const fg_paged_desc hd = wi == own ? own_cache : a.caches[c];
+      const int t = n.pos[b], tau = n.ids[b], had = a.rows[c];
+      if (t < 0) continue;
+      const Put put = item_put(n, it, hd, special, punct, live_rows(hd, had), t, tau);
+      if (put.at >= 0) put_token<T, D>(a, n, c, hd, put, t);
     }
-  };
-#pragma unroll
-  for (int j = 0; j < RG::kStages - 1; ++j) {
-    if (j < mine) issue(j);
-    cp_async_commit();
-  }
-
-  // the group's queries, rotated, in shared memory
-  {
-    const int Hkv = H / R;
-    const size_t g0 = (size_t)(c / Hkv) * H + (size_t)(c % Hkv) * R;
-    float2 cs[PER];
-    if (n.rope.rot > 0 && warp < R)
-      row_angles<PER>(cs, n.rope.rot, n.rope.style, [&](int p) {
-        float2 y;
-        rope_cos_sin((unsigned)t, n.rope.turns[p], y.x, y.y);
-        return y;
-      });
-    for (int qi = warp; qi < R; qi += kWarps) {
-      float x[PER];
-      load_row<PER>((const T*)n.q + (g0 + qi) * D, x);
-      if (n.rope.rot > 0) rotate_row<PER>(x, cs, n.rope.rot, n.rope.style);
-      uint32_t top = 0;
-#pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        qs[qi][lane * PER + k] = x[k];
-        top = max(top, finite_bits(x[k]));
-      }
-      top = __reduce_max_sync(0xffffffffu, top);
-      // the exponent that brings the largest value to [2^13, 2^14)
-      if (lane == 0) sm_m[0][qi] = (float)max(-110, (int)(top >> 23) - 127 - 13);
-    }
-  }
-  __syncthreads();
-  // operand fragments: k-step 4 i + w takes dimensions 64 i + 16 t4 + 4 w + 0..3
-  uint32_t qa[4 * KI][kWide ? 4 : 2];
-  int eq = 0;
-  if (g < R) {
-    eq = (int)sm_m[0][g];
-    const float inv = pow2f(-eq);
-#pragma unroll
-    for (int i = 0; i < KI; ++i)
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        float x[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = qs[g][64 * i + 16 * t4 + 4 * w + k] * inv;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t hi = pack_f16x2(x[2 * k], x[2 * k + 1]);
-          qa[4 * i + w][k] = hi;
-          if constexpr (kWide) {  // what is left, times 2^11
-            const float2 f = unpack_f16x2(hi);
-            qa[4 * i + w][2 + k] =
-                pack_f16x2((x[2 * k] - f.x) * 2048.f, (x[2 * k + 1] - f.y) * 2048.f);
-          }
-        }
-      }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4 * KI; ++i)
-#pragma unroll
-      for (int k = 0; k < (kWide ? 4 : 2); ++k) qa[i][k] = 0;
+    __syncwarp();
+    if (lane == 0) sm100::mbar_arrive(&bars.puts);
+  } else if (lane == 0) {
+    sm100::mbar_arrive(&bars.puts);
   }
 
   // this lane's rows of a block and their places in a stage: key kr (and + 8) for the scores,
   // keys va, vb (and + 8) for the values and the weights
+  const uint32_t base = sm100::smem_addr(ring_smem) + (uint32_t)(warp * kBlockRows * D);
   const int kr = RG::slot_key(g), va = RG::slot_key(2 * t4), vb = RG::slot_key(2 * t4 + 1);
   uint32_t k_off[KI];
 #pragma unroll
@@ -345,240 +518,304 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
   const int vp = D == 128 ? g : g >> 1, vo = D == 128 ? 0 : (g & 1) * 8;
   const uint32_t va_off = (uint32_t)(RG::kV + va * D + ((vp ^ RG::swizzle(va)) << 4) + vo);
   const uint32_t vb_off = (uint32_t)(RG::kV + vb * D + ((vp ^ RG::swizzle(vb)) << 4) + vo);
+  uint32_t syncs = 0;
+  auto sync_warps = [&]() {  // the four computing warps
+    __syncwarp();
+    if (lane == 0) sm100::mbar_arrive(&bars.sync);
+    wait_bar(&bars, &bars.sync, syncs++ & 1, a.dev_err);
+  };
 
-  // lanes without a query keep a maximum that no score passes: weight 0
-  float m = g < R ? FG_NEG_INF : 1e30f, l = 0.f;
-  float o[MT][4];
-#pragma unroll
-  for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-
+  int stage = 0, half = 0;
 #pragma unroll 1
-  for (int j = 0; j < mine; ++j) {
-    cp_async_wait<RG::kStages - 2>();
-    __syncwarp();  // the stage has landed for every lane; the one before it is free
-    if (j + RG::kStages - 1 < mine) issue(j + RG::kStages - 1);
-    cp_async_commit();
-    const uint32_t st = stages + (uint32_t)((j % RG::kStages) * RG::kStride);
-    const int meta = lds4(st + RG::kMeta);
-    const int ek = (int)(signed char)(meta & 0xff), ev = (int)(signed char)((meta >> 8) & 0xff);
-    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int wi = wi0; wi < wi_end; ++wi) {
+    // lanes without a query keep a maximum that no score passes: weight 0
+    float m = g < R ? FG_NEG_INF : 1e30f, l = 0.f;
+    float o[MT][4];
 #pragma unroll
-    for (int i = 0; i < KI; ++i) {
-      const uint4 k0 = lds16(st + k_off[i]), k1 = lds16(st + k_off[i] + 8 * D);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t x = word4(k0, w), y = word4(k1, w);
-        const uint32_t(&q)[kWide ? 4 : 2] = qa[4 * i + w];
-        const uint32_t q2 = kWide ? q[kWide ? 2 : 0] : 0u, q3 = kWide ? q[kWide ? 3 : 0] : 0u;
-        mma_f16_16816(s0, q[0], q2, q[1], q3, decode2(x), decode2(x >> 16));
-        mma_f16_16816(s1, q[0], q2, q[1], q3, decode2(y), decode2(y >> 16));
+    for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    uint32_t qa[4 * KI][kWide ? 4 : 2];
+    int eq = 0;
+    int last = 0, item = 0, cache = 0, alone = 0;
+#pragma unroll 1
+    for (bool opening = true; !last; opening = false, ++stage) {
+      const int slot = stage % RG::kStages;
+      wait_bar(&bars, &bars.full[slot], stage / RG::kStages & 1, a.dev_err);
+      if (*(volatile int*)&bars.stop) return;  // the copies in flight are the streaming warp's
+      const uint8_t* sp = ring_smem + slot * RG::kStride;
+      const StageInfo* info = reinterpret_cast<const StageInfo*>(sp + RG::kInfo);
+      last = info->last;
+      if (last) {
+        item = info->item;
+        cache = info->cache;
+        alone = info->alone;
       }
-    }
-    Piece<D> v[4];  // keys va, vb, va + 8, vb + 8
-    v[0].load(st + va_off);
-    v[1].load(st + vb_off);
-    v[2].load(st + va_off + 8 * D);
-    v[3].load(st + vb_off + 8 * D);
-    // scores in base 2, V's exponent added: those keys and query g
-    const int e = max(-126, min(127, ek + eq));
-    const float kf = pow2f(e) * sl2, fv = (float)ev;
-    float x[4] = {s0[0], s0[1], s1[0], s1[1]};
-    if constexpr (kWide) {
-      x[0] += s0[2] * (1.f / 2048.f);
-      x[1] += s0[3] * (1.f / 2048.f);
-      x[2] += s1[2] * (1.f / 2048.f);
-      x[3] += s1[3] * (1.f / 2048.f);
-    }
+      if (opening) {
+        // operand fragments: k-step 4 i + w takes dimensions 64 i + 16 t4 + 4 w + 0..3
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = fmaf(x[i], kf, fv);
-    const int row = r0 + (warp + j * kWarps) * kBlockRows;
-    if (ring || row + kBlockRows > r1 || meta == kNoPage) {  // uniform: rows may be missing
-      const unsigned w = (unsigned)hd.w;
+        for (int i = 0; i < KI; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = (i & 1 ? vb : va) + (i & 2 ? 8 : 0);
-        bool ok = row + key < r1 && meta != kNoPage;
-        if (ring) {  // in the window: position in (t - w, t]
-          const int p = lds4(st + RG::kPos + key * 4);
-          ok = ok && p >= 0 && (unsigned)t - (unsigned)p < w;
+          for (int w = 0; w < 4; ++w) {
+            uint2 x = make_uint2(0, 0), y = make_uint2(0, 0);
+            if (g < R) {
+              const uint8_t* q = sp + RG::kQ + (g * D + 64 * i + 16 * t4 + 4 * w) * 2;
+              x = *reinterpret_cast<const uint2*>(q);
+              if constexpr (kWide) y = *reinterpret_cast<const uint2*>(q + RG::kQTerm);
+            }
+            qa[4 * i + w][0] = x.x;
+            qa[4 * i + w][1] = x.y;
+            if constexpr (kWide) {
+              qa[4 * i + w][2] = y.x;
+              qa[4 * i + w][3] = y.y;
+            }
+          }
+        eq = g < R ? reinterpret_cast<const int*>(sp + RG::kQExp)[g] : 0;
+      }
+      const int row = info->row + warp * kBlockRows, end = info->end, kind = info->kind;
+      if (kind == kNone || row >= end) {  // uniform over the warp: no rows here
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&bars.empty[slot]);
+        continue;
+      }
+      const uint32_t ex = info->exps[warp >> 1] >> (16 * (warp & 1));
+      const int ek = (int)(signed char)(ex & 0xff), ev = (int)(signed char)((ex >> 8) & 0xff);
+      const uint32_t st = base + (uint32_t)(slot * RG::kStride);
+      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < KI; ++i) {
+        const uint4 k0 = lds16(st + k_off[i]), k1 = lds16(st + k_off[i] + 8 * D);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t x = word4(k0, w), y = word4(k1, w);
+          const uint32_t(&q)[kWide ? 4 : 2] = qa[4 * i + w];
+          const uint32_t q2 = kWide ? q[kWide ? 2 : 0] : 0u, q3 = kWide ? q[kWide ? 3 : 0] : 0u;
+          mma_f16_16816(s0, q[0], q2, q[1], q3, decode2(x), decode2(x >> 16));
+          mma_f16_16816(s1, q[0], q2, q[1], q3, decode2(y), decode2(y >> 16));
         }
-        if (!ok) {
-          x[i] = FG_NEG_INF;
-          v[i].zero();  // such a row may hold anything, also NaN
-        }
       }
-    }
-    float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    if (__any_sync(0xffffffffu, top > m)) {
-      const float mn = fmaxf(m, top);
-      const float corr = m == FG_NEG_INF ? 0.f : ex2(m - mn);
-      m = mn;
-      l *= corr;
-      const float c0 = __shfl_sync(0xffffffffu, corr, 8 * t4);
-      const float c1 = __shfl_sync(0xffffffffu, corr, 8 * t4 + 4);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        o[i][0] *= c0;
-        o[i][1] *= c1;
-        o[i][2] *= c0;
-        o[i][3] *= c1;
-      }
-    }
-    const float base = (m == FG_NEG_INF ? 0.f : m) - kPBits;
-    float p[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = ex2(x[i] - base);
-    const uint32_t p01 = pack_f16x2(p[0], p[1]), p23 = pack_f16x2(p[2], p[3]);
-    // the sum takes the weights in 32 bits: f16 would lose those that a small
-    // exponent of V makes small
-    l = fmaf((p[0] + p[1]) + (p[2] + p[3]), pow2f(-ev), l);
-    uint32_t r01 = 0, r23 = 0;
-    if constexpr (kWide) {
-      const float2 f01 = unpack_f16x2(p01), f23 = unpack_f16x2(p23);
-      r01 = pack_f16x2(p[0] - f01.x, p[1] - f01.y);
-      r23 = pack_f16x2(p[2] - f23.x, p[3] - f23.y);
-    }
-#pragma unroll
-    for (int w = 0; w < PW; ++w) {
-      const uint32_t a0 = v[0].word(w), a1 = v[1].word(w), a2 = v[2].word(w), a3 = v[3].word(w);
-      // byte pairs (key, next key) of dimensions 4 w, 4 w + 1 and 4 w + 2, 4 w + 3
-      const uint32_t lo01 = __byte_perm(a0, a1, 0x5140), hi01 = __byte_perm(a0, a1, 0x7362);
-      const uint32_t lo23 = __byte_perm(a2, a3, 0x5140), hi23 = __byte_perm(a2, a3, 0x7362);
-      const uint32_t f0 = decode2(lo01), f1 = decode2(lo01 >> 16), f2 = decode2(lo23),
-                     f3 = decode2(lo23 >> 16);
-      const uint32_t h0 = decode2(hi01), h1 = decode2(hi01 >> 16), h2 = decode2(hi23),
-                     h3 = decode2(hi23 >> 16);
-      mma_f16_16816(o[2 * w], f0, f1, f2, f3, p01, p23);
-      mma_f16_16816(o[2 * w + 1], h0, h1, h2, h3, p01, p23);
+      Piece<D> v[4];  // keys va, vb, va + 8, vb + 8
+      v[0].load(st + va_off);
+      v[1].load(st + vb_off);
+      v[2].load(st + va_off + 8 * D);
+      v[3].load(st + vb_off + 8 * D);
+      // scores in base 2, V's exponent added: those keys and query g
+      const int e = max(-126, min(127, ek + eq));
+      const float kf = pow2f(e) * sl2, fv = (float)ev;
+      float x[4] = {s0[0], s0[1], s1[0], s1[1]};
       if constexpr (kWide) {
-        mma_f16_16816(o[2 * w], f0, f1, f2, f3, r01, r23);
-        mma_f16_16816(o[2 * w + 1], h0, h1, h2, h3, r01, r23);
+        x[0] += s0[2] * (1.f / 2048.f);
+        x[1] += s0[3] * (1.f / 2048.f);
+        x[2] += s1[2] * (1.f / 2048.f);
+        x[3] += s1[3] * (1.f / 2048.f);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = fmaf(x[i], kf, fv);
+      if (kind == kRing || row + kBlockRows > end) {  // uniform: rows may be missing
+        const int t = info->t, w = info->w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = (i & 1 ? vb : va) + (i & 2 ? 8 : 0);
+          bool ok = row + key < end;
+          if (kind == kRing) {  // in the window: position in (t - w, t]
+            const int p = reinterpret_cast<const int*>(sp + RG::kPos)[warp * kBlockRows + key];
+            ok = ok && p >= 0 && (unsigned)t - (unsigned)p < (unsigned)w;
+          }
+          if (!ok) {
+            x[i] = FG_NEG_INF;
+            v[i].zero();  // such a row may hold anything, also NaN
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      if (lane == 0) sm100::mbar_arrive(&bars.empty[slot]);
+      float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      if (__any_sync(0xffffffffu, top > m)) {
+        const float mn = fmaxf(m, top);
+        const float corr = m == FG_NEG_INF ? 0.f : ex2(m - mn);
+        m = mn;
+        l *= corr;
+        const float c0 = __shfl_sync(0xffffffffu, corr, 8 * t4);
+        const float c1 = __shfl_sync(0xffffffffu, corr, 8 * t4 + 4);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          o[i][0] *= c0;
+          o[i][1] *= c1;
+          o[i][2] *= c0;
+          o[i][3] *= c1;
+        }
+      }
+      const float off = (m == FG_NEG_INF ? 0.f : m) - kPBits;
+      float p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = ex2(x[i] - off);
+      const uint32_t p01 = pack_f16x2(p[0], p[1]), p23 = pack_f16x2(p[2], p[3]);
+      // the sum takes the weights in 32 bits: f16 would lose those that a small
+      // exponent of V makes small
+      l = fmaf((p[0] + p[1]) + (p[2] + p[3]), pow2f(-ev), l);
+      uint32_t r01 = 0, r23 = 0;
+      if constexpr (kWide) {
+        const float2 f01 = unpack_f16x2(p01), f23 = unpack_f16x2(p23);
+        r01 = pack_f16x2(p[0] - f01.x, p[1] - f01.y);
+        r23 = pack_f16x2(p[2] - f23.x, p[3] - f23.y);
+      }
+#pragma unroll
+      for (int w = 0; w < PW; ++w) {
+        const uint32_t a0 = v[0].word(w), a1 = v[1].word(w), a2 = v[2].word(w), a3 = v[3].word(w);
+        // byte pairs (key, next key) of dimensions 4 w, 4 w + 1 and 4 w + 2, 4 w + 3
+        const uint32_t lo01 = __byte_perm(a0, a1, 0x5140), hi01 = __byte_perm(a0, a1, 0x7362);
+        const uint32_t lo23 = __byte_perm(a2, a3, 0x5140), hi23 = __byte_perm(a2, a3, 0x7362);
+        const uint32_t f0 = decode2(lo01), f1 = decode2(lo01 >> 16), f2 = decode2(lo23),
+                       f3 = decode2(lo23 >> 16);
+        const uint32_t h0 = decode2(hi01), h1 = decode2(hi01 >> 16), h2 = decode2(hi23),
+                       h3 = decode2(hi23 >> 16);
+        mma_f16_16816(o[2 * w], f0, f1, f2, f3, p01, p23);
+        mma_f16_16816(o[2 * w + 1], h0, h1, h2, h3, p01, p23);
+        if constexpr (kWide) {
+          mma_f16_16816(o[2 * w], f0, f1, f2, f3, r01, r23);
+          mma_f16_16816(o[2 * w + 1], h0, h1, h2, h3, r01, r23);
+        }
       }
     }
-  }
-  cp_async_wait<0>();
-  l += __shfl_xor_sync(0xffffffffu, l, 1);
-  l += __shfl_xor_sync(0xffffffffu, l, 2);
-
-  // O^T: rows 16 j + g, + 8 are dimensions (D / 8) g + 2 j, + 1; columns queries 2 t4, 2 t4 + 1
-  __syncthreads();  // every warp is done with its ring: the warps' sums take its place
-  float* sums = reinterpret_cast<float*>(ring_smem);  // [kWarps][R][D]
-  static_assert(kWarps * kMaxR * D * 4 <= kWarps * RG::kWarpBytes, "the sums fit the rings");
-  if (t4 == 0 && g < R) {
-    sm_m[warp][g] = m;
-    sm_l[warp][g] = l;
-  }
-#pragma unroll
-  for (int qc = 0; qc < 2; ++qc) {
-    const int qi = 2 * t4 + qc;
-    if (qi < R) {
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-        *reinterpret_cast<float2*>(&sums[(warp * R + qi) * D + (D / 8) * g + 2 * j]) =
-            make_float2(o[j][qc], o[j][qc + 2]);
+    if (item < 0) continue;
+    // the item is through: merge the four warps
+    float(&sm_m)[kWarps][kMaxR] = sm_ml[half][0], (&sm_l)[kWarps][kMaxR] = sm_ml[half][1];
+    half ^= 1;  // the other half may still be read
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (t4 == 0 && g < R) {
+      sm_m[warp][g] = m;
+      sm_l[warp][g] = l;
     }
-  }
-  __syncthreads();
-  if (threadIdx.x < R) {
-    const int qi = threadIdx.x;
-    float M = FG_NEG_INF;
+    sync_warps();
+    // O^T: rows 16 j + g, + 8 are dimensions (D / 8) g + 2 j, + 1; columns queries 2 t4, 2 t4 + 1
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][qi]);
-    float L = 0.f;
+    for (int qc = 0; qc < 2; ++qc) {
+      const int qi = 2 * t4 + qc;
+      if (qi < R) {
+        float M = FG_NEG_INF;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = sm_m[w][qi] == FG_NEG_INF ? 0.f : exp2f(sm_m[w][qi] - M);
-      sm_f[w][qi] = f;
-      L += sm_l[w][qi] * f;
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][qi]);
+        const float mine = sm_m[warp][qi];
+        const float f = mine == FG_NEG_INF ? 1.f : exp2f(mine - M);  // (0, or NaN: as they are)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+          *reinterpret_cast<float2*>(&sums[(warp * R + qi) * D + (D / 8) * g + 2 * j]) =
+              make_float2(o[j][qc] * f, o[j][qc + 2] * f);
+      }
     }
-    const size_t slot = (size_t)blockIdx.x * R + qi;
-    n.part_ml[2 * slot] = M;
-    n.part_ml[2 * slot + 1] = L;
-  }
-  __syncthreads();
-  for (int x = threadIdx.x; x < R * D; x += kThreads) {
-    const int qi = x / D, dd = x % D;
-    float A = 0.f;
+    sync_warps();
+    const size_t g0 = (size_t)(cache / (H / R)) * H + (size_t)(cache % (H / R)) * R;
+    for (int x = warp * 32 + lane; x < R * D; x += kWarps * 32) {
+      const int qi = x / D;
+      float A = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) A = fmaf(sm_f[w][qi], sums[(w * R + qi) * D + dd], A);
-    n.part_acc[((size_t)blockIdx.x * R + qi) * D + dd] = A;
+      for (int w = 0; w < kWarps; ++w) A += sums[w * R * D + x];
+      float M = FG_NEG_INF, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][qi]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        L += sm_l[w][qi] * (sm_m[w][qi] == FG_NEG_INF ? 1.f : exp2f(sm_m[w][qi] - M));
+      if (alone) {
+        store_out((T*)n.out + g0 * D + x, L == 0.f ? 0.f : A / L);
+      } else {
+        n.part_acc[(size_t)item * R * D + x] = A;
+        if (x % D == 0) {
+          n.part_ml[2 * ((size_t)item * R + qi)] = M;
+          n.part_ml[2 * ((size_t)item * R + qi) + 1] = L;
+        }
+      }
+    }
   }
 }
 
-// One CTA of D threads per query head: merges its items and writes the output;
-// one member of a group also writes the cache's new row count.
+// One warp per query head of a cache with several items: merges them and
+// writes the output; one member of a group also writes the cache's new row
+// count.
+constexpr int kCombineWarps = 4;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(D) q8_combine_kernel(const PagedArgs a, const PagedDecodeArgs n,
-                                                       int H, int R, int HLkv) {
-  const int gq = blockIdx.x, t = threadIdx.x;
-  const int c = kv_head(gq, H, R), qi = (gq % H) % R;
-  const int b = c / HLkv;
+__global__ void __launch_bounds__(kCombineWarps * 32)
+    q8_combine_kernel(const PagedArgs a, const PagedDecodeArgs n, int G, int H, int R, int HLkv) {
+  constexpr int PER = D / 32;
+  constexpr int kAhead = 4;  // items with loads in flight
+  const int gq = blockIdx.x * kCombineWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const bool in = gq < G;
+  const int c = in ? kv_head(gq, H, R) : 0, qi = (gq % H) % R, b = c / HLkv;
   const fg_paged_desc hd = a.caches[c];
-  const int2 range = a.ranges[c];
+  const int4 range = a.ranges[c];
+  const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   griddep_wait();
   griddep_launch_dependents();
-  const bool bump = t == 0 && qi == 0;
-  if (n.pos[b] < 0) {
-    if (bump) a.rows_out[c] = a.rows[c];
+  if (!in || range.y == 1) return;  // a cache's only item has written the result and the count
+  const int t = n.pos[b], had = a.rows[c], tau = n.k_new ? n.ids[b] : 0;
+  if (t < 0) {
+    if (qi == 0 && lane == 0) a.rows_out[c] = had;
     return;
   }
-  bool stored = false;  // the new token belongs to the never-evicted segment
-  if (n.k_new && qi == 0 && t < 32) {
-    const int tau = n.ids[b];
-    const bool s = warp_id_in(tau, n.special, n.ns);
-    const bool sp = s || warp_id_in(tau, n.punct, n.np);
-    stored = joins_static(hd.policy, s, sp);
-  }
-  float M = FG_NEG_INF, L = 0.f, acc = 0.f;
-  for (int i0 = 0; i0 < range.y; i0 += 8) {
-    float m[8], l[8], x[8];
+  float M = FG_NEG_INF, L = 0.f, acc[PER];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+  for (int k = 0; k < PER; ++k) acc[k] = 0.f;
+  for (int i0 = 0; i0 < range.y; i0 += kAhead) {
+    float m[kAhead], l[kAhead], x[kAhead][PER];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
       const bool ok = i0 + j < range.y;
       const size_t slot = ((size_t)range.x + i0 + j) * R + qi;
-      m[j] = ok ? n.part_ml[2 * slot] : FG_NEG_INF;
-      l[j] = ok ? n.part_ml[2 * slot + 1] : 0.f;
-      x[j] = ok ? n.part_acc[slot * D + t] : 0.f;
+      const float2 ml = ok ? *reinterpret_cast<const float2*>(n.part_ml + 2 * slot)
+                           : make_float2(FG_NEG_INF, 0.f);
+      m[j] = ml.x;
+      l[j] = ml.y;
+      if (ok) load_row<PER>(n.part_acc + slot * D, x[j]);
+      else
+#pragma unroll
+        for (int k = 0; k < PER; ++k) x[j][k] = 0.f;
     }
-    float mc = m[0];
+    float Mn = M;
 #pragma unroll
-    for (int j = 1; j < 8; ++j) mc = fmaxf(mc, m[j]);
-    const float Mn = fmaxf(M, mc);
-    const float f = M == FG_NEG_INF ? 0.f : exp2f(M - Mn);
+    for (int j = 0; j < kAhead; ++j) Mn = fmaxf(Mn, m[j]);
+    const float f = M == FG_NEG_INF ? 1.f : exp2f(M - Mn);
     L *= f;
-    acc *= f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int k = 0; k < PER; ++k) acc[k] *= f;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
       // an item without rows, or one whose scores are all NaN, has maximum -inf: its sums count
       // as they are (0, or NaN)
       const float wgt = m[j] == FG_NEG_INF ? 1.f : exp2f(m[j] - Mn);
       L = fmaf(wgt, l[j], L);
-      acc = fmaf(wgt, x[j], acc);
+#pragma unroll
+      for (int k = 0; k < PER; ++k) acc[k] = fmaf(wgt, x[j][k], acc[k]);
     }
     M = Mn;
   }
-  store_out((T*)n.out + (size_t)gq * D + t, L == 0.f ? 0.f : acc / L);
-  if (bump) {
-    const int had = a.rows[c];
-    const bool put =
-        stored && had >= 0 && page_at(a, hd.first_page, hd.max_pages, had / kPageRows) >= 0;
-    a.rows_out[c] = had + (put ? 1 : 0);
+#pragma unroll
+  for (int k = 0; k < PER; ++k)
+    store_out((T*)n.out + (size_t)gq * D + lane * PER + k, L == 0.f ? 0.f : acc[k] / L);
+  if (qi == 0) {
+    bool stored = false;  // the new token joined the never-evicted segment and found a page
+    if (n.k_new) {
+      const bool s = special.has(tau), sp = s || punct.has(tau);
+      stored = joins_static(hd.policy, s, sp) && had >= 0 &&
+               page_at(a, hd.first_page, hd.max_pages, had / kPageRows) >= 0;
+    }
+    if (lane == 0) a.rows_out[c] = had + (stored ? 1 : 0);
   }
 }
 
 template <typename T, int D>
 cudaError_t run_decode_q8(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
                           cudaStream_t s) {
-  constexpr int smem = kWarps * Ring<D>::kWarpBytes;
+  const int smem = Ring<D, sizeof(T) == 4>::kBytes + kWarps * pd.R * D * (int)sizeof(float);
   cudaError_t e = cudaFuncSetAttribute(q8_split_kernel<T, D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess)
-    e = launch_pdl(q8_split_kernel<T, D>, a.n_work, kThreads, smem, s, a, n, pd.H, pd.R, pd.HLkv,
+    e = launch_pdl(q8_split_kernel<T, D>, a.n_ctas, kThreads, smem, s, a, n, pd.H, pd.R, pd.HLkv,
                    pd.sl2);
-  if (e == cudaSuccess)
-    e = launch_pdl(q8_combine_kernel<T, D>, pd.G, D, 0, s, a, n, pd.H, pd.R, pd.HLkv);
+  if (e == cudaSuccess && a.n_work > pd.Gkv)  // else every cache has one item
+    e = launch_pdl(q8_combine_kernel<T, D>, cdiv(pd.G, kCombineWarps), kCombineWarps * 32, 0, s, a,
+                   n, pd.G, pd.H, pd.R, pd.HLkv);
   return e;
 }
 

@@ -70,53 +70,110 @@ __global__ void __launch_bounds__(256) paged_fill_kernel(const fg_paged_desc* __
   for (int i = lane; i < d.ring_pages; i += 32) table[d.ring_page + i] = page + now + i;
 }
 
-// Decode items of a cache at `rpw` rows per item: its never-evicted segment
-// (at least one) and its ring.  Descriptors the plan did not write may say
+// Pages of a cache that a decode step reads: its never-evicted segment's (at
+// least one) and its ring's.  Descriptors the plan did not write may say
 // anything: what lies past the table is not counted.
-__device__ __forceinline__ int cache_items(const fg_paged_desc& d, int rows, int table_len,
-                                           int rpw) {
-  const long long cap = (long long)min(max(d.max_pages, 0), table_len) * kPageRows;
-  const long long ring = (long long)min(max(d.ring_pages, 0), table_len) * kPageRows;
-  const long long seg = max(0LL, min((long long)rows, cap)), w = max(0LL, min((long long)d.w, ring));
-  return (int)(max(1LL, (seg + rpw - 1) / rpw) + (w + rpw - 1) / rpw);
+__device__ __forceinline__ int2 cache_pages(const fg_paged_desc& d, int rows, int table_len) {
+  const int seg = min(max(d.max_pages, 0), table_len), ring = min(max(d.ring_pages, 0), table_len);
+  return make_int2(max(1, min(cdiv(max(rows, 0), kPageRows), seg)),
+                   min(cdiv(max(d.w, 0), kPageRows), ring));
 }
 
-// One CTA: items of every cache at the chosen item size, and their offsets.
+// One CTA: how the decode step is cut into items.
+//
+// Small steps: every cache on its own, in equal items of at most kItemPages
+// pages with a thread block each, for the shortest chain.  Larger ones: the
+// caches' pages end to end, each cache led by kItemCost pages' worth for what
+// an item costs beside its pages, cut into equal lengths for a whole number
+// of waves of resident thread blocks, so that no wave is part empty; a block
+// takes the one or more items that fall in its length.
+// ranges[c] = (first item, items, start of the cache end to end, length or 0).
+constexpr int kItemCost = 4;
+constexpr int kLengthTarget = 64;  // pages a thread block takes in a wave, about
+
 __global__ void __launch_bounds__(kPlanThreads) paged_schedule_kernel(
     const fg_paged_desc* __restrict__ caches, const int32_t* __restrict__ rows, int G,
-    int table_len, int wide_at, int2* __restrict__ ranges, long long* __restrict__ totals) {
+    int table_len, int slots, int4* __restrict__ ranges, long long* __restrict__ totals) {
   __shared__ long long scr[33];
-  long long small = 0;
+  long long small = 0, cost = 0;
   for (int base = 0; base < G; base += blockDim.x) {
     const int c = base + threadIdx.x;
-    long long items = 0, tot;
-    if (c < G) items = cache_items(caches[c], rows[c], table_len, kQ8RowsPerWork);
+    long long items = 0, pages = 0, tot;
+    if (c < G) {
+      const int2 p = cache_pages(caches[c], rows[c], table_len);
+      pages = (long long)p.x + p.y + kItemCost;
+      items = ((long long)p.x + p.y + kItemPages - 1) / kItemPages;
+    }
     block_exclusive_scan(items, scr, &tot);
     small += tot;
+    block_exclusive_scan(pages, scr, &tot);
+    cost += tot;
   }
-  const int rpw = small >= wide_at ? kQ8RowsPerWorkWide : kQ8RowsPerWork;
-  long long item_base = 0;
+  long long len = 0;
+  if (small > 2LL * slots) {
+    const long long wave = (long long)slots * kLengthTarget;
+    const long long waves = max(1LL, (cost + wave / 2) / wave);
+    len = (cost + slots * waves - 1) / (slots * waves);
+  }
+  long long item_base = 0, cost_base = 0;
   for (int base = 0; base < G; base += blockDim.x) {
     const int c = base + threadIdx.x;
-    long long items = 0, tot;
-    if (c < G) items = cache_items(caches[c], rows[c], table_len, rpw);
-    const long long at = item_base + block_exclusive_scan(items, scr, &tot);
-    if (c < G) ranges[c] = make_int2((int)min(at, 0x7fffffffLL), (int)items);
+    long long items = 0, pages = 0, tot;
+    if (c < G) {
+      const int2 p = cache_pages(caches[c], rows[c], table_len);
+      pages = (long long)p.x + p.y;
+    }
+    const long long span = c < G ? pages + kItemCost : 0;
+    const long long at = cost_base + block_exclusive_scan(span, scr, &tot);
+    cost_base += tot;
+    if (c < G)
+      items = len > 0 ? (at + span - 1) / len - at / len + 1
+                      : (pages + kItemPages - 1) / kItemPages;
+    const long long first = item_base + block_exclusive_scan(items, scr, &tot);
     item_base += tot;
+    if (c < G)
+      ranges[c] = make_int4((int)min(first, 0x7fffffffLL), (int)items,
+                            (int)min(at, 0x7fffffffLL), (int)len);
   }
   if (threadIdx.x == 0) {
-    totals[3] = item_base;
-    totals[4] = rpw;
+    totals[3] = cost > 0x7fffffffLL ? -1 : item_base;
+    totals[4] = len > 0 ? (cost + len - 1) / len : item_base;
   }
 }
 
-__global__ void __launch_bounds__(256) paged_worklist_kernel(const int2* __restrict__ ranges, int G,
-                                                             int max_work, int2* __restrict__ work) {
+// One warp per cache: its items, and where they begin a thread block.
+__global__ void __launch_bounds__(256) paged_items_kernel(
+    const fg_paged_desc* __restrict__ caches, const int32_t* __restrict__ rows, int G,
+    int table_len, const int4* __restrict__ ranges, int max_work, PagedItem* __restrict__ items,
+    int32_t* __restrict__ cta_first, const long long* __restrict__ totals) {
   const int c = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (c >= G) return;
-  const int2 r = ranges[c];
-  const int end = (int)min((long long)r.x + r.y, (long long)max_work);
-  for (int i = r.x + lane; i < end && i >= r.x; i += 32) work[i] = make_int2(c, i - r.x);
+  if (c >= G || totals[3] < 0 || totals[3] > max_work || totals[4] > max_work) return;
+  const int4 r = ranges[c];
+  const int2 p = cache_pages(caches[c], rows[c], table_len);
+  const int pages = p.x + p.y;
+  for (int i = lane; i < r.y; i += 32) {
+    long long p0, p1;
+    if (r.w > 0) {
+      const long long k = r.z / r.w + i, start = (long long)r.z + kItemCost;
+      p0 = max(0LL, k * r.w - start);
+      p1 = min((long long)pages, (k + 1) * r.w - start);
+      if (p1 < p0) p1 = p0 = 0;  // the length ends within the cache's lead
+      if (i > 0 || r.z % r.w == 0) cta_first[k] = r.x + i;
+    } else {
+      p0 = (long long)i * pages / r.y;
+      p1 = (long long)(i + 1) * pages / r.y;
+      cta_first[r.x + i] = r.x + i;
+    }
+    PagedItem it;
+    it.cache = c;
+    it.last = p0 <= p.x - 1 && p.x - 1 < p1;
+    it.seg0 = (int)min(p0, (long long)p.x);
+    it.seg1 = (int)min(p1, (long long)p.x);
+    it.ring0 = (int)max(p0 - p.x, 0LL);
+    it.ring1 = (int)max(p1 - p.x, 0LL);
+    items[r.x + i] = it;
+  }
+  if (c == G - 1 && lane == 0) cta_first[totals[4]] = (int)totals[3];
 }
 
 // ---------------------------------------------------------------------------
@@ -289,11 +346,13 @@ cudaError_t launch_paged_plan(int Gkv, int w, int reserve, const int2* cinfo, fg
 }
 
 cudaError_t launch_paged_schedule(int Gkv, const fg_paged_desc* caches, const int32_t* rows,
-                                  int table_len, int max_work, int sms, int2* ranges, int2* work,
-                                  long long* totals, cudaStream_t s) {
-  paged_schedule_kernel<<<1, kPlanThreads, 0, s>>>(caches, rows, Gkv, table_len, 64 * sms,
-                                                    ranges, totals);
-  paged_worklist_kernel<<<cdiv(Gkv, 8), 256, 0, s>>>(ranges, Gkv, max_work, work);
+                                  int table_len, int max_work, int sms, int4* ranges,
+                                  PagedItem* items, int32_t* cta_first, long long* totals,
+                                  cudaStream_t s) {
+  paged_schedule_kernel<<<1, kPlanThreads, 0, s>>>(caches, rows, Gkv, table_len, 3 * sms, ranges,
+                                                   totals);
+  paged_items_kernel<<<cdiv(Gkv, 8), 256, 0, s>>>(caches, rows, Gkv, table_len, ranges, max_work,
+                                                  items, cta_first, totals);
   return cudaGetLastError();
 }
 

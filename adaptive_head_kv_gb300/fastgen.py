@@ -82,7 +82,7 @@ class PagedCacheStruct(ctypes.Structure):
                 ("next_page", ctypes.c_void_p), ("sched", ctypes.c_void_p),
                 ("sched_bytes", ctypes.c_int64), ("n_pages", ctypes.c_int32),
                 ("table_len", ctypes.c_int32), ("n_work", ctypes.c_int32),
-                ("rows_per_work", ctypes.c_int32)]
+                ("n_ctas", ctypes.c_int32)]
 
 
 class PagedInfo(ctypes.Structure):

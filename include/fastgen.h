@@ -506,8 +506,8 @@ typedef struct {
   int64_t sched_bytes;
   int32_t n_pages;
   int32_t table_len;
-  int32_t n_work;        /* set by fastgen_paged_plan and fastgen_paged_schedule */
-  int32_t rows_per_work; /* likewise */
+  int32_t n_work; /* work items; set by fastgen_paged_plan and fastgen_paged_schedule */
+  int32_t n_ctas; /* thread blocks that share them; likewise */
 } fg_paged_cache;
 
 typedef struct {
@@ -525,7 +525,7 @@ size_t fastgen_paged_sched_bytes(const fg_params* p, int32_t table_len);
  * share the union cache): writes caches, rows, page_table (the prompt's pages in order, -1 where a
  * cache may grow), next_page and the work list.  Needs those buffers, table_len >=
  * fastgen_paged_table_len and sched_bytes; the page buffers may be NULL until n_pages is known.
- * *info, cache->n_work and cache->rows_per_work (HOST) are set: SYNCHRONOUS on `stream`.
+ * *info, cache->n_work and cache->n_ctas (HOST) are set: SYNCHRONOUS on `stream`.
  * Errors: FG_EINVAL, FG_EDTYPE, FG_EWORKSPACE for a short table or sched. */
 fg_status fastgen_paged_plan(const fg_params* p, const int8_t* policy, const uint8_t* keep,
                              int32_t max_new_tokens, fg_paged_cache* cache, fg_paged_info* info,

@@ -36,7 +36,7 @@ def cache(p, **kw):
         setattr(c, name, FAKE)
     c.table_len = 100
     c.sched_bytes = fg.fastgen_paged_sched_bytes(p, 100)
-    c.n_pages, c.n_work, c.rows_per_work = 50, 40, 256
+    c.n_pages, c.n_work, c.n_ctas = 50, 40, 30
     for k, v in kw.items():
         setattr(c, k, v)
     return c
@@ -64,7 +64,8 @@ def test_sizes():
     assert fg.fastgen_paged_table_len(P(r_l=0.0), 0) == 8 * 2
     assert fg.fastgen_paged_table_len(p, -1) == 0 and fg.fastgen_paged_table_len(P(d=96), 1) == 0
     assert fg.fastgen_paged_table_len(P(B=4000, L=100, n=100000), 100000) == 0  # past 2^31
-    assert fg.fastgen_paged_sched_bytes(p, 24) == 256 + al(8 * 8) + (24 // 4 + 16) * 8
+    assert fg.fastgen_paged_sched_bytes(p, 24) == (256 + al(8 * 16) + al((24 // 4 + 17) * 24)
+                                                     + (24 // 4 + 18) * 4)
     assert fg.fastgen_paged_sched_bytes(p, 0) == 0
     assert fg.fastgen_append_q8_workspace_bytes(p, 5) == (al(2 * 2 * 5 * 4) + al(8 * 2 * 4)
                                                           + al(2 * 5 * 64 * 8))
@@ -173,7 +174,7 @@ def test_decode_rejects_on_host():
 
     for kw in LAYOUT + PAGES + [
             dict(sched=None), dict(sched=FAKE + 32), dict(n_work=0), dict(n_work=7),
-            dict(n_work=1 << 20), dict(rows_per_work=0), dict(rows_per_work=300),
+            dict(n_work=1 << 20), dict(n_ctas=0), dict(n_ctas=41),
             dict(next_page=None), dict(q=None), dict(q=FAKE + 8), dict(k=None), dict(v=None),
             dict(v=FAKE + 8), dict(ids=None), dict(ns=9999), dict(at=None), dict(out=None),
             dict(out=FAKE + 4), dict(ws=None), dict(ws=FAKE + 16), dict(err=None),
