@@ -89,7 +89,7 @@ __device__ __forceinline__ int2 cache_pages(const fg_paged_desc& d, int rows, in
 // takes the one or more items that fall in its length.
 // ranges[c] = (first item, items, start of the cache end to end, length or 0).
 constexpr int kItemCost = 4;
-constexpr int kLengthTarget = 64;  // pages a thread block takes in a wave, about
+constexpr int kLengthTarget = 128; // pages a thread block takes in a wave, about
 
 __global__ void __launch_bounds__(kPlanThreads) paged_schedule_kernel(
     const fg_paged_desc* __restrict__ caches, const int32_t* __restrict__ rows, int G,
