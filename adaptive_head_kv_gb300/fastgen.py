@@ -351,6 +351,18 @@ def fastgen_profile_stall_test(params, Q, K, token_ids, special_ids, punct_ids, 
 # run on the tensors' device, on its current stream unless one is given.
 
 
+_T = None  # torch, once one of these calls needs it
+
+
+def _torch():
+    global _T
+    if _T is None:
+        import torch
+
+        _T = torch
+    return _T
+
+
 def _refuse(where: str, what: str) -> None:
     raise FastGenError(FG_EINVAL, f"{where}: {what}")
 
@@ -361,43 +373,45 @@ def _heads(p: Params) -> tuple[int, int]:
     return layers * p.H, layers * (p.Hkv or p.H)
 
 
-def _is(x, where: str, name: str, dtype, count: int, device):
-    """The address of tensor x, which must be contiguous, of that type (or one
-    of those types) and device, with `count` elements."""
-    if x.dtype != dtype and not (isinstance(dtype, tuple) and x.dtype in dtype):
-        _refuse(where, f"{name} has type {x.dtype}")
-    if x.numel() != count:
-        _refuse(where, f"{name} has {x.numel()} elements, not {count}")
-    if x.device != device or not x.is_contiguous():
-        _refuse(where, f"{name} must be contiguous and on {device}")
+def _is(x, where: str, name: str, dtype, count: int, dev: int) -> int:
+    """The address of tensor x, which must be contiguous, of that type, on
+    device `dev` (-1: the CPU), with `count` elements."""
+    if (x.dtype is not dtype or x.numel() != count or x.get_device() != dev
+            or not x.is_contiguous()):
+        _refuse(where, f"{name} must be contiguous, {count} elements of {dtype} on device {dev}; "
+                       f"got {tuple(x.shape)} of {x.dtype} on {x.device}")
     return x.data_ptr()
 
 
-def _ids(x, where: str, name: str, device):
-    return None if x is None else _is(x, where, name, _torch().int32, x.numel(), device)
-
-
-def _torch():
-    import torch
-
-    return torch
+def _id_set(x, where: str, name: str, dev: int):
+    if x is None:
+        return None, 0
+    n = x.numel()
+    return _is(x, where, name, _T.int32, n, dev), n
 
 
 def _elem(p: Params):
-    torch = _torch()
+    torch = _T or _torch()
     return torch.bfloat16 if p.dtype == FG_BF16 else torch.float32
 
 
-def _run(where: str, device, stream, fn, *args) -> None:
-    """Calls fn(*args, stream) with `device` current."""
-    torch = _torch()
-    if device.type != "cuda":
-        _refuse(where, f"tensors on {device}")
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)), where)
+def _run(where: str, dev: int, stream, fn, *args) -> None:
+    """Calls fn(*args, stream) with device `dev` current."""
+    torch = _T or _torch()
+    if dev < 0:
+        _refuse(where, "tensors must be on a GPU")
+    here = torch.cuda.current_device()
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if dev == here:
+        st = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream)), where)
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != FG_OK:
+        raise FastGenError(st, where)
 
 
 class Rope:
@@ -409,7 +423,7 @@ class Rope:
         torch = _torch()
         if turns.dtype != torch.int64 or not turns.is_contiguous():
             _refuse("Rope", "turns must be a contiguous int64 tensor")
-        self.turns, self.device = turns, turns.device
+        self.turns, self.dev = turns, turns.get_device()
         self.c = RopeStruct(turns.data_ptr(), 2 * turns.numel(), style)
 
     @classmethod
@@ -421,11 +435,11 @@ class Rope:
         return cls(fastgen_rope_table(inv_freq).to(device), style)
 
 
-def _rope(rope, where: str, device):
+def _rope(rope, where: str, dev: int):
     if rope is None:
         return None
-    if rope.device != device:
-        _refuse(where, f"rope must be on {device}")
+    if rope.dev != dev:
+        _refuse(where, f"rope must be on device {dev}")
     return rope.c
 
 
@@ -445,13 +459,14 @@ def fastgen_rope(params, Q, K, pos, rope, Q_out, K_out, stream=None) -> None:
     dt, size = _elem(p), p.n * p.d
     if rope is None or (Q is None and K is None):
         _refuse(w, "no rotation, or nothing to rotate")
-    dev = (K if Q is None else Q).device
-    ptr = [None if x is None else _is(x, w, name, dt, count * size, dev)
-           for x, name, count in ((Q, "Q", G), (K, "K", Gkv), (Q_out, "Q_out", G),
-                                  (K_out, "K_out", Gkv))]
-    at = None if pos is None else _is(pos, w, "pos", _torch().int32, p.B * p.n, dev)
-    _run(w, dev, stream, lib().fastgen_rope, p, ptr[0], ptr[1], at, _rope(rope, w, dev), ptr[2],
-         ptr[3])
+    dev = (K if Q is None else Q).get_device()
+    _run(w, dev, stream, lib().fastgen_rope, p,
+         None if Q is None else _is(Q, w, "Q", dt, G * size, dev),
+         None if K is None else _is(K, w, "K", dt, Gkv * size, dev),
+         None if pos is None else _is(pos, w, "pos", _T.int32, p.B * p.n, dev),
+         _rope(rope, w, dev),
+         None if Q_out is None else _is(Q_out, w, "Q_out", dt, G * size, dev),
+         None if K_out is None else _is(K_out, w, "K_out", dt, Gkv * size, dev))
 
 
 def fastgen_paged_table_len(params, max_new_tokens: int) -> int:
@@ -474,8 +489,8 @@ class PagedCache:
                  rows_out=None):
         torch, w = _torch(), "PagedCache"
         Gkv = _heads(params)[1]
-        dev, i32 = page_table.device, torch.int32
-        self.device, self.d = dev, params.d
+        dev, i32 = page_table.get_device(), torch.int32
+        self.dev, self.d, self.count = dev, params.d, Gkv
         c = self.c = PagedCacheStruct()
         c.table_len = page_table.numel()
         c.page_table = _is(page_table, w, "page_table", i32, page_table.numel(), dev)
@@ -486,7 +501,7 @@ class PagedCache:
         need = fastgen_paged_sched_bytes(params, c.table_len)
         if need == 0:
             _refuse(w, "parameters or table length")
-        self.sched = torch.empty(need, dtype=torch.uint8, device=dev)
+        self.sched = torch.empty(need, dtype=torch.uint8, device=page_table.device)
         c.sched, c.sched_bytes = self.sched.data_ptr(), need
         self.page_table, self.caches, self.rows, self.next_page = page_table, caches, rows, next_page
         self.rows_out = rows if rows_out is None else rows_out
@@ -497,11 +512,11 @@ class PagedCache:
     def set_pages(self, k_pages, v_pages, exps, pos) -> None:
         torch, w, c = _torch(), "PagedCache", self.c
         pages, row = exps.numel() // 8, FG_PAGE_ROWS * self.d
-        codes = (torch.float8_e4m3fn, torch.uint8)
-        c.k_pages = _is(k_pages, w, "k_pages", codes, pages * row, self.device)
-        c.v_pages = _is(v_pages, w, "v_pages", codes, pages * row, self.device)
-        c.exps = _is(exps, w, "exps", torch.int8, pages * 8, self.device)
-        c.pos = _is(pos, w, "pos", torch.int32, pages * FG_PAGE_ROWS, self.device)
+        codes = torch.uint8 if k_pages.dtype is torch.uint8 else torch.float8_e4m3fn
+        c.k_pages = _is(k_pages, w, "k_pages", codes, pages * row, self.dev)
+        c.v_pages = _is(v_pages, w, "v_pages", codes, pages * row, self.dev)
+        c.exps = _is(exps, w, "exps", torch.int8, pages * 8, self.dev)
+        c.pos = _is(pos, w, "pos", torch.int32, pages * FG_PAGE_ROWS, self.dev)
         c.n_pages = pages
         self.k_pages, self.v_pages, self.exps, self.pos = k_pages, v_pages, exps, pos
 
@@ -511,21 +526,22 @@ class PagedCache:
 
 def fastgen_paged_plan(params, policy, keep, max_new_tokens, cache, stream=None) -> PagedInfo:
     w, torch = "fastgen_paged_plan", _torch()
-    G, dev, info = _heads(params)[0], cache.device, PagedInfo()
+    G, dev, info = _heads(params)[0], cache.dev, PagedInfo()
     _run(w, dev, stream, lib().fastgen_paged_plan, params,
          _is(policy, w, "policy", torch.int8, G, dev),
-         _is(keep, w, "keep", torch.uint8, G * params.n, dev), max_new_tokens, cache.c, info)
+         _is(keep, w, "keep", torch.uint8, G * params.n, dev), max_new_tokens,
+         _of_cache(params, cache, w), info)
     return info
 
 
 def fastgen_paged_schedule(params, cache, stream=None) -> None:
-    _run("fastgen_paged_schedule", cache.device, stream, lib().fastgen_paged_schedule, params,
-         cache.c)
+    w = "fastgen_paged_schedule"
+    _run(w, cache.dev, stream, lib().fastgen_paged_schedule, params, _of_cache(params, cache, w))
 
 
 def _of_cache(p, cache, w: str):
     """The cache's struct, if it belongs to these parameters."""
-    if cache.rows.numel() != _heads(p)[1] or cache.d != p.d:
+    if cache.count != p.B * p.L * (p.Hkv or p.H) or cache.d != p.d:
         _refuse(w, "the cache was made for other parameters")
     return cache.c
 
@@ -533,7 +549,7 @@ def _of_cache(p, cache, w: str):
 def fastgen_compact_q8(params, K, V, keep, cache, dev_err, stream=None) -> None:
     w, p, torch = "fastgen_compact_q8", params, _torch()
     G, Gkv = _heads(p)
-    dev, dt, size = cache.device, _elem(p), Gkv * p.n * p.d
+    dev, dt, size = cache.dev, _elem(p), Gkv * p.n * p.d
     _run(w, dev, stream, lib().fastgen_compact_q8, p, _is(K, w, "K", dt, size, dev),
          _is(V, w, "V", dt, size, dev), _is(keep, w, "keep", torch.uint8, G * p.n, dev),
          _of_cache(p, cache, w), _is(dev_err, w, "dev_err", torch.int32, 1, dev))
@@ -548,17 +564,17 @@ def fastgen_append_q8(params, cache, k_new, v_new, new_ids, n_new, special_ids, 
     """Appends m tokens: k_new, v_new [Gkv, m, d], new_ids [B, m], n_new [B] or
     None (m each), pos [B] the first new position of each sequence (< 0: idle)."""
     w, p, torch = "fastgen_append_q8", params, _torch()
-    Gkv, dev, dt, i32 = _heads(p)[1], cache.device, _elem(p), torch.int32
-    m = new_ids.numel() // p.B
+    B, dev, dt, i32 = p.B, cache.dev, _elem(p), torch.int32
+    m = new_ids.numel() // B
+    rows, ws = cache.count * m * p.d, workspace.numel()
+    special, punct = (_id_set(special_ids, w, "special_ids", dev),
+                      _id_set(punct_ids, w, "punct_ids", dev))
     _run(w, dev, stream, lib().fastgen_append_q8, p, _of_cache(p, cache, w),
-         _is(k_new, w, "k_new", dt, Gkv * m * p.d, dev),
-         _is(v_new, w, "v_new", dt, Gkv * m * p.d, dev),
-         _is(new_ids, w, "new_ids", i32, p.B * m, dev), m,
-         None if n_new is None else _is(n_new, w, "n_new", i32, p.B, dev),
-         _ids(special_ids, w, "special_ids", dev), _count(special_ids),
-         _ids(punct_ids, w, "punct_ids", dev), _count(punct_ids),
-         _is(pos, w, "pos", i32, p.B, dev), _rope(rope, w, dev),
-         _is(workspace, w, "workspace", torch.uint8, workspace.numel(), dev), workspace.numel(),
+         _is(k_new, w, "k_new", dt, rows, dev), _is(v_new, w, "v_new", dt, rows, dev),
+         _is(new_ids, w, "new_ids", i32, B * m, dev), m,
+         None if n_new is None else _is(n_new, w, "n_new", i32, B, dev), special[0], special[1],
+         punct[0], punct[1], _is(pos, w, "pos", i32, B, dev), _rope(rope, w, dev),
+         _is(workspace, w, "workspace", torch.uint8, ws, dev), ws,
          _is(dev_err, w, "dev_err", i32, 1, dev))
 
 
@@ -571,15 +587,16 @@ def fastgen_decode_attn_q8(params, cache, q, k_new, v_new, new_ids, special_ids,
     """One generation step: q, out [G, d], k_new, v_new [Gkv, d] (None: nothing is
     appended), new_ids [B], pos [B] int32 on the device (< 0: idle)."""
     w, p, torch = "fastgen_decode_attn_q8", params, _torch()
-    (G, Gkv), dev, dt, i32 = _heads(p), cache.device, _elem(p), torch.int32
-    new = [None if x is None else _is(x, w, name, dt, Gkv * p.d, dev)
-           for x, name in ((k_new, "k_new"), (v_new, "v_new"))]
+    B, d, dev, dt, i32 = p.B, p.d, cache.dev, _elem(p), torch.int32
+    queries, rows, ws = B * p.L * p.H * d, cache.count * d, workspace.numel()
+    special, punct = (_id_set(special_ids, w, "special_ids", dev),
+                      _id_set(punct_ids, w, "punct_ids", dev))
     _run(w, dev, stream, lib().fastgen_decode_attn_q8, p, _of_cache(p, cache, w),
-         _is(q, w, "q", dt, G * p.d, dev), new[0], new[1],
-         None if new_ids is None else _is(new_ids, w, "new_ids", i32, p.B, dev),
-         _ids(special_ids, w, "special_ids", dev), _count(special_ids),
-         _ids(punct_ids, w, "punct_ids", dev), _count(punct_ids),
-         _is(pos, w, "pos", i32, p.B, dev), _rope(rope, w, dev),
-         _is(out, w, "out", dt, G * p.d, dev),
-         _is(workspace, w, "workspace", torch.uint8, workspace.numel(), dev), workspace.numel(),
+         _is(q, w, "q", dt, queries, dev),
+         None if k_new is None else _is(k_new, w, "k_new", dt, rows, dev),
+         None if v_new is None else _is(v_new, w, "v_new", dt, rows, dev),
+         None if new_ids is None else _is(new_ids, w, "new_ids", i32, B, dev), special[0],
+         special[1], punct[0], punct[1], _is(pos, w, "pos", i32, B, dev), _rope(rope, w, dev),
+         _is(out, w, "out", dt, queries, dev),
+         _is(workspace, w, "workspace", torch.uint8, ws, dev), ws,
          _is(dev_err, w, "dev_err", i32, 1, dev))
