@@ -108,6 +108,29 @@ __device__ __forceinline__ bool warp_id_in(int id, const int32_t* __restrict__ s
   return __any_sync(0xffffffffu, hit);
 }
 
+// A small id set over the lanes of a warp, read ahead of its use: lane l holds
+// entry l; entries past 32 are looked up when asked.
+struct LaneSet {
+  const int32_t* set;
+  int cnt, id;
+  __device__ __forceinline__ LaneSet(const int32_t* s, int n) : set(s), cnt(n) {
+    const int lane = threadIdx.x & 31;
+    id = lane < n ? __ldg(s + lane) : 0;
+  }
+  // Is this lane's x an entry?  All lanes call.
+  __device__ __forceinline__ bool has_mine(int x) const {
+    bool hit = false;
+    for (int i = 0; i < min(cnt, 32); ++i) hit |= __shfl_sync(0xffffffffu, id, i) == x;
+    return hit || (cnt > 32 && id_in(x, set + 32, cnt - 32));
+  }
+  // Is x, the same in every lane, an entry?  All lanes call.
+  __device__ __forceinline__ bool has(int x) const {
+    const int lane = threadIdx.x & 31;
+    if (__any_sync(0xffffffffu, lane < cnt && id == x)) return true;
+    return cnt > 32 && warp_id_in(x, set + 32, cnt - 32);
+  }
+};
+
 // 16-byte global -> shared copy in the background, and its groups.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -228,25 +251,25 @@ __device__ __forceinline__ void load_row(const float* p, float (&x)[PER]) {
   }
 }
 
-// Puts NR new rows into a block (all lanes call): row i of x goes to row
-// first + i where bit i of mask is set.  The block's exponent grows when they
-// need it, and then its other codes are rounded again; fresh: the block
-// starts with these rows.
-template <int D, int NR>
-__device__ __forceinline__ void put_rows(const float (&x)[NR][D / 32], uint32_t mask, int first,
-                                         bool fresh, uint8_t* codes, int8_t* exp_at) {
-  constexpr int PER = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int had = fresh ? -128 : *exp_at;
+// Largest magnitude of the lane's values of a row, as bits.
+template <int PER>
+__device__ __forceinline__ uint32_t row_top(const float (&x)[PER]) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < NR; ++i)
-    if (mask >> i & 1) {
-#pragma unroll
-      for (int k = 0; k < PER; ++k) top = max(top, finite_bits(x[i][k]));
-    }
-  top = __reduce_max_sync(0xffffffffu, top);
-  const int now = max(had, block_exponent(top));
+  for (int k = 0; k < PER; ++k) top = max(top, finite_bits(x[k]));
+  return top;
+}
+
+// Opens a block for new rows whose largest magnitude has the bits `top` (the
+// lane's; all lanes call): its exponent grows when they need it, and then its
+// codes are rounded again; fresh: the block starts with these rows.  Returns
+// the factor of the new rows' values.
+template <int D>
+__device__ __forceinline__ float open_block(uint32_t top, bool fresh, uint8_t* codes,
+                                            int8_t* exp_at) {
+  const int lane = threadIdx.x & 31;
+  const int had = fresh ? -128 : *exp_at;
+  const int now = max(had, block_exponent(__reduce_max_sync(0xffffffffu, top)));
   if (!fresh && now > had) {
     const uint32_t f = half2_pow2_neg(now - had);
 #pragma unroll
@@ -261,19 +284,23 @@ __device__ __forceinline__ void put_rows(const float (&x)[NR][D / 32], uint32_t 
     }
   }
   __syncwarp();  // the exponent has been read, the old codes are in place
-  const float inv = pow2f(-now);
-#pragma unroll
-  for (int i = 0; i < NR; ++i)
-    if (mask >> i & 1) {
-      uint8_t* p = codes + (size_t)(first + i) * D + lane * PER;
-      if constexpr (PER == 4)
-        *reinterpret_cast<uint32_t*>(p) =
-            code4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
-      else
-        *reinterpret_cast<unsigned short*>(p) =
-            (unsigned short)code2(x[i][0] * inv, x[i][1] * inv);
-    }
   if (lane == 0) *exp_at = (int8_t)now;
+  return pow2f(-now);
+}
+
+// Codes a row of an open block.
+template <int PER>
+__device__ __forceinline__ void code_row(const float (&x)[PER], float inv, uint8_t* row) {
+  uint8_t* p = row + (threadIdx.x & 31) * PER;
+  if constexpr (PER == 4)
+    *reinterpret_cast<uint32_t*>(p) = code4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+  else
+    *reinterpret_cast<unsigned short*>(p) = (unsigned short)code2(x[0] * inv, x[1] * inv);
+}
+
+// Rows of a never-evicted segment that its table can hold.
+__device__ __forceinline__ int live_rows(const fg_paged_desc& hd, int rows) {
+  return (int)max(0LL, min((long long)rows, (long long)hd.max_pages * kPageRows));
 }
 
 struct AppendArgs {

@@ -156,22 +156,6 @@ __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
                : "memory");
 }
 
-// A small id set over the lanes of a warp, read ahead of its use: lane l holds
-// entry l; entries past 32 are looked up when asked.
-struct LaneSet {
-  const int32_t* set;
-  int cnt, id;
-  __device__ __forceinline__ LaneSet(const int32_t* s, int n) : set(s), cnt(n) {
-    const int lane = threadIdx.x & 31;
-    id = lane < n ? __ldg(s + lane) : 0;
-  }
-  __device__ __forceinline__ bool has(int x) const {  // all lanes call
-    const int lane = threadIdx.x & 31;
-    if (__any_sync(0xffffffffu, lane < cnt && id == x)) return true;
-    return cnt > 32 && warp_id_in(x, set + 32, cnt - 32);
-  }
-};
-
 // Where the step's token goes in a cache, if it falls in an item's pages.
 struct Put {
   int at;     // row of the segment or slot of the ring, -1: not in this item
@@ -193,10 +177,6 @@ __device__ __forceinline__ Put item_put(const PagedDecodeArgs& n, const PagedIte
   if (p.ring ? ring_mine : seg_mine) p.at = p.ring ? slot : old;
   return p;
 }
-__device__ __forceinline__ int live_rows(const fg_paged_desc& hd, int rows) {
-  return (int)max(0LL, min((long long)rows, (long long)hd.max_pages * kPageRows));
-}
-
 __device__ __forceinline__ uint32_t word4(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
@@ -209,9 +189,9 @@ __device__ __forceinline__ void put_token(const PagedArgs& a, const PagedDecodeA
   const int lane = threadIdx.x & 31;
   const int first = put.ring ? hd.ring_page : hd.first_page;
   const int entries = put.ring ? hd.ring_pages : hd.max_pages;
-  float xk[1][PER], xv[1][PER];
-  load_row<PER>((const T*)n.k_new + (size_t)c * D, xk[0]);
-  load_row<PER>((const T*)n.v_new + (size_t)c * D, xv[0]);
+  float xk[PER], xv[PER];
+  load_row<PER>((const T*)n.k_new + (size_t)c * D, xk);
+  load_row<PER>((const T*)n.v_new + (size_t)c * D, xv);
   const int i = put.at / kPageRows;
   int page = page_at(a, first, entries, i);
   if (page < 0) {
@@ -241,14 +221,15 @@ __device__ __forceinline__ void put_token(const PagedArgs& a, const PagedDecodeA
       rope_cos_sin((unsigned)t, n.rope.turns[p], y.x, y.y);
       return y;
     });
-    rotate_row<PER>(xk[0], cs, n.rope.rot, n.rope.style);
+    rotate_row<PER>(xk, cs, n.rope.rot, n.rope.style);
   }
   const int r = put.at % kPageRows, blk = r / kBlockRows;
   const size_t row = (size_t)page * kPageRows + blk * kBlockRows;
   const bool fresh = !put.ring && r % kBlockRows == 0;
   int8_t* ex = a.exps + ((size_t)page * kPageBlocks + blk) * 2;
-  put_rows<D, 1>(xk, 1u, r % kBlockRows, fresh, a.kp + row * D, ex);
-  put_rows<D, 1>(xv, 1u, r % kBlockRows, fresh, a.vp + row * D, ex + 1);
+  uint8_t *kb = a.kp + row * D, *vb = a.vp + row * D;
+  code_row<PER>(xk, open_block<D>(row_top<PER>(xk), fresh, kb, ex), kb + r % kBlockRows * D);
+  code_row<PER>(xv, open_block<D>(row_top<PER>(xv), fresh, vb, ex + 1), vb + r % kBlockRows * D);
   if (lane == 0) a.pos[(size_t)page * kPageRows + r] = t;
 }
 

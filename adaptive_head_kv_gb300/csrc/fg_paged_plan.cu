@@ -177,17 +177,107 @@ __global__ void __launch_bounds__(256) paged_items_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// Coding the kept rows.  One CTA per (cache, kChunkRows rows of its
-// never-evicted segment or of its ring).  A segment's CTA first finds the
-// positions of its rows: a scan of the keep codes, in which each thread counts
-// its positions' never-evicted codes.  Then each warp takes blocks of 16 rows:
-// the rows' K and V in registers (one pass over the data), the block's largest
-// magnitudes, the exponents, the codes.  Bound by HBM: 2 * eb + 2 bytes a
-// value.
-constexpr int kCodeThreads = 256;
-constexpr int kCodeWarps = kCodeThreads / 32;
-constexpr int kChunkRows = 512;
-constexpr int kScanPer = 16;  // positions per thread and scan step
+// Coding the kept rows.  One CTA per (cache, a chunk of the rows of
+// its never-evicted segment or of its ring).  A segment's CTA first finds the
+// positions of its rows: every thread turns kScanPer keep codes into bits, and
+// a scan of their counts ranks them.  Then each warp takes the K or the V of a
+// block of 16 rows: the rows in registers (one pass over the data), the
+// block's largest magnitude, the exponent, the codes.  Bound by HBM: 2 * eb + 2
+// bytes a value; the arithmetic on bf16 stays packed as long as it can (the
+// largest magnitude as two 16-bit integers a word, the scaling as one product
+// a pair), since unpacked it took more of the SM's time than the loads.
+//
+// A CTA has as many threads as its chunk has rows: 128, so that one CTA's
+// search hides behind its neighbours' rows, or 512 where a long prompt or a
+// large group makes the search (every CTA reads the codes before its chunk)
+// outweigh 128 rows.  Measured with 128 / 512, groups of 1 and 8: 2048
+// positions 36.8 / 41.6 us, 16384 40.1 / 41.9, 32768 25.7 / 23.4; 8 x 8192
+// 29.5 / 25.3, 8 x 16384 39.3 / 26.7.
+constexpr int kLongSearch = 24576;  // codes of a group
+constexpr int kScanPer = 32;  // positions per thread and scan step
+
+// Bit i: byte i of the 16 bytes at p is FG_KEEP_STATIC.  p is 16-byte aligned
+// and may reach over the ends of the buffer [lo, hi), of which nothing else is
+// read.
+__device__ __forceinline__ uint32_t static_bits16(const uint8_t* p, const uint8_t* lo,
+                                                  const uint8_t* hi) {
+  uint32_t bits = 0;
+  if (p >= lo && p + 16 <= hi) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t s = __vcmpeq4(w[k], 0x01010101u * FG_KEEP_STATIC) & 0x01010101u;
+      bits |= ((s * 0x01020408u) >> 24) << (4 * k);  // byte i's flag to bit i
+    }
+  } else {
+    for (int k = 0; k < 16; ++k)
+      if (p + k >= lo && p + k < hi && p[k] == FG_KEEP_STATIC) bits |= 1u << k;
+  }
+  return bits;
+}
+
+// Bit i: code at p + i is FG_KEEP_STATIC, for 32 codes at any address.
+__device__ __forceinline__ uint32_t static_bits32(const uint8_t* p, const uint8_t* lo,
+                                                  const uint8_t* hi) {
+  const int s = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+  const uint8_t* q = p - s;
+  const uint32_t w = static_bits16(q, lo, hi) | static_bits16(q + 16, lo, hi) << 16;
+  return s ? __funnelshift_r(w, static_bits16(q + 32, lo, hi), s) : w;
+}
+
+// Codes of a lane's 16 bytes of values times the power of two `inv`.
+__device__ __forceinline__ void code16(const uint4& x, float inv, uint8_t* p, const float*) {
+  *reinterpret_cast<uint32_t*>(p) =
+      code4(__uint_as_float(x.x) * inv, __uint_as_float(x.y) * inv, __uint_as_float(x.z) * inv,
+            __uint_as_float(x.w) * inv);
+}
+__device__ __forceinline__ uint32_t code_bf16x4(uint32_t a, uint32_t b, uint32_t inv2) {
+  // the products are exact: a power of two, and what underflows is far below half a code
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(inv2));
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(inv2));
+  return code4(bf16_lo(a), bf16_hi(a), bf16_lo(b), bf16_hi(b));
+}
+__device__ __forceinline__ void code16(const uint4& x, float inv, uint8_t* p,
+                                       const __nv_bfloat16*) {
+  const uint32_t h = __float_as_uint(inv) >> 16, inv2 = h | (h << 16);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(code_bf16x4(x.x, x.y, inv2), code_bf16x4(x.z, x.w, inv2));
+}
+
+// Bits of the largest magnitude (of finite values only) of the lane's N pieces.
+template <int N>
+__device__ __forceinline__ uint32_t lane_top(const uint4 (&x)[N], const float*) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    top = max(max(top, finite_bits(__uint_as_float(x[i].x))),
+              max(max(finite_bits(__uint_as_float(x[i].y)), finite_bits(__uint_as_float(x[i].z))),
+                  finite_bits(__uint_as_float(x[i].w))));
+  return top;
+}
+template <int N>
+__device__ __forceinline__ uint32_t lane_top(const uint4 (&x)[N], const __nv_bfloat16*) {
+  constexpr uint32_t kAbs = 0x7fff7fffu;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    top = __vmaxu2(top, __vmaxu2(x[i].x & kAbs, x[i].y & kAbs));
+    top = __vmaxu2(top, __vmaxu2(x[i].z & kAbs, x[i].w & kAbs));
+  }
+  top = max(top & 0xffffu, top >> 16);
+  if (top >= 0x7f80u) {  // an infinity or a NaN: again, one value at a time
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        top = max(top, max(finite_bits(bf16_lo(w[k])), finite_bits(bf16_hi(w[k]))) >> 16);
+    }
+  }
+  return top << 16;
+}
 
 // Codes a block of 16 rows: src[i] is the prompt position of row i, or -1.
 template <typename T, int D>
@@ -205,85 +295,58 @@ __device__ __forceinline__ void code_block(const T* __restrict__ X, const int* s
     const int j = src[i * RPI + sub];
     x[i] = j >= 0 ? ldg_stream(X + (size_t)j * D + gl * E) : make_uint4(0, 0, 0, 0);
   }
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    float f[E];
-    unpack16(x[i], f, (const T*)nullptr);
-#pragma unroll
-    for (int e = 0; e < E; ++e) top = max(top, finite_bits(f[e]));
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  const int e = block_exponent(top);
+  const int e = block_exponent(__reduce_max_sync(0xffffffffu, lane_top(x, (const T*)nullptr)));
   const float inv = pow2f(-e);
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int r = i * RPI + sub;
-    float f[E];
-    unpack16(x[i], f, (const T*)nullptr);
-    uint32_t w[E / 4];
-#pragma unroll
-    for (int k = 0; k < E / 4; ++k)
-      w[k] = code4(f[4 * k] * inv, f[4 * k + 1] * inv, f[4 * k + 2] * inv, f[4 * k + 3] * inv);
-    if (src[r] >= 0) {
-      uint8_t* p = dst + (size_t)r * D + gl * E;
-      if constexpr (E == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-      else *reinterpret_cast<uint32_t*>(p) = w[0];
-    }
+    if (src[r] >= 0) code16(x[i], inv, dst + (size_t)r * D + gl * E, (const T*)nullptr);
   }
   if (lane == 0) *exp_dst = (int8_t)e;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kCodeThreads) compact_q8_kernel(
+template <typename T, int D, int kChunkRows>
+__global__ void __launch_bounds__(kChunkRows) compact_q8_kernel(
     const T* __restrict__ K, const T* __restrict__ V, const uint8_t* __restrict__ keep, int n,
-    int H, int R, int seg_chunks, int chunks, const PagedArgs a) {
+    int G, int H, int R, int seg_chunks, int chunks, const PagedArgs a) {
+  constexpr int kCodeThreads = kChunkRows;
   __shared__ int src[kChunkRows];
   __shared__ int scr[33];
   const int c = blockIdx.x / chunks;
   int chunk = blockIdx.x % chunks;
   const fg_paged_desc d = a.caches[c];
+  const int rows = a.rows[c];
   const bool ring = chunk >= seg_chunks;
   if (ring) chunk -= seg_chunks;
   const int lo = chunk * kChunkRows;
-  const int total = ring ? d.w : (int)min((long long)a.rows[c], (long long)d.max_pages * kPageRows);
-  if (!ring && chunk == 0 && threadIdx.x == 0 && a.rows[c] > total)
-    atomicOr(a.dev_err, kErrInvalid);
+  const int total = ring ? d.w : (int)min((long long)rows, (long long)d.max_pages * kPageRows);
+  if (!ring && chunk == 0 && threadIdx.x == 0 && rows > total) atomicOr(a.dev_err, kErrInvalid);
   if (lo >= total) return;
   const int hi = min(lo + kChunkRows, total);
   const int Hkv = H / R;
   const size_t g0 = (size_t)(c / Hkv) * H + (size_t)(c % Hkv) * R;  // first query head
-  for (int i = threadIdx.x; i < kChunkRows; i += kCodeThreads) src[i] = -1;
+  src[threadIdx.x] = -1;
   __syncthreads();
   if (!ring) {
-    // static bits of kScanPer positions of a thread (any member keeps them so)
+    const uint8_t* end = keep + (size_t)G * n;
     int seen = 0;  // never-evicted rows before the step
     for (int base = 0; base < n && seen < hi; base += kCodeThreads * kScanPer) {
       const int j0 = base + threadIdx.x * kScanPer;
-      uint32_t bits = 0;
-      for (int m = 0; m < R; ++m) {
-        const uint8_t* row = keep + (g0 + m) * (size_t)n;
-        if (j0 + kScanPer <= n && (reinterpret_cast<uintptr_t>(row + j0) & 15) == 0) {
-          const uint4 v = *reinterpret_cast<const uint4*>(row + j0);
-          const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t s = __vcmpeq4(ws[k], 0x01010101u * FG_KEEP_STATIC) & 0x01010101u;
-            bits |= ((s * 0x01020408u) >> 24) << (4 * k);  // byte i's flag to bit i
-          }
-        } else {
-          for (int k = 0; k < kScanPer; ++k)
-            if (j0 + k < n && row[j0 + k] == FG_KEEP_STATIC) bits |= 1u << k;
-        }
+      uint32_t bits = 0;  // any member keeps the position so
+      if (j0 < n) {
+        for (int m = 0; m < R; ++m)
+          bits |= static_bits32(keep + (g0 + m) * (size_t)n + j0, keep, end);
+        if (n - j0 < kScanPer) bits &= (1u << (n - j0)) - 1;
       }
       int tot;
       int rank = seen + block_exclusive_scan(__popc(bits), scr, &tot);
-      while (bits) {
-        const int k = __ffs(bits) - 1;
-        bits &= bits - 1;
-        if (rank >= lo && rank < hi) src[rank - lo] = j0 + k;
-        ++rank;
-      }
+      if (rank < hi && rank + __popc(bits) > lo)
+        while (bits) {
+          const int k = __ffs(bits) - 1;
+          bits &= bits - 1;
+          if (rank >= lo && rank < hi) src[rank - lo] = j0 + k;
+          ++rank;
+        }
       seen += tot;
     }
   } else {
@@ -302,9 +365,9 @@ __global__ void __launch_bounds__(kCodeThreads) compact_q8_kernel(
   }
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const T* Kc = K + (size_t)c * n * D;
-  const T* Vc = V + (size_t)c * n * D;
-  for (int b = warp; b * kBlockRows < hi - lo; b += kCodeWarps) {
+  const int blocks = cdiv(hi - lo, kBlockRows);
+  for (int task = warp; task < 2 * blocks; task += kCodeThreads / 32) {
+    const int b = task >> 1, which = task & 1;
     const int row = lo + b * kBlockRows;
     const int page = ring ? page_at(a, d.ring_page, d.ring_pages, row / kPageRows)
                           : page_at(a, d.first_page, d.max_pages, row / kPageRows);
@@ -314,24 +377,30 @@ __global__ void __launch_bounds__(kCodeThreads) compact_q8_kernel(
     }
     const int r = row % kPageRows;
     const int* bs = src + b * kBlockRows;
-    if (lane < kBlockRows && row + lane < hi && (ring || bs[lane] >= 0))
+    if (which == 0 && lane < kBlockRows && row + lane < hi && (ring || bs[lane] >= 0))
       a.pos[(size_t)page * kPageRows + r + lane] = bs[lane];
-    const size_t off = ((size_t)page * kPageRows + r) * D;
-    int8_t* ex = a.exps + ((size_t)page * kPageBlocks + r / kBlockRows) * 2;
-    code_block<T, D>(Kc, bs, a.kp + off, ex);
-    code_block<T, D>(Vc, bs, a.vp + off, ex + 1);
+    code_block<T, D>((which ? V : K) + (size_t)c * n * D, bs,
+                     (which ? a.vp : a.kp) + ((size_t)page * kPageRows + r) * D,
+                     a.exps + ((size_t)page * kPageBlocks + r / kBlockRows) * 2 + which);
   }
+}
+
+template <typename T, int D, int kChunkRows>
+cudaError_t run_compact_chunk(const ProfileDims& pd, const void* K, const void* V,
+                           const uint8_t* keep, const PagedArgs& a, cudaStream_t s) {
+  const int seg = cdiv(pd.n, kChunkRows), chunks = seg + cdiv(pd.w, kChunkRows);
+  const long long grid = (long long)pd.Gkv * chunks;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  compact_q8_kernel<T, D, kChunkRows><<<(unsigned)grid, kChunkRows, 0, s>>>(
+      (const T*)K, (const T*)V, keep, pd.n, pd.G, pd.H, pd.R, seg, chunks, a);
+  return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t run_compact_q8(const ProfileDims& pd, const void* K, const void* V,
                            const uint8_t* keep, const PagedArgs& a, cudaStream_t s) {
-  const int seg = cdiv(pd.n, kChunkRows), chunks = seg + cdiv(pd.w, kChunkRows);
-  const long long grid = (long long)pd.Gkv * chunks;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  compact_q8_kernel<T, D><<<(unsigned)grid, kCodeThreads, 0, s>>>(
-      (const T*)K, (const T*)V, keep, pd.n, pd.H, pd.R, seg, chunks, a);
-  return cudaGetLastError();
+  return (long long)pd.n * pd.R > kLongSearch ? run_compact_chunk<T, D, 512>(pd, K, V, keep, a, s)
+                            : run_compact_chunk<T, D, 128>(pd, K, V, keep, a, s);
 }
 
 }  // namespace
