@@ -117,7 +117,8 @@ struct LaneSet {
     const int lane = threadIdx.x & 31;
     id = lane < n ? __ldg(s + lane) : 0;
   }
-  // Is this lane's x an entry?  All lanes call.
+  // Is this lane's x an entry?  All lanes of the warp call, so never behind a
+  // condition that differs between them (nor the right side of || or &&).
   __device__ __forceinline__ bool has_mine(int x) const {
     bool hit = false;
     for (int i = 0; i < min(cnt, 32); ++i) hit |= __shfl_sync(0xffffffffu, id, i) == x;
@@ -251,26 +252,87 @@ __device__ __forceinline__ void load_row(const float* p, float (&x)[PER]) {
   }
 }
 
-// Largest magnitude of the lane's values of a row, as bits.
-template <int PER>
-__device__ __forceinline__ uint32_t row_top(const float (&x)[PER]) {
+// ------------------------------------------ 16-byte pieces of rows in lanes
+// The arithmetic on bf16 stays packed as long as it can (the largest
+// magnitude as two 16-bit integers a word, the scaling as one product a
+// pair): unpacked it took more of an SM's time than the loads.
+
+// Codes of a lane's 16 bytes of values times the power of two `inv`.
+__device__ __forceinline__ void code16(const uint4& x, float inv, uint8_t* p, const float*) {
+  *reinterpret_cast<uint32_t*>(p) =
+      code4(__uint_as_float(x.x) * inv, __uint_as_float(x.y) * inv, __uint_as_float(x.z) * inv,
+            __uint_as_float(x.w) * inv);
+}
+__device__ __forceinline__ uint32_t code_bf16x4(uint32_t a, uint32_t b, uint32_t inv2) {
+  // the products are exact: a power of two, and what underflows is far below half a code
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(inv2));
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(inv2));
+  return code4(bf16_lo(a), bf16_hi(a), bf16_lo(b), bf16_hi(b));
+}
+__device__ __forceinline__ void code16(const uint4& x, float inv, uint8_t* p,
+                                       const __nv_bfloat16*) {
+  const uint32_t h = __float_as_uint(inv) >> 16, inv2 = h | (h << 16);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(code_bf16x4(x.x, x.y, inv2), code_bf16x4(x.z, x.w, inv2));
+}
+
+// Bits of the largest finite magnitude among N values: one maximum a value,
+// which passes over NaN; an infinity is rare and costs a second look.
+template <int N>
+__device__ __forceinline__ uint32_t top_bits(const float (&x)[N]) {
+  float top = 0.f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) top = fmaxf(top, fabsf(x[k]));
+  uint32_t bits = __float_as_uint(top);
+  if (bits >= 0x7f800000u) {
+    bits = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) bits = max(bits, finite_bits(x[k]));
+  }
+  return bits;
+}
+
+// Bits of the largest magnitude (of finite values only) of the lane's N pieces.
+template <int N>
+__device__ __forceinline__ uint32_t lane_top(const uint4 (&x)[N], const float*) {
+  float f[4 * N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) unpack16(x[i], f + 4 * i, (const float*)nullptr);
+  return top_bits<4 * N>(f);
+}
+template <int N>
+__device__ __forceinline__ uint32_t lane_top(const uint4 (&x)[N], const __nv_bfloat16*) {
+  constexpr uint32_t kAbs = 0x7fff7fffu;
   uint32_t top = 0;
 #pragma unroll
-  for (int k = 0; k < PER; ++k) top = max(top, finite_bits(x[k]));
-  return top;
+  for (int i = 0; i < N; ++i) {
+    top = __vmaxu2(top, __vmaxu2(x[i].x & kAbs, x[i].y & kAbs));
+    top = __vmaxu2(top, __vmaxu2(x[i].z & kAbs, x[i].w & kAbs));
+  }
+  top = max(top & 0xffffu, top >> 16);
+  if (top >= 0x7f80u) {  // an infinity or a NaN: again, one value at a time
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        top = max(top, max(finite_bits(bf16_lo(w[k])), finite_bits(bf16_hi(w[k]))) >> 16);
+    }
+  }
+  return top << 16;
 }
 
 // Opens a block for new rows whose largest magnitude has the bits `top` (the
-// lane's; all lanes call): its exponent grows when they need it, and then its
-// codes are rounded again; fresh: the block starts with these rows.  Returns
-// the factor of the new rows' values.
+// lane's; all lanes call): its exponent, `had` so far (below kExpMin: the block
+// starts with these rows), grows when they need it, and then its codes are
+// rounded again.  Returns the factor of the new rows' values.
 template <int D>
-__device__ __forceinline__ float open_block(uint32_t top, bool fresh, uint8_t* codes,
+__device__ __forceinline__ float open_block(uint32_t top, int had, uint8_t* codes,
                                             int8_t* exp_at) {
   const int lane = threadIdx.x & 31;
-  const int had = fresh ? -128 : *exp_at;
   const int now = max(had, block_exponent(__reduce_max_sync(0xffffffffu, top)));
-  if (!fresh && now > had) {
+  if (had >= kExpMin && now > had) {
     const uint32_t f = half2_pow2_neg(now - had);
 #pragma unroll
     for (int i = 0; i < kBlockRows * D / 512; ++i) {

@@ -6,12 +6,12 @@
 // classifies the tokens, one a lane, and takes the K or the V rows of a
 // destination block of 16 rows at a time.
 //
-// More, two launches.  The first (per sequence and 256 caches) classifies the
-// tokens once, lists the special and the special-or-punctuation ones (every
-// cache of the sequence takes its never-evicted rows from one of these lists
-// or from all tokens), takes the pages that the segments grow into, writes
-// the new row counts and forms the (cos, sin) of every position once for all
-// caches.  The second gives each warp the K or the V rows of one destination
+// More, two launches.  In the first, every CTA counts its sequence's special
+// and special-or-punctuation tokens (one also lists them: a cache takes its
+// never-evicted rows from one of these lists or from all tokens), its warps
+// take the pages that kPlanCaches caches grow into, 32 at a time, and write
+// the new row counts; its threads form the (cos, sin) of every position once
+// for all caches.  The second gives each warp the K or the V rows of one destination
 // block of 16 rows.  In both a block's exponent is settled once and its codes
 // are rounded again at most once.
 //
@@ -25,85 +25,123 @@ namespace {
 constexpr int kThreads = 256;
 
 __device__ __forceinline__ int new_tokens(const AppendArgs& n, int b) {
-  if (n.pos[b] < 0) return 0;
-  return n.n_new ? max(0, min(n.n_new[b], n.m)) : n.m;
+  const int pos = n.pos[b], cnt = n.n_new ? n.n_new[b] : n.m;  // asked for together
+  return pos < 0 ? 0 : max(0, min(cnt, n.m));
 }
+
+constexpr int kPlanCaches = 8;   // caches of a CTA of the first launch
 
 __global__ void __launch_bounds__(kThreads) append_plan_kernel(const PagedArgs a,
                                                                const AppendArgs n, int HLkv) {
   __shared__ int scr[33];
+  __shared__ int sm_count[2][kThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.y;
   const int cnt = new_tokens(n, b);
-  const int local = blockIdx.x * kThreads + threadIdx.x;  // cache of the sequence
   int n_s = 0, n_sp = 0;  // special, special or punctuation tokens
-  if (blockIdx.x * kThreads < HLkv) {  // uniform over the CTA
+  if (blockIdx.x == 0) {
     int32_t* ls = n.lists + (size_t)b * 2 * n.m;
     int32_t* lsp = ls + n.m;
     for (int base = 0; base < cnt; base += kThreads) {
       const int i = base + threadIdx.x;
-      bool s = false, sp = false;
-      if (i < cnt) {
-        const int tau = n.ids[(size_t)b * n.m + i];
-        s = id_in(tau, n.special, n.ns);
-        sp = s || id_in(tau, n.punct, n.np);
-      }
+      const int tau = i < cnt ? n.ids[(size_t)b * n.m + i] : 0;
+      const bool is_s = special.has_mine(tau), is_p = punct.has_mine(tau);  // every lane asks
+      const bool s = is_s && i < cnt, sp = (is_s || is_p) && i < cnt;
       int tot;
       const int before = block_exclusive_scan((int)s + ((int)sp << 16), scr, &tot);
-      if (blockIdx.x == 0) {
-        if (s) ls[n_s + (before & 0xffff)] = i;
-        if (sp) lsp[n_sp + (before >> 16)] = i;
-      }
+      if (s) ls[n_s + (before & 0xffff)] = i;
+      if (sp) lsp[n_sp + (before >> 16)] = i;
       n_s += tot & 0xffff;
       n_sp += tot >> 16;
     }
-  }
-  if (local < HLkv) {
-    const int c = b * HLkv + local;
-    const fg_paged_desc d = a.caches[c];
-    const int had = a.rows[c];
-    const long long cap = (long long)d.max_pages * kPageRows;
-    const int old = (int)max(0LL, min((long long)had, cap));
-    if (old != had) atomicOr(a.dev_err, kErrInvalid);
-    const int want = d.policy == FG_POLICY_FULL ? cnt : d.policy == FG_POLICY_S ? n_s : n_sp;
-    int now = (int)min((long long)old + want, min(cap, 0x7fffffffLL));
-    if (now - old < want) atomicOr(a.dev_err, kErrCapacity);
-    if (now > old) {
-      for (int i = old / kPageRows; i <= (now - 1) / kPageRows; ++i) {
-        if (d.first_page < 0 || d.first_page > a.table_len - 1 - i) {
-          atomicOr(a.dev_err, kErrInvalid);
-          now = max(old, i * kPageRows);
-          break;
-        }
-        int32_t* entry = a.table + d.first_page + i;
-        int page = *entry;
-        if (page < 0) {
-          page = atomicAdd(a.next_page, 1);
-          if (page < 0 || page >= a.n_pages) {
-            atomicOr(a.dev_err, kErrCapacity);
-            now = max(old, i * kPageRows);
-            break;
-          }
-          *entry = page;
-        } else if (page >= a.n_pages) {
-          atomicOr(a.dev_err, kErrInvalid);
-          now = max(old, i * kPageRows);
-          break;
-        }
+  } else if (blockIdx.x * kPlanCaches < HLkv) {  // the counts alone
+    for (int base = 0; base < cnt; base += 4 * kThreads) {
+      int tau[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = base + u * kThreads + threadIdx.x;
+        tau[u] = i < cnt ? n.ids[(size_t)b * n.m + i] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool in = base + u * kThreads + threadIdx.x < cnt;
+        const bool s = special.has_mine(tau[u]), p = punct.has_mine(tau[u]);
+        n_s += __popc(__ballot_sync(0xffffffffu, s && in));
+        n_sp += __popc(__ballot_sync(0xffffffffu, (s || p) && in));
       }
     }
-    n.old[2 * c] = old;
-    n.old[2 * c + 1] = now - old;
-    a.rows_out[c] = cnt > 0 ? now : had;
+    if (lane == 0) {
+      sm_count[0][warp] = n_s;
+      sm_count[1][warp] = n_sp;
+    }
+    __syncthreads();
+    n_s = n_sp = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      n_s += sm_count[0][w];
+      n_sp += sm_count[1][w];
+    }
+  }
+  for (int k = warp; k < kPlanCaches; k += kThreads / 32) {
+    const int local = blockIdx.x * kPlanCaches + k;  // cache of the sequence
+    if (local >= HLkv) break;
+    const int c = b * HLkv + local;
+    const fg_paged_desc d = a.caches[c];
+    const int had = a.rows[c], old = live_rows(d, had);
+    const int want = d.policy == FG_POLICY_FULL ? cnt : d.policy == FG_POLICY_S ? n_s : n_sp;
+    const long long cap = min((long long)d.max_pages * kPageRows, 0x7fffffffLL);
+    int now = (int)min((long long)old + want, max(cap, (long long)old));
+    int err = old != had && cnt > 0 ? kErrInvalid : 0;
+    if (now - old < want) err |= kErrCapacity;
+    const int end = now > old ? (now - 1) / kPageRows + 1 : 0;
+    for (int base = old / kPageRows; base < end; base += 32) {
+      const int i = base + lane;
+      const bool need = i < end;
+      const bool in_table = d.first_page >= 0 && d.first_page <= a.table_len - 1 - i;
+      int page = need && in_table ? a.table[d.first_page + i] : a.n_pages;
+      const uint32_t missing = __ballot_sync(0xffffffffu, need && page < 0);
+      if (missing) {
+        int first = 0;
+        if (lane == 0) first = atomicAdd(a.next_page, __popc(missing));
+        first = __shfl_sync(0xffffffffu, first, 0);
+        if (missing >> lane & 1) {
+          const long long p = (long long)first + __popc(missing & ((1u << lane) - 1));
+          if (first >= 0 && p < a.n_pages) {
+            page = (int)p;
+            a.table[d.first_page + i] = page;
+          } else {
+            err |= kErrCapacity;
+          }
+        } else if (need && page >= a.n_pages) {
+          err |= kErrInvalid;
+        }
+      } else if (need && page >= a.n_pages) {
+        err |= kErrInvalid;
+      }
+      // what fits before the first page that is not there is stored
+      const uint32_t bad = __ballot_sync(0xffffffffu, need && (page < 0 || page >= a.n_pages));
+      if (bad) {
+        now = max(old, (base + __ffs(bad) - 1) * kPageRows);
+        break;
+      }
+    }
+    if (err) atomicOr(a.dev_err, err);
+    if (lane == 0) {
+      n.old[2 * c] = old;
+      n.old[2 * c + 1] = now - old;
+      a.rows_out[c] = cnt > 0 ? now : had;
+    }
   }
   const int pairs = n.rope.rot / 2;
   if (pairs > 0 && cnt > 0) {
     const unsigned first = (unsigned)n.pos[b];
     float2* out = n.angles + (size_t)b * n.m * pairs;
-    for (int x = local; x < cnt * pairs; x += gridDim.x * kThreads) {
+    for (long long x = (long long)blockIdx.x * kThreads + threadIdx.x; x < (long long)cnt * pairs;
+         x += gridDim.x * kThreads) {
       float2 cs;
-      rope_cos_sin(first + x / pairs, n.rope.turns[x % pairs], cs.x, cs.y);
+      rope_cos_sin(first + (unsigned)(x / pairs), n.rope.turns[x % pairs], cs.x, cs.y);
       out[x] = cs;
     }
   }
@@ -126,6 +164,8 @@ __device__ __forceinline__ void append_block(const PagedArgs& a, const AppendArg
     return;
   }
   if (which == 0 && tok >= 0) a.pos[(size_t)page * kPageRows + r + lane] = (int)(p0 + tok);
+  int8_t* exp_at = a.exps + ((size_t)page * kPageBlocks + r / kBlockRows) * 2 + which;
+  const int had = fresh ? -128 : *exp_at;  // asked for before the rows
   const T* src = (const T*)(which ? n.v_new : n.k_new) + (size_t)c * n.m * D;
   uint8_t* codes = (which ? a.vp : a.kp) + ((size_t)page * kPageRows + r) * D;
   const bool turn = which == 0 && n.rope.rot > 0;
@@ -148,7 +188,6 @@ __device__ __forceinline__ void append_block(const PagedArgs& a, const AppendArg
       row_angles<PER>(cs, n.rope.rot, n.rope.style, [&](int p) { return angle(t, p); });
       rotate_row<PER>(x[i], cs, n.rope.rot, n.rope.style);
     }
-    return m;
   };
   auto skip = [](uint32_t m) {
 #pragma unroll
@@ -164,11 +203,10 @@ __device__ __forceinline__ void append_block(const PagedArgs& a, const AppendArg
     for (int i = 0; i < kHold; ++i) {
       if (left == 0) break;
       left &= left - 1;
-      top = max(top, row_top<PER>(x[i]));
+      top = max(top, top_bits<PER>(x[i]));
     }
   }
-  const float inv = open_block<D>(
-      top, fresh, codes, a.exps + ((size_t)page * kPageBlocks + r / kBlockRows) * 2 + which);
+  const float inv = open_block<D>(top, had, codes, exp_at);
   const bool held = skip(mask) == 0;
   for (uint32_t m = mask; m; m = skip(m)) {
     if (!held) {
@@ -182,6 +220,94 @@ __device__ __forceinline__ void append_block(const PagedArgs& a, const AppendArg
       code_row<PER>(x[i], inv, codes + (__ffs(left) - 1) * D);
       left &= left - 1;
     }
+  }
+}
+
+// The same for many rows: 16-byte pieces, a row over D / E lanes, all of the
+// block's rows in registers (a lane of a warp that held whole rows would have
+// two or four values of each and spend most of its instructions on addresses).
+template <typename T, int D>
+__device__ __forceinline__ void append_full_block(const PagedArgs& a, const AppendArgs& n, int c,
+                                                  int tok, unsigned p0, int page, int r,
+                                                  int which, bool fresh,
+                                                  const float2* __restrict__ angles) {
+  constexpr int E = Vec16<T>::kElems, LPR = D / E, RPI = 32 / LPR, NI = kBlockRows / RPI;
+  const int lane = threadIdx.x & 31, sub = lane / LPR, gl = lane % LPR, e0 = gl * E;
+  if (!__any_sync(0xffffffffu, tok >= 0)) return;
+  if (page < 0) {
+    if (lane == 0) atomicOr(a.dev_err, kErrInvalid);
+    return;
+  }
+  int8_t* exp_at = a.exps + ((size_t)page * kPageBlocks + r / kBlockRows) * 2 + which;
+  const int had = fresh ? -128 : *exp_at;
+  if (which == 0 && tok >= 0) a.pos[(size_t)page * kPageRows + r + lane] = (int)(p0 + tok);
+  const T* src = (const T*)(which ? n.v_new : n.k_new) + (size_t)c * n.m * D + e0;
+  uint8_t* codes = (which ? a.vp : a.kp) + ((size_t)page * kPageRows + r) * D;
+  uint8_t* dst = codes + sub * D + e0;
+  int t[NI];
+  uint4 x[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    t[i] = __shfl_sync(0xffffffffu, tok, i * RPI + sub);
+    x[i] = t[i] >= 0 ? ldg_stream(src + (size_t)t[i] * D) : make_uint4(0, 0, 0, 0);
+  }
+  const int rot = n.rope.rot, h = rot / 2;
+  if (which == 0 && rot > 0) {
+    const bool inter = n.rope.style == FG_ROPE_INTERLEAVED, first = e0 < h;
+    // the lane that holds the other half of this lane's pairs
+    const int other = inter || e0 >= rot ? lane : first ? lane + h / E : lane - h / E;
+    float f[NI][E];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      unpack16(x[i], f[i], (const T*)nullptr);
+      float y[E];
+      if (!inter) {
+        uint4 z;
+        z.x = __shfl_sync(0xffffffffu, x[i].x, other);
+        z.y = __shfl_sync(0xffffffffu, x[i].y, other);
+        z.z = __shfl_sync(0xffffffffu, x[i].z, other);
+        z.w = __shfl_sync(0xffffffffu, x[i].w, other);
+        unpack16(z, y, (const T*)nullptr);
+      }
+      if (t[i] >= 0 && e0 < rot) {
+        const float2* cs = angles + (size_t)t[i] * h;
+        if (inter) {
+#pragma unroll
+          for (int k = 0; k < E; k += 2) {
+            const float2 w = __ldg(cs + (e0 + k) / 2);
+            const float u = f[i][k], v = f[i][k + 1];
+            f[i][k] = u * w.x - v * w.y;
+            f[i][k + 1] = v * w.x + u * w.y;
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < E; ++k) {
+            const float2 w = __ldg(cs + e0 + k - (first ? 0 : h));
+            f[i][k] = first ? f[i][k] * w.x - y[k] * w.y : f[i][k] * w.x + y[k] * w.y;
+          }
+        }
+      }
+      top = max(top, top_bits<E>(f[i]));
+    }
+    const float inv = open_block<D>(top, had, codes, exp_at);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      if (t[i] < 0) continue;
+      uint32_t w[E / 4];
+#pragma unroll
+      for (int k = 0; k < E / 4; ++k)
+        w[k] = code4(f[i][4 * k] * inv, f[i][4 * k + 1] * inv, f[i][4 * k + 2] * inv,
+                     f[i][4 * k + 3] * inv);
+      uint8_t* p = dst + i * RPI * D;
+      if constexpr (E == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(p) = w[0];
+    }
+  } else {
+    const float inv = open_block<D>(lane_top<NI>(x, (const T*)nullptr), had, codes, exp_at);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if (t[i] >= 0) code16(x[i], inv, dst + i * RPI * D, (const T*)nullptr);
   }
 }
 
@@ -212,14 +338,14 @@ __host__ __device__ inline int touched(int m, bool wrap) {
 }
 
 constexpr int kFew = 32;
-constexpr int kFewWarps = 4;
+constexpr int kFewWarps = 2;
 
 // One CTA per cache, at most kFew tokens (lane i: token i).
 template <typename T, int D>
 __global__ void __launch_bounds__(kFewWarps * 32)
     append_few_kernel(const PagedArgs a, const AppendArgs n, int HLkv) {
   __shared__ int sm_page[2], sm_stored;
-  __shared__ float2 sm_angle[kFew][D / 2];
+  extern __shared__ float2 sm_angle[];  // [m][rot / 2]
   const int c = blockIdx.x, b = c / HLkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const fg_paged_desc d = a.caches[c];
@@ -235,7 +361,7 @@ __global__ void __launch_bounds__(kFewWarps * 32)
   // the pages that the new rows may fall in (at most two), as they are
   const int page0 = old / kPageRows;
   int page = lane < 2 ? page_at(a, d.first_page, d.max_pages, page0 + lane) : -1;
-  const bool s = special.has_mine(tau), sp = punct.has_mine(tau) || s;
+  const bool s = special.has_mine(tau), p = punct.has_mine(tau), sp = s || p;
   const bool to_static = lane < cnt && (d.policy == FG_POLICY_FULL ? true
                                         : d.policy == FG_POLICY_S  ? s
                                                                    : sp);
@@ -283,7 +409,7 @@ __global__ void __launch_bounds__(kFewWarps * 32)
   for (int x = threadIdx.x; x < cnt * pairs; x += kFewWarps * 32) {
     float2 cs;
     rope_cos_sin(p0 + (unsigned)(x / pairs), n.rope.turns[x % pairs], cs.x, cs.y);
-    sm_angle[x / pairs][x % pairs] = cs;
+    sm_angle[x] = cs;
   }
   __syncthreads();
   const int stored = sm_stored;
@@ -291,7 +417,7 @@ __global__ void __launch_bounds__(kFewWarps * 32)
   const int seg = stored > 0 ? (old + stored - 1) / kBlockRows - old / kBlockRows + 1 : 0;
   const int in = d.policy == FG_POLICY_SPFL && d.w > 0 ? min(cnt, d.w) : 0;
   const int ring = in > 0 ? min(cdiv(d.w, kBlockRows), touched(in, true)) : 0;
-  auto angle = [&](int tok, int p) { return sm_angle[tok][p]; };
+  auto angle = [&](int tok, int p) { return sm_angle[tok * pairs + p]; };
   for (int task = warp; task < 2 * (seg + ring); task += kFewWarps) {
     const int which = task & 1, j = task >> 1;
     if (j < seg) {
@@ -358,22 +484,22 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const PagedArgs a, 
     page = page_at(a, d.ring_page, d.ring_pages, row / kPageRows);
     tok = o.tok;
     const int tau = tok >= 0 ? n.ids[(size_t)b * n.m + tok] : 0;
-    const bool s = special.has_mine(tau), sp = punct.has_mine(tau) || s;
-    if (sp) tok = -1;  // the never-evicted segment takes it
+    const bool s = special.has_mine(tau), p = punct.has_mine(tau);
+    if (s || p) tok = -1;  // the never-evicted segment takes it
   }
   const float2* angles = n.angles + (size_t)b * n.m * (n.rope.rot / 2);
-  append_block<T, D, kBlockRows>(a, n, c, tok, p0, page, row % kPageRows, which, fresh,
-                     [&](int t, int p) { return angles[(size_t)t * (n.rope.rot / 2) + p]; });
+  append_full_block<T, D>(a, n, c, tok, p0, page, row % kPageRows, which, fresh, angles);
 }
 
 template <typename T, int D>
 cudaError_t run_append(const ProfileDims& pd, const PagedArgs& a, const AppendArgs& n,
                        cudaStream_t s) {
   if (n.m <= kFew)
-    return launch_pdl(append_few_kernel<T, D>, pd.Gkv, kFewWarps * 32, 0, s, a, n, pd.HLkv);
+    return launch_pdl(append_few_kernel<T, D>, pd.Gkv, kFewWarps * 32,
+                      (size_t)n.m * (n.rope.rot / 2) * sizeof(float2), s, a, n, pd.HLkv);
   // enough CTAs per sequence for its caches and, in long calls, its angles
   const int for_angles = (int)min((long long)64, ((long long)n.m * (n.rope.rot / 2) + 1023) / 1024);
-  const int per_seq = max(cdiv(pd.HLkv, kThreads), for_angles);
+  const int per_seq = max(cdiv(pd.HLkv, kPlanCaches), for_angles);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(per_seq, pd.B);
   cfg.blockDim = dim3(kThreads);

@@ -225,11 +225,12 @@ __device__ __forceinline__ void put_token(const PagedArgs& a, const PagedDecodeA
   }
   const int r = put.at % kPageRows, blk = r / kBlockRows;
   const size_t row = (size_t)page * kPageRows + blk * kBlockRows;
-  const bool fresh = !put.ring && r % kBlockRows == 0;
   int8_t* ex = a.exps + ((size_t)page * kPageBlocks + blk) * 2;
+  const bool fresh = !put.ring && r % kBlockRows == 0;
+  const int had_k = fresh ? -128 : ex[0], had_v = fresh ? -128 : ex[1];
   uint8_t *kb = a.kp + row * D, *vb = a.vp + row * D;
-  code_row<PER>(xk, open_block<D>(row_top<PER>(xk), fresh, kb, ex), kb + r % kBlockRows * D);
-  code_row<PER>(xv, open_block<D>(row_top<PER>(xv), fresh, vb, ex + 1), vb + r % kBlockRows * D);
+  code_row<PER>(xk, open_block<D>(top_bits<PER>(xk), had_k, kb, ex), kb + r % kBlockRows * D);
+  code_row<PER>(xv, open_block<D>(top_bits<PER>(xv), had_v, vb, ex + 1), vb + r % kBlockRows * D);
   if (lane == 0) a.pos[(size_t)page * kPageRows + r] = t;
 }
 

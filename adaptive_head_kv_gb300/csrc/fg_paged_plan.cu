@@ -183,9 +183,7 @@ __global__ void __launch_bounds__(256) paged_items_kernel(
 // a scan of their counts ranks them.  Then each warp takes the K or the V of a
 // block of 16 rows: the rows in registers (one pass over the data), the
 // block's largest magnitude, the exponent, the codes.  Bound by HBM: 2 * eb + 2
-// bytes a value; the arithmetic on bf16 stays packed as long as it can (the
-// largest magnitude as two 16-bit integers a word, the scaling as one product
-// a pair), since unpacked it took more of the SM's time than the loads.
+// bytes a value.
 //
 // A CTA has as many threads as its chunk has rows: 128, so that one CTA's
 // search hides behind its neighbours' rows, or 512 where a long prompt or a
@@ -224,59 +222,6 @@ __device__ __forceinline__ uint32_t static_bits32(const uint8_t* p, const uint8_
   const uint8_t* q = p - s;
   const uint32_t w = static_bits16(q, lo, hi) | static_bits16(q + 16, lo, hi) << 16;
   return s ? __funnelshift_r(w, static_bits16(q + 32, lo, hi), s) : w;
-}
-
-// Codes of a lane's 16 bytes of values times the power of two `inv`.
-__device__ __forceinline__ void code16(const uint4& x, float inv, uint8_t* p, const float*) {
-  *reinterpret_cast<uint32_t*>(p) =
-      code4(__uint_as_float(x.x) * inv, __uint_as_float(x.y) * inv, __uint_as_float(x.z) * inv,
-            __uint_as_float(x.w) * inv);
-}
-__device__ __forceinline__ uint32_t code_bf16x4(uint32_t a, uint32_t b, uint32_t inv2) {
-  // the products are exact: a power of two, and what underflows is far below half a code
-  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(inv2));
-  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(inv2));
-  return code4(bf16_lo(a), bf16_hi(a), bf16_lo(b), bf16_hi(b));
-}
-__device__ __forceinline__ void code16(const uint4& x, float inv, uint8_t* p,
-                                       const __nv_bfloat16*) {
-  const uint32_t h = __float_as_uint(inv) >> 16, inv2 = h | (h << 16);
-  *reinterpret_cast<uint2*>(p) =
-      make_uint2(code_bf16x4(x.x, x.y, inv2), code_bf16x4(x.z, x.w, inv2));
-}
-
-// Bits of the largest magnitude (of finite values only) of the lane's N pieces.
-template <int N>
-__device__ __forceinline__ uint32_t lane_top(const uint4 (&x)[N], const float*) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    top = max(max(top, finite_bits(__uint_as_float(x[i].x))),
-              max(max(finite_bits(__uint_as_float(x[i].y)), finite_bits(__uint_as_float(x[i].z))),
-                  finite_bits(__uint_as_float(x[i].w))));
-  return top;
-}
-template <int N>
-__device__ __forceinline__ uint32_t lane_top(const uint4 (&x)[N], const __nv_bfloat16*) {
-  constexpr uint32_t kAbs = 0x7fff7fffu;
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    top = __vmaxu2(top, __vmaxu2(x[i].x & kAbs, x[i].y & kAbs));
-    top = __vmaxu2(top, __vmaxu2(x[i].z & kAbs, x[i].w & kAbs));
-  }
-  top = max(top & 0xffffu, top >> 16);
-  if (top >= 0x7f80u) {  // an infinity or a NaN: again, one value at a time
-    top = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        top = max(top, max(finite_bits(bf16_lo(w[k])), finite_bits(bf16_hi(w[k]))) >> 16);
-    }
-  }
-  return top << 16;
 }
 
 // Codes a block of 16 rows: src[i] is the prompt position of row i, or -1.
