@@ -13,13 +13,14 @@
 // that holds one is streamed last of its item, once that is done.
 //
 // Both products run as warp MMAs in f16, which holds every e4m3 code exactly:
-//   S[16 x 16 keys] = Q[16 x d] . K^T    queries in rows 0-7; rows 8-15 hold
-//                                        what f16 loses of fp32 queries
-//   O^T[d x 8]     += V^T[d x 16 keys] . P^T
+//   S^T[16 keys x 8] = K[16 keys x d] . Q^T
+//   O^T[d x 8]      += V^T[d x 16 keys] . P^T
+// with the group's queries as the 8 columns (fp32 queries and weights in two
+// f16 terms).
 // The dimension order inside a product is free as long as both operands agree,
-// so a lane's operand fragments are 16 consecutive bytes of a row; S's
-// accumulators are P^T's operand fragment as they stand.  The order of the
-// keys is free as well: with 16-byte pieces swizzled by the row, slot_key
+// so a lane's operand fragments are 16 consecutive bytes of a row; S^T's
+// accumulators become P^T's operand with one 8x8 transpose per 8 keys.  The
+// order of the keys is free as well: with 16-byte pieces swizzled by the row, slot_key
 // puts the rows that a load phase touches on different banks.  The exponents
 // of a block are two numbers for the whole MMA: K's scales the scores, V's is
 // added to them in base 2, so that the weight carries it and the sum divides
@@ -29,7 +30,10 @@
 //
 // Bound by HBM: 2 d bytes a row.  Unpacking costs one conversion per two
 // codes; scoring on the SIMT lanes would cost four instructions per two
-// codes and query, past the row stream's pace at two queries already.
+// codes and query, past the row stream's pace at two queries already.  The
+// MMA that takes e4m3 operands (k = 32, queries as sums of three e4m3 terms)
+// was slower (7B shape 52 -> 64 us): with operands that change it runs at
+// 0.30 a nanosecond and SM, the f16 one (k = 16) at 0.66.
 #include <type_traits>
 
 #include "fg_paged.cuh"
@@ -50,6 +54,14 @@ __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8x8 b16 matrix held one row pair per lane (lane l: row l/4,
+// columns 2(l%4), 2(l%4)+1).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // (lo, hi) -> f16x2, nearest even; values past f16's range become infinite.
@@ -360,6 +372,7 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
         if (lane == 0) reinterpret_cast<int*>(st + RG::kQExp)[qi] = eq;
       }
     };
+    const bool late = stage == 0 && pages > RG::kStages;
     // an item without a page has one empty stage
     for (int k = 0; k == 0 || k < pages; ++k, ++stage) {
       const int slot = stage % RG::kStages;
@@ -399,7 +412,9 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
         if (ring && lane < kPageRows / 4)
           cp_async16(st + RG::kPos + lane * 16, a.pos + (size_t)page * kPageRows + lane * 4);
       }
-      if (k == 0) put_queries(ring_smem + slot * RG::kStride);
+      // while the ring is empty, its other stages' copies go out before the queries are formed
+      const bool queries = late ? k + 1 == min(max(pages, 1), RG::kStages) : k == 0;
+      if (queries) put_queries(ring_smem + (late ? 0 : slot) * RG::kStride);
       if (!with_put) {
         ex.x = __shfl_sync(0xffffffffu, exp_l.x, k & 31);
         ex.y = __shfl_sync(0xffffffffu, exp_l.y, k & 31);
@@ -419,7 +434,8 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
         info->w = hd.w;
       }
       arrive_after_copies(&bars->full[slot]);
-      sm100::mbar_arrive(&bars->full[slot]);
+      if (k > 0 || !late) sm100::mbar_arrive(&bars->full[slot]);
+      if (queries && late) sm100::mbar_arrive(&bars->full[0]);  // the first stage is complete now
     }
     if (alone) {  // no other reader of the count is left once the rows are put
       wait_puts();
@@ -510,13 +526,16 @@ __global__ void __launch_bounds__(kThreads, 3)
   int stage = 0, half = 0;
 #pragma unroll 1
   for (int wi = wi0; wi < wi_end; ++wi) {
-    // lanes without a query keep a maximum that no score passes: weight 0
-    float m = g < R ? FG_NEG_INF : 1e30f, l = 0.f;
+    // of queries 2 t4 and 2 t4 + 1 over the lane's keys; columns without a query keep a maximum
+    // that no score passes: weight 0
+    float m[2], l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) m[q] = 2 * t4 + q < R ? FG_NEG_INF : 1e30f;
     float o[MT][4];
 #pragma unroll
     for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     uint32_t qa[4 * KI][kWide ? 4 : 2];
-    int eq = 0;
+    int eq[2] = {0, 0};
     int last = 0, item = 0, cache = 0, alone = 0;
 #pragma unroll 1
     for (bool opening = true; !last; opening = false, ++stage) {
@@ -550,7 +569,9 @@ __global__ void __launch_bounds__(kThreads, 3)
               qa[4 * i + w][3] = y.y;
             }
           }
-        eq = g < R ? reinterpret_cast<const int*>(sp + RG::kQExp)[g] : 0;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          eq[q] = 2 * t4 + q < R ? reinterpret_cast<const int*>(sp + RG::kQExp)[2 * t4 + q] : 0;
       }
       const int row = info->row + warp * kBlockRows, end = info->end, kind = info->kind;
       if (kind == kNone || row >= end) {  // uniform over the warp: no rows here
@@ -561,17 +582,19 @@ __global__ void __launch_bounds__(kThreads, 3)
       const uint32_t ex = info->exps[warp >> 1] >> (16 * (warp & 1));
       const int ek = (int)(signed char)(ex & 0xff), ev = (int)(signed char)((ex >> 8) & 0xff);
       const uint32_t st = base + (uint32_t)(slot * RG::kStride);
-      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+      // scores of key kr ([0], [1]) and key kr + 8 ([2], [3]) with queries 2 t4 and 2 t4 + 1
+      float x[4] = {0.f, 0.f, 0.f, 0.f}, xl[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < KI; ++i) {
         const uint4 k0 = lds16(st + k_off[i]), k1 = lds16(st + k_off[i] + 8 * D);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const uint32_t x = word4(k0, w), y = word4(k1, w);
+          const uint32_t y0 = word4(k0, w), y1 = word4(k1, w);
           const uint32_t(&q)[kWide ? 4 : 2] = qa[4 * i + w];
-          const uint32_t q2 = kWide ? q[kWide ? 2 : 0] : 0u, q3 = kWide ? q[kWide ? 3 : 0] : 0u;
-          mma_f16_16816(s0, q[0], q2, q[1], q3, decode2(x), decode2(x >> 16));
-          mma_f16_16816(s1, q[0], q2, q[1], q3, decode2(y), decode2(y >> 16));
+          const uint32_t f0 = decode2(y0), f1 = decode2(y1), f2 = decode2(y0 >> 16),
+                         f3 = decode2(y1 >> 16);
+          mma_f16_16816(x, f0, f1, f2, f3, q[0], q[1]);
+          if constexpr (kWide) mma_f16_16816(xl, f0, f1, f2, f3, q[2], q[3]);
         }
       }
       Piece<D> v[4];  // keys va, vb, va + 8, vb + 8
@@ -579,67 +602,70 @@ __global__ void __launch_bounds__(kThreads, 3)
       v[1].load(st + vb_off);
       v[2].load(st + va_off + 8 * D);
       v[3].load(st + vb_off + 8 * D);
-      // scores in base 2, V's exponent added: those keys and query g
-      const int e = max(-126, min(127, ek + eq));
-      const float kf = pow2f(e) * sl2, fv = (float)ev;
-      float x[4] = {s0[0], s0[1], s1[0], s1[1]};
-      if constexpr (kWide) {
-        x[0] += s0[2] * (1.f / 2048.f);
-        x[1] += s0[3] * (1.f / 2048.f);
-        x[2] += s1[2] * (1.f / 2048.f);
-        x[3] += s1[3] * (1.f / 2048.f);
-      }
+      // in base 2, V's exponent added
+      const float fv = (float)ev;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = fmaf(x[i], kf, fv);
+      for (int q = 0; q < 2; ++q) {
+        const float kf = pow2f(max(-126, min(127, ek + eq[q]))) * sl2;
+#pragma unroll
+        for (int h = 0; h < 4; h += 2) {
+          if constexpr (kWide) x[q + h] = fmaf(xl[q + h], 1.f / 2048.f, x[q + h]);
+          x[q + h] = fmaf(x[q + h], kf, fv);
+        }
+      }
       if (kind == kRing || row + kBlockRows > end) {  // uniform: rows may be missing
         const int t = info->t, w = info->w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = (i & 1 ? vb : va) + (i & 2 ? 8 : 0);
+        auto there = [&](int key) {
           bool ok = row + key < end;
           if (kind == kRing) {  // in the window: position in (t - w, t]
             const int p = reinterpret_cast<const int*>(sp + RG::kPos)[warp * kBlockRows + key];
             ok = ok && p >= 0 && (unsigned)t - (unsigned)p < (unsigned)w;
           }
-          if (!ok) {
-            x[i] = FG_NEG_INF;
-            v[i].zero();  // such a row may hold anything, also NaN
-          }
-        }
+          return ok;
+        };
+        if (!there(kr)) x[0] = x[1] = FG_NEG_INF;
+        if (!there(kr + 8)) x[2] = x[3] = FG_NEG_INF;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // such a row may hold anything, also NaN
+          if (!there((i & 1 ? vb : va) + (i & 2 ? 8 : 0))) v[i].zero();
       }
       __syncwarp();  // every lane has read the stage
       if (lane == 0) sm100::mbar_arrive(&bars.empty[slot]);
-      float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      if (__any_sync(0xffffffffu, top > m)) {
-        const float mn = fmaxf(m, top);
-        const float corr = m == FG_NEG_INF ? 0.f : ex2(m - mn);
-        m = mn;
-        l *= corr;
-        const float c0 = __shfl_sync(0xffffffffu, corr, 8 * t4);
-        const float c1 = __shfl_sync(0xffffffffu, corr, 8 * t4 + 4);
+      float top[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          o[i][0] *= c0;
-          o[i][1] *= c1;
-          o[i][2] *= c0;
-          o[i][3] *= c1;
+        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1)
+            top[q] = fmaxf(top[q], __shfl_xor_sync(0xffffffffu, top[q], d));
+          const float mn = fmaxf(m[q], top[q]);
+          const float corr = m[q] == FG_NEG_INF ? 0.f : ex2(m[q] - mn);
+          m[q] = mn;
+          l[q] *= corr;
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            o[i][q] *= corr;
+            o[i][q + 2] *= corr;
+          }
         }
       }
-      const float off = (m == FG_NEG_INF ? 0.f : m) - kPBits;
       float p[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = ex2(x[i] - off);
-      const uint32_t p01 = pack_f16x2(p[0], p[1]), p23 = pack_f16x2(p[2], p[3]);
-      // the sum takes the weights in 32 bits: f16 would lose those that a small
-      // exponent of V makes small
-      l = fmaf((p[0] + p[1]) + (p[2] + p[3]), pow2f(-ev), l);
+      for (int q = 0; q < 2; ++q) {
+        const float off = (m[q] == FG_NEG_INF ? 0.f : m[q]) - kPBits;
+        p[q] = ex2(x[q] - off);
+        p[q + 2] = ex2(x[q + 2] - off);
+        // the sum takes the weights in 32 bits: f16 would lose those that a small
+        // exponent of V makes small
+        l[q] = fmaf(p[q] + p[q + 2], pow2f(-ev), l[q]);
+      }
+      const uint32_t lo = pack_f16x2(p[0], p[1]), hi = pack_f16x2(p[2], p[3]);
+      const uint32_t p01 = transpose8x8(lo), p23 = transpose8x8(hi);
       uint32_t r01 = 0, r23 = 0;
       if constexpr (kWide) {
-        const float2 f01 = unpack_f16x2(p01), f23 = unpack_f16x2(p23);
-        r01 = pack_f16x2(p[0] - f01.x, p[1] - f01.y);
-        r23 = pack_f16x2(p[2] - f23.x, p[3] - f23.y);
+        const float2 f01 = unpack_f16x2(lo), f23 = unpack_f16x2(hi);
+        r01 = transpose8x8(pack_f16x2(p[0] - f01.x, p[1] - f01.y));
+        r23 = transpose8x8(pack_f16x2(p[2] - f23.x, p[3] - f23.y));
       }
 #pragma unroll
       for (int w = 0; w < PW; ++w) {
@@ -663,11 +689,14 @@ __global__ void __launch_bounds__(kThreads, 3)
     // the item is through: merge the four warps
     float(&sm_m)[kWarps][kMaxR] = sm_ml[half][0], (&sm_l)[kWarps][kMaxR] = sm_ml[half][1];
     half ^= 1;  // the other half may still be read
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    if (t4 == 0 && g < R) {
-      sm_m[warp][g] = m;
-      sm_l[warp][g] = l;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[q] += __shfl_xor_sync(0xffffffffu, l[q], d);
+      if (g == 0 && 2 * t4 + q < R) {
+        sm_m[warp][2 * t4 + q] = m[q];
+        sm_l[warp][2 * t4 + q] = l[q];
+      }
     }
     sync_warps();
     // O^T: rows 16 j + g, + 8 are dimensions (D / 8) g + 2 j, + 1; columns queries 2 t4, 2 t4 + 1
@@ -678,8 +707,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         float M = FG_NEG_INF;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][qi]);
-        const float mine = sm_m[warp][qi];
-        const float f = mine == FG_NEG_INF ? 1.f : exp2f(mine - M);  // (0, or NaN: as they are)
+        const float f = m[qc] == FG_NEG_INF ? 1.f : exp2f(m[qc] - M);  // (0, or NaN: as they are)
 #pragma unroll
         for (int j = 0; j < MT; ++j)
           *reinterpret_cast<float2*>(&sums[(warp * R + qi) * D + (D / 8) * g + 2 * j]) =
