@@ -395,12 +395,21 @@ def _elem(p: Params):
     return torch.bfloat16 if p.dtype == FG_BF16 else torch.float32
 
 
+class _Sizes:
+    """What the checks of a call need of its parameters."""
+
+    def __init__(self, p: Params):
+        self.B, self.d, self.n, self.dt = p.B, p.d, p.n, _elem(p)
+        self.G, self.Gkv = _heads(p)
+        self.queries, self.rows = self.G * p.d, self.Gkv * p.d  # values of one row each
+
+
 def _run(where: str, dev: int, stream, fn, *args) -> None:
     """Calls fn(*args, stream) with device `dev` current."""
     torch = _T or _torch()
     if dev < 0:
         _refuse(where, "tensors must be on a GPU")
-    here = torch.cuda.current_device()
+    here = torch._C._cuda_getDevice()
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
     elif not isinstance(stream, int):
@@ -488,9 +497,10 @@ class PagedCache:
     def __init__(self, params, k_pages, v_pages, exps, pos, page_table, caches, rows, next_page,
                  rows_out=None):
         torch, w = _torch(), "PagedCache"
-        Gkv = _heads(params)[1]
+        self.key, self.sizes = bytes(params), _Sizes(params)
+        Gkv = self.sizes.Gkv
         dev, i32 = page_table.get_device(), torch.int32
-        self.dev, self.d, self.count = dev, params.d, Gkv
+        self.dev, self.d = dev, params.d
         c = self.c = PagedCacheStruct()
         c.table_len = page_table.numel()
         c.page_table = _is(page_table, w, "page_table", i32, page_table.numel(), dev)
@@ -524,35 +534,38 @@ class PagedCache:
         fastgen_paged_schedule(params, self, stream)
 
 
+def _of_cache(p: Params, cache, w: str):
+    """The sizes of a call on `cache`, which must have been made for the same
+    sequences, heads and head dim (other parameters may differ)."""
+    if bytes(p) == cache.key:
+        return cache.sizes
+    z = _Sizes(p)
+    if z.Gkv != cache.sizes.Gkv or z.B != cache.sizes.B or z.d != cache.d:
+        _refuse(w, "the cache was made for other parameters")
+    return z
+
+
 def fastgen_paged_plan(params, policy, keep, max_new_tokens, cache, stream=None) -> PagedInfo:
     w, torch = "fastgen_paged_plan", _torch()
-    G, dev, info = _heads(params)[0], cache.dev, PagedInfo()
+    z, dev, info = _of_cache(params, cache, w), cache.dev, PagedInfo()
     _run(w, dev, stream, lib().fastgen_paged_plan, params,
-         _is(policy, w, "policy", torch.int8, G, dev),
-         _is(keep, w, "keep", torch.uint8, G * params.n, dev), max_new_tokens,
-         _of_cache(params, cache, w), info)
+         _is(policy, w, "policy", torch.int8, z.G, dev),
+         _is(keep, w, "keep", torch.uint8, z.G * z.n, dev), max_new_tokens, cache.c, info)
     return info
 
 
 def fastgen_paged_schedule(params, cache, stream=None) -> None:
     w = "fastgen_paged_schedule"
-    _run(w, cache.dev, stream, lib().fastgen_paged_schedule, params, _of_cache(params, cache, w))
-
-
-def _of_cache(p, cache, w: str):
-    """The cache's struct, if it belongs to these parameters."""
-    if cache.count != p.B * p.L * (p.Hkv or p.H) or cache.d != p.d:
-        _refuse(w, "the cache was made for other parameters")
-    return cache.c
+    _of_cache(params, cache, w)
+    _run(w, cache.dev, stream, lib().fastgen_paged_schedule, params, cache.c)
 
 
 def fastgen_compact_q8(params, K, V, keep, cache, dev_err, stream=None) -> None:
-    w, p, torch = "fastgen_compact_q8", params, _torch()
-    G, Gkv = _heads(p)
-    dev, dt, size = cache.dev, _elem(p), Gkv * p.n * p.d
-    _run(w, dev, stream, lib().fastgen_compact_q8, p, _is(K, w, "K", dt, size, dev),
-         _is(V, w, "V", dt, size, dev), _is(keep, w, "keep", torch.uint8, G * p.n, dev),
-         _of_cache(p, cache, w), _is(dev_err, w, "dev_err", torch.int32, 1, dev))
+    w, torch = "fastgen_compact_q8", _torch()
+    z, dev = _of_cache(params, cache, w), cache.dev
+    _run(w, dev, stream, lib().fastgen_compact_q8, params, _is(K, w, "K", z.dt, z.rows * z.n, dev),
+         _is(V, w, "V", z.dt, z.rows * z.n, dev), _is(keep, w, "keep", torch.uint8, z.G * z.n, dev),
+         cache.c, _is(dev_err, w, "dev_err", torch.int32, 1, dev))
 
 
 def fastgen_append_q8_workspace_bytes(params, m: int) -> int:
@@ -563,17 +576,17 @@ def fastgen_append_q8(params, cache, k_new, v_new, new_ids, n_new, special_ids, 
                       rope, workspace, dev_err, stream=None) -> None:
     """Appends m tokens: k_new, v_new [Gkv, m, d], new_ids [B, m], n_new [B] or
     None (m each), pos [B] the first new position of each sequence (< 0: idle)."""
-    w, p, torch = "fastgen_append_q8", params, _torch()
-    B, dev, dt, i32 = p.B, cache.dev, _elem(p), torch.int32
-    m = new_ids.numel() // B
-    rows, ws = cache.count * m * p.d, workspace.numel()
-    special, punct = (_id_set(special_ids, w, "special_ids", dev),
-                      _id_set(punct_ids, w, "punct_ids", dev))
-    _run(w, dev, stream, lib().fastgen_append_q8, p, _of_cache(p, cache, w),
-         _is(k_new, w, "k_new", dt, rows, dev), _is(v_new, w, "v_new", dt, rows, dev),
-         _is(new_ids, w, "new_ids", i32, B * m, dev), m,
-         None if n_new is None else _is(n_new, w, "n_new", i32, B, dev), special[0], special[1],
-         punct[0], punct[1], _is(pos, w, "pos", i32, B, dev), _rope(rope, w, dev),
+    w, torch = "fastgen_append_q8", _torch()
+    z, dev, i32 = _of_cache(params, cache, w), cache.dev, torch.int32
+    m, ws = new_ids.numel() // z.B, workspace.numel()
+    special, n_special = _id_set(special_ids, w, "special_ids", dev)
+    punct, n_punct = _id_set(punct_ids, w, "punct_ids", dev)
+    _run(w, dev, stream, lib().fastgen_append_q8, params, cache.c,
+         _is(k_new, w, "k_new", z.dt, z.rows * m, dev),
+         _is(v_new, w, "v_new", z.dt, z.rows * m, dev),
+         _is(new_ids, w, "new_ids", i32, z.B * m, dev), m,
+         None if n_new is None else _is(n_new, w, "n_new", i32, z.B, dev), special, n_special,
+         punct, n_punct, _is(pos, w, "pos", i32, z.B, dev), _rope(rope, w, dev),
          _is(workspace, w, "workspace", torch.uint8, ws, dev), ws,
          _is(dev_err, w, "dev_err", i32, 1, dev))
 
@@ -586,17 +599,16 @@ def fastgen_decode_attn_q8(params, cache, q, k_new, v_new, new_ids, special_ids,
                            rope, out, workspace, dev_err, stream=None) -> None:
     """One generation step: q, out [G, d], k_new, v_new [Gkv, d] (None: nothing is
     appended), new_ids [B], pos [B] int32 on the device (< 0: idle)."""
-    w, p, torch = "fastgen_decode_attn_q8", params, _torch()
-    B, d, dev, dt, i32 = p.B, p.d, cache.dev, _elem(p), torch.int32
-    queries, rows, ws = B * p.L * p.H * d, cache.count * d, workspace.numel()
-    special, punct = (_id_set(special_ids, w, "special_ids", dev),
-                      _id_set(punct_ids, w, "punct_ids", dev))
-    _run(w, dev, stream, lib().fastgen_decode_attn_q8, p, _of_cache(p, cache, w),
-         _is(q, w, "q", dt, queries, dev),
-         None if k_new is None else _is(k_new, w, "k_new", dt, rows, dev),
-         None if v_new is None else _is(v_new, w, "v_new", dt, rows, dev),
-         None if new_ids is None else _is(new_ids, w, "new_ids", i32, B, dev), special[0],
-         special[1], punct[0], punct[1], _is(pos, w, "pos", i32, B, dev), _rope(rope, w, dev),
-         _is(out, w, "out", dt, queries, dev),
+    w, torch = "fastgen_decode_attn_q8", _torch()
+    z, dev, i32, ws = _of_cache(params, cache, w), cache.dev, torch.int32, workspace.numel()
+    special, n_special = _id_set(special_ids, w, "special_ids", dev)
+    punct, n_punct = _id_set(punct_ids, w, "punct_ids", dev)
+    _run(w, dev, stream, lib().fastgen_decode_attn_q8, params, cache.c,
+         _is(q, w, "q", z.dt, z.queries, dev),
+         None if k_new is None else _is(k_new, w, "k_new", z.dt, z.rows, dev),
+         None if v_new is None else _is(v_new, w, "v_new", z.dt, z.rows, dev),
+         None if new_ids is None else _is(new_ids, w, "new_ids", i32, z.B, dev), special,
+         n_special, punct, n_punct, _is(pos, w, "pos", i32, z.B, dev), _rope(rope, w, dev),
+         _is(out, w, "out", z.dt, z.queries, dev),
          _is(workspace, w, "workspace", torch.uint8, ws, dev), ws,
          _is(dev_err, w, "dev_err", i32, 1, dev))
