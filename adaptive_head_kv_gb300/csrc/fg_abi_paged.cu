@@ -167,6 +167,7 @@ fg_status fastgen_rope(const fg_params* p, const void* Q, const void* K, const i
 int32_t fastgen_paged_table_len(const fg_params* p, int32_t max_new_tokens) {
   if (check_params(p) != FG_OK || max_new_tokens < 0) return 0;
   const long long rows = (long long)p->n + max_new_tokens;
+  if (rows > 0x7fffffffLL - fg::kPageRows) return 0;
   const long long w = ratio_count(p->r_l, p->n);
   const long long len = ((rows + fg::kPageRows - 1) / fg::kPageRows +
                          (w + fg::kPageRows - 1) / fg::kPageRows) * kv_count(p);

@@ -248,8 +248,8 @@ __device__ __forceinline__ void put_token(const PagedArgs& a, const PagedDecodeA
 
 // The streaming warp.
 template <typename T, int D>
-__device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDecodeArgs& n, int H,
-                                             int R, int HLkv, uint8_t* ring_smem, Bars* bars,
+__device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDecodeArgs& n, int Gkv,
+                                             int H, int R, int HLkv, uint8_t* ring_smem, Bars* bars,
                                              int wi, int wi_end, PagedItem it, fg_paged_desc hd,
                                              int items, const LaneSet& special,
                                              const LaneSet& punct) {
@@ -266,14 +266,16 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
   int stage = 0;
   bool opened = true;  // hd and items are the first item's
   for (; wi < wi_end; ++wi) {
-    const int c = it.cache, b = c / HLkv;
+    const bool known = (unsigned)it.cache < (unsigned)Gkv;
+    if (!known && lane == 0) atomicOr(a.dev_err, kErrInvalid);
+    const int c = known ? it.cache : 0, b = c / HLkv;
     if (!opened) {
       hd = a.caches[c];
       items = a.ranges[c].y;
     }
     opened = false;
-    const bool alone = items == 1;
-    const int t = n.pos[b], had = a.rows[c], tau = n.k_new ? n.ids[b] : 0;
+    const bool alone = items == 1 && known;
+    const int t = known ? n.pos[b] : -1, had = a.rows[c], tau = n.k_new ? n.ids[b] : 0;
     const PagedItem cur = it;
     if (wi + 1 < wi_end) it = a.items[wi + 1];  // known by the time this item is through
     // the group's queries and the angles' turns, on their way while the pages are looked up
@@ -449,7 +451,8 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 3)
-    q8_split_kernel(const PagedArgs a, const PagedDecodeArgs n, int H, int R, int HLkv, float sl2) {
+    q8_split_kernel(const PagedArgs a, const PagedDecodeArgs n, int G, int H, int R, int HLkv,
+                    float sl2) {
   constexpr bool kWide = sizeof(T) == 4;  // fp32: queries and weights in two f16 terms
   using RG = Ring<D, kWide>;
   constexpr int KI = D / 64;   // 16-byte pieces of a K row per lane
@@ -462,7 +465,11 @@ __global__ void __launch_bounds__(kThreads, 3)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
-  const int wi0 = a.cta_first[blockIdx.x], wi_end = a.cta_first[blockIdx.x + 1];
+  // a list of another cache may say anything: its items are bounded here, its
+  // caches where they are used
+  const int wi0 = max(0, min(a.cta_first[blockIdx.x], a.n_work - 1));
+  const int wi_end = max(wi0 + 1, min(a.cta_first[blockIdx.x + 1], a.n_work));
+  const int Gkv = G / R;
   if (threadIdx.x == 0) {
     for (int i = 0; i < RG::kStages; ++i) {
       sm100::mbar_init(&bars.full[i], 64);  // every streaming lane: its copies, and its stores
@@ -476,14 +483,15 @@ __global__ void __launch_bounds__(kThreads, 3)
   // what the schedule and the caller have fixed is read before the wait
   const int own = min(wi0 + (warp == kWarps ? 0 : warp), wi_end - 1);
   const PagedItem own_item = a.items[own];
-  const fg_paged_desc own_cache = a.caches[own_item.cache];
-  const int own_items = a.ranges[own_item.cache].y;
+  const int own_c = (unsigned)own_item.cache < (unsigned)Gkv ? own_item.cache : 0;
+  const fg_paged_desc own_cache = a.caches[own_c];
+  const int own_items = a.ranges[own_c].y;
   const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
   if (warp == kWarps) {
-    stream_items<T, D>(a, n, H, R, HLkv, ring_smem, &bars, wi0, wi_end, own_item, own_cache,
+    stream_items<T, D>(a, n, Gkv, H, R, HLkv, ring_smem, &bars, wi0, wi_end, own_item, own_cache,
                        own_items, special, punct);
     return;
   }
@@ -493,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     for (int wi = wi0 + warp; wi < wi_end; wi += kWarps) {
       const PagedItem it = wi == own ? own_item : a.items[wi];
       const int c = it.cache, b = c / HLkv;
+      if ((unsigned)c >= (unsigned)Gkv) continue;
       const fg_paged_desc hd = wi == own ? own_cache : a.caches[c];
       const int t = n.pos[b], tau = n.ids[b], had = a.rows[c];
       if (t < 0) continue;
@@ -754,7 +763,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   const bool in = gq < G;
   const int c = in ? kv_head(gq, H, R) : 0, qi = (gq % H) % R, b = c / HLkv;
   const fg_paged_desc hd = a.caches[c];
-  const int4 range = a.ranges[c];
+  int4 range = a.ranges[c];
+  range.x = max(0, min(range.x, a.n_work));
+  range.y = min(range.y, a.n_work - range.x);
   const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   griddep_wait();
   griddep_launch_dependents();
@@ -821,8 +832,8 @@ cudaError_t run_decode_q8(const ProfileDims& pd, const PagedArgs& a, const Paged
   cudaError_t e = cudaFuncSetAttribute(q8_split_kernel<T, D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess)
-    e = launch_pdl(q8_split_kernel<T, D>, a.n_ctas, kThreads, smem, s, a, n, pd.H, pd.R, pd.HLkv,
-                   pd.sl2);
+    e = launch_pdl(q8_split_kernel<T, D>, a.n_ctas, kThreads, smem, s, a, n, pd.G, pd.H, pd.R,
+                   pd.HLkv, pd.sl2);
   if (e == cudaSuccess && a.n_work > pd.Gkv)  // else every cache has one item
     e = launch_pdl(q8_combine_kernel<T, D>, cdiv(pd.G, kCombineWarps), kCombineWarps * 32, 0, s, a,
                    n, pd.G, pd.H, pd.R, pd.HLkv);

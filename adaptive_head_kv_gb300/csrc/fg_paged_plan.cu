@@ -253,7 +253,7 @@ __device__ __forceinline__ void code_block(const T* __restrict__ X, const int* s
 template <typename T, int D, int kChunkRows>
 __global__ void __launch_bounds__(kChunkRows) compact_q8_kernel(
     const T* __restrict__ K, const T* __restrict__ V, const uint8_t* __restrict__ keep, int n,
-    int G, int H, int R, int seg_chunks, int chunks, const PagedArgs a) {
+    int G, int H, int R, int max_w, int seg_chunks, int chunks, const PagedArgs a) {
   constexpr int kCodeThreads = kChunkRows;
   __shared__ int src[kChunkRows];
   __shared__ int scr[33];
@@ -337,7 +337,7 @@ cudaError_t run_compact_chunk(const ProfileDims& pd, const void* K, const void* 
   const long long grid = (long long)pd.Gkv * chunks;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   compact_q8_kernel<T, D, kChunkRows><<<(unsigned)grid, kChunkRows, 0, s>>>(
-      (const T*)K, (const T*)V, keep, pd.n, pd.G, pd.H, pd.R, seg, chunks, a);
+      (const T*)K, (const T*)V, keep, pd.n, pd.G, pd.H, pd.R, pd.w, seg, chunks, a);
   return cudaGetLastError();
 }
 

@@ -88,8 +88,13 @@ class FastGenSession:
                                        self.dev_err, self.stream)
 
     def prefill_with_policy(self, Q, K, V, token_ids, policy_map):
+        Q, K = self._ready(Q, K)
         self.profile_with_policy(Q, K, token_ids, policy_map)
         self.compact(K, V)
+
+    def _ready(self, Q, K):
+        """A prompt's queries and keys as they are profiled and cached."""
+        return Q, K
 
     def compact(self, K, V):
         if self.pos_pool is not None:  # pools from an earlier prompt: plan and gather in one call
@@ -130,6 +135,7 @@ class FastGenSession:
             self.dws = self._empty((max(need, 256),), torch.uint8)
 
     def prefill(self, Q, K, V, token_ids):
+        Q, K = self._ready(Q, K)
         self.profile(Q, K, token_ids)
         self.compact(K, V)
 
@@ -154,6 +160,7 @@ class FastGenSession:
             V.copy_(hV, non_blocking=True)
             v_ready.record(cs)
         main.wait_event(qk_ready)
+        Q, K = self._ready(Q, K)
         self.profile(Q, K, token_ids)
         main.wait_event(v_ready)
         self.compact(K, V)
@@ -226,9 +233,9 @@ class PagedSession(FastGenSession):
     of e4m3 codes in pages that a cache takes when it grows, several tokens
     at a time (append), and a position per sequence.
 
-    rope (fastgen.Rope): prefill, append and decode then take queries and keys
-    as projected and rotate them at their positions; None: they are taken as
-    they are.  pages: size of the page pool; None gives the worst case (every
+    rope (fastgen.Rope): the prefill calls, append and decode then take queries
+    and keys as projected and rotate them at their positions (profile, compact
+    and profile_attn take them rotated); None: they are taken as they are.  pages: size of the page pool; None gives the worst case (every
     cache growing by max_new_tokens rows).  A smaller pool that runs out is
     reported as FG_ECAPACITY by fastgen_read_error(dev_err)."""
 
@@ -254,15 +261,8 @@ class PagedSession(FastGenSession):
         fg.fastgen_rope(self.p, Q, K, pos, self.rope, out[0], out[1], self.stream)
         return out
 
-    def prefill(self, Q, K, V, token_ids):
-        if self.rope is not None:
-            Q, K = self.rotate(Q, K)
-        super().prefill(Q, K, V, token_ids)
-
-    def prefill_with_policy(self, Q, K, V, token_ids, policy_map):
-        if self.rope is not None:
-            Q, K = self.rotate(Q, K)
-        super().prefill_with_policy(Q, K, V, token_ids, policy_map)
+    def _ready(self, Q, K):
+        return (Q, K) if self.rope is None else self.rotate(Q, K)
 
     def compact(self, K, V):
         """Plans the paged caches of the profiled prompt and codes its kept
@@ -291,9 +291,22 @@ class PagedSession(FastGenSession):
             self.dws = self._empty((max(need, 256),), torch.uint8)
 
     def _positions(self, pos):
-        if isinstance(pos, int):
+        """pos, or that position for every sequence, made on the session's stream."""
+        if not isinstance(pos, int):
+            return pos
+        s = self.stream
+        if isinstance(s, int):
+            s = torch.cuda.ExternalStream(s, self.device)
+        with torch.cuda.stream(s):  # None: the current one
             return torch.full((self.p.B,), pos, dtype=torch.int32, device=self.device)
-        return pos
+
+    def descriptors(self):
+        """Host copy of the paged descriptors."""
+        import ctypes
+
+        raw = self.cache.caches.cpu().numpy().tobytes()
+        assert len(raw) == self.Gkv * ctypes.sizeof(fg.PagedDesc)
+        return (fg.PagedDesc * self.Gkv).from_buffer_copy(raw)
 
     def append(self, k_new, v_new, new_ids, pos, n_new=None):
         """Appends m tokens to every cache: k_new, v_new [Gkv, m, d], new_ids

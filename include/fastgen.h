@@ -474,9 +474,10 @@ fg_status fastgen_rope(const fg_params* p, const void* Q, const void* K, const i
  * buffers belong to the caller, who may also lay out caches, rows and
  * page_table (pages in any order, entries assigned ahead) itself.
  *
- * An entry or a descriptor that names no page of the pool, or a row count past
- * its segment, is never followed: those rows count as absent and 4 is ORed
- * into *dev_err (FG_EINVAL from fastgen_read_error).
+ * w is ceil(r_l n) of fg_params or 0.  An entry or a descriptor that names no
+ * page of the pool, a larger w, or a row count past its segment is never
+ * followed: those rows count as absent and 4 is ORed into *dev_err (FG_EINVAL
+ * from fastgen_read_error).
  * ------------------------------------------------------------------------ */
 #define FG_PAGE_ROWS 64
 #define FG_BLOCK_ROWS 16
@@ -553,8 +554,8 @@ fg_status fastgen_compact_q8(const fg_params* p, const void* K, const void* V, c
  * from n_new[b] on, are left out; what belongs to them is not touched.  rows_out gets the new
  * counts.  When a segment's table or the pool has no page left, the tokens from there on are not
  * stored and 1 is ORed into *dev_err (FG_ECAPACITY).
- * m: 1 .. 2^20.  The workspace (256-byte aligned) holds nothing between calls; calls that share
- * one must not overlap.  Asynchronous.  Errors: FG_EINVAL, FG_EDTYPE, FG_EWORKSPACE. */
+ * m: 1 .. 2^20; pos[b] + m below 2^31.  The workspace (256-byte aligned) holds nothing between
+ * calls; calls that share one, or a cache, must not overlap.  Asynchronous.  Errors: FG_EINVAL, FG_EDTYPE, FG_EWORKSPACE. */
 size_t fastgen_append_q8_workspace_bytes(const fg_params* p, int32_t m);
 
 fg_status fastgen_append_q8(const fg_params* p, const fg_paged_cache* cache, const void* k_new,
@@ -576,8 +577,10 @@ fg_status fastgen_append_q8(const fg_params* p, const fg_paged_cache* cache, con
  * value; without rotation they are exact), fp32 queries with 22; the softmax weights times their
  * row's value exponent likewise, and those below 2^-40 of the largest of them count as zero in
  * the product.  Sums are 32-bit.
- * Arguments else as fastgen_decode_attn; needs a work list.  Asynchronous.
- * Errors: FG_EINVAL, FG_EDTYPE, FG_EWORKSPACE; dev_err as above. */
+ * Arguments else as fastgen_decode_attn; needs a work list.  The workspace holds nothing between
+ * calls; calls that share one, or a cache, must not overlap.  Asynchronous.
+ * Errors: FG_EINVAL, FG_EDTYPE, FG_EWORKSPACE; dev_err as above, and 2 if a wait of the kernel on
+ * its own copies ran out (about 1 s; never in normal operation). */
 size_t fastgen_decode_q8_workspace_bytes(const fg_params* p, const fg_paged_cache* cache);
 
 fg_status fastgen_decode_attn_q8(const fg_params* p, const fg_paged_cache* cache, const void* q,

@@ -640,3 +640,190 @@ def test_session_from_projections_to_steps(dtype, H, Hkv, d, half):
         h.check_out(out, Q[:, t], [t] * B, turn)
     assert fg.fastgen_read_error(s.dev_err) == fg.FG_OK
     assert s.check_guards() == 0
+
+
+# --------------------------------------------------------- calls less usual
+@pytest.mark.parametrize("kw", [dict(B=2, L=16, H=32, n=70), dict(B=3, L=14, H=32, Hkv=32, n=33, d=64),
+                                dict(B=4, L=16, H=32, Hkv=16, n=20, dtype="fp32")])
+def test_many_caches_share_thread_blocks(kw):
+    """More items than thread blocks: a block takes several caches, and parts of them."""
+    s = Setup(20, max_new=8, **kw)
+    assert s.cache.c.n_ctas < s.cache.c.n_work or s.gk < 900
+    s.compact()
+    for st in range(3):
+        ids, k, v = s.tokens(st, 1)
+        pos = [s.n + st if b != 1 else -1 for b in range(s.B)]
+        q = torch.randn(s.G, s.d, generator=gen(st)).to(DT[s.dtype])
+        out = s.decode(q, ids, k, v, pos)
+        s.ref_append(ids, k, v, pos)
+        s.check_out(out, q, pos)
+    s.check()
+    assert int(s.err.item()) == 0
+
+
+def test_long_items_and_a_schedule_from_before_the_growth():
+    """The last item of a segment takes thousands of later rows; then the list is made anew."""
+    s = Setup(21, L=1, H=8, Hkv=2, n=30, policies=[4, 4, 4, 4, 3, 3, 1, 0], max_new=5000, r_l=0.9)
+    s.compact()
+    at = 30
+    for m in (2500, 33, 32, 1):
+        ids, k, v = s.tokens(m, m)
+        s.append(ids, k, v, [at])
+        s.ref_append(ids, k, v, [at])
+        at += m
+    s.check()
+    q = torch.randn(s.G, s.d, generator=gen(1)).to(torch.bfloat16)
+    old = s.decode(q, None, None, None, [at - 1])
+    s.check_out(old, q, [at - 1])
+    s.cache.schedule(s.p)
+    assert s.cache.c.n_work > 2
+    s.check_out(s.decode(q, None, None, None, [at - 1]), q, [at - 1])
+    assert int(s.err.item()) == 0
+
+
+@pytest.mark.parametrize("m", [1, 7, 40])
+def test_id_sets_none_empty_and_longer_than_a_warp(m):
+    many = torch.arange(5000, 5070, dtype=torch.int32)
+    for special, punct in ((None, None), (many, many + 1000), (many[:0], many[:33])):
+        s = Setup(22, L=1, H=5, n=60, max_new=100)
+        s.special, s.punct = (None if x is None else x.cuda() for x in (special, punct))
+        s.compact()
+        ids, k, v = s.tokens(3, m)
+        ids[:, ::2] = 5000 + 69 if special is not None and len(special) else 5032
+        ids[:, 1::5] = 6069
+        real = (SPECIAL[:], PUNCT[:])
+        SPECIAL[:], PUNCT[:] = ([] if x is None else x.tolist() for x in (special, punct))
+        try:
+            s.append(ids, k, v, [60])
+            s.ref_append(ids, k, v, [60])
+            s.check()
+            q = torch.randn(s.G, s.d, generator=gen(1)).to(torch.bfloat16)
+            out = s.decode(q, ids[:, :1], k[:, :1], v[:, :1], [60 + m])
+            s.ref_append(ids[:, :1], k[:, :1], v[:, :1], [60 + m])
+            s.check()
+            s.check_out(out, q, [60 + m])
+        finally:
+            SPECIAL[:], PUNCT[:] = real
+
+
+def test_nothing_to_do():
+    """Idle batches and counts of zero leave everything as it was."""
+    s = Setup(23, B=2, L=1, H=3, n=50)
+    s.compact()
+    before = [x.clone() for x in (s.cache.k_pages, s.cache.v_pages, s.cache.exps, s.cache.pos,
+                                  s.cache.page_table, s.cache.rows, s.cache.next_page)]
+    for m in (3, 40):
+        ids, k, v = s.tokens(1, m)
+        s.append(ids, k, v, [50, 50], [0, 0])
+        s.append(ids, k, v, [-1, -7])
+    q = torch.randn(s.G, s.d, generator=gen(1)).to(torch.bfloat16)
+    out = s.decode(q, ids[:, :1], k[:, :1], v[:, :1], [-1, -1])
+    assert (out == 3.5).all()
+    for x, y in zip(before, (s.cache.k_pages, s.cache.v_pages, s.cache.exps, s.cache.pos,
+                             s.cache.page_table, s.cache.rows, s.cache.next_page)):
+        assert torch.equal(x, y)
+    assert int(s.err.item()) == 0
+
+
+def test_graphs_that_share_a_workspace_and_take_pages():
+    """Two captured steps of two caches, one workspace, replayed in turn while the caches grow
+    into pages not taken at capture."""
+    a, b = (Setup(x, L=1, H=4, n=60, policies=[4, 3, 4, 1], max_new=80) for x in (24, 25))
+    ws = torch.empty(max(fg.fastgen_decode_q8_workspace_bytes(x.p, x.cache) for x in (a, b)),
+                     dtype=torch.uint8, device="cuda")
+    graphs = []
+    for s in (a, b):
+        s.compact()
+        ids, k, v = s.tokens(1, 1)
+        q = torch.randn(s.G, s.d, generator=gen(1)).to(torch.bfloat16)
+        io = [dev(x) for x in (q, k, v, ids)] + [dev([60], torch.int32),
+                                                 torch.zeros(s.G, s.d, dtype=torch.bfloat16,
+                                                             device="cuda")]
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fg.fastgen_decode_attn_q8(s.p, s.cache, io[0], io[1], io[2], io[3], s.special, s.punct,
+                                      io[4], None, io[5], ws, s.err)
+            io[4] += 1
+        graphs.append((s, g, io, (ids, k, v, q)))
+    for st in range(70):
+        for s, g, io, (ids, k, v, q) in graphs:
+            g.replay()
+            s.ref_append(ids, k, v, [60 + st])
+            if st % 23 == 0 or st == 69:
+                s.check_out(io[5], q, [60 + st])
+    for s in (a, b):
+        s.check()
+        assert int(s.err.item()) == 0
+
+
+def test_a_list_of_another_cache_is_flagged():
+    """A work list that does not belong to the cache: refused or flagged, never followed."""
+    s = Setup(26, L=1, H=4, n=90)
+    s.compact()
+    torch.cuda.synchronize()
+    s.cache.sched.view(torch.int32)[64 + 16:].fill_(1 << 28)
+    q = torch.randn(s.G, s.d, generator=gen(1)).to(torch.bfloat16)
+    s.decode(q, None, None, None, [89])
+    assert fg.fastgen_read_error(s.err) == fg.FG_EINVAL
+    s.err.zero_()
+    s.cache.schedule(s.p)
+    s.check_out(s.decode(q, None, None, None, [89]), q, [89])
+    # descriptors that claim the same table over and over need more items than there can be
+    s.cache.caches[:, 2] = 0
+    s.cache.caches[:, 3] = 1 << 20
+    s.cache.rows.fill_(1 << 26)
+    for _ in range(2):
+        try:
+            s.cache.schedule(s.p)
+        except fg.FastGenError as e:
+            assert e.status == fg.FG_EINVAL
+    # a ring larger than the window of the parameters
+    t = Setup(27, L=1, H=4, n=90)
+    t.cache.caches[3, 1] = 91
+    t.compact()
+    assert fg.fastgen_read_error(t.err) == fg.FG_EINVAL
+
+
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_session_from_host_buffers_small_pool_and_stream(own_stream):
+    """prefill_host rotates as prefill does; a pool without room to grow reports its capacity."""
+    from adaptive_head_kv_gb300.session import PagedSession, make_params
+
+    B, L, H, n, d = 1, 2, 4, 100, 64
+    p = make_params(B, L, H, n, d, "bf16", 0.95, 0.3, 0.3)
+    rope = fg.Rope.make(d, 10000.0, fg.FG_ROPE_HALF)
+    stream = torch.cuda.Stream() if own_stream else None
+    g = gen(1)
+    Q, K, V = (torch.randn(L * H, n, d, generator=g).to(torch.bfloat16) for _ in range(3))
+    ids = torch.randint(100, 200, (B, n), generator=g, dtype=torch.int32)
+    sessions = []
+    for host in (False, True):
+        s = PagedSession(p, SPECIAL, PUNCT, 100, rope=rope, pages=0,
+                         stream=None if host else stream)
+        torch.cuda.synchronize()
+        if host:
+            h = [x.pin_memory() for x in (Q, K, V, ids)]
+            s.prefill_host(*h, *(torch.empty_like(x, device="cuda") for x in h))
+        else:
+            s.prefill(dev(Q), dev(K), dev(V), dev(ids))
+        torch.cuda.synchronize()
+        sessions.append(s)
+    a, b = sessions
+    assert torch.equal(a.policy, b.policy) and torch.equal(a.keep, b.keep)
+    assert a.cache.c.n_pages == a.info.pages
+    pa, pb = P.GpuPages(a.cache), P.GpuPages(b.cache)
+    for c in range(L * H):
+        x, y = (z.segment(c, False, int(z.rows[c])) for z in (pa, pb))
+        for key in x:
+            assert np.array_equal(x[key], y[key])
+    one = lambda: dev(torch.randn(L * H, d, generator=g).to(torch.bfloat16))
+    tok = dev([[150]], torch.int32)
+    assert [x.policy for x in a.descriptors()] == a.policy.cpu().tolist()
+    full = any(x.policy == 4 for x in a.descriptors())
+    for t in range(n, n + 64):
+        torch.cuda.synchronize()
+        a.decode(one(), one(), one(), tok, t)
+    torch.cuda.synchronize()
+    want = fg.FG_ECAPACITY if full else fg.FG_OK
+    assert fg.fastgen_read_error(a.dev_err) == want
