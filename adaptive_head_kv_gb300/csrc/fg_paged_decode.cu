@@ -118,14 +118,14 @@ struct Piece<64> {
 // exponents, and the item it belongs to.
 struct StageInfo {
   int row, end;      // first row (or slot) of the page, end of the item's rows
-  int kind;          // kSeg, kRing, kNone: no page
-  int last;          // the item's last page
+  int flags;         // kSeg, kRing or kNone (no page); kLast: the item's last page
+  int t;             // the sequence's position
   uint32_t exps[2];  // of the page's four blocks: (K, V) bytes
-  int item, cache;   // item -1: of a sequence that takes no part
+  int w;             // ring slots
   int alone;         // the cache's only item: its sums are the result
-  int t, w;          // the sequence's position, ring slots
+  int item, cache;   // item -1: of a sequence that takes no part
 };
-enum { kSeg, kRing, kNone };
+enum { kSeg, kRing, kNone, kKind = 3, kLast = 4 };
 
 // A stage: a page's K and V codes, its rows' positions, StageInfo, and, in an
 // item's first stage, the group's queries: f16 terms and the exponent each
@@ -156,12 +156,14 @@ struct Bars {
   uint64_t full[5], empty[5], puts, sync;
   int stop;
 };
-__device__ __forceinline__ void wait_bar(Bars* s, uint64_t* bar, uint32_t parity, int32_t* err) {
-  if (*(volatile int*)&s->stop) return;
-  if (!sm100::mbar_wait(bar, parity)) {
-    *(volatile int*)&s->stop = 1;
-    atomicOr(err, kErrDevice);
-  }
+// False once a wait has run out.
+__device__ __forceinline__ bool wait_bar(Bars* s, uint64_t* bar, uint32_t parity, int32_t* err) {
+  if (sm100::mbar_try_wait(bar, parity)) return true;
+  if (*(volatile int*)&s->stop) return false;
+  if (sm100::mbar_wait(bar, parity)) return true;
+  *(volatile int*)&s->stop = 1;
+  atomicOr(err, kErrDevice);
+  return false;
 }
 __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_addr(bar))
@@ -289,8 +291,7 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
       wait_bar(bars, &bars->empty[slot], (stage / RG::kStages & 1) ^ 1, a.dev_err);
       if (lane == 0) {
         StageInfo* info = reinterpret_cast<StageInfo*>(ring_smem + slot * RG::kStride + RG::kInfo);
-        info->kind = kNone;
-        info->last = 1;
+        info->flags = kNone | kLast;
         info->item = -1;
         if (alone) a.rows_out[c] = had;
       }
@@ -425,8 +426,8 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
         StageInfo* info = reinterpret_cast<StageInfo*>(ring_smem + slot * RG::kStride + RG::kInfo);
         info->row = row;
         info->end = end;
-        info->kind = page < 0 || pages == 0 ? kNone : ring ? kRing : kSeg;
-        info->last = k + 1 >= pages;
+        info->flags = (page < 0 || pages == 0 ? kNone : ring ? kRing : kSeg) |
+                      (k + 1 >= pages ? kLast : 0);
         info->exps[0] = ex.x;
         info->exps[1] = ex.y;
         info->item = wi;
@@ -549,11 +550,23 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll 1
     for (bool opening = true; !last; opening = false, ++stage) {
       const int slot = stage % RG::kStages;
-      wait_bar(&bars, &bars.full[slot], stage / RG::kStages & 1, a.dev_err);
-      if (*(volatile int*)&bars.stop) return;  // the copies in flight are the streaming warp's
+      if (!wait_bar(&bars, &bars.full[slot], stage / RG::kStages & 1, a.dev_err))
+        return;  // the copies in flight are the streaming warp's
+      // everything that the block needs first is asked for together
       const uint8_t* sp = ring_smem + slot * RG::kStride;
       const StageInfo* info = reinterpret_cast<const StageInfo*>(sp + RG::kInfo);
-      last = info->last;
+      const uint32_t st = base + (uint32_t)(slot * RG::kStride);
+      const uint4 head = *reinterpret_cast<const uint4*>(info);
+      const uint32_t exps = info->exps[warp >> 1];
+      uint4 k0[KI], k1[KI];
+#pragma unroll
+      for (int i = 0; i < KI; ++i) {
+        k0[i] = lds16(st + k_off[i]);
+        k1[i] = lds16(st + k_off[i] + 8 * D);
+      }
+      const int row = (int)head.x + warp * kBlockRows, end = (int)head.y;
+      const int kind = head.z & kKind;
+      last = head.z & kLast;
       if (last) {
         item = info->item;
         cache = info->cache;
@@ -582,23 +595,20 @@ __global__ void __launch_bounds__(kThreads, 3)
         for (int q = 0; q < 2; ++q)
           eq[q] = 2 * t4 + q < R ? reinterpret_cast<const int*>(sp + RG::kQExp)[2 * t4 + q] : 0;
       }
-      const int row = info->row + warp * kBlockRows, end = info->end, kind = info->kind;
       if (kind == kNone || row >= end) {  // uniform over the warp: no rows here
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(&bars.empty[slot]);
         continue;
       }
-      const uint32_t ex = info->exps[warp >> 1] >> (16 * (warp & 1));
+      const uint32_t ex = exps >> (16 * (warp & 1));
       const int ek = (int)(signed char)(ex & 0xff), ev = (int)(signed char)((ex >> 8) & 0xff);
-      const uint32_t st = base + (uint32_t)(slot * RG::kStride);
       // scores of key kr ([0], [1]) and key kr + 8 ([2], [3]) with queries 2 t4 and 2 t4 + 1
       float x[4] = {0.f, 0.f, 0.f, 0.f}, xl[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < KI; ++i) {
-        const uint4 k0 = lds16(st + k_off[i]), k1 = lds16(st + k_off[i] + 8 * D);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const uint32_t y0 = word4(k0, w), y1 = word4(k1, w);
+          const uint32_t y0 = word4(k0[i], w), y1 = word4(k1[i], w);
           const uint32_t(&q)[kWide ? 4 : 2] = qa[4 * i + w];
           const uint32_t f0 = decode2(y0), f1 = decode2(y1), f2 = decode2(y0 >> 16),
                          f3 = decode2(y1 >> 16);
@@ -623,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         }
       }
       if (kind == kRing || row + kBlockRows > end) {  // uniform: rows may be missing
-        const int t = info->t, w = info->w;
+        const int t = (int)head.w, w = info->w;
         auto there = [&](int key) {
           bool ok = row + key < end;
           if (kind == kRing) {  // in the window: position in (t - w, t]
