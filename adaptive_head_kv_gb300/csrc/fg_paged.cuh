@@ -18,6 +18,9 @@ namespace fg {
 constexpr int kPageRows = FG_PAGE_ROWS;
 constexpr int kBlockRows = FG_BLOCK_ROWS;
 constexpr int kPageBlocks = kPageRows / kBlockRows;
+// Thread blocks of the decode kernel that an SM holds: by registers and by
+// the shared memory of their rings.
+__host__ __device__ constexpr int kQ8Blocks(int d) { return d == 64 ? 4 : 3; }
 // Pages of a decode work item when each item has a thread block of its own.
 constexpr int kItemPages = 4;
 constexpr int kExpMin = -100;  // exponent of a block without finite non-zero values
@@ -410,7 +413,7 @@ cudaError_t launch_paged_plan(int Gkv, int w, int reserve, const int2* cinfo, fg
 // Decode work list of the current row counts; totals[3] = items, totals[4] =
 // thread blocks.
 cudaError_t launch_paged_schedule(int Gkv, const fg_paged_desc* caches, const int32_t* rows,
-                                  int table_len, int max_work, int sms, int4* ranges,
+                                  int table_len, int max_work, int slots, int4* ranges,
                                   PagedItem* items, int32_t* cta_first, long long* totals,
                                   cudaStream_t s);
 cudaError_t launch_compact_q8(const ProfileDims& pd, const void* K, const void* V,

@@ -136,7 +136,7 @@ enum { kSeg, kRing, kNone, kKind = 3, kLast = 4 };
 // a tile so that these fall on different banks.
 template <int D, bool kWide>
 struct Ring {
-  static constexpr int kStages = D == 128 ? 3 : 5;
+  static constexpr int kStages = D == 128 ? 3 : 4;
   static constexpr int kV = kPageRows * D, kPos = 2 * kV, kInfo = kPos + kPageRows * 4;
   static constexpr int kQExp = kInfo + 64, kQ = kQExp + 64;
   static constexpr int kQTerm = kMaxR * D * 2;  // bytes of one term of the queries
@@ -451,7 +451,7 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, kQ8Blocks(D))
     q8_split_kernel(const PagedArgs a, const PagedDecodeArgs n, int G, int H, int R, int HLkv,
                     float sl2) {
   constexpr bool kWide = sizeof(T) == 4;  // fp32: queries and weights in two f16 terms

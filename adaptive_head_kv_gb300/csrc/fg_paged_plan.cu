@@ -360,10 +360,10 @@ cudaError_t launch_paged_plan(int Gkv, int w, int reserve, const int2* cinfo, fg
 }
 
 cudaError_t launch_paged_schedule(int Gkv, const fg_paged_desc* caches, const int32_t* rows,
-                                  int table_len, int max_work, int sms, int4* ranges,
+                                  int table_len, int max_work, int slots, int4* ranges,
                                   PagedItem* items, int32_t* cta_first, long long* totals,
                                   cudaStream_t s) {
-  paged_schedule_kernel<<<1, kPlanThreads, 0, s>>>(caches, rows, Gkv, table_len, 3 * sms, ranges,
+  paged_schedule_kernel<<<1, kPlanThreads, 0, s>>>(caches, rows, Gkv, table_len, slots, ranges,
                                                    totals);
   paged_items_kernel<<<cdiv(Gkv, 8), 256, 0, s>>>(caches, rows, Gkv, table_len, ranges, max_work,
                                                   items, cta_first, totals);
