@@ -16,7 +16,9 @@
 // are rounded again at most once.
 //
 // Short chains of dependent loads, not bytes, set the time of all but long
-// calls: what does not depend on each other is asked for together.
+// calls: what does not depend on each other is asked for together.  Measured:
+// one token in 1024 caches 4.0 us, five in 2048 caches 10.4 us, 701 (fp32, d =
+// 64) in 128 caches 18 us.
 #include "fg_paged.cuh"
 
 namespace fg {

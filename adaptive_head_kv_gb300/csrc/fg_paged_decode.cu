@@ -34,6 +34,12 @@
 // MMA that takes e4m3 operands (k = 32, queries as sums of three e4m3 terms)
 // was slower (7B shape 52 -> 64 us): with operands that change it runs at
 // 0.30 a nanosecond and SM, the f16 one (k = 16) at 0.66.
+//
+// Measured (bf16, d = 128, of the 6.78 TB/s that a copy reaches): 1024 caches
+// of the 7B shape (278 MB) 51 us, 0.80; 8192 caches 353 us, 0.93; 512 caches of
+// 32768 positions 287 us, 0.99; groups of 8 on 16384 positions 303 us, 0.94;
+// fp32 0.87; d = 64 0.78 (a block of 16 rows costs a warp about 1500 cycles,
+// less than half of them for its bytes); 32 caches of 128 positions 5.6 us.
 #include <type_traits>
 
 #include "fg_paged.cuh"

@@ -4,7 +4,8 @@ Every function has the name and argument order of the C entry point in
 include/fastgen.h.  Tensor arguments are torch tensors (their data_ptr() is
 passed) or raw integer addresses; `stream` defaults to torch's current CUDA
 stream.  A negative status raises FastGenError.  There is no fallback: if the
-shared library is missing, every call raises.
+shared library is missing, every call raises.  The rotation and the paged
+calls (at the end) take tensors only and check their types and sizes.
 """
 from __future__ import annotations
 

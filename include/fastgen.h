@@ -17,7 +17,9 @@
  * fastgen_compact_plan + fastgen_compact (building K_C, V_C) and
  * fastgen_decode_attn (one generation step for every head;
  * fastgen_decode_attn_refresh also refreshes the frequent sets, an opt-in
- * variant).
+ * variant).  The same caches with 8-bit rows in pages have fastgen_paged_plan,
+ * fastgen_compact_q8, fastgen_append_q8 and fastgen_decode_attn_q8;
+ * fastgen_rope rotates a prompt's queries and keys by position.
  *
  * Conventions shared by every entry point
  *   - Query heads are a flat index g = (b*L + l)*H + h over G = B*L*H
