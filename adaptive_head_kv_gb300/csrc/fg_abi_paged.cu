@@ -117,9 +117,9 @@ fg_status schedule(const fg_params* p, fg_paged_cache* c, long long* totals_read
   const int Gkv = kv_count(p);
   const Sched o = sched_parts(p, c);
   const long long most = sched_max_work(Gkv, c->table_len);
-  cudaError_t e = fg::launch_paged_schedule(Gkv, c->caches, c->rows, c->table_len, (int)most,
-                                            fg::kQ8Blocks(p->d) * sms, o.ranges, o.items,
-                                            o.cta_first, o.totals, s);
+  cudaError_t e = fg::launch_paged_schedule(Gkv, group_size(p), c->caches, c->rows, c->table_len,
+                                            (int)most, fg::q8_slots(p->d, sms), o.ranges,
+                                            o.items, o.cta_first, o.totals, s);
   long long h[5] = {0, 0, 0, 0, 0};
   if (e == cudaSuccess) e = cudaMemcpyAsync(h, o.totals, sizeof(h), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);

@@ -847,6 +847,15 @@ cudaError_t run_decode_q8(const ProfileDims& pd, const PagedArgs& a, const Paged
   const int smem = Ring<D, sizeof(T) == 4>::kBytes + kWarps * pd.R * D * (int)sizeof(float);
   cudaError_t e = cudaFuncSetAttribute(q8_split_kernel<T, D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // d = 64: with the split of an SM's memory that its own size asks for, SMs at
+  // times took in fewer than four blocks beside the previous combine's (64 -> 59
+  // us, 2048 caches of 2048 positions); d = 128 runs slower with less L1 (51.3 ->
+  // 52.0 us, 7B shape)
+  if (D == 64)
+    for (const void* f : {(const void*)q8_split_kernel<T, D>, (const void*)q8_combine_kernel<T, D>})
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared);
   if (e == cudaSuccess)
     e = launch_pdl(q8_split_kernel<T, D>, a.n_ctas, kThreads, smem, s, a, n, pd.G, pd.H, pd.R,
                    pd.HLkv, pd.sl2);

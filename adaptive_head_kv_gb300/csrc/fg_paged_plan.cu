@@ -83,17 +83,21 @@ __device__ __forceinline__ int2 cache_pages(const fg_paged_desc& d, int rows, in
 //
 // Small steps: every cache on its own, in equal items of at most kItemPages
 // pages with a thread block each, for the shortest chain.  Larger ones: the
-// caches' pages end to end, each cache led by kItemCost pages' worth for what
+// caches' pages end to end, each cache led by item_cost pages' worth for what
 // an item costs beside its pages, cut into equal lengths for a whole number
 // of waves of resident thread blocks, so that no wave is part empty; a block
 // takes the one or more items that fall in its length.
 // ranges[c] = (first item, items, start of the cache end to end, length or 0).
-constexpr int kItemCost = 4;
+// What an item costs grows with the queries of a group, whose sums the warps
+// merge: fitted to thread blocks' times, 3.1 pages' worth for one query, 4.2
+// for 4, 6 to 7 for 8 (d = 128).
+int item_cost(int R) { return 3 + R / 2; }
 constexpr int kLengthTarget = 128; // pages a thread block takes in a wave, about
 
 __global__ void __launch_bounds__(kPlanThreads) paged_schedule_kernel(
     const fg_paged_desc* __restrict__ caches, const int32_t* __restrict__ rows, int G,
-    int table_len, int slots, int4* __restrict__ ranges, long long* __restrict__ totals) {
+    int table_len, int slots, int item_cost, int4* __restrict__ ranges,
+    long long* __restrict__ totals) {
   __shared__ long long scr[33];
   long long small = 0, cost = 0;
   for (int base = 0; base < G; base += blockDim.x) {
@@ -101,7 +105,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_schedule_kernel(
     long long items = 0, pages = 0, tot;
     if (c < G) {
       const int2 p = cache_pages(caches[c], rows[c], table_len);
-      pages = (long long)p.x + p.y + kItemCost;
+      pages = (long long)p.x + p.y + item_cost;
       items = ((long long)p.x + p.y + kItemPages - 1) / kItemPages;
     }
     block_exclusive_scan(items, scr, &tot);
@@ -123,7 +127,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_schedule_kernel(
       const int2 p = cache_pages(caches[c], rows[c], table_len);
       pages = (long long)p.x + p.y;
     }
-    const long long span = c < G ? pages + kItemCost : 0;
+    const long long span = c < G ? pages + item_cost : 0;
     const long long at = cost_base + block_exclusive_scan(span, scr, &tot);
     cost_base += tot;
     if (c < G)
@@ -144,8 +148,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_schedule_kernel(
 // One warp per cache: its items, and where they begin a thread block.
 __global__ void __launch_bounds__(256) paged_items_kernel(
     const fg_paged_desc* __restrict__ caches, const int32_t* __restrict__ rows, int G,
-    int table_len, const int4* __restrict__ ranges, int max_work, PagedItem* __restrict__ items,
-    int32_t* __restrict__ cta_first, const long long* __restrict__ totals) {
+    int table_len, int item_cost, const int4* __restrict__ ranges, int max_work,
+    PagedItem* __restrict__ items, int32_t* __restrict__ cta_first,
+    const long long* __restrict__ totals) {
   const int c = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (c >= G || totals[3] < 0 || totals[3] > max_work || totals[4] > max_work) return;
   const int4 r = ranges[c];
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(256) paged_items_kernel(
   for (int i = lane; i < r.y; i += 32) {
     long long p0, p1;
     if (r.w > 0) {
-      const long long k = r.z / r.w + i, start = (long long)r.z + kItemCost;
+      const long long k = r.z / r.w + i, start = (long long)r.z + item_cost;
       p0 = max(0LL, k * r.w - start);
       p1 = min((long long)pages, (k + 1) * r.w - start);
       if (p1 < p0) p1 = p0 = 0;  // the length ends within the cache's lead
@@ -361,14 +366,14 @@ cudaError_t launch_paged_plan(int Gkv, int w, int reserve, const int2* cinfo, fg
   return cudaGetLastError();
 }
 
-cudaError_t launch_paged_schedule(int Gkv, const fg_paged_desc* caches, const int32_t* rows,
+cudaError_t launch_paged_schedule(int Gkv, int R, const fg_paged_desc* caches, const int32_t* rows,
                                   int table_len, int max_work, int slots, int4* ranges,
                                   PagedItem* items, int32_t* cta_first, long long* totals,
                                   cudaStream_t s) {
-  paged_schedule_kernel<<<1, kPlanThreads, 0, s>>>(caches, rows, Gkv, table_len, slots, ranges,
-                                                   totals);
-  paged_items_kernel<<<cdiv(Gkv, 8), 256, 0, s>>>(caches, rows, Gkv, table_len, ranges, max_work,
-                                                  items, cta_first, totals);
+  paged_schedule_kernel<<<1, kPlanThreads, 0, s>>>(caches, rows, Gkv, table_len, slots,
+                                                   item_cost(R), ranges, totals);
+  paged_items_kernel<<<cdiv(Gkv, 8), 256, 0, s>>>(caches, rows, Gkv, table_len, item_cost(R),
+                                                  ranges, max_work, items, cta_first, totals);
   return cudaGetLastError();
 }
 

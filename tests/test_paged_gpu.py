@@ -661,6 +661,32 @@ def test_many_caches_share_thread_blocks(kw):
     assert int(s.err.item()) == 0
 
 
+@pytest.mark.parametrize("kw,idle", [
+    (dict(B=4, L=4, H=8, n=2600, d=64, policies=[4, 4, 3, 4]), [[0], [3], [1, 2], [0, 1, 2], []]),
+    (dict(B=40, L=3, H=8, n=70), [[0, 5, 31, 32, 39], range(1, 40), range(39), [7], range(40)]),
+    (dict(B=3, L=10, H=64, Hkv=32, n=50, dtype="fp32"), [[1], [0, 2]]),
+    (dict(B=2, L=2, H=64, Hkv=32, n=4200, policies=[4, 3, 1, 2]), [[0], [1]]),
+    # every cache as long, lengths that end where caches do: no room for more items
+    (dict(B=2, L=2, H=64, Hkv=16, n=4200, policies=[4, 3, 4, 1]), [[0], [1]]),
+])
+def test_idle_sequences_of_a_large_step(kw, idle):
+    """The list is cut again for the sequences that take part, whichever they are."""
+    s = Setup(28, max_new=8, **kw)
+    assert int(s.cache.sched.view(torch.int32)[64 + 3]) > 0  # a list of equal lengths
+    s.compact()
+    now = np.full(s.B, s.n)
+    for st, off in enumerate(idle):
+        ids, k, v = s.tokens(st, 1)
+        pos = [-1 if b in off else int(now[b]) for b in range(s.B)]
+        q = torch.randn(s.G, s.d, generator=gen(st)).to(DT[s.dtype])
+        out = s.decode(q, ids, k, v, pos)
+        s.ref_append(ids, k, v, pos)
+        s.check_out(out, q, pos)
+        now += [p >= 0 for p in pos]
+    s.check()
+    assert int(s.err.item()) == 0
+
+
 def test_long_items_and_a_schedule_from_before_the_growth():
     """The last item of a segment takes thousands of later rows; then the list is made anew."""
     s = Setup(21, L=1, H=8, Hkv=2, n=30, policies=[4, 4, 4, 4, 3, 3, 1, 0], max_new=5000, r_l=0.9)
