@@ -17,8 +17,8 @@
 //
 // Short chains of dependent loads, not bytes, set the time of all but long
 // calls: what does not depend on each other is asked for together.  Measured:
-// one token in 1024 caches 4.0 us, five in 2048 caches 10.4 us, 701 (fp32, d =
-// 64) in 128 caches 18 us.
+// one token in 1024 caches 4.0 us, five in 2048 caches 10.3 us, 701 (fp32, d =
+// 64) in 128 caches 17 us, 512 in 1024 caches (229 MB) 92 us.
 #include "fg_paged.cuh"
 
 namespace fg {
@@ -273,20 +273,26 @@ __device__ __forceinline__ void append_full_block(const PagedArgs& a, const Appe
         unpack16(z, y, (const T*)nullptr);
       }
       if (t[i] >= 0 && e0 < rot) {
-        const float2* cs = angles + (size_t)t[i] * h;
+        // two pairs' (cos, sin) a load
+        const float4* cs = reinterpret_cast<const float4*>(
+            angles + (size_t)t[i] * h + (inter ? e0 / 2 : e0 - (first ? 0 : h)));
         if (inter) {
 #pragma unroll
-          for (int k = 0; k < E; k += 2) {
-            const float2 w = __ldg(cs + (e0 + k) / 2);
-            const float u = f[i][k], v = f[i][k + 1];
-            f[i][k] = u * w.x - v * w.y;
-            f[i][k + 1] = v * w.x + u * w.y;
+          for (int k = 0; k < E; k += 4) {
+            const float4 w = __ldg(cs + k / 4);
+            const float u = f[i][k], v = f[i][k + 2];
+            f[i][k] = u * w.x - f[i][k + 1] * w.y;
+            f[i][k + 1] = f[i][k + 1] * w.x + u * w.y;
+            f[i][k + 2] = v * w.z - f[i][k + 3] * w.w;
+            f[i][k + 3] = f[i][k + 3] * w.z + v * w.w;
           }
         } else {
+          const float sign = first ? -1.f : 1.f;
 #pragma unroll
-          for (int k = 0; k < E; ++k) {
-            const float2 w = __ldg(cs + e0 + k - (first ? 0 : h));
-            f[i][k] = first ? f[i][k] * w.x - y[k] * w.y : f[i][k] * w.x + y[k] * w.y;
+          for (int k = 0; k < E; k += 2) {
+            const float4 w = __ldg(cs + k / 2);
+            f[i][k] = f[i][k] * w.x + sign * y[k] * w.y;
+            f[i][k + 1] = f[i][k + 1] * w.z + sign * y[k + 1] * w.w;
           }
         }
       }
@@ -319,16 +325,17 @@ struct RingBlock {
   int block, tok;
 };
 __device__ __forceinline__ RingBlock ring_block(unsigned p0, int cnt, int in, int w, int j) {
-  const int lane = threadIdx.x & 31;
-  const unsigned last = p0 + (unsigned)cnt - 1, uw = (unsigned)w;
+  const int lane = threadIdx.x & 31, blocks = cdiv(w, kBlockRows);
+  const int last = (int)((p0 + (unsigned)cnt - 1) % (unsigned)w);  // the last token's slot
+  const int first = last + 1 - in;                                 // the first's, in (-w, w)
   RingBlock o;
-  o.block = (int)(((last + 1 - (unsigned)in) % uw / kBlockRows + (unsigned)j) %
-                  (unsigned)cdiv(w, kBlockRows));
+  o.block = (first < 0 ? first + w : first) / kBlockRows + j;  // j <= blocks
+  if (o.block >= blocks) o.block -= blocks;
   o.tok = -1;
-  const unsigned slot = (unsigned)(o.block * kBlockRows + lane);
-  if (lane < kBlockRows && slot < uw) {
-    const unsigned back = (last % uw + uw - slot) % uw;  // the slot's position is last - back
-    if (back < (unsigned)in) o.tok = cnt - 1 - (int)back;
+  const int slot = o.block * kBlockRows + lane;
+  if (lane < kBlockRows && slot < w) {
+    const int back = last - slot + (slot > last ? w : 0);  // the slot's position is the last's - back
+    if (back < in) o.tok = cnt - 1 - back;
   }
   return o;
 }
@@ -339,7 +346,11 @@ __host__ __device__ inline int touched(int m, bool wrap) {
   return m <= 1 ? m : (m + kBlockRows - 2) / kBlockRows + 1 + (wrap ? 1 : 0);
 }
 
-constexpr int kFew = 32;
+// Calls of up to kFew tokens take one launch: its time grows by a microsecond a
+// token, the other's first 16 tokens cost nothing.  32 caches: 12 tokens 11.6
+// against 8.9 us, 32 tokens 27 against 9.6; 2048 caches: 9 tokens 16 against 19
+// us, 16 tokens 26 against 23.6.  (At most 32: a token a lane.)
+constexpr int kFew = 8;
 constexpr int kFewWarps = 2;
 
 // One CTA per cache, at most kFew tokens (lane i: token i).
@@ -441,15 +452,19 @@ __global__ void __launch_bounds__(kFewWarps * 32)
 
 // One warp per (cache, destination block, K or V).  seg_blocks: blocks that
 // the call's rows of a never-evicted segment may touch; ring_blocks likewise.
+// Four blocks an SM, although a block of rotated rows then leaves some of them
+// in local memory: the chain of loads that opens a block needs the warps
+// (7B shape, 512 tokens: three blocks without spills 135 us, four 92, five
+// 105).  Without the blocks' work the same grid takes 29 us.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) append_q8_kernel(const PagedArgs a, const AppendArgs n,
+__global__ void __launch_bounds__(kThreads, 4) append_q8_kernel(const PagedArgs a, const AppendArgs n,
                                                              int HLkv, int seg_blocks,
                                                              int ring_blocks, int max_w,
-                                                             long long tasks) {
-  const long long task = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+                                                             uint32_t tasks) {
+  const uint32_t task = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const int which = (int)(task & 1), per = seg_blocks + ring_blocks;
-  const int j = (int)((task >> 1) % per);
+  const uint32_t per = seg_blocks + ring_blocks;
+  const int which = (int)(task & 1), j = (int)((task >> 1) % per);
   const bool in_grid = task < tasks;
   const int c = in_grid ? (int)((task >> 1) / per) : 0, b = c / HLkv;
   const fg_paged_desc d = a.caches[c];
@@ -517,9 +532,9 @@ cudaError_t run_append(const ProfileDims& pd, const PagedArgs& a, const AppendAr
   const int ring = min(cdiv(pd.w, kBlockRows), touched(min(n.m, pd.w), true));
   const long long tasks = 2LL * pd.Gkv * (seg + ring);
   const long long grid = (tasks + kThreads / 32 - 1) / (kThreads / 32);
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (tasks > 0xffffffffLL - kThreads / 32) return cudaErrorInvalidValue;
   return launch_pdl(append_q8_kernel<T, D>, (unsigned)grid, kThreads, 0, s, a, n, pd.HLkv, seg,
-                    ring, pd.w, tasks);
+                    ring, pd.w, (uint32_t)tasks);
 }
 
 }  // namespace
