@@ -256,8 +256,18 @@ __device__ __forceinline__ void code_block(const T* __restrict__ X, const int* s
   if (lane == 0) *exp_dst = (int8_t)e;
 }
 
+// CTAs of `chunk` threads that an SM is to hold, by the bytes of a row: a warp's
+// 16 rows take as many registers a lane as a row has 8 bytes.  With / without
+// the bound: 128 bytes (bf16, d = 64; 128 threads) 41.4 / 45.6 us, 256 bytes
+// 478 / 489 us (4096 caches; 512 threads, 32768 positions 22.1 / 23.0); rows of
+// 512 bytes would spill (65 / 55 us).
+constexpr int compact_blocks(int row_bytes, int chunk) {
+  return row_bytes > 256 ? 1 : chunk > 128 ? 2 : row_bytes > 128 ? 8 : 12;
+}
+
 template <typename T, int D, int kChunkRows>
-__global__ void __launch_bounds__(kChunkRows) compact_q8_kernel(
+__global__ void __launch_bounds__(kChunkRows, compact_blocks(D * sizeof(T), kChunkRows))
+    compact_q8_kernel(
     const T* __restrict__ K, const T* __restrict__ V, const uint8_t* __restrict__ keep, int n,
     int G, int H, int R, int max_w, int seg_chunks, int chunks, const PagedArgs a) {
   constexpr int kCodeThreads = kChunkRows;
