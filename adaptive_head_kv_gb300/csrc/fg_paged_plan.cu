@@ -195,9 +195,9 @@ __global__ void __launch_bounds__(256) paged_items_kernel(
 // search hides behind its neighbours' rows, or 512 where a long prompt or a
 // large group makes the search (every CTA reads the codes before its chunk)
 // outweigh 128 rows.  Measured with 128 / 512, groups of 1 and 8: 2048
-// positions 36.8 / 41.6 us, 16384 40.1 / 41.9, 32768 25.7 / 23.4; 8 x 8192
-// 29.5 / 25.3, 8 x 16384 39.3 / 26.7.
-constexpr int kLongSearch = 24576;  // codes of a group
+// positions 36.7 / 39.8 us, 16384 38.2 / 37.3, 32768 25.5 / 22.1; 8 x 4096
+// 24.9 / 23.6, 8 x 8192 29.2 / 24.3, 8 x 16384 39.1 / 25.0.
+constexpr int kLongSearch = 12288;  // codes of a group
 constexpr int kScanPer = 32;  // positions per thread and scan step
 
 // Bit i: byte i of the 16 bytes at p is FG_KEEP_STATIC.  p is 16-byte aligned
