@@ -89,12 +89,23 @@ __device__ __forceinline__ uint32_t half2_pow2_neg(int k) {
 
 // cos and sin of 2 pi * pos * turns / 2^64.  The product keeps the fraction
 // of the turn exactly (modulo one turn, at any position), so nothing of the
-// angle is lost at far positions; the fraction's top 32 bits, as a signed
-// number of half turns in [-1, 1), are within 2^-25 of it after rounding.
+// angle is lost at far positions.  The fraction's top 32 bits, as a signed
+// number of half turns in [-1, 1), do not fit a float: what its rounding leaves
+// over (at most 2^-25 half turns) is added to first order (kFull), so that the
+// result is off by little more than sincospif itself.  Without it an angle is
+// off by up to 2^-23, enough where the rotated value is rounded to 11 bits.
+template <bool kFull = true>
 __device__ __forceinline__ void rope_cos_sin(uint32_t pos, unsigned long long turns, float& c,
                                              float& s) {
   const int frac = (int)((unsigned long long)pos * turns >> 32);
-  sincospif((float)frac * 4.656612873077393e-10f, &s, &c);
+  const float most = (float)frac;
+  sincospif(most * 4.656612873077393e-10f, &s, &c);
+  if constexpr (kFull) {
+    const float rest = (float)(frac - __float2int_rn(most)) * 1.46291808e-9f;  // pi 2^-31
+    const float c0 = c;
+    c = fmaf(-s, rest, c);
+    s = fmaf(c0, rest, s);
+  }
 }
 
 // Streaming 16-byte load of memory that the kernel also writes (not the

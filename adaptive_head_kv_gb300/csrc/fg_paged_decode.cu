@@ -353,7 +353,7 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
       if (n.rope.rot > 0)
         row_angles<PER>(cs, n.rope.rot, n.rope.style, [&](int p) {
           float2 y;
-          rope_cos_sin((unsigned)t, n.rope.turns[p], y.x, y.y);
+          rope_cos_sin<kWide>((unsigned)t, n.rope.turns[p], y.x, y.y);
           return y;
         });
 #pragma unroll
