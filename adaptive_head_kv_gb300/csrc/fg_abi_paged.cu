@@ -93,10 +93,12 @@ fg::PagedArgs paged_args(const fg_params* p, const fg_paged_cache* c, int32_t* d
     a.ranges = o.ranges;
     a.items = o.items;
     a.cta_first = o.cta_first;
+    a.totals = o.totals;
   } else {
     a.ranges = nullptr;
     a.items = nullptr;
     a.cta_first = nullptr;
+    a.totals = nullptr;
   }
   a.n_pages = c->n_pages;
   a.table_len = c->table_len;
@@ -118,7 +120,7 @@ fg_status schedule(const fg_params* p, fg_paged_cache* c, long long* totals_read
   const Sched o = sched_parts(p, c);
   const long long most = sched_max_work(Gkv, c->table_len);
   cudaError_t e = fg::launch_paged_schedule(Gkv, group_size(p), c->caches, c->rows, c->table_len,
-                                            (int)most, fg::q8_slots(p->d, sms), o.ranges,
+                                            (int)most, fg::q8_slots(dims(p), sms), o.ranges,
                                             o.items, o.cta_first, o.totals, s);
   long long h[5] = {0, 0, 0, 0, 0};
   if (e == cudaSuccess) e = cudaMemcpyAsync(h, o.totals, sizeof(h), cudaMemcpyDeviceToHost, s);

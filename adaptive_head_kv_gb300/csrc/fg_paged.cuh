@@ -18,14 +18,6 @@ namespace fg {
 constexpr int kPageRows = FG_PAGE_ROWS;
 constexpr int kBlockRows = FG_BLOCK_ROWS;
 constexpr int kPageBlocks = kPageRows / kBlockRows;
-// Thread blocks of the decode kernel that an SM holds: by registers and by
-// the shared memory of their rings.
-__host__ __device__ constexpr int kQ8Blocks(int d) { return d == 64 ? 4 : 3; }
-// Thread blocks that a wave counts on: one or two less than the SMs hold.
-// Right behind the previous step's combine the last block at times found no
-// room, and started only when another ended (grouped 4k shape: 456 blocks on 152
-// SMs 63 us, 452 blocks 54.5 us).
-inline int q8_slots(int d, int sms) { return kQ8Blocks(d) * sms - sms / 64; }
 // Pages of a decode work item when each item has a thread block of its own.
 constexpr int kItemPages = 4;
 constexpr int kExpMin = -100;  // exponent of a block without finite non-zero values
@@ -189,6 +181,7 @@ struct PagedArgs {
   const int4* ranges;      // [Gkv] x, y: first work item and items of each cache
   const PagedItem* items;  // [n_work]
   const int32_t* cta_first;  // [n_ctas + 1] first item of each thread block
+  const long long* totals;   // [3], [4]: the list's items and thread blocks
   int n_pages, table_len, n_work, n_ctas;
   int32_t* dev_err;
 };
@@ -438,5 +431,7 @@ cudaError_t launch_append_q8(const ProfileDims& pd, const PagedArgs& a, const Ap
                              cudaStream_t s);
 cudaError_t launch_decode_q8(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
                              cudaStream_t s);
+// Thread blocks of the decode kernel that a wave counts on.
+int q8_slots(const ProfileDims& pd, int sms);
 
 }  // namespace fg

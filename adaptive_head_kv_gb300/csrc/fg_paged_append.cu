@@ -38,9 +38,9 @@ __global__ void __launch_bounds__(kThreads) append_plan_kernel(const PagedArgs a
   __shared__ int scr[33];
   __shared__ int sm_count[2][kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   griddep_wait();
   griddep_launch_dependents();
+  const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   const int b = blockIdx.y;
   const int cnt = new_tokens(n, b);
   int n_s = 0, n_sp = 0;  // special, special or punctuation tokens
@@ -361,10 +361,10 @@ __global__ void __launch_bounds__(kFewWarps * 32)
   extern __shared__ float2 sm_angle[];  // [m][rot / 2]
   const int c = blockIdx.x, b = c / HLkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const fg_paged_desc d = a.caches[c];
-  const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   griddep_wait();
   griddep_launch_dependents();
+  const fg_paged_desc d = a.caches[c];
+  const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   const int pos = n.pos[b], had = a.rows[c];
   const int tau = lane < n.m ? n.ids[(size_t)b * n.m + lane] : 0;
   int cnt = n.n_new ? max(0, min(n.n_new[b], n.m)) : n.m;
@@ -467,11 +467,11 @@ __global__ void __launch_bounds__(kThreads, 4) append_q8_kernel(const PagedArgs 
   const int which = (int)(task & 1), j = (int)((task >> 1) % per);
   const bool in_grid = task < tasks;
   const int c = in_grid ? (int)((task >> 1) / per) : 0, b = c / HLkv;
-  const fg_paged_desc d = a.caches[c];
-  const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   griddep_wait();
   griddep_launch_dependents();
   if (!in_grid) return;
+  const fg_paged_desc d = a.caches[c];
+  const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   const int2 rows = *reinterpret_cast<const int2*>(n.old + 2 * c);  // before the call, stored
   const int cnt = new_tokens(n, b);
   if (cnt == 0) return;
@@ -526,13 +526,13 @@ cudaError_t run_append(const ProfileDims& pd, const PagedArgs& a, const AppendAr
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, append_plan_kernel, a, n, pd.HLkv);
-  if (e != cudaSuccess) return e;
   const int seg = touched(n.m, false);
   const int ring = min(cdiv(pd.w, kBlockRows), touched(min(n.m, pd.w), true));
   const long long tasks = 2LL * pd.Gkv * (seg + ring);
   const long long grid = (tasks + kThreads / 32 - 1) / (kThreads / 32);
   if (tasks > 0xffffffffLL - kThreads / 32) return cudaErrorInvalidValue;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, append_plan_kernel, a, n, pd.HLkv);
+  if (e != cudaSuccess) return e;
   return launch_pdl(append_q8_kernel<T, D>, (unsigned)grid, kThreads, 0, s, a, n, pd.HLkv, seg,
                     ring, pd.w, (uint32_t)tasks);
 }

@@ -36,10 +36,10 @@
 // 0.30 a nanosecond and SM, the f16 one (k = 16) at 0.66.
 //
 // Measured (bf16, d = 128, of the 6.78 TB/s that a copy reaches): 1024 caches
-// of the 7B shape (278 MB) 51 us, 0.80; 8192 caches 353 us, 0.93; 512 caches of
-// 32768 positions 287 us, 0.99; groups of 8 on 16384 positions 303 us, 0.94;
-// fp32 0.87; d = 64 0.78 (a block of 16 rows costs a warp about 1500 cycles,
-// less than half of them for its bytes); 32 caches of 128 positions 5.6 us.
+// of the 7B shape (278 MB) 51 us, 0.80; 8192 caches 351 us, 0.93; 512 caches of
+// 32768 positions 288 us, 0.98; groups of 8 on 16384 positions 299 us, 0.95;
+// fp32 0.87; d = 64 0.77 (a block of 16 rows costs a warp about 1500 cycles,
+// less than half of them for its bytes); 32 caches of 128 positions 5.8 us.
 #include <type_traits>
 
 #include "fg_paged.cuh"
@@ -456,8 +456,16 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// Thread blocks that an SM's registers hold.
+constexpr int kBlocks(int d) { return d == 64 ? 4 : 3; }
+
+// Is the list the one that the call was made (or captured) with?
+__device__ __forceinline__ bool same_list(const PagedArgs& a) {
+  return a.totals[3] == a.n_work && a.totals[4] == a.n_ctas;
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, kQ8Blocks(D))
+__global__ void __launch_bounds__(kThreads, kBlocks(D))
     q8_split_kernel(const PagedArgs a, const PagedDecodeArgs n, int G, int H, int R, int HLkv,
                     float sl2) {
   constexpr bool kWide = sizeof(T) == 4;  // fp32: queries and weights in two f16 terms
@@ -487,16 +495,21 @@ __global__ void __launch_bounds__(kThreads, kQ8Blocks(D))
     bars.stop = 0;
     sm100::fence_barrier_init();
   }
-  // what the schedule and the caller have fixed is read before the wait
+  // what the schedule has fixed is read before the wait
   const int own = min(wi0 + (warp == kWarps ? 0 : warp), wi_end - 1);
   const PagedItem own_item = a.items[own];
   const int own_c = (unsigned)own_item.cache < (unsigned)Gkv ? own_item.cache : 0;
   const fg_paged_desc own_cache = a.caches[own_c];
   const int own_items = a.ranges[own_c].y;
-  const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
+  const bool listed = same_list(a);
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
+  if (!listed) {
+    if (threadIdx.x == 0) atomicOr(a.dev_err, kErrInvalid);
+    return;
+  }
+  const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   if (warp == kWarps) {
     stream_items<T, D>(a, n, Gkv, H, R, HLkv, ring_smem, &bars, wi0, wi_end, own_item, own_cache,
                        own_items, special, punct);
@@ -782,10 +795,12 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   int4 range = a.ranges[c];
   range.x = max(0, min(range.x, a.n_work));
   range.y = min(range.y, a.n_work - range.x);
-  const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
+  const bool listed = same_list(a);
   griddep_wait();
   griddep_launch_dependents();
-  if (!in || range.y == 1) return;  // a cache's only item has written the result and the count
+  const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
+  // (a cache's only item has written the result and the count)
+  if (!in || range.y == 1 || !listed) return;
   const int t = n.pos[b], had = a.rows[c], tau = n.k_new ? n.ids[b] : 0;
   if (t < 0) {
     if (qi == 0 && lane == 0) a.rows_out[c] = had;
@@ -842,9 +857,14 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
 }
 
 template <typename T, int D>
+int split_smem(int R) {
+  return Ring<D, sizeof(T) == 4>::kBytes + kWarps * R * D * (int)sizeof(float);
+}
+
+template <typename T, int D>
 cudaError_t run_decode_q8(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
                           cudaStream_t s) {
-  const int smem = Ring<D, sizeof(T) == 4>::kBytes + kWarps * pd.R * D * (int)sizeof(float);
+  const int smem = split_smem<T, D>(pd.R);
   cudaError_t e = cudaFuncSetAttribute(q8_split_kernel<T, D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   // d = 64: with the split of an SM's memory that its own size asks for, SMs at
@@ -865,7 +885,25 @@ cudaError_t run_decode_q8(const ProfileDims& pd, const PagedArgs& a, const Paged
   return e;
 }
 
+// As many as the SMs hold less one or two: right behind the previous step's
+// combine the last block at times found no room, and started only when another
+// ended (grouped 4k shape: 456 blocks on 152 SMs 63 us, 452 blocks 54.5 us).
+// Shared memory (228 KB an SM, of which a block also takes 1 KB and its static
+// part) is the limit for fp32 groups of 8 at d = 128: two blocks (counting on three
+// left a part-filled second wave: 128 caches of 8192 positions 51.6 us, now 37).
+template <typename T, int D>
+int slots(int R, int sms) {
+  const int room = 228 * 1024 / (split_smem<T, D>(R) + 1024 + 1024);
+  return (room < kBlocks(D) ? room : kBlocks(D)) * sms - sms / 64;
+}
+
 }  // namespace
+
+int q8_slots(const ProfileDims& pd, int sms) {
+  if (pd.dtype == FG_FP32)
+    return pd.d == 64 ? slots<float, 64>(pd.R, sms) : slots<float, 128>(pd.R, sms);
+  return pd.d == 64 ? slots<__nv_bfloat16, 64>(pd.R, sms) : slots<__nv_bfloat16, 128>(pd.R, sms);
+}
 
 cudaError_t launch_decode_q8(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
                              cudaStream_t s) {

@@ -235,9 +235,10 @@ class PagedSession(FastGenSession):
 
     rope (fastgen.Rope): the prefill calls, append and decode then take queries
     and keys as projected and rotate them at their positions (profile, compact
-    and profile_attn take them rotated); None: they are taken as they are.  pages: size of the page pool; None gives the worst case (every
-    cache growing by max_new_tokens rows).  A smaller pool that runs out is
-    reported as FG_ECAPACITY by fastgen_read_error(dev_err)."""
+    and profile_attn take them rotated); None: they are taken as they are.
+    pages: size of the page pool; None gives the worst case (every cache
+    growing by max_new_tokens rows).  A smaller pool that runs out is reported
+    as FG_ECAPACITY by fastgen_read_error(dev_err)."""
 
     def __init__(self, params: fg.Params, special_ids, punct_ids, max_new_tokens: int,
                  device="cuda", stream=None, guard=False, rope=None, pages=None):
@@ -249,6 +250,7 @@ class PagedSession(FastGenSession):
             E((fg.fastgen_paged_table_len(params, self.max_new),), i32), E((Gkv, 6), i32),
             E((Gkv,), i32), E((1,), i32))
         self.aws = None
+        self._outgrown = []  # workspaces that a captured call may still use
         self._rotated = None
 
     def rotate(self, Q, K, pos=None, out=None):
@@ -281,13 +283,15 @@ class PagedSession(FastGenSession):
 
     def reschedule(self):
         """Splits the decode work by the caches' present sizes (worth a call
-        now and then in a long generation; graphs captured before it are void)."""
+        now and then in a long generation; steps captured before it are void:
+        they are reported as FG_EINVAL and do nothing)."""
         self.cache.schedule(self.p, self.stream)
         self._size_decode_workspace()
 
     def _size_decode_workspace(self):
         need = fg.fastgen_decode_q8_workspace_bytes(self.p, self.cache)
         if self.dws is None or self.dws.numel() < need:
+            self._outgrown.append(self.dws)
             self.dws = self._empty((max(need, 256),), torch.uint8)
 
     def _positions(self, pos):
@@ -315,6 +319,7 @@ class PagedSession(FastGenSession):
         m = new_ids.numel() // self.p.B
         need = fg.fastgen_append_q8_workspace_bytes(self.p, m)
         if self.aws is None or self.aws.numel() < need:
+            self._outgrown.append(self.aws)
             self.aws = self._empty((max(need, 256),), torch.uint8)
         fg.fastgen_append_q8(self.p, self.cache, k_new, v_new, new_ids, n_new, self.special,
                              self.punct, self._positions(pos), self.rope, self.aws, self.dev_err,

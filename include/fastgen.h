@@ -536,7 +536,9 @@ fg_status fastgen_paged_plan(const fg_params* p, const int8_t* policy, const uin
 
 /* The decode work list of the current rows (needed before the first decode of caches that
  * fastgen_paged_plan did not lay out, and worth a call now and then in a long generation: the last
- * item of a segment takes every row appended later).  SYNCHRONOUS on `stream`. */
+ * item of a segment takes every row appended later).  A step captured before is captured again:
+ * with a list of other numbers of items or thread blocks it does nothing and ORs 4 into *dev_err.
+ * SYNCHRONOUS on `stream`. */
 fg_status fastgen_paged_schedule(const fg_params* p, fg_paged_cache* cache, void* stream);
 
 /* Gathers and codes the kept prompt rows: K, V [Gkv, n, d] dtype and keep [G, n] as

@@ -783,6 +783,86 @@ def test_graphs_that_share_a_workspace_and_take_pages():
         assert int(s.err.item()) == 0
 
 
+def test_a_captured_append_outlives_a_longer_one():
+    """The session's workspace grows with a longer call; the captured call keeps its own."""
+    from adaptive_head_kv_gb300.session import PagedSession, make_params
+
+    B, L, H, n, d, m = 2, 2, 4, 90, 64, 20
+    p = make_params(B, L, H, n, d, "bf16", 0.9, 0.3, 0.3)
+    rope = fg.Rope(table(d)[1])
+    g, gk = gen(30), B * L * H
+    prompt = [dev(torch.randn(gk, n, d, generator=g).to(torch.bfloat16)) for _ in range(3)]
+    ids = dev(torch.randint(100, 300, (B, n), generator=g, dtype=torch.int32))
+    turns = []
+    for k in (m, 300, m):
+        turns.append([dev(torch.randn(gk, k, d, generator=g).to(torch.bfloat16)) for _ in range(2)]
+                     + [dev(torch.randint(100, 300, (B, k), generator=g, dtype=torch.int32))])
+    at = [n, n + m, n + m + 300]
+    a, b = (PagedSession(p, SPECIAL, PUNCT, 400, rope=rope) for _ in range(2))
+    for s in (a, b):
+        s.prefill_with_policy(*prompt, ids, torch.arange(gk, dtype=torch.int8) % 5)
+    for x, t in zip(turns, at):
+        a.append(*x, t)
+    held, pos = [x.clone() for x in turns[0]], dev([n] * B, torch.int32)
+    b.append(*held, dev([-1] * B, torch.int32))  # no sequence: sizes the workspace
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.append(*held, pos)
+    graph.replay()
+    b.append(*turns[1], at[1])
+    other = torch.full((1 << 20,), 0xA5, dtype=torch.uint8, device="cuda")  # takes what was freed
+    for x, y in zip(held, turns[2]):
+        x.copy_(y)
+    pos.fill_(at[2])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (other == 0xA5).all()
+    assert torch.equal(a.cache.rows, b.cache.rows) and int(a.dev_err) == 0 == int(b.dev_err)
+    x, y = P.GpuPages(a.cache), P.GpuPages(b.cache)
+    for c in range(gk):
+        for ring, count in ((False, int(x.rows[c])), (True, int(x.caches[c][1]))):
+            if count == 0:
+                continue
+            u, v = x.segment(c, ring, count), y.segment(c, ring, count)
+            for key in u:
+                assert np.array_equal(u[key], v[key], equal_nan=True), (c, ring, key)
+
+
+def test_a_step_captured_before_the_list_was_made_anew_is_flagged():
+    """Its thread blocks would not be the new list's: nothing is done, and the error word says so."""
+    s = Setup(29, L=1, H=8, Hkv=2, n=30, policies=[4], max_new=1500)
+    s.compact()
+    q = torch.randn(s.G, s.d, generator=gen(1)).to(torch.bfloat16)
+    qd, pos = dev(q), dev([29], torch.int32)
+    out = torch.zeros(s.G, s.d, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(fg.fastgen_decode_q8_workspace_bytes(s.p, s.cache), dtype=torch.uint8,
+                     device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fg.fastgen_decode_attn_q8(s.p, s.cache, qd, None, None, None, s.special, s.punct, pos, None,
+                                  out, ws, s.err)
+    graph.replay()
+    s.check_out(out, q, [29])
+    ids, k, v = s.tokens(1, 1400)
+    s.append(ids, k, v, [30])
+    s.ref_append(ids, k, v, [30])
+    pos.fill_(1429)
+    graph.replay()  # the old list: its last items take the later rows
+    s.check_out(out, q, [1429])
+    before = s.cache.c.n_work
+    s.cache.schedule(s.p)
+    assert s.cache.c.n_work != before
+    out.fill_(3.5)
+    graph.replay()
+    assert fg.fastgen_read_error(s.err) == fg.FG_EINVAL
+    assert (out == 3.5).all()
+    s.err.zero_()
+    s.check_out(s.decode(q, None, None, None, [1429]), q, [1429])
+    assert fg.fastgen_read_error(s.err) == fg.FG_OK
+
+
 def test_a_list_of_another_cache_is_flagged():
     """A work list that does not belong to the cache: refused or flagged, never followed."""
     s = Setup(26, L=1, H=4, n=90)
