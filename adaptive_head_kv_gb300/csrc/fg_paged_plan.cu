@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(256) paged_items_kernel(
 // block of 16 rows: the rows in registers (one pass over the data), the
 // block's largest magnitude, the exponent, the codes.  Bound by HBM: 2 * eb + 2
 // bytes a value.  Measured (bf16, d = 128, 2048 positions): 256 caches (192 MB)
-// 37 us, 5.2 TB/s; 4096 caches (3.1 GB) 493 us, 6.2 TB/s.
+// 37 us, 5.2 TB/s; 4096 caches (3.1 GB) 480 us, 6.4 TB/s.
 //
 // A CTA has as many threads as its chunk has rows: 128, so that one CTA's
 // search hides behind its neighbours' rows, or 512 where a long prompt or a
