@@ -334,7 +334,8 @@ __device__ __forceinline__ RingBlock ring_block(unsigned p0, int cnt, int in, in
   o.tok = -1;
   const int slot = o.block * kBlockRows + lane;
   if (lane < kBlockRows && slot < w) {
-    const int back = last - slot + (slot > last ? w : 0);  // the slot's position is the last's - back
+    // the slot's position is the last token's less `back`
+    const int back = last - slot + (slot > last ? w : 0);
     if (back < in) o.tok = cnt - 1 - back;
   }
   return o;
@@ -457,10 +458,9 @@ __global__ void __launch_bounds__(kFewWarps * 32)
 // (7B shape, 512 tokens: three blocks without spills 135 us, four 92, five
 // 105).  Without the blocks' work the same grid takes 29 us.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 4) append_q8_kernel(const PagedArgs a, const AppendArgs n,
-                                                             int HLkv, int seg_blocks,
-                                                             int ring_blocks, int max_w,
-                                                             uint32_t tasks) {
+__global__ void __launch_bounds__(kThreads, 4)
+    append_q8_kernel(const PagedArgs a, const AppendArgs n, int HLkv, int seg_blocks,
+                     int ring_blocks, int max_w, uint32_t tasks) {
   const uint32_t task = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const uint32_t per = seg_blocks + ring_blocks;

@@ -125,8 +125,8 @@ cudaError_t run_rope(const ProfileDims& pd, const void* Q, const void* K, const 
   const int tiles = cdiv(pd.n, ROWS), chunks = cdiv(hq + hk, kHeads);
   const long long grid = (long long)tiles * chunks * pd.B;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_pdl(rope_kernel<T, D>, (unsigned)grid, kThreads, 0, s, (const T*)Q, (const T*)K, pos,
-                    rope, (T*)Qo, (T*)Ko, pd.n, hq, hk, tiles, chunks);
+  return launch_pdl(rope_kernel<T, D>, (unsigned)grid, kThreads, 0, s, (const T*)Q, (const T*)K,
+                    pos, rope, (T*)Qo, (T*)Ko, pd.n, hq, hk, tiles, chunks);
 }
 
 }  // namespace

@@ -559,7 +559,8 @@ fg_status fastgen_compact_q8(const fg_params* p, const void* K, const void* V, c
  * counts.  When a segment's table or the pool has no page left, the tokens from there on are not
  * stored and 1 is ORed into *dev_err (FG_ECAPACITY).
  * m: 1 .. 2^20; pos[b] + m below 2^31.  The workspace (256-byte aligned) holds nothing between
- * calls; calls that share one, or a cache, must not overlap.  Asynchronous.  Errors: FG_EINVAL, FG_EDTYPE, FG_EWORKSPACE. */
+ * calls; calls that share one, or a cache, must not overlap.  Asynchronous.
+ * Errors: FG_EINVAL, FG_EDTYPE, FG_EWORKSPACE. */
 size_t fastgen_append_q8_workspace_bytes(const fg_params* p, int32_t m);
 
 fg_status fastgen_append_q8(const fg_params* p, const fg_paged_cache* cache, const void* k_new,
