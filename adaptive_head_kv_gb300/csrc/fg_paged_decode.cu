@@ -15,8 +15,13 @@
 // Both products run as warp MMAs in f16, which holds every e4m3 code exactly:
 //   S^T[16 keys x 8] = K[16 keys x d] . Q^T
 //   O^T[d x 8]      += V^T[d x 16 keys] . P^T
-// with the group's queries as the 8 columns (fp32 queries and weights in two
-// f16 terms).
+// Queries and weights take two f16 terms each (22 bits): a group of up to four
+// has them side by side, column 2 i the first term of query i and 2 i + 1 the
+// second, so that a lane holds both and they cost no MMA.  A group of eight takes
+// a second MMA for the second terms in fp32, and one term (11 bits) in bf16:
+// second MMAs cost it 19 % (192 caches of 16384 positions 75 -> 89 us; the
+// queries' alone 84, the weights' alone 84), where its outputs' distance from
+// the definition, 0.00156, is 0.00150 by their own rounding to bf16.
 // The dimension order inside a product is free as long as both operands agree,
 // so a lane's operand fragments are 16 consecutive bytes of a row; S^T's
 // accumulators become P^T's operand with one 8x8 transpose per 8 keys.  The
@@ -24,9 +29,8 @@
 // puts the rows that a load phase touches on different banks.  The exponents
 // of a block are two numbers for the whole MMA: K's scales the scores, V's is
 // added to them in base 2, so that the weight carries it and the sum divides
-// it out again.  A weight enters the product in f16, times 2^15: 11 bits (22
-// in two terms for fp32), and nothing below 2^-40 of the largest weight times
-// 2^exponent.
+// it out again.  A weight enters the product in f16, times 2^15: nothing below
+// 2^-40 of the largest weight times 2^exponent.
 //
 // Bound by HBM: 2 d bytes a row.  Unpacking costs one conversion per two
 // codes; scoring on the SIMT lanes would cost four instructions per two
@@ -133,6 +137,12 @@ struct StageInfo {
 };
 enum { kSeg, kRing, kNone, kKind = 3, kLast = 4 };
 
+// Second MMAs for the queries' and weights' second terms?
+template <typename T>
+__host__ __device__ constexpr bool wide(bool fold) {
+  return !fold && sizeof(T) == 4;
+}
+
 // A stage: a page's K and V codes, its rows' positions, StageInfo, and, in an
 // item's first stage, the group's queries: f16 terms and the exponent each
 // query was divided by.  Row r's 16-byte piece c sits at piece c ^ swizzle(r).
@@ -140,13 +150,14 @@ enum { kSeg, kRing, kNone, kKind = 3, kLast = 4 };
 // pieces of one half (d = 128) or all pieces (d = 64) of two rows, one of the
 // V fragments two adjacent pieces of four rows; slot_key orders the 8 keys of
 // a tile so that these fall on different banks.
-template <int D, bool kWide>
+template <int D, bool kFold, bool kWide>
 struct Ring {
   static constexpr int kStages = D == 128 ? 3 : 4;
   static constexpr int kV = kPageRows * D, kPos = 2 * kV, kInfo = kPos + kPageRows * 4;
   static constexpr int kQExp = kInfo + 64, kQ = kQExp + 64;
-  static constexpr int kQTerm = kMaxR * D * 2;  // bytes of one term of the queries
-  static constexpr int kStride = (kQ + (kWide ? 2 : 1) * kQTerm + 127) / 128 * 128;
+  // term t of query i: column 2 i + t, or of two sets of columns
+  static constexpr int kQNext = (kFold ? 2 : 1) * D * 2, kQTerm = (kFold ? 1 : kMaxR) * D * 2;
+  static constexpr int kStride = (kQ + (kWide ? 2 : 1) * kMaxR * D * 2 + 127) / 128 * 128;
   static constexpr int kBytes = kStages * kStride;
   __device__ static int swizzle(int r) { return D == 128 ? r & 7 : r & 2; }
   __device__ static int slot_key(int n) {
@@ -255,15 +266,16 @@ __device__ __forceinline__ void put_token(const PagedArgs& a, const PagedDecodeA
 }
 
 // The streaming warp.
-template <typename T, int D>
+template <typename T, int D, bool kFold>
 __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDecodeArgs& n, int Gkv,
                                              int H, int R, int HLkv, uint8_t* ring_smem, Bars* bars,
                                              int wi, int wi_end, PagedItem it, fg_paged_desc hd,
                                              int items, const LaneSet& special,
                                              const LaneSet& punct) {
-  constexpr bool kWide = sizeof(T) == 4;
-  using RG = Ring<D, kWide>;
+  constexpr bool kWide = wide<T>(kFold), kTwo = kFold || kWide;
+  using RG = Ring<D, kFold, kWide>;
   constexpr int PER = D / 32, CPR = D / 16;  // values per lane of a row; 16-byte pieces per row
+  constexpr int kQueries = kFold ? kMaxR / 2 : kMaxR;
   const int lane = threadIdx.x & 31;
   const uint32_t base = sm100::smem_addr(ring_smem);
   bool puts_done = false;
@@ -288,9 +300,9 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
     if (wi + 1 < wi_end) it = a.items[wi + 1];  // known by the time this item is through
     // the group's queries and the angles' turns, on their way while the pages are looked up
     const size_t g0 = (size_t)(c / (H / R)) * H + (size_t)(c % (H / R)) * R;
-    float x[kMaxR][PER];
+    float x[kQueries][PER];
 #pragma unroll
-    for (int qi = 0; qi < kMaxR; ++qi)
+    for (int qi = 0; qi < kQueries; ++qi)
       if (qi < R) load_row<PER>((const T*)n.q + (g0 + qi) * D, x[qi]);
     if (t < 0) {  // the sequence takes no part: one empty stage says so
       const int slot = stage % RG::kStages;
@@ -347,17 +359,17 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
     };
     fetch(0);
     // the group's queries into an item's first stage: rotated, divided by the power of two that
-    // brings the largest value to [2^13, 2^14), as f16 (fp32: and what f16 loses, times 2^11)
+    // brings the largest value to [2^13, 2^14), as f16 (two terms: and what f16 loses, times 2^11)
     auto put_queries = [&](uint8_t* st) {
       float2 cs[PER];
       if (n.rope.rot > 0)
         row_angles<PER>(cs, n.rope.rot, n.rope.style, [&](int p) {
           float2 y;
-          rope_cos_sin<kWide>((unsigned)t, n.rope.turns[p], y.x, y.y);
+          rope_cos_sin<kTwo>((unsigned)t, n.rope.turns[p], y.x, y.y);
           return y;
         });
 #pragma unroll
-      for (int qi = 0; qi < kMaxR; ++qi) {
+      for (int qi = 0; qi < kQueries; ++qi) {
         if (qi >= R) break;
         if (n.rope.rot > 0) rotate_row<PER>(x[qi], cs, n.rope.rot, n.rope.style);
         uint32_t top = 0;
@@ -370,9 +382,9 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
         for (int k = 0; k < PER; k += 2) {
           const float u = x[qi][k] * inv, v = x[qi][k + 1] * inv;
           const uint32_t hi = pack_f16x2(u, v);
-          uint8_t* q = st + RG::kQ + (qi * D + lane * PER + k) * 2;
+          uint8_t* q = st + RG::kQ + qi * RG::kQNext + (lane * PER + k) * 2;
           *reinterpret_cast<uint32_t*>(q) = hi;
-          if constexpr (kWide) {
+          if constexpr (kTwo) {
             const float2 f = unpack_f16x2(hi);
             *reinterpret_cast<uint32_t*>(q + RG::kQTerm) =
                 pack_f16x2((u - f.x) * 2048.f, (v - f.y) * 2048.f);
@@ -464,12 +476,15 @@ __device__ __forceinline__ bool same_list(const PagedArgs& a) {
   return a.totals[3] == a.n_work && a.totals[4] == a.n_ctas;
 }
 
-template <typename T, int D>
+// kFold: groups of up to four queries.  A lane then has one query (t4) and, in
+// its two columns, that query's two terms; else two queries (2 t4, 2 t4 + 1).
+template <typename T, int D, bool kFold>
 __global__ void __launch_bounds__(kThreads, kBlocks(D))
     q8_split_kernel(const PagedArgs a, const PagedDecodeArgs n, int G, int H, int R, int HLkv,
                     float sl2) {
-  constexpr bool kWide = sizeof(T) == 4;  // fp32: queries and weights in two f16 terms
-  using RG = Ring<D, kWide>;
+  constexpr bool kWide = wide<T>(kFold);
+  using RG = Ring<D, kFold, kWide>;
+  constexpr int NQ = kFold ? 1 : 2;  // queries of a lane
   constexpr int KI = D / 64;   // 16-byte pieces of a K row per lane
   constexpr int PW = D / 32;   // words of a lane's V piece
   constexpr int MT = D / 16;   // 16-row tiles of O^T
@@ -480,6 +495,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
+  const int q0 = NQ * t4;  // the lane's first query
   // a list of another cache may say anything: its items are bounded here, its
   // caches where they are used
   const int wi0 = max(0, min(a.cta_first[blockIdx.x], a.n_work - 1));
@@ -511,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
   }
   const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   if (warp == kWarps) {
-    stream_items<T, D>(a, n, Gkv, H, R, HLkv, ring_smem, &bars, wi0, wi_end, own_item, own_cache,
+    stream_items<T, D, kFold>(a, n, Gkv, H, R, HLkv, ring_smem, &bars, wi0, wi_end, own_item, own_cache,
                        own_items, special, punct);
     return;
   }
@@ -555,16 +571,19 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
   int stage = 0, half = 0;
 #pragma unroll 1
   for (int wi = wi0; wi < wi_end; ++wi) {
-    // of queries 2 t4 and 2 t4 + 1 over the lane's keys; columns without a query keep a maximum
-    // that no score passes: weight 0
-    float m[2], l[2] = {0.f, 0.f};
+    // of the lane's queries over its keys; lanes without a query keep a maximum that no score
+    // passes: weight 0
+    float m[NQ], l[NQ];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) m[q] = 2 * t4 + q < R ? FG_NEG_INF : 1e30f;
+    for (int q = 0; q < NQ; ++q) {
+      m[q] = q0 + q < R ? FG_NEG_INF : 1e30f;
+      l[q] = 0.f;
+    }
     float o[MT][4];
 #pragma unroll
     for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    uint32_t qa[4 * KI][kWide ? 4 : 2];
-    int eq[2] = {0, 0};
+    uint32_t qa[4 * KI][kWide ? 4 : 2];  // (kWide: the second terms behind the first)
+    int eq[NQ] = {};
     int last = 0, item = 0, cache = 0, alone = 0;
 #pragma unroll 1
     for (bool opening = true; !last; opening = false, ++stage) {
@@ -598,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             uint2 x = make_uint2(0, 0), y = make_uint2(0, 0);
-            if (g < R) {
+            if (g < (kFold ? 2 * R : R)) {
               const uint8_t* q = sp + RG::kQ + (g * D + 64 * i + 16 * t4 + 4 * w) * 2;
               x = *reinterpret_cast<const uint2*>(q);
               if constexpr (kWide) y = *reinterpret_cast<const uint2*>(q + RG::kQTerm);
@@ -611,8 +630,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
             }
           }
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-          eq[q] = 2 * t4 + q < R ? reinterpret_cast<const int*>(sp + RG::kQExp)[2 * t4 + q] : 0;
+        for (int q = 0; q < NQ; ++q)
+          eq[q] = q0 + q < R ? reinterpret_cast<const int*>(sp + RG::kQExp)[q0 + q] : 0;
       }
       if (kind == kNone || row >= end) {  // uniform over the warp: no rows here
         __syncwarp();
@@ -621,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
       }
       const uint32_t ex = exps >> (16 * (warp & 1));
       const int ek = (int)(signed char)(ex & 0xff), ev = (int)(signed char)((ex >> 8) & 0xff);
-      // scores of key kr ([0], [1]) and key kr + 8 ([2], [3]) with queries 2 t4 and 2 t4 + 1
+      // columns 2 t4 and 2 t4 + 1 of key kr ([0], [1]) and of key kr + 8 ([2], [3])
       float x[4] = {0.f, 0.f, 0.f, 0.f}, xl[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < KI; ++i) {
@@ -640,15 +659,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
       v[1].load(st + vb_off);
       v[2].load(st + va_off + 8 * D);
       v[3].load(st + vb_off + 8 * D);
-      // in base 2, V's exponent added
+      // scores of the lane's queries with keys kr and kr + 8 in base 2, V's exponent added
       const float fv = (float)ev;
+      float sc[NQ][2];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < NQ; ++q) {
         const float kf = pow2f(max(-126, min(127, ek + eq[q]))) * sl2;
 #pragma unroll
-        for (int h = 0; h < 4; h += 2) {
-          if constexpr (kWide) x[q + h] = fmaf(xl[q + h], 1.f / 2048.f, x[q + h]);
-          x[q + h] = fmaf(x[q + h], kf, fv);
+        for (int h = 0; h < 2; ++h) {
+          const float y = kFold   ? fmaf(x[2 * h + 1], 1.f / 2048.f, x[2 * h])
+                          : kWide ? fmaf(xl[2 * h + q], 1.f / 2048.f, x[2 * h + q])
+                                  : x[2 * h + q];
+          sc[q][h] = fmaf(y, kf, fv);
         }
       }
       if (kind == kRing || row + kBlockRows > end) {  // uniform: rows may be missing
@@ -661,18 +683,27 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
           }
           return ok;
         };
-        if (!there(kr)) x[0] = x[1] = FG_NEG_INF;
-        if (!there(kr + 8)) x[2] = x[3] = FG_NEG_INF;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (!there(kr + 8 * h))
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) sc[q][h] = FG_NEG_INF;
 #pragma unroll
         for (int i = 0; i < 4; ++i)  // such a row may hold anything, also NaN
           if (!there((i & 1 ? vb : va) + (i & 2 ? 8 : 0))) v[i].zero();
       }
       __syncwarp();  // every lane has read the stage
       if (lane == 0) sm100::mbar_arrive(&bars.empty[slot]);
-      float top[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
-      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+      float top[NQ];
+      bool rises = false;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < NQ; ++q) {
+        top[q] = fmaxf(sc[q][0], sc[q][1]);
+        rises |= top[q] > m[q];
+      }
+      if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1)
             top[q] = fmaxf(top[q], __shfl_xor_sync(0xffffffffu, top[q], d));
@@ -681,29 +712,37 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
           m[q] = mn;
           l[q] *= corr;
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            o[i][q] *= corr;
-            o[i][q + 2] *= corr;
-          }
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (kFold || (k & 1) == q) o[i][k] *= corr;
         }
       }
-      float p[4];
+      float p[NQ][2];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < NQ; ++q) {
         const float off = (m[q] == FG_NEG_INF ? 0.f : m[q]) - kPBits;
-        p[q] = ex2(x[q] - off);
-        p[q + 2] = ex2(x[q + 2] - off);
+        p[q][0] = ex2(sc[q][0] - off);
+        p[q][1] = ex2(sc[q][1] - off);
         // the sum takes the weights in 32 bits: f16 would lose those that a small
         // exponent of V makes small
-        l[q] = fmaf(p[q] + p[q + 2], pow2f(-ev), l[q]);
+        l[q] = fmaf(p[q][0] + p[q][1], pow2f(-ev), l[q]);
       }
-      const uint32_t lo = pack_f16x2(p[0], p[1]), hi = pack_f16x2(p[2], p[3]);
-      const uint32_t p01 = transpose8x8(lo), p23 = transpose8x8(hi);
-      uint32_t r01 = 0, r23 = 0;
-      if constexpr (kWide) {
-        const float2 f01 = unpack_f16x2(lo), f23 = unpack_f16x2(hi);
-        r01 = transpose8x8(pack_f16x2(p[0] - f01.x, p[1] - f01.y));
-        r23 = transpose8x8(pack_f16x2(p[2] - f23.x, p[3] - f23.y));
+      uint32_t p01, p23, r01 = 0, r23 = 0;  // of keys kr and kr + 8; r: second terms
+      if constexpr (kFold) {
+        const float2 f = unpack_f16x2(pack_f16x2(p[0][0], p[0][1]));
+        p01 = transpose8x8(pack_f16x2(f.x, p[0][0] - f.x));
+        p23 = transpose8x8(pack_f16x2(f.y, p[0][1] - f.y));
+      } else {
+        const uint32_t lo = pack_f16x2(p[0][0], p[NQ - 1][0]),
+                       hi = pack_f16x2(p[0][1], p[NQ - 1][1]);
+        p01 = transpose8x8(lo);
+        p23 = transpose8x8(hi);
+        if constexpr (kWide) {
+          const float2 f01 = unpack_f16x2(lo), f23 = unpack_f16x2(hi);
+          r01 = transpose8x8(pack_f16x2(p[0][0] - f01.x, p[NQ - 1][0] - f01.y));
+          r23 = transpose8x8(pack_f16x2(p[0][1] - f23.x, p[NQ - 1][1] - f23.y));
+        }
       }
 #pragma unroll
       for (int w = 0; w < PW; ++w) {
@@ -728,28 +767,29 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
     float(&sm_m)[kWarps][kMaxR] = sm_ml[half][0], (&sm_l)[kWarps][kMaxR] = sm_ml[half][1];
     half ^= 1;  // the other half may still be read
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < NQ; ++q) {
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) l[q] += __shfl_xor_sync(0xffffffffu, l[q], d);
-      if (g == 0 && 2 * t4 + q < R) {
-        sm_m[warp][2 * t4 + q] = m[q];
-        sm_l[warp][2 * t4 + q] = l[q];
+      if (g == 0 && q0 + q < R) {
+        sm_m[warp][q0 + q] = m[q];
+        sm_l[warp][q0 + q] = l[q];
       }
     }
     sync_warps();
-    // O^T: rows 16 j + g, + 8 are dimensions (D / 8) g + 2 j, + 1; columns queries 2 t4, 2 t4 + 1
+    // O^T: rows 16 j + g, + 8 are dimensions (D / 8) g + 2 j, + 1; the columns as the queries'
 #pragma unroll
-    for (int qc = 0; qc < 2; ++qc) {
-      const int qi = 2 * t4 + qc;
+    for (int q = 0; q < NQ; ++q) {
+      const int qi = q0 + q;
       if (qi < R) {
         float M = FG_NEG_INF;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][qi]);
-        const float f = m[qc] == FG_NEG_INF ? 1.f : exp2f(m[qc] - M);  // (0, or NaN: as they are)
+        const float f = m[q] == FG_NEG_INF ? 1.f : exp2f(m[q] - M);  // (0, or NaN: as they are)
 #pragma unroll
         for (int j = 0; j < MT; ++j)
           *reinterpret_cast<float2*>(&sums[(warp * R + qi) * D + (D / 8) * g + 2 * j]) =
-              make_float2(o[j][qc] * f, o[j][qc + 2] * f);
+              kFold ? make_float2((o[j][0] + o[j][1]) * f, (o[j][2] + o[j][3]) * f)
+                    : make_float2(o[j][q] * f, o[j][q + 2] * f);
       }
     }
     sync_warps();
@@ -856,33 +896,41 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   }
 }
 
-template <typename T, int D>
+constexpr int kFoldR = 4;  // queries whose two terms fill the MMA's eight columns
+
+template <typename T, int D, bool kFold>
 int split_smem(int R) {
-  return Ring<D, sizeof(T) == 4>::kBytes + kWarps * R * D * (int)sizeof(float);
+  return Ring<D, kFold, wide<T>(kFold)>::kBytes + kWarps * R * D * (int)sizeof(float);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kFold>
 cudaError_t run_decode_q8(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
                           cudaStream_t s) {
-  const int smem = split_smem<T, D>(pd.R);
-  cudaError_t e = cudaFuncSetAttribute(q8_split_kernel<T, D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const auto split = q8_split_kernel<T, D, kFold>;
+  const int smem = split_smem<T, D, kFold>(pd.R);
+  cudaError_t e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   // d = 64: with the split of an SM's memory that its own size asks for, SMs at
   // times took in fewer than four blocks beside the previous combine's (64 -> 59
   // us, 2048 caches of 2048 positions); d = 128 runs slower with less L1 (51.3 ->
   // 52.0 us, 7B shape)
   if (D == 64)
-    for (const void* f : {(const void*)q8_split_kernel<T, D>, (const void*)q8_combine_kernel<T, D>})
+    for (const void* f : {(const void*)split, (const void*)q8_combine_kernel<T, D>})
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                                  cudaSharedmemCarveoutMaxShared);
   if (e == cudaSuccess)
-    e = launch_pdl(q8_split_kernel<T, D>, a.n_ctas, kThreads, smem, s, a, n, pd.G, pd.H, pd.R,
-                   pd.HLkv, pd.sl2);
+    e = launch_pdl(split, a.n_ctas, kThreads, smem, s, a, n, pd.G, pd.H, pd.R, pd.HLkv, pd.sl2);
   if (e == cudaSuccess && a.n_work > pd.Gkv)  // else every cache has one item
     e = launch_pdl(q8_combine_kernel<T, D>, cdiv(pd.G, kCombineWarps), kCombineWarps * 32, 0, s, a,
                    n, pd.G, pd.H, pd.R, pd.HLkv);
   return e;
+}
+
+template <typename T, int D>
+cudaError_t run_decode_q8(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
+                          cudaStream_t s) {
+  return pd.R <= kFoldR ? run_decode_q8<T, D, true>(pd, a, n, s)
+                        : run_decode_q8<T, D, false>(pd, a, n, s);
 }
 
 // As many as the SMs hold less one or two: right behind the previous step's
@@ -893,7 +941,8 @@ cudaError_t run_decode_q8(const ProfileDims& pd, const PagedArgs& a, const Paged
 // left a part-filled second wave: 128 caches of 8192 positions 51.6 us, now 37).
 template <typename T, int D>
 int slots(int R, int sms) {
-  const int room = 228 * 1024 / (split_smem<T, D>(R) + 1024 + 1024);
+  const int smem = R <= kFoldR ? split_smem<T, D, true>(R) : split_smem<T, D, false>(R);
+  const int room = 228 * 1024 / (smem + 1024 + 1024);
   return (room < kBlocks(D) ? room : kBlocks(D)) * sms - sms / 64;
 }
 

@@ -578,10 +578,10 @@ fg_status fastgen_append_q8(const fg_params* p, const fg_paged_cache* cache, con
  *   out[g] = sum_j softmax_j(s q_g . k_j) v_j   (zeros if empty)
  * with q [G, d] rotated at pos[b] and the rows as stored.  k_new, v_new NULL: nothing is
  * appended; pos[b] is then the position of the newest token, and new_ids may be NULL.
- * bf16 queries enter the products with 11 bits after rotation (rounding at most 2^-12 of each
- * value; without rotation they are exact), fp32 queries with 22; the softmax weights times their
- * row's value exponent likewise, and those below 2^-40 of the largest of them count as zero in
- * the product.  Sums are 32-bit.
+ * Queries, after rotation, and the softmax weights times their row's value exponent enter the
+ * products with 22 bits (rounding at most 2^-22 of each value), in bf16 groups of eight with 11
+ * (2^-11; queries that are not rotated are exact); weights so scaled below 2^-40 of the largest
+ * of them count as zero in the product.  Sums are 32-bit.
  * Arguments else as fastgen_decode_attn; needs a work list.  The workspace holds nothing between
  * calls; calls that share one, or a cache, must not overlap.  Asynchronous.
  * Errors: FG_EINVAL, FG_EDTYPE, FG_EWORKSPACE; dev_err as above, and 2 if a wait of the kernel on
