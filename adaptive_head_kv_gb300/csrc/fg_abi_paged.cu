@@ -283,7 +283,7 @@ fg_status fastgen_append_q8(const fg_params* p, const fg_paged_cache* cache, con
                                           (cudaStream_t)stream));
 }
 
-// [(M, L) n_work x R][sums n_work x R x d]
+// [(maximum, sum) of the scores n_work x R][outputs n_work x R x d]
 size_t fastgen_decode_q8_workspace_bytes(const fg_params* p, const fg_paged_cache* cache) {
   if (check_params(p) != FG_OK || !cache || cache->n_work < 0) return 0;
   const size_t nw = (size_t)cache->n_work * group_size(p);

@@ -28,8 +28,10 @@
 // order of the keys is free as well: with 16-byte pieces swizzled by the row, slot_key
 // puts the rows that a load phase touches on different banks.  The exponents
 // of a block are two numbers for the whole MMA: K's scales the scores, V's is
-// added to them in base 2, so that the weight carries it and the sum divides
-// it out again.  A weight enters the product in f16, times 2^15: nothing below
+// added to them in base 2, so that a weight of the product carries it.  The
+// softmax's own sum is kept apart, against the maximum of the scores alone: a
+// row counts in it however small its values are beside others (a block of zeros
+// has the least exponent).  A weight enters the product in f16, times 2^15: nothing below
 // 2^-40 of the largest weight times 2^exponent.
 //
 // Bound by HBM: 2 d bytes a row.  Unpacking costs one conversion per two
@@ -55,6 +57,9 @@ namespace {
 constexpr int kWarps = 4;  // that compute
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kMaxR = 8;
+// Maximum before the first score, finite so that differences are: what has none weighs 0, and a
+// NaN in its sum stays.
+constexpr float kNoScore = -3.402823466e38f;
 constexpr float kPBits = 15.f;  // weights are formed times 2^15, near the top of f16's range
 
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -489,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
   constexpr int PW = D / 32;   // words of a lane's V piece
   constexpr int MT = D / 16;   // 16-row tiles of O^T
   extern __shared__ __align__(128) uint8_t ring_smem[];
-  __shared__ float sm_ml[2][2][kWarps][kMaxR];
+  __shared__ float sm_ml[2][3][kWarps][kMaxR];
   __shared__ Bars bars;
   float* sums = reinterpret_cast<float*>(ring_smem + RG::kBytes);  // [kWarps][R][D]
 
@@ -573,10 +578,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
   for (int wi = wi0; wi < wi_end; ++wi) {
     // of the lane's queries over its keys; lanes without a query keep a maximum that no score
     // passes: weight 0
-    float m[NQ], l[NQ];
+    float m[NQ], ms[NQ], l[NQ];  // maximum of score + V's exponent; of the scores, and their sum
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      m[q] = q0 + q < R ? FG_NEG_INF : 1e30f;
+      m[q] = ms[q] = q0 + q < R ? kNoScore : 1e30f;
       l[q] = 0.f;
     }
     float o[MT][4];
@@ -659,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
       v[1].load(st + vb_off);
       v[2].load(st + va_off + 8 * D);
       v[3].load(st + vb_off + 8 * D);
-      // scores of the lane's queries with keys kr and kr + 8 in base 2, V's exponent added
+      // scores of the lane's queries with keys kr and kr + 8 in base 2
       const float fv = (float)ev;
       float sc[NQ][2];
 #pragma unroll
@@ -670,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
           const float y = kFold   ? fmaf(x[2 * h + 1], 1.f / 2048.f, x[2 * h])
                           : kWide ? fmaf(xl[2 * h + q], 1.f / 2048.f, x[2 * h + q])
                                   : x[2 * h + q];
-          sc[q][h] = fmaf(y, kf, fv);
+          sc[q][h] = y * kf;
         }
       }
       if (kind == kRing || row + kBlockRows > end) {  // uniform: rows may be missing
@@ -699,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
         top[q] = fmaxf(sc[q][0], sc[q][1]);
-        rises |= top[q] > m[q];
+        rises |= top[q] > ms[q] || top[q] + fv > m[q];
       }
       if (__any_sync(0xffffffffu, rises)) {
 #pragma unroll
@@ -707,10 +712,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1)
             top[q] = fmaxf(top[q], __shfl_xor_sync(0xffffffffu, top[q], d));
-          const float mn = fmaxf(m[q], top[q]);
-          const float corr = m[q] == FG_NEG_INF ? 0.f : ex2(m[q] - mn);
+          const float mn = fmaxf(m[q], top[q] + fv), sn = fmaxf(ms[q], top[q]);
+          const float corr = ex2(m[q] - mn);
+          l[q] *= ex2(ms[q] - sn);
           m[q] = mn;
-          l[q] *= corr;
+          ms[q] = sn;
 #pragma unroll
           for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -721,12 +727,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
       float p[NQ][2];
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
-        const float off = (m[q] == FG_NEG_INF ? 0.f : m[q]) - kPBits;
-        p[q][0] = ex2(sc[q][0] - off);
-        p[q][1] = ex2(sc[q][1] - off);
-        // the sum takes the weights in 32 bits: f16 would lose those that a small
-        // exponent of V makes small
-        l[q] = fmaf(p[q][0] + p[q][1], pow2f(-ev), l[q]);
+        const float up = fv - m[q] + kPBits;
+        p[q][0] = ex2(sc[q][0] + up);
+        p[q][1] = ex2(sc[q][1] + up);
+        l[q] += ex2(sc[q][0] - ms[q]) + ex2(sc[q][1] - ms[q]);
       }
       uint32_t p01, p23, r01 = 0, r23 = 0;  // of keys kr and kr + 8; r: second terms
       if constexpr (kFold) {
@@ -764,7 +768,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
     }
     if (item < 0) continue;
     // the item is through: merge the four warps
-    float(&sm_m)[kWarps][kMaxR] = sm_ml[half][0], (&sm_l)[kWarps][kMaxR] = sm_ml[half][1];
+    float(&sm_m)[kWarps][kMaxR] = sm_ml[half][0], (&sm_s)[kWarps][kMaxR] = sm_ml[half][1],
+        (&sm_l)[kWarps][kMaxR] = sm_ml[half][2];
     half ^= 1;  // the other half may still be read
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
@@ -772,6 +777,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
       for (int d = 4; d < 32; d <<= 1) l[q] += __shfl_xor_sync(0xffffffffu, l[q], d);
       if (g == 0 && q0 + q < R) {
         sm_m[warp][q0 + q] = m[q];
+        sm_s[warp][q0 + q] = ms[q];
         sm_l[warp][q0 + q] = l[q];
       }
     }
@@ -781,10 +787,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
     for (int q = 0; q < NQ; ++q) {
       const int qi = q0 + q;
       if (qi < R) {
-        float M = FG_NEG_INF;
+        float M = kNoScore;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][qi]);
-        const float f = m[q] == FG_NEG_INF ? 1.f : exp2f(m[q] - M);  // (0, or NaN: as they are)
+        const float f = exp2f(m[q] - M);
 #pragma unroll
         for (int j = 0; j < MT; ++j)
           *reinterpret_cast<float2*>(&sums[(warp * R + qi) * D + (D / 8) * g + 2 * j]) =
@@ -799,18 +805,22 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
       float A = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) A += sums[w * R * D + x];
-      float M = FG_NEG_INF, L = 0.f;
+      float M = kNoScore, S = kNoScore, L = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][qi]);
+      for (int w = 0; w < kWarps; ++w) {
+        M = fmaxf(M, sm_m[w][qi]);
+        S = fmaxf(S, sm_s[w][qi]);
+      }
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        L += sm_l[w][qi] * (sm_m[w][qi] == FG_NEG_INF ? 1.f : exp2f(sm_m[w][qi] - M));
+      for (int w = 0; w < kWarps; ++w) L += sm_l[w][qi] * exp2f(sm_s[w][qi] - S);
+      // the item's own output: the sums are in units of 2^(M - kPBits), L in 2^S
+      const float y = L == 0.f ? 0.f : A / L * exp2f(M - S - kPBits);
       if (alone) {
-        store_out((T*)n.out + g0 * D + x, L == 0.f ? 0.f : A / L);
+        store_out((T*)n.out + g0 * D + x, y);
       } else {
-        n.part_acc[(size_t)item * R * D + x] = A;
+        n.part_acc[(size_t)item * R * D + x] = y;
         if (x % D == 0) {
-          n.part_ml[2 * ((size_t)item * R + qi)] = M;
+          n.part_ml[2 * ((size_t)item * R + qi)] = S;
           n.part_ml[2 * ((size_t)item * R + qi) + 1] = L;
         }
       }
@@ -846,7 +856,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     if (qi == 0 && lane == 0) a.rows_out[c] = had;
     return;
   }
-  float M = FG_NEG_INF, L = 0.f, acc[PER];
+  float M = kNoScore, L = 0.f, acc[PER];  // of the items so far: maximum, sum, output
 #pragma unroll
   for (int k = 0; k < PER; ++k) acc[k] = 0.f;
   for (int i0 = 0; i0 < range.y; i0 += kAhead) {
@@ -856,7 +866,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
       const bool ok = i0 + j < range.y;
       const size_t slot = ((size_t)range.x + i0 + j) * R + qi;
       const float2 ml = ok ? *reinterpret_cast<const float2*>(n.part_ml + 2 * slot)
-                           : make_float2(FG_NEG_INF, 0.f);
+                           : make_float2(kNoScore, 0.f);
       m[j] = ml.x;
       l[j] = ml.y;
       if (ok) load_row<PER>(n.part_acc + slot * D, x[j]);
@@ -867,24 +877,29 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     float Mn = M;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) Mn = fmaxf(Mn, m[j]);
-    const float f = M == FG_NEG_INF ? 1.f : exp2f(M - Mn);
-    L *= f;
-#pragma unroll
-    for (int k = 0; k < PER; ++k) acc[k] *= f;
+    // 2^(m - Mn) as the square of h: a weight below what a float holds may still meet values
+    // that make it count
+    const float fh = exp2f(0.5f * (M - Mn));
+    float h[kAhead], Ln = L * fh * fh;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      // an item without rows, or one whose scores are all NaN, has maximum -inf: its sums count
-      // as they are (0, or NaN)
-      const float wgt = m[j] == FG_NEG_INF ? 1.f : exp2f(m[j] - Mn);
-      L = fmaf(wgt, l[j], L);
-#pragma unroll
-      for (int k = 0; k < PER; ++k) acc[k] = fmaf(wgt, x[j][k], acc[k]);
+      h[j] = exp2f(0.5f * (m[j] - Mn));
+      Ln = fmaf(l[j] * h[j], h[j], Ln);
     }
+    // means of means: nothing passes the largest value
+    const float r = Ln == 0.f ? 0.f : 1.f / Ln;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) acc[k] = acc[k] * (L * r) * fh * fh;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int k = 0; k < PER; ++k) acc[k] = fmaf(x[j][k] * (l[j] * r) * h[j], h[j], acc[k]);
+    L = Ln;
     M = Mn;
   }
 #pragma unroll
   for (int k = 0; k < PER; ++k)
-    store_out((T*)n.out + (size_t)gq * D + lane * PER + k, L == 0.f ? 0.f : acc[k] / L);
+    store_out((T*)n.out + (size_t)gq * D + lane * PER + k, acc[k]);
   if (qi == 0) {
     bool stored = false;  // the new token joined the never-evicted segment and found a page
     if (n.k_new) {

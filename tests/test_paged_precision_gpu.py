@@ -65,3 +65,48 @@ def test_decode_rounds_nothing_but_its_result(kw, rot, half):
         out = s.decode(q, None, None, None, [at], rope)
         check_near(s, out, q, [at], rot, half, inv)
     assert int(s.err.item()) == 0
+
+
+@pytest.mark.parametrize("kw,order", [(kw, order) for order in ("first", "last", "turns") for kw in (
+    dict(H=2, n=160), dict(H=8, Hkv=2, n=240, d=64), dict(H=8, Hkv=1, n=1300))]
+    + [(dict(B=16, L=8, H=8, n=130, r_l=0.0), "turns")])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_values_of_zero_beside_large_ones_keep_their_weight(kw, order, dtype):
+    """Blocks of zero values have the least exponent; their rows hold half the attention all the
+    same, in one item, in several and in shared thread blocks."""
+    def plant(s):
+        block = torch.arange(s.n) // 16
+        half = s.n // 32
+        zero = {"first": block < half, "last": block >= half, "turns": block % 2 == 0}[order]
+        s.V[:] = (s.V.float() * size).to(s.V.dtype)
+        s.V[:, zero] = 0
+        s.V[:, ~zero, 1] = size
+        s.K[:, zero] *= 1.25
+    for size in (2.0 ** 36, 2.0 ** 100) if "B" not in kw else (2.0 ** 60,):
+        s = T.Setup(41, dtype=dtype, policies=[4], plant=plant, **{"L": 1, **kw})
+        s.compact()
+        q = torch.randn(s.G, s.d, generator=T.gen(1)).to(T.DT[dtype])
+        out = s.decode(q, None, None, None, [s.n - 1] * s.B)
+        s.check_out(out, q, [s.n - 1] * s.B)
+        assert int(s.err.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n", [192, 2600])
+def test_small_weights_meet_large_values(n, dtype):
+    """Rows of weight 2^-100 and less whose values outweigh all others, in one item and across
+    items."""
+    def plant(s):
+        s.K[:] = 0
+        s.V[:] = (s.V.float() * 2.0 ** -60).to(s.V.dtype)
+        s.K[:, -32:, 0] = -16.0
+        s.V[:, -32:] = (torch.rand(s.gk, 32, s.d, generator=T.gen(5)) + 0.5).to(s.V.dtype) * 2.0 ** 60
+    s = T.Setup(42, L=1, H=2, n=n, dtype=dtype, policies=[4], plant=plant)
+    s.compact()
+    for first in (4.0, 50.0, 80.0, 110.0):
+        q = torch.zeros(s.G, s.d)
+        q[:, 0] = first
+        q = q.to(T.DT[dtype])
+        out = s.decode(q, None, None, None, [n - 1])
+        s.check_out(out, q, [n - 1])
+    assert int(s.err.item()) == 0
