@@ -104,6 +104,7 @@ fg::PagedArgs paged_args(const fg_params* p, const fg_paged_cache* c, int32_t* d
   a.table_len = c->table_len;
   a.n_work = c->n_work;
   a.n_ctas = c->n_ctas;
+  a.max_w = ratio_count(p->r_l, p->n);
   a.dev_err = dev_err;
   return a;
 }
@@ -119,9 +120,10 @@ fg_status schedule(const fg_params* p, fg_paged_cache* c, long long* totals_read
   const int Gkv = kv_count(p);
   const Sched o = sched_parts(p, c);
   const long long most = sched_max_work(Gkv, c->table_len);
-  cudaError_t e = fg::launch_paged_schedule(Gkv, group_size(p), c->caches, c->rows, c->table_len,
-                                            (int)most, fg::q8_slots(dims(p), sms), o.ranges,
-                                            o.items, o.cta_first, o.totals, s);
+  const fg::ProfileDims pd = dims(p);
+  cudaError_t e = fg::launch_paged_schedule(Gkv, pd.R, c->caches, c->rows, pd.w, c->table_len,
+                                            (int)most, fg::q8_slots(pd, sms), o.ranges, o.items,
+                                            o.cta_first, o.totals, s);
   long long h[5] = {0, 0, 0, 0, 0};
   if (e == cudaSuccess) e = cudaMemcpyAsync(h, o.totals, sizeof(h), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);

@@ -183,11 +183,20 @@ struct PagedArgs {
   const int32_t* cta_first;  // [n_ctas + 1] first item of each thread block
   const long long* totals;   // [3], [4]: the list's items and thread blocks
   int n_pages, table_len, n_work, n_ctas;
+  int max_w;  // ring slots of the call's parameters
   int32_t* dev_err;
 };
 
 // Bits of dev_err.
 constexpr int kErrCapacity = 1, kErrDevice = 2, kErrInvalid = 4;
+
+// A cache's descriptor.  A ring that the parameters do not allow has w = -1: no
+// row of it is read or written, and who sees it flags it.
+__device__ __forceinline__ fg_paged_desc cache_at(const PagedArgs& a, int c) {
+  fg_paged_desc d = a.caches[c];
+  if ((unsigned)d.w > (unsigned)a.max_w) d.w = -1;
+  return d;
+}
 
 // Page of entry `i` of a segment with `entries` entries from `first`; -1 when
 // the entry does not exist or holds no page of the pool.
@@ -422,7 +431,7 @@ cudaError_t launch_paged_plan(int Gkv, int w, int reserve, const int2* cinfo, fg
 // Decode work list of the current row counts; totals[3] = items, totals[4] =
 // thread blocks.
 cudaError_t launch_paged_schedule(int Gkv, int R, const fg_paged_desc* caches, const int32_t* rows,
-                                  int table_len, int max_work, int slots, int4* ranges,
+                                  int max_w, int table_len, int max_work, int slots, int4* ranges,
                                   PagedItem* items, int32_t* cta_first, long long* totals,
                                   cudaStream_t s);
 cudaError_t launch_compact_q8(const ProfileDims& pd, const void* K, const void* V,

@@ -90,12 +90,12 @@ __global__ void __launch_bounds__(kThreads) append_plan_kernel(const PagedArgs a
     const int local = blockIdx.x * kPlanCaches + k;  // cache of the sequence
     if (local >= HLkv) break;
     const int c = b * HLkv + local;
-    const fg_paged_desc d = a.caches[c];
+    const fg_paged_desc d = cache_at(a, c);
     const int had = a.rows[c], old = live_rows(d, had);
     const int want = d.policy == FG_POLICY_FULL ? cnt : d.policy == FG_POLICY_S ? n_s : n_sp;
     const long long cap = min((long long)d.max_pages * kPageRows, 0x7fffffffLL);
     int now = (int)min((long long)old + want, max(cap, (long long)old));
-    int err = old != had && cnt > 0 ? kErrInvalid : 0;
+    int err = (old != had || d.w < 0) && cnt > 0 ? kErrInvalid : 0;
     if (now - old < want) err |= kErrCapacity;
     const int end = now > old ? (now - 1) / kPageRows + 1 : 0;
     for (int base = old / kPageRows; base < end; base += 32) {
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kFewWarps * 32)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();
   griddep_launch_dependents();
-  const fg_paged_desc d = a.caches[c];
+  const fg_paged_desc d = cache_at(a, c);
   const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   const int pos = n.pos[b], had = a.rows[c];
   const int tau = lane < n.m ? n.ids[(size_t)b * n.m + lane] : 0;
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kFewWarps * 32)
                           min((long long)d.max_pages * kPageRows, 0x7fffffffLL) - old);
     stored = max(stored, 0);
     if (lane == 0) {
-      if (old != had && cnt > 0) atomicOr(a.dev_err, kErrInvalid);
+      if ((old != had || d.w < 0) && cnt > 0) atomicOr(a.dev_err, kErrInvalid);
       if (stored < want) atomicOr(a.dev_err, kErrCapacity);
     }
     const int need = stored > 0 ? (old + stored - 1) / kPageRows - page0 + 1 : 0;
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kFewWarps * 32)
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 4)
     append_q8_kernel(const PagedArgs a, const AppendArgs n, int HLkv, int seg_blocks,
-                     int ring_blocks, int max_w, uint32_t tasks) {
+                     int ring_blocks, uint32_t tasks) {
   const uint32_t task = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const uint32_t per = seg_blocks + ring_blocks;
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   griddep_wait();
   griddep_launch_dependents();
   if (!in_grid) return;
-  const fg_paged_desc d = a.caches[c];
+  const fg_paged_desc d = cache_at(a, c);
   const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   const int2 rows = *reinterpret_cast<const int2*>(n.old + 2 * c);  // before the call, stored
   const int cnt = new_tokens(n, b);
@@ -490,10 +490,6 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
   } else {
     if (d.policy != FG_POLICY_SPFL || d.w <= 0) return;
-    if (d.w > max_w) {  // a descriptor of another shape: ring_blocks would not reach all of it
-      if (lane == 0) atomicOr(a.dev_err, kErrInvalid);
-      return;
-    }
     const int in = min(cnt, d.w);  // only the last w tokens can be in the window
     if (j - seg_blocks >= cdiv(d.w, kBlockRows)) return;
     const RingBlock o = ring_block(p0, cnt, in, d.w, j - seg_blocks);
@@ -534,7 +530,7 @@ cudaError_t run_append(const ProfileDims& pd, const PagedArgs& a, const AppendAr
   cudaError_t e = cudaLaunchKernelEx(&cfg, append_plan_kernel, a, n, pd.HLkv);
   if (e != cudaSuccess) return e;
   return launch_pdl(append_q8_kernel<T, D>, (unsigned)grid, kThreads, 0, s, a, n, pd.HLkv, seg,
-                    ring, pd.w, (uint32_t)tasks);
+                    ring, (uint32_t)tasks);
 }
 
 }  // namespace

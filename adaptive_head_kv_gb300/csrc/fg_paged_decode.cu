@@ -161,7 +161,8 @@ struct Ring {
   static constexpr int kV = kPageRows * D, kPos = 2 * kV, kInfo = kPos + kPageRows * 4;
   static constexpr int kQExp = kInfo + 64, kQ = kQExp + 64;
   // term t of query i: column 2 i + t, or of two sets of columns
-  static constexpr int kQNext = (kFold ? 2 : 1) * D * 2, kQTerm = (kFold ? 1 : kMaxR) * D * 2;
+  static constexpr int kQNext = (kFold ? 2 : 1) * D * 2;
+  [[maybe_unused]] static constexpr int kQTerm = (kFold ? 1 : kMaxR) * D * 2;
   static constexpr int kStride = (kQ + (kWide ? 2 : 1) * kMaxR * D * 2 + 127) / 128 * 128;
   static constexpr int kBytes = kStages * kStride;
   __device__ static int swizzle(int r) { return D == 128 ? r & 7 : r & 2; }
@@ -295,7 +296,7 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
     if (!known && lane == 0) atomicOr(a.dev_err, kErrInvalid);
     const int c = known ? it.cache : 0, b = c / HLkv;
     if (!opened) {
-      hd = a.caches[c];
+      hd = cache_at(a, c);
       items = a.ranges[c].y;
     }
     opened = false;
@@ -324,7 +325,7 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
       continue;
     }
     const int old = live_rows(hd, had);
-    if (old != had && cur.last && lane == 0) atomicOr(a.dev_err, kErrInvalid);
+    if ((old != had || hd.w < 0) && cur.last && lane == 0) atomicOr(a.dev_err, kErrInvalid);
     const Put put = item_put(n, cur, hd, special, punct, old, t, tau);
     int seg_end = cur.last ? old : (int)min((long long)old, (long long)cur.seg1 * kPageRows);
     const int ring_end = (int)min((long long)hd.w, (long long)cur.ring1 * kPageRows);
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
   const int own = min(wi0 + (warp == kWarps ? 0 : warp), wi_end - 1);
   const PagedItem own_item = a.items[own];
   const int own_c = (unsigned)own_item.cache < (unsigned)Gkv ? own_item.cache : 0;
-  const fg_paged_desc own_cache = a.caches[own_c];
+  const fg_paged_desc own_cache = cache_at(a, own_c);
   const int own_items = a.ranges[own_c].y;
   const bool listed = same_list(a);
   __syncthreads();
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
       const PagedItem it = wi == own ? own_item : a.items[wi];
       const int c = it.cache, b = c / HLkv;
       if ((unsigned)c >= (unsigned)Gkv) continue;
-      const fg_paged_desc hd = wi == own ? own_cache : a.caches[c];
+      const fg_paged_desc hd = wi == own ? own_cache : cache_at(a, c);
       const int t = n.pos[b], tau = n.ids[b], had = a.rows[c];
       if (t < 0) continue;
       const Put put = item_put(n, it, hd, special, punct, live_rows(hd, had), t, tau);

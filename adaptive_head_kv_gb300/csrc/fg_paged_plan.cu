@@ -72,11 +72,12 @@ __global__ void __launch_bounds__(256) paged_fill_kernel(const fg_paged_desc* __
 
 // Pages of a cache that a decode step reads: its never-evicted segment's (at
 // least one) and its ring's.  Descriptors the plan did not write may say
-// anything: what lies past the table is not counted.
-__device__ __forceinline__ int2 cache_pages(const fg_paged_desc& d, int rows, int table_len) {
+// anything: what lies past the table is not counted, nor a ring of more than max_w slots.
+__device__ __forceinline__ int2 cache_pages(const fg_paged_desc& d, int rows, int max_w,
+                                            int table_len) {
   const int seg = min(max(d.max_pages, 0), table_len), ring = min(max(d.ring_pages, 0), table_len);
   return make_int2(max(1, min(cdiv(max(rows, 0), kPageRows), seg)),
-                   min(cdiv(max(d.w, 0), kPageRows), ring));
+                   min(cdiv((unsigned)d.w <= (unsigned)max_w ? d.w : 0, kPageRows), ring));
 }
 
 // One CTA: how the decode step is cut into items.
@@ -95,7 +96,7 @@ int item_cost(int R) { return 3 + R / 2; }
 constexpr int kLengthTarget = 128; // pages a thread block takes in a wave, about
 
 __global__ void __launch_bounds__(kPlanThreads) paged_schedule_kernel(
-    const fg_paged_desc* __restrict__ caches, const int32_t* __restrict__ rows, int G,
+    const fg_paged_desc* __restrict__ caches, const int32_t* __restrict__ rows, int G, int max_w,
     int table_len, int slots, int item_cost, int4* __restrict__ ranges,
     long long* __restrict__ totals) {
   __shared__ long long scr[33];
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_schedule_kernel(
     const int c = base + threadIdx.x;
     long long items = 0, pages = 0, tot;
     if (c < G) {
-      const int2 p = cache_pages(caches[c], rows[c], table_len);
+      const int2 p = cache_pages(caches[c], rows[c], max_w, table_len);
       pages = (long long)p.x + p.y + item_cost;
       items = ((long long)p.x + p.y + kItemPages - 1) / kItemPages;
     }
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_schedule_kernel(
     const int c = base + threadIdx.x;
     long long items = 0, pages = 0, tot;
     if (c < G) {
-      const int2 p = cache_pages(caches[c], rows[c], table_len);
+      const int2 p = cache_pages(caches[c], rows[c], max_w, table_len);
       pages = (long long)p.x + p.y;
     }
     const long long span = c < G ? pages + item_cost : 0;
@@ -147,14 +148,14 @@ __global__ void __launch_bounds__(kPlanThreads) paged_schedule_kernel(
 
 // One warp per cache: its items, and where they begin a thread block.
 __global__ void __launch_bounds__(256) paged_items_kernel(
-    const fg_paged_desc* __restrict__ caches, const int32_t* __restrict__ rows, int G,
+    const fg_paged_desc* __restrict__ caches, const int32_t* __restrict__ rows, int G, int max_w,
     int table_len, int item_cost, const int4* __restrict__ ranges, int max_work,
     PagedItem* __restrict__ items, int32_t* __restrict__ cta_first,
     const long long* __restrict__ totals) {
   const int c = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (c >= G || totals[3] < 0 || totals[3] > max_work || totals[4] > max_work) return;
   const int4 r = ranges[c];
-  const int2 p = cache_pages(caches[c], rows[c], table_len);
+  const int2 p = cache_pages(caches[c], rows[c], max_w, table_len);
   const int pages = p.x + p.y;
   for (int i = lane; i < r.y; i += 32) {
     long long p0, p1;
@@ -269,7 +270,7 @@ template <typename T, int D, int kChunkRows>
 __global__ void __launch_bounds__(kChunkRows, compact_blocks(D * sizeof(T), kChunkRows))
     compact_q8_kernel(
     const T* __restrict__ K, const T* __restrict__ V, const uint8_t* __restrict__ keep, int n,
-    int G, int H, int R, int max_w, int seg_chunks, int chunks, const PagedArgs a) {
+    int G, int H, int R, int seg_chunks, int chunks, const PagedArgs a) {
   constexpr int kCodeThreads = kChunkRows;
   __shared__ int src[kChunkRows];
   __shared__ int scr[33];
@@ -277,14 +278,16 @@ __global__ void __launch_bounds__(kChunkRows, compact_blocks(D * sizeof(T), kChu
   int chunk = blockIdx.x % chunks;
   griddep_wait();
   griddep_launch_dependents();
-  const fg_paged_desc d = a.caches[c];
+  const fg_paged_desc d = cache_at(a, c);
   const int rows = a.rows[c];
   const bool ring = chunk >= seg_chunks;
   if (ring) chunk -= seg_chunks;
   const int lo = chunk * kChunkRows;
-  const int total = ring ? d.w : (int)min((long long)rows, (long long)d.max_pages * kPageRows);
-  if (!ring && chunk == 0 && threadIdx.x == 0 && rows > total) atomicOr(a.dev_err, kErrInvalid);
-  if (lo >= total) return;
+  const int total = ring ? d.w : live_rows(d, rows);
+  const bool first = !ring && chunk == 0;
+  if (first && threadIdx.x == 0 && (rows != total || rows > n || d.w < 0))
+    atomicOr(a.dev_err, kErrInvalid);
+  if (lo >= total && !first) return;
   const int hi = min(lo + kChunkRows, total);
   const int Hkv = H / R;
   const size_t g0 = (size_t)(c / Hkv) * H + (size_t)(c % Hkv) * R;  // first query head
@@ -293,7 +296,8 @@ __global__ void __launch_bounds__(kChunkRows, compact_blocks(D * sizeof(T), kChu
   if (!ring) {
     const uint8_t* end = keep + (size_t)G * n;
     int seen = 0;  // never-evicted rows before the step
-    for (int base = 0; base < n && seen < hi; base += kCodeThreads * kScanPer) {
+    // (the CTA of the last rows looks at the whole prompt: every kept position has a row)
+    for (int base = 0; base < n && (seen < hi || hi == total); base += kCodeThreads * kScanPer) {
       const int j0 = base + threadIdx.x * kScanPer;
       uint32_t bits = 0;  // any member keeps the position so
       if (j0 < n) {
@@ -312,6 +316,7 @@ __global__ void __launch_bounds__(kChunkRows, compact_blocks(D * sizeof(T), kChu
         }
       seen += tot;
     }
+    if (hi == total && seen != total && threadIdx.x == 0) atomicOr(a.dev_err, kErrInvalid);
   } else {
     // slot s holds the one position of [n - w, n) that is s modulo w
     for (int s = lo + threadIdx.x; s < hi; s += kCodeThreads) {
@@ -355,7 +360,7 @@ cudaError_t run_compact_chunk(const ProfileDims& pd, const void* K, const void* 
   const long long grid = (long long)pd.Gkv * chunks;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   return launch_pdl(compact_q8_kernel<T, D, kChunkRows>, (unsigned)grid, kChunkRows, 0, s,
-                    (const T*)K, (const T*)V, keep, pd.n, pd.G, pd.H, pd.R, pd.w, seg, chunks, a);
+                    (const T*)K, (const T*)V, keep, pd.n, pd.G, pd.H, pd.R, seg, chunks, a);
 }
 
 template <typename T, int D>
@@ -377,13 +382,14 @@ cudaError_t launch_paged_plan(int Gkv, int w, int reserve, const int2* cinfo, fg
 }
 
 cudaError_t launch_paged_schedule(int Gkv, int R, const fg_paged_desc* caches, const int32_t* rows,
-                                  int table_len, int max_work, int slots, int4* ranges,
+                                  int max_w, int table_len, int max_work, int slots, int4* ranges,
                                   PagedItem* items, int32_t* cta_first, long long* totals,
                                   cudaStream_t s) {
-  paged_schedule_kernel<<<1, kPlanThreads, 0, s>>>(caches, rows, Gkv, table_len, slots,
+  paged_schedule_kernel<<<1, kPlanThreads, 0, s>>>(caches, rows, Gkv, max_w, table_len, slots,
                                                    item_cost(R), ranges, totals);
-  paged_items_kernel<<<cdiv(Gkv, 8), 256, 0, s>>>(caches, rows, Gkv, table_len, item_cost(R),
-                                                  ranges, max_work, items, cta_first, totals);
+  paged_items_kernel<<<cdiv(Gkv, 8), 256, 0, s>>>(caches, rows, Gkv, max_w, table_len,
+                                                  item_cost(R), ranges, max_work, items, cta_first,
+                                                  totals);
   return cudaGetLastError();
 }
 

@@ -479,7 +479,7 @@ fg_status fastgen_rope(const fg_params* p, const void* Q, const void* K, const i
  * w is ceil(r_l n) of fg_params or 0.  An entry or a descriptor that names no
  * page of the pool, a larger w, or a row count past its segment is never
  * followed: those rows count as absent and 4 is ORed into *dev_err (FG_EINVAL
- * from fastgen_read_error).
+ * from fastgen_read_error).  Every call takes n and r_l of the caches' prompt.
  * ------------------------------------------------------------------------ */
 #define FG_PAGE_ROWS 64
 #define FG_BLOCK_ROWS 16
@@ -542,8 +542,10 @@ fg_status fastgen_paged_plan(const fg_params* p, const int8_t* policy, const uin
 fg_status fastgen_paged_schedule(const fg_params* p, fg_paged_cache* cache, void* stream);
 
 /* Gathers and codes the kept prompt rows: K, V [Gkv, n, d] dtype and keep [G, n] as
- * fastgen_compact.  Writes codes, exponents and positions of the rows in use and -1 as the
- * position of ring slots without a row; every other byte of a page stays.
+ * fastgen_compact, with as many never-evicted positions in a cache as its rows say (else 4 is
+ * ORed into *dev_err and the first ones are coded).  Writes codes, exponents and positions of the
+ * rows in use and -1 as the position of ring slots without a row; every other byte of a page
+ * stays.
  * Asynchronous.  Errors: FG_EINVAL, FG_EDTYPE; dev_err as above. */
 fg_status fastgen_compact_q8(const fg_params* p, const void* K, const void* V, const uint8_t* keep,
                              const fg_paged_cache* cache, int32_t* dev_err, void* stream);
