@@ -206,6 +206,16 @@ __device__ __forceinline__ int page_at(const PagedArgs& a, int first, int entrie
   return page >= 0 && page < a.n_pages ? page : -1;
 }
 
+// Takes `want` pages of the pool: the first one's number, of which those below n_pages are the
+// caller's (a negative number: none).  What the pool does not have goes back to the counter, so
+// that it ends at n_pages and a larger pool goes on from there.
+__device__ __forceinline__ int take_pages(const PagedArgs& a, int want) {
+  const int first = atomicAdd(a.next_page, want);
+  const int got = first < 0 ? 0 : max(0, min(want, a.n_pages - first));
+  if (got < want) atomicSub(a.next_page, want - got);
+  return first;
+}
+
 // ------------------------------------------------- rows held by one warp
 // A row of D values over the 32 lanes: lane l has values l * PER ..
 

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) append_plan_kernel(const PagedArgs a
       const uint32_t missing = __ballot_sync(0xffffffffu, need && page < 0);
       if (missing) {
         int first = 0;
-        if (lane == 0) first = atomicAdd(a.next_page, __popc(missing));
+        if (lane == 0) first = take_pages(a, __popc(missing));
         first = __shfl_sync(0xffffffffu, first, 0);
         if (missing >> lane & 1) {
           const long long p = (long long)first + __popc(missing & ((1u << lane) - 1));
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kFewWarps * 32)
           const int e = page0 + i;
           if (d.first_page >= 0 && d.first_page <= a.table_len - 1 - e &&
               a.table[d.first_page + e] < 0) {
-            p = atomicAdd(a.next_page, 1);
+            p = take_pages(a, 1);
             if (p >= 0 && p < a.n_pages) {
               a.table[d.first_page + e] = p;
             } else {

@@ -238,7 +238,7 @@ __device__ __forceinline__ void put_token(const PagedArgs& a, const PagedDecodeA
         err = kErrCapacity;
       } else if (!put.ring && first >= 0 && first <= a.table_len - 1 - i &&
                  a.table[first + i] < 0) {
-        page = atomicAdd(a.next_page, 1);
+        page = take_pages(a, 1);
         if (page >= 0 && page < a.n_pages) {
           a.table[first + i] = page;
         } else {

@@ -504,7 +504,7 @@ typedef struct {
   int32_t* rows;         /* [Gkv] rows of the never-evicted segments */
   int32_t* rows_out;     /* [Gkv] the counts after a call; may be rows.  Another buffer leaves
                             rows as it was, so that the same call can be made again. */
-  int32_t* next_page;    /* [1] first page no cache has taken */
+  int32_t* next_page;    /* [1] first page no cache has taken (n_pages: the pool is used up) */
   void* sched;           /* the decode work list, 256-byte aligned */
   int64_t sched_bytes;
   int32_t n_pages;

@@ -95,3 +95,45 @@ def test_rows_that_are_not_the_kept_positions_are_flagged(n, H, Hkv):
     s.compact()
     assert int(s.err.item()) == 0
     s.check()
+
+
+@pytest.mark.parametrize("m", [1, 8, 70, 0])
+def test_a_pool_that_ran_out_goes_on_when_it_is_made_larger(m):
+    """Calls that find no page leave the counter at the pool's end, however often they are made; a
+    larger pool with the old pages in front serves from there on.  m = 0: decode steps."""
+    s = T.Setup(52, B=2, L=2, H=3, n=64, policies=[4, 3, 4], max_new=400, pages=1)
+    s.compact()
+    at, room = 64, [r.rows for r in s.ref]
+    for step in range(3):
+        ids, k, v = s.tokens(step, max(m, 1))
+        pos = [at + step * max(m, 1)] * 2
+        if m:
+            s.append(ids, k, v, pos)
+        else:
+            q = torch.randn(s.G, s.d, generator=T.gen(step)).to(T.DT[s.dtype])
+            s.decode(q, ids, k, v, pos)
+        assert fg.fastgen_read_error(s.err) == fg.FG_ECAPACITY
+        assert int(s.cache.next_page.item()) == s.cache.c.n_pages
+        room = s.cache.rows.cpu().tolist()
+        s.ref_append(ids, k, v, pos, room=room)
+    s.check()
+    s.err.zero_()
+    old, count = s.cache, s.cache.c.n_pages
+    kept = [x.clone() for x in (old.k_pages, old.v_pages, old.exps, old.pos)]
+    s.set_pages(count + 60)
+    for x, y in zip((s.cache.k_pages, s.cache.v_pages, s.cache.exps, s.cache.pos), kept):
+        x[:count] = y
+    at += 3 * max(m, 1)
+    for step in range(70 if m == 0 else 3):
+        ids, k, v = s.tokens(10 + step, max(m, 1))
+        pos = [at + step * max(m, 1)] * 2
+        if m:
+            s.append(ids, k, v, pos)
+        else:
+            q = torch.randn(s.G, s.d, generator=T.gen(step)).to(T.DT[s.dtype])
+            s.decode(q, ids, k, v, pos)
+        s.ref_append(ids, k, v, pos)
+    assert fg.fastgen_read_error(s.err) == fg.FG_OK
+    gpu = s.check()
+    taken = [x for c in range(s.gk) for r in (False, True) for x in gpu.pages(c, r) if x >= 0]
+    assert sorted(taken) == list(range(int(s.cache.next_page.item())))  # each page once, none lost
