@@ -517,16 +517,17 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
     bars.stop = 0;
     sm100::fence_barrier_init();
   }
-  // what the schedule has fixed is read before the wait
+  // the work list is read before the wait (fastgen_paged_schedule waits until it is there); the
+  // caller's own buffers, descriptors too, behind it
   const int own = min(wi0 + (warp == kWarps ? 0 : warp), wi_end - 1);
   const PagedItem own_item = a.items[own];
   const int own_c = (unsigned)own_item.cache < (unsigned)Gkv ? own_item.cache : 0;
-  const fg_paged_desc own_cache = cache_at(a, own_c);
   const int own_items = a.ranges[own_c].y;
   const bool listed = same_list(a);
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
+  const fg_paged_desc own_cache = cache_at(a, own_c);
   if (!listed) {
     if (threadIdx.x == 0) atomicOr(a.dev_err, kErrInvalid);
     return;
@@ -842,7 +843,6 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   const int gq = blockIdx.x * kCombineWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const bool in = gq < G;
   const int c = in ? kv_head(gq, H, R) : 0, qi = (gq % H) % R, b = c / HLkv;
-  const fg_paged_desc hd = a.caches[c];
   int4 range = a.ranges[c];
   range.x = max(0, min(range.x, a.n_work));
   range.y = min(range.y, a.n_work - range.x);
@@ -852,6 +852,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   // (a cache's only item has written the result and the count)
   if (!in || range.y == 1 || !listed) return;
+  const fg_paged_desc hd = a.caches[c];
   const int t = n.pos[b], had = a.rows[c], tau = n.k_new ? n.ids[b] : 0;
   if (t < 0) {
     if (qi == 0 && lane == 0) a.rows_out[c] = had;

@@ -137,3 +137,44 @@ def test_a_pool_that_ran_out_goes_on_when_it_is_made_larger(m):
     gpu = s.check()
     taken = [x for c in range(s.gk) for r in (False, True) for x in gpu.pages(c, r) if x >= 0]
     assert sorted(taken) == list(range(int(s.cache.next_page.item())))  # each page once, none lost
+
+
+@pytest.mark.parametrize("n", [60, 1300])
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_step_sees_descriptors_that_the_launch_before_it_wrote(n, captured):
+    """Policies copied into the descriptors on the device, right before each step, with nothing
+    between: the step places its token by them."""
+    steps = 24
+    s = T.Setup(53, L=1, H=4, n=n, policies=[4], max_new=steps + 4)
+    s.compact()
+    desc = [s.cache.caches.clone(), s.cache.caches.clone()]
+    desc[1][:, 0] = P.S
+    ids, k, v = s.tokens(1, 1)
+    ids[:] = 200  # neither special nor punctuation
+    q = torch.randn(s.G, s.d, generator=T.gen(1)).to(torch.bfloat16)
+    io = [T.dev(x) for x in (q, k, v, ids)]
+    pos = [T.dev([n + i], torch.int32) for i in range(steps)]
+    outs = torch.zeros(steps, s.G, s.d, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(fg.fastgen_decode_q8_workspace_bytes(s.p, s.cache), dtype=torch.uint8,
+                     device="cuda")
+
+    def run():
+        for i in range(steps):
+            s.cache.caches.copy_(desc[i % 2])
+            fg.fastgen_decode_attn_q8(s.p, s.cache, *io, s.special, s.punct, pos[i], None, outs[i],
+                                      ws, s.err)
+
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        graph.replay()
+    else:
+        run()
+    torch.cuda.synchronize()
+    for i in range(steps):
+        if i % 2 == 0:
+            s.ref_append(ids, k, v, [n + i])
+        s.check_out(outs[i], q, [n + i])
+    assert s.cache.rows.tolist() == [n + steps // 2] * s.gk and int(s.err.item()) == 0
