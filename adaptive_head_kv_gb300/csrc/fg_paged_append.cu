@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   griddep_wait();
   griddep_launch_dependents();
   if (!in_grid) return;
-  const fg_paged_desc d = cache_at(a, c);
+  const fg_paged_desc d = a.caches[c];
   const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   const int2 rows = *reinterpret_cast<const int2*>(n.old + 2 * c);  // before the call, stored
   const int cnt = new_tokens(n, b);
@@ -489,7 +489,8 @@ __global__ void __launch_bounds__(kThreads, 4)
       tok = d.policy == FG_POLICY_FULL ? k : list[k];
     }
   } else {
-    if (d.policy != FG_POLICY_SPFL || d.w <= 0) return;
+    // (a ring that the parameters do not allow has been flagged)
+    if (d.policy != FG_POLICY_SPFL || (unsigned)(d.w - 1) >= (unsigned)a.max_w) return;
     const int in = min(cnt, d.w);  // only the last w tokens can be in the window
     if (j - seg_blocks >= cdiv(d.w, kBlockRows)) return;
     const RingBlock o = ring_block(p0, cnt, in, d.w, j - seg_blocks);
