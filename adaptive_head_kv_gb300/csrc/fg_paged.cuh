@@ -190,12 +190,10 @@ struct PagedArgs {
 // Bits of dev_err.
 constexpr int kErrCapacity = 1, kErrDevice = 2, kErrInvalid = 4;
 
-// A cache's descriptor.  A ring that the parameters do not allow has w = -1: no
-// row of it is read or written, and who sees it flags it.
-__device__ __forceinline__ fg_paged_desc cache_at(const PagedArgs& a, int c) {
-  fg_paged_desc d = a.caches[c];
-  if ((unsigned)d.w > (unsigned)a.max_w) d.w = -1;
-  return d;
+// Slots of a cache's ring.  Of one that the parameters do not allow no row is
+// read or written: it has none, and who sees d.w differ flags it.
+__device__ __forceinline__ int ring_slots(const fg_paged_desc& d, int max_w) {
+  return (unsigned)d.w <= (unsigned)max_w ? d.w : 0;
 }
 
 // Page of entry `i` of a segment with `entries` entries from `first`; -1 when

@@ -90,12 +90,12 @@ __global__ void __launch_bounds__(kThreads) append_plan_kernel(const PagedArgs a
     const int local = blockIdx.x * kPlanCaches + k;  // cache of the sequence
     if (local >= HLkv) break;
     const int c = b * HLkv + local;
-    const fg_paged_desc d = cache_at(a, c);
+    const fg_paged_desc d = a.caches[c];
     const int had = a.rows[c], old = live_rows(d, had);
     const int want = d.policy == FG_POLICY_FULL ? cnt : d.policy == FG_POLICY_S ? n_s : n_sp;
     const long long cap = min((long long)d.max_pages * kPageRows, 0x7fffffffLL);
     int now = (int)min((long long)old + want, max(cap, (long long)old));
-    int err = (old != had || d.w < 0) && cnt > 0 ? kErrInvalid : 0;
+    int err = (old != had || d.w != ring_slots(d, a.max_w)) && cnt > 0 ? kErrInvalid : 0;
     if (now - old < want) err |= kErrCapacity;
     const int end = now > old ? (now - 1) / kPageRows + 1 : 0;
     for (int base = old / kPageRows; base < end; base += 32) {
@@ -364,14 +364,14 @@ __global__ void __launch_bounds__(kFewWarps * 32)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();
   griddep_launch_dependents();
-  const fg_paged_desc d = cache_at(a, c);
+  const fg_paged_desc d = a.caches[c];
   const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   const int pos = n.pos[b], had = a.rows[c];
   const int tau = lane < n.m ? n.ids[(size_t)b * n.m + lane] : 0;
   int cnt = n.n_new ? max(0, min(n.n_new[b], n.m)) : n.m;
   if (pos < 0) cnt = 0;
   const unsigned p0 = (unsigned)pos;
-  const int old = live_rows(d, had);
+  const int old = live_rows(d, had), w = ring_slots(d, a.max_w);
   // the pages that the new rows may fall in (at most two), as they are
   const int page0 = old / kPageRows;
   int page = lane < 2 ? page_at(a, d.first_page, d.max_pages, page0 + lane) : -1;
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kFewWarps * 32)
                           min((long long)d.max_pages * kPageRows, 0x7fffffffLL) - old);
     stored = max(stored, 0);
     if (lane == 0) {
-      if ((old != had || d.w < 0) && cnt > 0) atomicOr(a.dev_err, kErrInvalid);
+      if ((old != had || d.w != w) && cnt > 0) atomicOr(a.dev_err, kErrInvalid);
       if (stored < want) atomicOr(a.dev_err, kErrCapacity);
     }
     const int need = stored > 0 ? (old + stored - 1) / kPageRows - page0 + 1 : 0;
@@ -429,8 +429,8 @@ __global__ void __launch_bounds__(kFewWarps * 32)
   const int stored = sm_stored;
   if (threadIdx.x == 0) a.rows_out[c] = cnt > 0 ? old + stored : had;  // every warp has read it
   const int seg = stored > 0 ? (old + stored - 1) / kBlockRows - old / kBlockRows + 1 : 0;
-  const int in = d.policy == FG_POLICY_SPFL && d.w > 0 ? min(cnt, d.w) : 0;
-  const int ring = in > 0 ? min(cdiv(d.w, kBlockRows), touched(in, true)) : 0;
+  const int in = d.policy == FG_POLICY_SPFL ? min(cnt, w) : 0;
+  const int ring = in > 0 ? min(cdiv(w, kBlockRows), touched(in, true)) : 0;
   auto angle = [&](int tok, int p) { return sm_angle[tok * pairs + p]; };
   for (int task = warp; task < 2 * (seg + ring); task += kFewWarps) {
     const int which = task & 1, j = task >> 1;
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kFewWarps * 32)
       append_block<T, D, 4>(a, n, c, tok, p0, sm_page[row / kPageRows - page0], row % kPageRows,
                          which, row >= old, angle);
     } else {
-      RingBlock o = ring_block(p0, cnt, in, d.w, j - seg);
+      RingBlock o = ring_block(p0, cnt, in, w, j - seg);
       if (o.tok >= 0 && (st >> o.tok & 1)) o.tok = -1;
       const int row = o.block * kBlockRows;
       append_block<T, D, 4>(a, n, c, o.tok, p0,
@@ -489,11 +489,11 @@ __global__ void __launch_bounds__(kThreads, 4)
       tok = d.policy == FG_POLICY_FULL ? k : list[k];
     }
   } else {
-    // (a ring that the parameters do not allow has been flagged)
-    if (d.policy != FG_POLICY_SPFL || (unsigned)(d.w - 1) >= (unsigned)a.max_w) return;
-    const int in = min(cnt, d.w);  // only the last w tokens can be in the window
-    if (j - seg_blocks >= cdiv(d.w, kBlockRows)) return;
-    const RingBlock o = ring_block(p0, cnt, in, d.w, j - seg_blocks);
+    const int w = ring_slots(d, a.max_w);
+    if (d.policy != FG_POLICY_SPFL || w == 0) return;
+    const int in = min(cnt, w);  // only the last w tokens can be in the window
+    if (j - seg_blocks >= cdiv(w, kBlockRows)) return;
+    const RingBlock o = ring_block(p0, cnt, in, w, j - seg_blocks);
     row = o.block * kBlockRows;
     page = page_at(a, d.ring_page, d.ring_pages, row / kPageRows);
     tok = o.tok;

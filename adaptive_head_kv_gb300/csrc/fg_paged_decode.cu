@@ -149,8 +149,8 @@ __host__ __device__ constexpr bool wide(bool fold) {
 }
 
 // A stage: a page's K and V codes, its rows' positions, StageInfo, and, in an
-// item's first stage, the group's queries: f16 terms and the exponent each
-// query was divided by.  Row r's 16-byte piece c sits at piece c ^ swizzle(r).
+// item's first stage, the group's queries: f16 terms and the power of
+// two each query was divided by.  Row r's 16-byte piece c sits at piece c ^ swizzle(r).
 // A load phase (8 lanes of 16 bytes, 16 of 8) of the K fragments touches all
 // pieces of one half (d = 128) or all pieces (d = 64) of two rows, one of the
 // V fragments two adjacent pieces of four rows; slot_key orders the 8 keys of
@@ -198,15 +198,15 @@ struct Put {
   int at;     // row of the segment or slot of the ring, -1: not in this item
   bool ring;
 };
-// All lanes call; `old`: rows of the segment before the step.
+// All lanes call; w: slots of the ring, `old`: rows of the segment before the step.
 __device__ __forceinline__ Put item_put(const PagedDecodeArgs& n, const PagedItem& it,
                                         const fg_paged_desc& hd, const LaneSet& special,
-                                        const LaneSet& punct, int old, int t, int tau) {
+                                        const LaneSet& punct, int w, int old, int t, int tau) {
   Put p{-1, false};
   if (!n.k_new) return p;
   const int page = old / kPageRows;
   const bool seg_mine = page >= it.seg0 && (it.last || page < it.seg1);
-  const int slot = hd.policy == FG_POLICY_SPFL && hd.w > 0 ? t % hd.w : -1;
+  const int slot = hd.policy == FG_POLICY_SPFL && w > 0 ? t % w : -1;
   const bool ring_mine = slot >= 0 && slot / kPageRows >= it.ring0 && slot / kPageRows < it.ring1;
   if (!seg_mine && !ring_mine) return p;
   const bool s = special.has(tau), sp = s || punct.has(tau);
@@ -296,7 +296,7 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
     if (!known && lane == 0) atomicOr(a.dev_err, kErrInvalid);
     const int c = known ? it.cache : 0, b = c / HLkv;
     if (!opened) {
-      hd = cache_at(a, c);
+      hd = a.caches[c];
       items = a.ranges[c].y;
     }
     opened = false;
@@ -324,9 +324,10 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
       ++stage;
       continue;
     }
+    if (hd.w != ring_slots(hd, a.max_w)) hd.w = -1;  // flagged below
     const int old = live_rows(hd, had);
     if ((old != had || hd.w < 0) && cur.last && lane == 0) atomicOr(a.dev_err, kErrInvalid);
-    const Put put = item_put(n, cur, hd, special, punct, old, t, tau);
+    const Put put = item_put(n, cur, hd, special, punct, hd.w, old, t, tau);
     int seg_end = cur.last ? old : (int)min((long long)old, (long long)cur.seg1 * kPageRows);
     const int ring_end = (int)min((long long)hd.w, (long long)cur.ring1 * kPageRows);
     auto pages_of = [](int page0, int end) {
@@ -396,7 +397,7 @@ __device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDeco
                 pack_f16x2((u - f.x) * 2048.f, (v - f.y) * 2048.f);
           }
         }
-        if (lane == 0) reinterpret_cast<int*>(st + RG::kQExp)[qi] = eq;
+        if (lane == 0) reinterpret_cast<float*>(st + RG::kQExp)[qi] = pow2f(eq);
       }
     };
     const bool late = stage == 0 && pages > RG::kStages;
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
-  const fg_paged_desc own_cache = cache_at(a, own_c);
+  const fg_paged_desc own_cache = a.caches[own_c];
   if (!listed) {
     if (threadIdx.x == 0) atomicOr(a.dev_err, kErrInvalid);
     return;
@@ -545,10 +546,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
       const PagedItem it = wi == own ? own_item : a.items[wi];
       const int c = it.cache, b = c / HLkv;
       if ((unsigned)c >= (unsigned)Gkv) continue;
-      const fg_paged_desc hd = wi == own ? own_cache : cache_at(a, c);
+      const fg_paged_desc hd = wi == own ? own_cache : a.caches[c];
       const int t = n.pos[b], tau = n.ids[b], had = a.rows[c];
       if (t < 0) continue;
-      const Put put = item_put(n, it, hd, special, punct, live_rows(hd, had), t, tau);
+      const Put put = item_put(n, it, hd, special, punct, ring_slots(hd, a.max_w),
+                               live_rows(hd, had), t, tau);
       if (put.at >= 0) put_token<T, D>(a, n, c, hd, put, t);
     }
     __syncwarp();
@@ -590,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
 #pragma unroll
     for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     uint32_t qa[4 * KI][kWide ? 4 : 2];  // (kWide: the second terms behind the first)
-    int eq[NQ] = {};
+    float fq[NQ] = {};  // what the queries were divided by, times the softmax scale
     int last = 0, item = 0, cache = 0, alone = 0;
 #pragma unroll 1
     for (bool opening = true; !last; opening = false, ++stage) {
@@ -638,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
           }
 #pragma unroll
         for (int q = 0; q < NQ; ++q)
-          eq[q] = q0 + q < R ? reinterpret_cast<const int*>(sp + RG::kQExp)[q0 + q] : 0;
+          fq[q] = q0 + q < R ? reinterpret_cast<const float*>(sp + RG::kQExp)[q0 + q] * sl2 : 0.f;
       }
       if (kind == kNone || row >= end) {  // uniform over the warp: no rows here
         __syncwarp();
@@ -667,11 +669,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
       v[2].load(st + va_off + 8 * D);
       v[3].load(st + vb_off + 8 * D);
       // scores of the lane's queries with keys kr and kr + 8 in base 2
-      const float fv = (float)ev;
+      const float fv = (float)ev, fk = pow2f(ek);
       float sc[NQ][2];
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
-        const float kf = pow2f(max(-126, min(127, ek + eq[q]))) * sl2;
+        const float kf = fminf(fk * fq[q], 1.7e38f);  // (a score of 0 stays 0)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float y = kFold   ? fmaf(x[2 * h + 1], 1.f / 2048.f, x[2 * h])

@@ -77,7 +77,7 @@ __device__ __forceinline__ int2 cache_pages(const fg_paged_desc& d, int rows, in
                                             int table_len) {
   const int seg = min(max(d.max_pages, 0), table_len), ring = min(max(d.ring_pages, 0), table_len);
   return make_int2(max(1, min(cdiv(max(rows, 0), kPageRows), seg)),
-                   min(cdiv((unsigned)d.w <= (unsigned)max_w ? d.w : 0, kPageRows), ring));
+                   min(cdiv(ring_slots(d, max_w), kPageRows), ring));
 }
 
 // One CTA: how the decode step is cut into items.
@@ -278,14 +278,14 @@ __global__ void __launch_bounds__(kChunkRows, compact_blocks(D * sizeof(T), kChu
   int chunk = blockIdx.x % chunks;
   griddep_wait();
   griddep_launch_dependents();
-  const fg_paged_desc d = cache_at(a, c);
+  const fg_paged_desc d = a.caches[c];
   const int rows = a.rows[c];
   const bool ring = chunk >= seg_chunks;
   if (ring) chunk -= seg_chunks;
   const int lo = chunk * kChunkRows;
-  const int total = ring ? d.w : live_rows(d, rows);
+  const int w = ring_slots(d, a.max_w), total = ring ? w : live_rows(d, rows);
   const bool first = !ring && chunk == 0;
-  if (first && threadIdx.x == 0 && (rows != total || rows > n || d.w < 0))
+  if (first && threadIdx.x == 0 && (rows != total || rows > n || d.w != w))
     atomicOr(a.dev_err, kErrInvalid);
   if (lo >= total && !first) return;
   const int hi = min(lo + kChunkRows, total);
@@ -320,8 +320,8 @@ __global__ void __launch_bounds__(kChunkRows, compact_blocks(D * sizeof(T), kChu
   } else {
     // slot s holds the one position of [n - w, n) that is s modulo w
     for (int s = lo + threadIdx.x; s < hi; s += kCodeThreads) {
-      const int back = (n - 1 - s) % d.w;
-      const int j = n - 1 - (back < 0 ? back + d.w : back);
+      const int back = (n - 1 - s) % w;
+      const int j = n - 1 - (back < 0 ? back + w : back);
       int st = 0, win = 0;
       for (int m = 0; m < R && j >= 0; ++m) {
         const int code = keep[(g0 + m) * (size_t)n + j];
