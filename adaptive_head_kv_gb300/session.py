@@ -238,20 +238,59 @@ class PagedSession(FastGenSession):
     and profile_attn take them rotated); None: they are taken as they are.
     pages: size of the page pool; None gives the worst case (every cache
     growing by max_new_tokens rows).  A smaller pool that runs out is reported
-    as FG_ECAPACITY by fastgen_read_error(dev_err)."""
+    as FG_ECAPACITY by fastgen_read_error(dev_err).
+
+    Captured append and decode calls keep the workspace they were captured
+    with."""
 
     def __init__(self, params: fg.Params, special_ids, punct_ids, max_new_tokens: int,
                  device="cuda", stream=None, guard=False, rope=None, pages=None):
         super().__init__(params, special_ids, punct_ids, max_new_tokens, device, stream, guard)
         self.rope, self.pages = rope, pages
-        Gkv, E, i32 = self.Gkv, self._empty, torch.int32
-        self.cache = fg.PagedCache(
-            params, None, None, None, None,
-            E((fg.fastgen_paged_table_len(params, self.max_new),), i32), E((Gkv, 6), i32),
-            E((Gkv,), i32), E((1,), i32))
+        self.cache = self._new_cache()
         self.aws = None
-        self._outgrown = []  # workspaces that a captured call may still use
+        self._held = []  # what captured calls may still use
         self._rotated = None
+
+    def _new_cache(self):
+        Gkv, E, i32 = self.Gkv, self._empty, torch.int32
+        return fg.PagedCache(
+            self.p, None, None, None, None,
+            E((fg.fastgen_paged_table_len(self.p, self.max_new),), i32), E((Gkv, 6), i32),
+            E((Gkv,), i32), E((1,), i32))
+
+    def _on_stream(self):
+        """Context in which torch works on the session's device and stream."""
+        s = self.stream
+        if isinstance(s, int):
+            s = torch.cuda.ExternalStream(s, self.device)
+        return torch.cuda.stream(torch.cuda.current_stream(self.device) if s is None else s)
+
+    def _hold(self, ws):
+        """Keeps the workspace of a call that is being captured."""
+        if self.stream is None and self.device.index in (None, torch.cuda.current_device()):
+            captured = torch.cuda.is_current_stream_capturing()
+        else:
+            with self._on_stream():
+                captured = torch.cuda.is_current_stream_capturing()
+        if captured:
+            self._held += [ws] if all(ws is not y for y in self._held) else []
+
+    def _grown(self, ws, need):
+        """A workspace of `need` bytes: ws, or a larger one."""
+        if ws is not None and ws.numel() >= need:
+            return ws
+        with self._on_stream():
+            self._release(ws)
+            return self._empty((max(need, 256 if ws is None else ws.numel() * 3 // 2),),
+                               torch.uint8)
+
+    def _release(self, *buffers):
+        """Buffers about to be dropped: their memory is free once the session's calls so far are
+        through (call on the session's stream)."""
+        for x in buffers:
+            if x is not None:
+                x.record_stream(torch.cuda.current_stream(x.device))
 
     def rotate(self, Q, K, pos=None, out=None):
         """Q and K rotated at pos [B, n] (None: 0 .. n-1) into `out` (a pair;
@@ -273,11 +312,12 @@ class PagedSession(FastGenSession):
                                           self.stream)
         want = self.info.max_pages if self.pages is None else max(self.pages, self.info.pages)
         if self.cache.exps is None or self.cache.c.n_pages < want:
-            rows, d = want * fg.FG_PAGE_ROWS, self.p.d
-            self.cache.set_pages(self._empty((rows, d), torch.uint8),
-                                 self._empty((rows, d), torch.uint8),
-                                 self._empty((want, 8), torch.int8),
-                                 self._empty((rows,), torch.int32))
+            rows, d, c = want * fg.FG_PAGE_ROWS, self.p.d, self.cache
+            with self._on_stream():
+                self._release(c.k_pages, c.v_pages, c.exps, c.pos)
+                c.set_pages(self._empty((rows, d), torch.uint8),
+                            self._empty((rows, d), torch.uint8), self._empty((want, 8), torch.int8),
+                            self._empty((rows,), torch.int32))
         self._size_decode_workspace()
         fg.fastgen_compact_q8(self.p, K, V, self.keep, self.cache, self.dev_err, self.stream)
 
@@ -289,19 +329,13 @@ class PagedSession(FastGenSession):
         self._size_decode_workspace()
 
     def _size_decode_workspace(self):
-        need = fg.fastgen_decode_q8_workspace_bytes(self.p, self.cache)
-        if self.dws is None or self.dws.numel() < need:
-            self._outgrown.append(self.dws)
-            self.dws = self._empty((max(need, 256),), torch.uint8)
+        self.dws = self._grown(self.dws, fg.fastgen_decode_q8_workspace_bytes(self.p, self.cache))
 
     def _positions(self, pos):
         """pos, or that position for every sequence, made on the session's stream."""
         if not isinstance(pos, int):
             return pos
-        s = self.stream
-        if isinstance(s, int):
-            s = torch.cuda.ExternalStream(s, self.device)
-        with torch.cuda.stream(s):  # None: the current one
+        with self._on_stream():
             return torch.full((self.p.B,), pos, dtype=torch.int32, device=self.device)
 
     def descriptors(self):
@@ -317,10 +351,8 @@ class PagedSession(FastGenSession):
         [B, m], pos [B] (or an int) the first new position of each sequence (< 0:
         left out), n_new [B] the tokens of each (None: m)."""
         m = new_ids.numel() // self.p.B
-        need = fg.fastgen_append_q8_workspace_bytes(self.p, m)
-        if self.aws is None or self.aws.numel() < need:
-            self._outgrown.append(self.aws)
-            self.aws = self._empty((max(need, 256),), torch.uint8)
+        self.aws = self._grown(self.aws, fg.fastgen_append_q8_workspace_bytes(self.p, m))
+        self._hold(self.aws)
         fg.fastgen_append_q8(self.p, self.cache, k_new, v_new, new_ids, n_new, self.special,
                              self.punct, self._positions(pos), self.rope, self.aws, self.dev_err,
                              self.stream)
@@ -329,6 +361,7 @@ class PagedSession(FastGenSession):
         """One generation step at pos [B] (or an int): the tokens appended, then
         q [G, d] attending; k_new = v_new = None attends only."""
         out = self.out if out is None else out
+        self._hold(self.dws)
         fg.fastgen_decode_attn_q8(self.p, self.cache, q, k_new, v_new, new_ids, self.special,
                                   self.punct, self._positions(pos), self.rope, out, self.dws,
                                   self.dev_err, self.stream)
