@@ -241,7 +241,9 @@ class PagedSession(FastGenSession):
     as FG_ECAPACITY by fastgen_read_error(dev_err).
 
     Captured append and decode calls keep the workspace they were captured
-    with."""
+    with.  A later prompt that wants more pages than there are gets a new cache
+    (self.cache); replaying calls captured on the one before then does nothing
+    and is reported as FG_EINVAL."""
 
     def __init__(self, params: fg.Params, special_ids, punct_ids, max_new_tokens: int,
                  device="cuda", stream=None, guard=False, rope=None, pages=None):
@@ -267,14 +269,14 @@ class PagedSession(FastGenSession):
         return torch.cuda.stream(torch.cuda.current_stream(self.device) if s is None else s)
 
     def _hold(self, ws):
-        """Keeps the workspace of a call that is being captured."""
+        """Keeps the workspace and the cache of a call that is being captured."""
         if self.stream is None and self.device.index in (None, torch.cuda.current_device()):
             captured = torch.cuda.is_current_stream_capturing()
         else:
             with self._on_stream():
                 captured = torch.cuda.is_current_stream_capturing()
         if captured:
-            self._held += [ws] if all(ws is not y for y in self._held) else []
+            self._held += [x for x in (ws, self.cache) if all(x is not y for y in self._held)]
 
     def _grown(self, ws, need):
         """A workspace of `need` bytes: ws, or a larger one."""
@@ -312,6 +314,8 @@ class PagedSession(FastGenSession):
                                           self.stream)
         want = self.info.max_pages if self.pages is None else max(self.pages, self.info.pages)
         if self.cache.exps is None or self.cache.c.n_pages < want:
+            if any(x is self.cache for x in self._held):
+                self._retire()
             rows, d, c = want * fg.FG_PAGE_ROWS, self.p.d, self.cache
             with self._on_stream():
                 self._release(c.k_pages, c.v_pages, c.exps, c.pos)
@@ -320,6 +324,21 @@ class PagedSession(FastGenSession):
                             self._empty((rows,), torch.int32))
         self._size_decode_workspace()
         fg.fastgen_compact_q8(self.p, K, V, self.keep, self.cache, self.dev_err, self.stream)
+
+    def _retire(self):
+        """A cache of new buffers for the planned prompt: captured calls hold the addresses of the
+        page pool that is about to be replaced.  The old cache's descriptors and work list then
+        allow nothing, so that a replay touches no page and reports FG_EINVAL."""
+        old, self.cache = self.cache, self._new_cache()
+        self.info = fg.fastgen_paged_plan(self.p, self.policy, self.keep, self.max_new, self.cache,
+                                          self.stream)
+        with self._on_stream():
+            self._release(old.k_pages, old.v_pages, old.exps, old.pos)
+            old.sched.zero_()
+            old.rows.zero_()
+            old.caches.copy_(torch.tensor([fg.FG_POLICY_FULL, -1, 0, 0, 0, 0], dtype=torch.int32,
+                                          device=old.caches.device).expand(self.Gkv, 6))
+        old.k_pages = old.v_pages = old.exps = old.pos = None
 
     def reschedule(self):
         """Splits the decode work by the caches' present sizes (worth a call

@@ -86,3 +86,66 @@ def test_outgrown_workspaces_go_unless_a_captured_call_holds_them():
     other.append(*x, at)
     same_caches(s, other)
     assert int(s.dev_err) == 0
+
+
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_calls_captured_on_a_pool_that_was_replaced_do_nothing_and_say_so(own_stream):
+    """A second prompt wants more pages.  Replays of append and decode captured before touch neither
+    the memory that the old pool had nor the new cache, and the error word says so; the session's
+    own calls go on."""
+    stream = torch.cuda.Stream() if own_stream else None
+    few, full = torch.zeros(G, dtype=torch.int8), torch.full((G,), 4, dtype=torch.int8)
+    s, fresh = session(100, stream=stream), session(100, stream=stream)
+    torch.cuda.synchronize()
+    s.prefill_with_policy(*prompt(1), few)
+    torch.cuda.synchronize()
+    short, long_, pos = turn(2, 4), turn(3, 20), dev_pos(N)
+    q = T.dev(torch.randn(G, D, generator=T.gen(5)).to(torch.bfloat16))
+    one = [x[:, 0].contiguous() for x in turn(4, 1)]
+    s.append(*long_, dev_pos(-1))  # sizes the workspace
+    out = torch.full((G, D), 3.5, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    graphs = []
+    for call in (lambda: s.append(*short, pos), lambda: s.append(*long_, pos),
+                 lambda: s.decode(q, *one, pos, out=out)):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=stream):
+            call()
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert int(s.dev_err) == 0
+    pool, before = s.cache.c.n_pages, s.cache
+    freed = [s.cache.k_pages.data_ptr(), s.cache.v_pages.data_ptr()]
+    for x in (s, fresh):
+        x.prefill_with_policy(*prompt(6), full)
+        torch.cuda.synchronize()
+    assert s.cache.c.n_pages > pool and s.cache is not before
+    assert before.k_pages is None and s.cache.k_pages.data_ptr() not in freed
+    torch.cuda.synchronize()
+    other = [torch.full((pool * 64 * D,), 0xA5, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    for g in graphs:
+        for _ in range(2):
+            g.replay()
+            torch.cuda.synchronize()
+            assert fg.fastgen_read_error(s.dev_err) == fg.FG_EINVAL
+            s.dev_err.zero_()
+    assert all(bool((x == 0xA5).all()) for x in other) and bool((out == 3.5).all())
+    same_caches(s, fresh)
+    outs = []
+    for x in (s, fresh):
+        x.append(*short, N)
+        torch.cuda.synchronize()
+        outs.append(x.decode(q, *one, dev_pos(N + 4)).clone())
+        torch.cuda.synchronize()
+    assert torch.equal(*outs) and int(s.dev_err) == 0
+    same_caches(s, fresh)
+
+
+def test_a_larger_pool_without_captured_calls_replaces_the_old_one():
+    s = session(100)
+    s.prefill_with_policy(*prompt(1), torch.zeros(G, dtype=torch.int8))
+    old, cache = weakref.ref(s.cache.k_pages), s.cache
+    s.prefill_with_policy(*prompt(6), torch.full((G,), 4, dtype=torch.int8))
+    gc.collect()
+    assert old() is None and s.cache is cache
