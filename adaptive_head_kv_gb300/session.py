@@ -236,6 +236,8 @@ class PagedSession(FastGenSession):
     rope (fastgen.Rope): the prefill calls, append and decode then take queries
     and keys as projected and rotate them at their positions (profile, compact
     and profile_attn take them rotated); None: they are taken as they are.
+    in_place: the prefill calls rotate the caller's Q and K themselves; without
+    it the session keeps a second pair of their size.
     pages: size of the page pool; None gives the worst case (every cache
     growing by max_new_tokens rows).  A smaller pool that runs out is reported
     as FG_ECAPACITY by fastgen_read_error(dev_err).
@@ -246,9 +248,9 @@ class PagedSession(FastGenSession):
     and is reported as FG_EINVAL."""
 
     def __init__(self, params: fg.Params, special_ids, punct_ids, max_new_tokens: int,
-                 device="cuda", stream=None, guard=False, rope=None, pages=None):
+                 device="cuda", stream=None, guard=False, rope=None, pages=None, in_place=False):
         super().__init__(params, special_ids, punct_ids, max_new_tokens, device, stream, guard)
-        self.rope, self.pages = rope, pages
+        self.rope, self.pages, self.in_place = rope, pages, in_place
         self.cache = self._new_cache()
         self.aws = None
         self._held = []  # what captured calls may still use
@@ -305,7 +307,9 @@ class PagedSession(FastGenSession):
         return out
 
     def _ready(self, Q, K):
-        return (Q, K) if self.rope is None else self.rotate(Q, K)
+        if self.rope is None:
+            return Q, K
+        return self.rotate(Q, K, out=(Q, K) if self.in_place else None)
 
     def compact(self, K, V):
         """Plans the paged caches of the profiled prompt and codes its kept

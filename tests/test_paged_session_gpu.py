@@ -149,3 +149,26 @@ def test_a_larger_pool_without_captured_calls_replaces_the_old_one():
     s.prefill_with_policy(*prompt(6), torch.full((G,), 4, dtype=torch.int8))
     gc.collect()
     assert old() is None and s.cache is cache
+
+
+@pytest.mark.parametrize("host", [False, True])
+def test_rotation_of_the_callers_tensors(host):
+    """in_place: the same caches without a second pair of queries and keys."""
+    pol = torch.arange(G, dtype=torch.int8) % 5
+    a, b = session(), session(in_place=True)
+    kept = [x.clone() for x in prompt(1)]
+    for s in (a, b):
+        x = [y.clone() for y in kept]
+        if host:
+            h = [y.cpu().pin_memory() for y in kept]
+            s.prefill_host(*h, *x)
+        else:
+            s.prefill_with_policy(*x, pol)
+        torch.cuda.synchronize()
+        same = [torch.equal(u, v) for u, v in zip(x, kept)]
+        assert same == [s is a, s is a, True, True]
+        if s is b:
+            assert b._rotated is None
+            assert torch.equal(x[0], a._rotated[0]) and torch.equal(x[1], a._rotated[1])
+    assert torch.equal(a.policy, b.policy)
+    same_caches(a, b)
