@@ -110,3 +110,64 @@ def test_small_weights_meet_large_values(n, dtype):
         out = s.decode(q, None, None, None, [n - 1])
         s.check_out(out, q, [n - 1])
     assert int(s.err.item()) == 0
+
+
+def turned(pos, turns):
+    """(cos, sin) of 2 pi pos turns / 2^64 for int64 turns, in 64 bits: the angle's fraction from the
+    integers."""
+    frac = (np.asarray(pos, dtype=np.uint64)[..., None]
+            * turns.cpu().numpy().astype(np.uint64)).astype(np.int64).astype(np.float64)
+    angle = frac * (2 * np.pi / 2.0 ** 64)
+    return np.cos(angle), np.sin(angle)
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rope_of_unit_pairs_is_cos_and_sin(d, half):
+    """Pairs (1, 0) and (0, 1) give cos and sin themselves.  sincospif is off by one unit in the last
+    place at most (2^-24 below 1), the first-order term's sum rounds by 2^-25, the fraction's bits past
+    the 32nd are 2^-29.3 of an angle: 1.6 * 2^-24.  What a float's 24 bits lose of the angle, left out,
+    would be up to pi 2^-25 = 1.57 * 2^-24 more."""
+    n = 512
+    p = fg.Params(1, 1, 2, n, d, fg.FG_FP32, 0.95, 0.3, 0.3, 0.0, 2)
+    _, turns = T.table(d)
+    rope = fg.Rope(turns, fg.FG_ROPE_HALF if half else fg.FG_ROPE_INTERLEAVED)
+    first = slice(0, d // 2) if half else slice(0, d, 2)
+    second = slice(d // 2, d) if half else slice(1, d, 2)
+    x = torch.zeros(2, n, d)
+    x[0, :, first] = 1.0
+    x[1, :, second] = 1.0
+    for start in (0, 100000, (1 << 30) + 7):
+        pos = T.dev(torch.arange(start, start + n, dtype=torch.int32)[None])
+        y = torch.empty(2, n, d, device="cuda")
+        fg.fastgen_rope(p, None, T.dev(x), pos, rope, None, y)
+        c, s = turned(np.arange(start, start + n), turns)
+        y = T.f64(y)
+        for got, want in ((y[0, :, first], c), (y[0, :, second], s),
+                          (y[1, :, first], -s), (y[1, :, second], c)):
+            assert np.abs(got - want).max() <= 1.6 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d,rot,half", [(128, 128, False), (128, 64, True), (64, 32, False), (64, 64, True)])
+def test_rope_is_near_its_definition(d, rot, half, dtype):
+    """cos and sin within 1.6 * 2^-24, a product and a fused sum in 32 bits: 2^-22 of |x| + |y| of the
+    pair, and the rounding to the type (bf16 2^-8)."""
+    n, H = 300, 6
+    p = fg.Params(2, 1, H, n, d, T.CODE[dtype], 0.95, 0.3, 0.3, 0.0, H)
+    _, turns = T.table(rot)
+    rope = fg.Rope(turns, fg.FG_ROPE_HALF if half else fg.FG_ROPE_INTERLEAVED)
+    x = torch.randn(2 * H, n, d, generator=T.gen(d + rot)).to(T.DT[dtype])
+    pos = torch.randint(0, 1 << 31, (2, n), generator=T.gen(1)).to(torch.int32)
+    y = torch.empty_like(x, device="cuda")
+    fg.fastgen_rope(p, T.dev(x), None, T.dev(pos), rope, y, None)
+    c, s = (t.reshape(2, 1, n, rot // 2) for t in turned(pos.numpy(), turns))
+    i, j = ((slice(0, rot // 2), slice(rot // 2, rot)) if half
+            else (slice(0, rot, 2), slice(1, rot, 2)))
+    x64, got = (T.f64(t).reshape(2, H, n, d) for t in (x, y))
+    a, b = x64[..., i], x64[..., j]
+    size = np.abs(a) + np.abs(b)
+    for want, z in ((a * c - b * s, got[..., i]), (b * c + a * s, got[..., j])):
+        bound = 2.0 ** -22 * size + (2.0 ** -8 if dtype == "bf16" else 0.0) * np.abs(want)
+        assert (np.abs(z - want) <= bound).all()
+    assert np.array_equal(got[..., rot:], x64[..., rot:])
