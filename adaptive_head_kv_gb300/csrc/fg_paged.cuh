@@ -6,8 +6,8 @@
 // code * 2^exponent.  Powers of two make the coding exact to reproduce (the
 // scaling itself never rounds) and let a block's exponent grow when a larger
 // row arrives: e4m3 keeps its fraction bits, only codes that fall among the
-// subnormals are rounded again (absolute error <= 2^-10 of the code range's
-// unit, i.e. 2^-18.8 of the block's largest value).
+// subnormals are rounded again (an error of 2^-10 in units of the new exponent,
+// 2^-17.8 of the block's largest value at most, each time it grows).
 #pragma once
 
 #include "fg_common.cuh"
@@ -143,16 +143,9 @@ struct LaneSet {
   }
 };
 
-// 16-byte global -> shared copy in the background, and its groups.
+// 16-byte global -> shared copy in the background.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 struct RopeArgs {

@@ -71,14 +71,6 @@ __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Transpose of an 8x8 b16 matrix held one row pair per lane (lane l: row l/4,
-// columns 2(l%4), 2(l%4)+1).
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
 // (lo, hi) -> f16x2, nearest even; values past f16's range become infinite.
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
@@ -93,11 +85,7 @@ __device__ __forceinline__ float2 unpack_f16x2(uint32_t w) {
   return f;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+using sm100::ex2;
 
 __device__ __forceinline__ uint4 lds16(uint32_t p) {
   uint4 v;
@@ -162,8 +150,8 @@ struct Ring {
   static constexpr int kQExp = kInfo + 64, kQ = kQExp + 64;
   // term t of query i: column 2 i + t, or of two sets of columns
   static constexpr int kQNext = (kFold ? 2 : 1) * D * 2;
-  [[maybe_unused]] static constexpr int kQTerm = (kFold ? 1 : kMaxR) * D * 2;
-  static constexpr int kStride = (kQ + (kWide ? 2 : 1) * kMaxR * D * 2 + 127) / 128 * 128;
+  static constexpr int kQTerm = (kFold ? 1 : kMaxR) * D * 2;
+  static constexpr int kStride = (kQ + kMaxR * D * 2 + (kWide ? kQTerm : 0) + 127) / 128 * 128;
   static constexpr int kBytes = kStages * kStride;
   __device__ static int swizzle(int r) { return D == 128 ? r & 7 : r & 2; }
   __device__ static int slot_key(int n) {
