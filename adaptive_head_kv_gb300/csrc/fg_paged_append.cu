@@ -16,9 +16,11 @@
 // are rounded again at most once.
 //
 // Short chains of dependent loads, not bytes, set the time of all but long
-// calls: what does not depend on each other is asked for together.  Measured:
-// one token in 1024 caches 4.0 us, five in 2048 caches 10.3 us, 701 (fp32, d =
-// 64) in 128 caches 17 us, 512 in 1024 caches (229 MB) 92 us.
+// calls: what does not depend on each other is asked for together.  Measured
+// (device time): one token in 1024 caches 4.0 us, five in 2048 caches 10.6 us
+// (two warps a cache take its blocks one after the other, and rows past the
+// fourth of a block are read and rotated twice), 701 (fp32, d = 64) in 128
+// caches 17 us, 512 in 1024 caches (229 MB) 93 us.
 #include "fg_paged.cuh"
 
 namespace fg {

@@ -31,8 +31,8 @@
 // added to them in base 2, so that a weight of the product carries it.  The
 // softmax's own sum is kept apart, against the maximum of the scores alone: a
 // row counts in it however small its values are beside others (a block of zeros
-// has the least exponent).  A weight enters the product in f16, times 2^15: nothing below
-// 2^-40 of the largest weight times 2^exponent.
+// has the least exponent).  A weight enters the product in f16, times 2^15:
+// nothing below 2^-40 of the largest weight times 2^exponent.
 //
 // Bound by HBM: 2 d bytes a row.  Unpacking costs one conversion per two
 // codes; scoring on the SIMT lanes would cost four instructions per two
@@ -41,11 +41,14 @@
 // was slower (7B shape 52 -> 64 us): with operands that change it runs at
 // 0.30 a nanosecond and SM, the f16 one (k = 16) at 0.66.
 //
-// Measured (bf16, d = 128, of the 6.78 TB/s that a copy reaches): 1024 caches
-// of the 7B shape (278 MB) 51 us, 0.80; 8192 caches 351 us, 0.93; 512 caches of
-// 32768 positions 288 us, 0.98; groups of 8 on 16384 positions 299 us, 0.95;
-// fp32 0.87; d = 64 0.77 (a block of 16 rows costs a warp about 1500 cycles,
-// less than half of them for its bytes); 32 caches of 128 positions 5.8 us.
+// Measured (device time; bf16, d = 128, of the 6.78 TB/s that a copy reaches):
+// 1024 caches of the 7B shape (278 MB) 51.5 us, 0.80; 8192 caches 349 us, 0.94;
+// 512 caches of 32768 positions 287 us, 0.99; 128 caches of 16384 positions,
+// groups of 8, 303 us, 0.94, groups of 4 292 us, 0.97; 8192 caches, fp32 351 us,
+// 0.94, d = 64 204 us, 0.80 (a block of 16 rows costs a warp about 1500 cycles,
+// less than half of them for its bytes); 32 caches of 128 positions 6.1 us.
+// A list made before the caches grew costs more: the last item of a segment
+// takes every later row (32 caches, 8192 rows since: 77 us, with a new list 14).
 #include <type_traits>
 
 #include "fg_paged.cuh"
@@ -523,8 +526,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
   }
   const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
   if (warp == kWarps) {
-    stream_items<T, D, kFold>(a, n, Gkv, H, R, HLkv, ring_smem, &bars, wi0, wi_end, own_item, own_cache,
-                       own_items, special, punct);
+    stream_items<T, D, kFold>(a, n, Gkv, H, R, HLkv, ring_smem, &bars, wi0, wi_end, own_item,
+                              own_cache, own_items, special, punct);
     return;
   }
 

@@ -345,9 +345,11 @@ class PagedSession(FastGenSession):
         old.k_pages = old.v_pages = old.exps = old.pos = None
 
     def reschedule(self):
-        """Splits the decode work by the caches' present sizes (worth a call
-        now and then in a long generation; steps captured before it are void:
-        they are reported as FG_EINVAL and do nothing)."""
+        """Splits the decode work by the caches' present sizes (worth a call every
+        few hundred tokens of a long generation: a full cache's later rows all
+        go to one thread block.  32 caches with 8192 rows since the prompt: 77 us
+        a step, after this call 14.  It waits for the GPU, 30 us; steps captured
+        before it are void: they are reported as FG_EINVAL and do nothing)."""
         self.cache.schedule(self.p, self.stream)
         self._size_decode_workspace()
 

@@ -535,8 +535,10 @@ fg_status fastgen_paged_plan(const fg_params* p, const int8_t* policy, const uin
                              void* stream);
 
 /* The decode work list of the current rows (needed before the first decode of caches that
- * fastgen_paged_plan did not lay out, and worth a call now and then in a long generation: the last
- * item of a segment takes every row appended later).  A step captured before is captured again:
+ * fastgen_paged_plan did not lay out, and worth a call every few hundred tokens of a long
+ * generation: the last item of a segment, a thread block, takes every row appended later, about
+ * 8 us a step for each 1000 of them where few caches leave nothing else to wait for).  A step
+ * captured before is captured again:
  * with a list of other numbers of items or thread blocks it does nothing and ORs 4 into *dev_err.
  * SYNCHRONOUS on `stream`. */
 fg_status fastgen_paged_schedule(const fg_params* p, fg_paged_cache* cache, void* stream);

@@ -67,7 +67,8 @@ def test_decode_rounds_nothing_but_its_result(kw, rot, half):
     assert int(s.err.item()) == 0
 
 
-@pytest.mark.parametrize("kw,order", [(kw, order) for order in ("first", "last", "turns") for kw in (
+@pytest.mark.parametrize("kw,order", [(kw, order) for order in ("first", "last", "turns")
+                                     for kw in (
     dict(H=2, n=160), dict(H=8, Hkv=2, n=240, d=64), dict(H=8, Hkv=1, n=1300))]
     + [(dict(B=16, L=8, H=8, n=130, r_l=0.0), "turns")])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -100,7 +101,8 @@ def test_small_weights_meet_large_values(n, dtype):
         s.K[:] = 0
         s.V[:] = (s.V.float() * 2.0 ** -60).to(s.V.dtype)
         s.K[:, -32:, 0] = -16.0
-        s.V[:, -32:] = (torch.rand(s.gk, 32, s.d, generator=T.gen(5)) + 0.5).to(s.V.dtype) * 2.0 ** 60
+        large = torch.rand(s.gk, 32, s.d, generator=T.gen(5)) + 0.5
+        s.V[:, -32:] = large.to(s.V.dtype) * 2.0 ** 60
     s = T.Setup(42, L=1, H=2, n=n, dtype=dtype, policies=[4], plant=plant)
     s.compact()
     for first in (4.0, 50.0, 80.0, 110.0):
@@ -113,8 +115,8 @@ def test_small_weights_meet_large_values(n, dtype):
 
 
 def turned(pos, turns):
-    """(cos, sin) of 2 pi pos turns / 2^64 for int64 turns, in 64 bits: the angle's fraction from the
-    integers."""
+    """(cos, sin) of 2 pi pos turns / 2^64 for int64 turns, in 64 bits: the angle's fraction from
+    the integers."""
     frac = (np.asarray(pos, dtype=np.uint64)[..., None]
             * turns.cpu().numpy().astype(np.uint64)).astype(np.int64).astype(np.float64)
     angle = frac * (2 * np.pi / 2.0 ** 64)
@@ -124,10 +126,10 @@ def turned(pos, turns):
 @pytest.mark.parametrize("half", [False, True])
 @pytest.mark.parametrize("d", [64, 128])
 def test_rope_of_unit_pairs_is_cos_and_sin(d, half):
-    """Pairs (1, 0) and (0, 1) give cos and sin themselves.  sincospif is off by one unit in the last
-    place at most (2^-24 below 1), the first-order term's sum rounds by 2^-25, the fraction's bits past
-    the 32nd are 2^-29.3 of an angle: 1.6 * 2^-24.  What a float's 24 bits lose of the angle, left out,
-    would be up to pi 2^-25 = 1.57 * 2^-24 more."""
+    """Pairs (1, 0) and (0, 1) give cos and sin themselves.  sincospif is off by one unit in the
+    last place at most (2^-24 below 1), the first-order term's sum rounds by 2^-25, the fraction's
+    bits past the 32nd are 2^-29.3 of an angle: 1.6 * 2^-24.  What a float's 24 bits lose of the
+    angle, left out, would be up to pi 2^-25 = 1.57 * 2^-24 more."""
     n = 512
     p = fg.Params(1, 1, 2, n, d, fg.FG_FP32, 0.95, 0.3, 0.3, 0.0, 2)
     _, turns = T.table(d)
@@ -149,10 +151,11 @@ def test_rope_of_unit_pairs_is_cos_and_sin(d, half):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("d,rot,half", [(128, 128, False), (128, 64, True), (64, 32, False), (64, 64, True)])
+@pytest.mark.parametrize("d,rot,half", [(128, 128, False), (128, 64, True), (64, 32, False),
+                                        (64, 64, True)])
 def test_rope_is_near_its_definition(d, rot, half, dtype):
-    """cos and sin within 1.6 * 2^-24, a product and a fused sum in 32 bits: 2^-22 of |x| + |y| of the
-    pair, and the rounding to the type (bf16 2^-8)."""
+    """cos and sin within 1.6 * 2^-24, a product and a fused sum in 32 bits: 2^-22 of |x| + |y| of
+    the pair, and the rounding to the type (bf16 2^-8)."""
     n, H = 300, 6
     p = fg.Params(2, 1, H, n, d, T.CODE[dtype], 0.95, 0.3, 0.3, 0.0, H)
     _, turns = T.table(rot)
