@@ -301,7 +301,8 @@ class PagedSession(FastGenSession):
         None: buffers of the session, reused by the next call)."""
         if out is None:
             if self._rotated is None:
-                self._rotated = (torch.empty_like(Q), torch.empty_like(K))
+                with self._on_stream():
+                    self._rotated = (torch.empty_like(Q), torch.empty_like(K))
             out = self._rotated
         fg.fastgen_rope(self.p, Q, K, pos, self.rope, out[0], out[1], self.stream)
         return out
@@ -333,7 +334,9 @@ class PagedSession(FastGenSession):
         """A cache of new buffers for the planned prompt: captured calls hold the addresses of the
         page pool that is about to be replaced.  The old cache's descriptors and work list then
         allow nothing, so that a replay touches no page and reports FG_EINVAL."""
-        old, self.cache = self.cache, self._new_cache()
+        old = self.cache
+        with self._on_stream():
+            self.cache = self._new_cache()
         self.info = fg.fastgen_paged_plan(self.p, self.policy, self.keep, self.max_new, self.cache,
                                           self.stream)
         with self._on_stream():

@@ -583,9 +583,11 @@ fg_status fastgen_append_q8(const fg_params* p, const fg_paged_cache* cache, con
  * with q [G, d] rotated at pos[b] and the rows as stored.  k_new, v_new NULL: nothing is
  * appended; pos[b] is then the position of the newest token, and new_ids may be NULL.
  * Queries, after rotation, and the softmax weights times their row's value exponent enter the
- * products with 22 bits (rounding at most 2^-22 of each value), in bf16 groups of eight with 11
- * (2^-11; queries that are not rotated are exact); weights so scaled below 2^-40 of the largest
- * of them count as zero in the product.  Sums are 32-bit.
+ * products with 22 bits: off by at most 2^-22 of each, or 2^-49 of the query's largest value and
+ * 2^-40 of the largest weight where that is more.  In bf16 groups of eight they have 11: 2^-11 of
+ * each, or 2^-38 and 2^-40 (queries that are not rotated are exact down to 2^-30 of the largest).
+ * Weights so scaled below 2^-40 of the largest count as zero in the product, but not in the
+ * softmax's sum.  Sums are 32-bit.
  * Arguments else as fastgen_decode_attn; needs a work list.  The workspace holds nothing between
  * calls; calls that share one, or a cache, must not overlap.  Asynchronous.
  * Errors: FG_EINVAL, FG_EDTYPE, FG_EWORKSPACE; dev_err as above, and 2 if a wait of the kernel on
