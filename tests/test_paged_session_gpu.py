@@ -172,3 +172,43 @@ def test_rotation_of_the_callers_tensors(host):
             assert torch.equal(x[0], a._rotated[0]) and torch.equal(x[1], a._rotated[1])
     assert torch.equal(a.policy, b.policy)
     same_caches(a, b)
+
+
+@pytest.mark.parametrize("which", ["default", "side"])
+def test_streams_given_as_addresses(which):
+    """A session on a raw stream address: buffers that grow, captured calls, int positions."""
+    side = torch.cuda.Stream()
+    address = 0 if which == "default" else side.cuda_stream
+    pol = torch.full((G,), 4, dtype=torch.int8)
+    a, b = session(), session(stream=address)
+    outs = []
+    q = T.dev(torch.randn(G, D, generator=T.gen(5)).to(torch.bfloat16))
+    one = [x[:, 0].contiguous() for x in turn(4, 1)]
+    for s in (a, b):
+        torch.cuda.synchronize()
+        s.prefill_with_policy(*prompt(1), pol)
+        at = N
+        for m in (2, 30, 100):
+            torch.cuda.synchronize()
+            s.append(*turn(m, m), at)
+            at += m
+        s.reschedule()
+        torch.cuda.synchronize()
+        outs.append(s.decode(q, *one, at).clone())
+        torch.cuda.synchronize()
+        outs[-1] = s.out.clone()
+    assert torch.equal(*outs) and int(b.dev_err) == 0
+    same_caches(a, b)
+    if which == "side":
+        pos = dev_pos(at + 1)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            b.decode(q, *one, pos)
+        assert any(x is b.dws for x in b._held)
+        graph.replay()
+        torch.cuda.synchronize()
+        a.decode(q, *one, pos)
+        torch.cuda.synchronize()
+        assert torch.equal(a.out, b.out)
+        same_caches(a, b)
