@@ -1,113 +1,12 @@
 // C ABI of the position rotation and of the paged 8-bit caches: argument
 // checks, workspace carving and the launch sequence of each call.
-#include "fg_abi_util.h"
-#include "fg_paged.cuh"
+#include "fg_abi_paged_util.h"
 
 static_assert(fg::kPageRows % fg::kBlockRows == 0, "pages are whole blocks");
 
 namespace {
 
 constexpr int kMaxAppend = 1 << 20;
-
-// rope may be null (no rotation).
-fg_status check_rope(const fg_rope* r, int d, fg::RopeArgs* out) {
-  out->turns = nullptr;
-  out->rot = 0;
-  out->style = FG_ROPE_INTERLEAVED;
-  if (!r) return FG_OK;
-  if (!r->turns || !aligned(r->turns, 8)) return FG_EINVAL;
-  if (r->rot_dim < 16 || r->rot_dim > d || r->rot_dim % 16 != 0) return FG_EINVAL;
-  if (r->style != FG_ROPE_INTERLEAVED && r->style != FG_ROPE_HALF) return FG_EINVAL;
-  out->turns = (const unsigned long long*)r->turns;
-  out->rot = r->rot_dim;
-  out->style = r->style;
-  return FG_OK;
-}
-
-// sched: [totals: 256 bytes][ranges int4 x Gkv][items][first items of the thread blocks]
-size_t sched_ranges_bytes(int Gkv) { return align_up((size_t)Gkv * sizeof(int4)); }
-size_t sched_items_bytes(long long work) { return align_up((size_t)work * sizeof(fg::PagedItem)); }
-
-// Work items a table of table_len entries can need: items of kItemPages
-// pages, one that a cache leaves over, one that the cut of a length adds.
-long long sched_max_work(int Gkv, int32_t table_len) {
-  return (long long)table_len / fg::kItemPages + 2LL * Gkv + 1;
-}
-
-struct Sched {
-  long long* totals;
-  int4* ranges;
-  fg::PagedItem* items;
-  int32_t* cta_first;
-};
-Sched sched_parts(const fg_params* p, const fg_paged_cache* c) {
-  char* s = (char*)c->sched;
-  Sched o;
-  o.totals = (long long*)s;
-  o.ranges = (int4*)(s + kAlign);
-  s += kAlign + sched_ranges_bytes(kv_count(p));
-  o.items = (fg::PagedItem*)s;
-  o.cta_first = (int32_t*)(s + sched_items_bytes(sched_max_work(kv_count(p), c->table_len)));
-  return o;
-}
-
-fg_status check_sched(const fg_params* p, const fg_paged_cache* c) {
-  if (!c->sched || !aligned(c->sched, kAlign)) return FG_EINVAL;
-  const size_t need = fastgen_paged_sched_bytes(p, c->table_len);
-  if (need == 0) return FG_EINVAL;
-  if (c->sched_bytes < 0 || (size_t)c->sched_bytes < need) return FG_EWORKSPACE;
-  return FG_OK;
-}
-
-// What every call needs of the table and the descriptors.
-fg_status check_layout(const fg_paged_cache* c) {
-  if (!c || !c->page_table || !c->caches || !c->rows || c->table_len < 1) return FG_EINVAL;
-  if (!aligned(c->page_table, 4) || !aligned(c->caches, 8) || !aligned(c->rows, 4))
-    return FG_EINVAL;
-  return FG_OK;
-}
-
-fg_status check_pages(const fg_paged_cache* c) {
-  fg_status st = check_layout(c);
-  if (st != FG_OK) return st;
-  if (!c->k_pages || !c->v_pages || !c->exps || !c->pos || c->n_pages < 1) return FG_EINVAL;
-  if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16) || !aligned(c->exps, 8) ||
-      !aligned(c->pos, 16))
-    return FG_EINVAL;
-  return FG_OK;
-}
-
-fg::PagedArgs paged_args(const fg_params* p, const fg_paged_cache* c, int32_t* dev_err) {
-  fg::PagedArgs a;
-  a.kp = (uint8_t*)c->k_pages;
-  a.vp = (uint8_t*)c->v_pages;
-  a.exps = c->exps;
-  a.pos = c->pos;
-  a.table = c->page_table;
-  a.caches = c->caches;
-  a.rows = c->rows;
-  a.rows_out = c->rows_out ? c->rows_out : c->rows;
-  a.next_page = c->next_page;
-  if (c->sched) {
-    const Sched o = sched_parts(p, c);
-    a.ranges = o.ranges;
-    a.items = o.items;
-    a.cta_first = o.cta_first;
-    a.totals = o.totals;
-  } else {
-    a.ranges = nullptr;
-    a.items = nullptr;
-    a.cta_first = nullptr;
-    a.totals = nullptr;
-  }
-  a.n_pages = c->n_pages;
-  a.table_len = c->table_len;
-  a.n_work = c->n_work;
-  a.n_ctas = c->n_ctas;
-  a.max_w = ratio_count(p->r_l, p->n);
-  a.dev_err = dev_err;
-  return a;
-}
 
 // Work list of the current rows, read back (synchronous).  totals_read gets
 // the first three totals when it is not null.
@@ -217,6 +116,47 @@ fg_status fastgen_paged_plan(const fg_params* p, const int8_t* policy, const uin
   return FG_OK;
 }
 
+int32_t fastgen_paged_fork_table_len(const fg_params* p, int32_t max_new_tokens) {
+  if (check_params(p) != FG_OK || max_new_tokens < 0 ||
+      max_new_tokens > 0x7fffffff - fg::kPageRows)
+    return 0;
+  const long long w = ratio_count(p->r_l, p->n);
+  const long long seg = (max_new_tokens + fg::kPageRows - 1) / fg::kPageRows;
+  const long long len =
+      ((seg > 0 ? seg : 1) + (w + fg::kPageRows - 1) / fg::kPageRows) * kv_count(p);
+  return len > 0x7fffffffLL - fg::kPageRows ? 0 : (int32_t)len;
+}
+
+fg_status fastgen_paged_fork(const fg_params* p, const fg_paged_cache* prefix,
+                             int32_t max_new_tokens, fg_paged_cache* cache, fg_paged_info* info,
+                             void* stream) {
+  fg_status st = check_params(p);
+  if (st != FG_OK) return st;
+  if (!prefix || !prefix->caches || !aligned(prefix->caches, 8) || !info || max_new_tokens < 0)
+    return FG_EINVAL;
+  if ((st = check_layout(cache)) != FG_OK) return st;
+  if (!cache->next_page || !aligned(cache->next_page, 4)) return FG_EINVAL;
+  const int32_t need = fastgen_paged_fork_table_len(p, max_new_tokens);
+  if (need == 0) return FG_EINVAL;
+  if (cache->table_len < need) return FG_EWORKSPACE;
+  if ((st = check_sched(p, cache)) != FG_OK) return st;
+  const fg::ProfileDims pd = dims(p);
+  cudaStream_t s = (cudaStream_t)stream;
+  const Sched o = sched_parts(p, cache);
+  int2* cinfo = (int2*)o.ranges;  // the ranges' place: read before they are written
+  cudaError_t e = fg::launch_fork(pd, prefix->caches, cinfo, s);
+  if (e == cudaSuccess)
+    e = fg::launch_paged_plan(pd.Gkv, pd.w, max_new_tokens, cinfo, cache->caches, cache->rows,
+                              cache->page_table, cache->next_page, o.totals, s);
+  if (e != cudaSuccess) return FG_ECUDA;
+  long long totals[3];
+  if ((st = schedule(p, cache, totals, s)) != FG_OK) return st == FG_EINVAL ? FG_ECUDA : st;
+  info->pages = (int32_t)totals[0];
+  info->max_pages = (int32_t)totals[1];
+  info->table_used = (int32_t)totals[2];
+  return FG_OK;
+}
+
 fg_status fastgen_paged_schedule(const fg_params* p, fg_paged_cache* cache, void* stream) {
   fg_status st = check_params(p);
   if (st != FG_OK) return st;
@@ -311,10 +251,7 @@ fg_status fastgen_decode_attn_q8(const fg_params* p, const fg_paged_cache* cache
       !aligned(v_new, 16) || !aligned(out, 16) || !aligned(new_ids, 4) || !aligned(pos, 4) ||
       !aligned(workspace, kAlign) || !aligned(dev_err, 4))
     return FG_EINVAL;
-  // a work list is there: one item a cache at least, no thread block without one
-  if (cache->n_work < kv_count(p) || cache->n_work > sched_max_work(kv_count(p), cache->table_len) ||
-      cache->n_ctas < 1 || cache->n_ctas > cache->n_work)
-    return FG_EINVAL;
+  if (!has_list(p, cache)) return FG_EINVAL;
   fg::PagedDecodeArgs n;
   if ((st = check_rope(rope, p->d, &n.rope)) != FG_OK) return st;
   if (workspace_bytes < fastgen_decode_q8_workspace_bytes(p, cache)) return FG_EWORKSPACE;
@@ -330,6 +267,7 @@ fg_status fastgen_decode_attn_q8(const fg_params* p, const fg_paged_cache* cache
   n.np = n_punct;
   n.out = out;
   char* ws = (char*)workspace;
+  n.row_sc = n.row_w = n.head_ml = nullptr;
   n.part_ml = (float*)ws;
   n.part_acc = (float*)(ws + align_up((size_t)cache->n_work * pd.R * 2 * sizeof(float)));
   return cuda_status(fg::launch_decode_q8(pd, paged_args(p, cache, dev_err), n,

@@ -419,6 +419,38 @@ struct PagedDecodeArgs {
   void* out;
   float* part_ml;
   float* part_acc;
+  // steps that keep the rows' weights: this step's scores [n_pages x kPageRows, R] (base 2), and
+  // the weights so far [n_pages x kPageRows]
+  float* row_sc;
+  float* row_w;
+  float* head_ml;  // [G, 2]: each query's maximum and sum
+};
+
+// What the shared caches of a batch give a step's combine: partial results of every query.
+struct PrefixParts {
+  int parts;         // of each cache (0: no shared caches)
+  int caches, nq;    // shared caches; queries of each: sequences x group size
+  const float* ml;   // [caches, parts, nq, 2]
+  const float* acc;  // [caches, parts, nq, d]
+};
+
+struct EvictArgs {
+  float* scores;
+  const int32_t* pos;  // [B]
+  int budget, recent;
+  // workspace
+  int32_t* moves;  // [Gkv] rows that move
+  int32_t* src;    // [Gkv, budget] the row that comes to this place, -1: none
+};
+
+struct ScoreArgs {
+  float* scores;
+  const float* colsum;  // [G, m]; null: zeros
+  const int32_t* ids;   // [B, m]
+  const int32_t* n_new; // [B]; null: m
+  const int32_t* pos;   // [B]; null: 0
+  const int32_t* special;
+  int ns, m;
 };
 
 cudaError_t launch_rope(const ProfileDims& pd, const void* Q, const void* K, const int32_t* pos,
@@ -441,6 +473,22 @@ cudaError_t launch_append_q8(const ProfileDims& pd, const PagedArgs& a, const Ap
                              cudaStream_t s);
 cudaError_t launch_decode_q8(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
                              cudaStream_t s);
+// One step with shared caches (px.nq > 0; `pre` their pages) and / or weights (n.row_w).
+cudaError_t launch_step_q8(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
+                           const PagedArgs& pre, const PrefixParts& px, cudaStream_t s);
+cudaError_t launch_prefix(const ProfileDims& pd, const PagedDecodeArgs& n, const PagedArgs& pre,
+                          const PrefixParts& px, cudaStream_t s);
+// Partial results of each shared cache.
+int prefix_parts(const ProfileDims& pd, int sms);
+// Policies of B sequences' caches behind shared ones, without rows: cinfo [Gkv].
+cudaError_t launch_fork(const ProfileDims& pd, const fg_paged_desc* prefix, int2* cinfo,
+                        cudaStream_t s);
+cudaError_t launch_paged_clear(const ProfileDims& pd, const PagedArgs& a, int32_t* rows,
+                               cudaStream_t s);
+cudaError_t launch_scores_q8(const ProfileDims& pd, const PagedArgs& a, const ScoreArgs& n,
+                             cudaStream_t s);
+cudaError_t launch_evict_q8(const ProfileDims& pd, const PagedArgs& a, const EvictArgs& n,
+                            cudaStream_t s);
 // Thread blocks of the decode kernel that a wave counts on.
 int q8_slots(const ProfileDims& pd, int sms);
 

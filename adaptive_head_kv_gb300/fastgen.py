@@ -27,7 +27,8 @@ FG_PAGE_ROWS, FG_BLOCK_ROWS = 64, 16
 # kernels launched by one call of each entry point (counted in the bench)
 LAUNCHES = {"profile": 4, "profile_attn": 5, "profile_with_policy": 5, "plan": 3, "compact": 1,
             "decode": 2, "decode_acc": 3, "refresh": 1, "refresh_init": 1, "rope": 1, "paged_plan": 5,
-            "paged_schedule": 2, "compact_q8": 1, "append_q8": 2, "decode_q8": 2}
+            "paged_schedule": 2, "compact_q8": 1, "append_q8": 2, "decode_q8": 2,
+            "decode_q8_ex": 4, "paged_fork": 5, "paged_clear": 1, "scores_q8": 1, "evict_q8": 2}
 
 EXPORTS = (
     "fastgen_status_string", "fastgen_version", "fastgen_profile_workspace_bytes",
@@ -39,6 +40,9 @@ EXPORTS = (
     "fastgen_rope", "fastgen_paged_table_len", "fastgen_paged_sched_bytes", "fastgen_paged_plan",
     "fastgen_paged_schedule", "fastgen_compact_q8", "fastgen_append_q8_workspace_bytes",
     "fastgen_append_q8", "fastgen_decode_q8_workspace_bytes", "fastgen_decode_attn_q8",
+    "fastgen_decode_q8_ex_workspace_bytes", "fastgen_decode_attn_q8_ex",
+    "fastgen_paged_fork_table_len", "fastgen_paged_fork", "fastgen_paged_clear",
+    "fastgen_scores_q8", "fastgen_evict_q8_workspace_bytes", "fastgen_evict_q8",
 )
 
 # size of the library-held scratch array used by fastgen_decode_attn_noalloc
@@ -150,6 +154,15 @@ _SIGS = {
     "fastgen_decode_q8_workspace_bytes": (_SZ, [_PP, _CP]),
     "fastgen_decode_attn_q8": (ctypes.c_int, [_PP, _CP, _P, _P, _P, _P, _P, _I32, _P, _I32, _P,
                                               _RP, _P, _P, _SZ, _P, _P]),
+    "fastgen_decode_q8_ex_workspace_bytes": (_SZ, [_PP, _CP, _CP, _I32]),
+    "fastgen_decode_attn_q8_ex": (ctypes.c_int, [_PP, _CP, _CP, _P, _P, _P, _P, _P, _P, _I32, _P,
+                                                 _I32, _P, _RP, _P, _P, _SZ, _P, _P]),
+    "fastgen_paged_fork_table_len": (_I32, [_PP, _I32]),
+    "fastgen_paged_fork": (ctypes.c_int, [_PP, _CP, _I32, _CP, ctypes.POINTER(PagedInfo), _P]),
+    "fastgen_paged_clear": (ctypes.c_int, [_PP, _CP, _P, _P]),
+    "fastgen_scores_q8": (ctypes.c_int, [_PP, _CP, _P, _P, _P, _I32, _P, _P, _P, _I32, _P, _P]),
+    "fastgen_evict_q8_workspace_bytes": (_SZ, [_PP, _I32]),
+    "fastgen_evict_q8": (ctypes.c_int, [_PP, _CP, _P, _I32, _I32, _P, _P, _SZ, _P, _P]),
 }
 
 
@@ -611,5 +624,101 @@ def fastgen_decode_attn_q8(params, cache, q, k_new, v_new, new_ids, special_ids,
          None if new_ids is None else _is(new_ids, w, "new_ids", i32, z.B, dev), special,
          n_special, punct, n_punct, _is(pos, w, "pos", i32, z.B, dev), _rope(rope, w, dev),
          _is(out, w, "out", z.dt, z.queries, dev),
+         _is(workspace, w, "workspace", torch.uint8, ws, dev), ws,
+         _is(dev_err, w, "dev_err", i32, 1, dev))
+
+
+# ------------------- steps behind a shared prompt, and caches within a budget
+def _prefix(p: Params, prefix, z, dev: int, w: str):
+    """The struct of shared caches: those of one sequence with the batch's layers and heads."""
+    if prefix is None:
+        return None
+    s = prefix.sizes
+    if s.B != 1 or s.Gkv * z.B != z.Gkv or prefix.d != z.d:
+        _refuse(w, "the prefix must hold the caches of one sequence of the same layers and heads")
+    if prefix.dev != dev:
+        _refuse(w, f"the prefix must be on device {dev}")
+    return prefix.c
+
+
+def _scores(x, cache, w: str, dev: int):
+    return _is(x, w, "scores", _T.float32, cache.c.n_pages * FG_PAGE_ROWS, dev)
+
+
+def fastgen_decode_q8_ex_workspace_bytes(params, cache, prefix=None, scores: bool = False) -> int:
+    return lib().fastgen_decode_q8_ex_workspace_bytes(
+        params, cache.c, None if prefix is None else prefix.c, int(bool(scores)))
+
+
+def fastgen_decode_attn_q8_ex(params, cache, prefix, scores, q, k_new, v_new, new_ids, special_ids,
+                              punct_ids, pos, rope, out, workspace, dev_err, stream=None) -> None:
+    """fastgen_decode_attn_q8 with shared caches (prefix: the PagedCache of one sequence, or
+    None) and the rows' weights (scores [n_pages, 64] float32, or None)."""
+    w, torch = "fastgen_decode_attn_q8_ex", _torch()
+    z, dev, i32, ws = _of_cache(params, cache, w), cache.dev, torch.int32, workspace.numel()
+    special, n_special = _id_set(special_ids, w, "special_ids", dev)
+    punct, n_punct = _id_set(punct_ids, w, "punct_ids", dev)
+    _run(w, dev, stream, lib().fastgen_decode_attn_q8_ex, params, cache.c,
+         _prefix(params, prefix, z, dev, w),
+         None if scores is None else _scores(scores, cache, w, dev),
+         _is(q, w, "q", z.dt, z.queries, dev),
+         None if k_new is None else _is(k_new, w, "k_new", z.dt, z.rows, dev),
+         None if v_new is None else _is(v_new, w, "v_new", z.dt, z.rows, dev),
+         None if new_ids is None else _is(new_ids, w, "new_ids", i32, z.B, dev), special,
+         n_special, punct, n_punct, _is(pos, w, "pos", i32, z.B, dev), _rope(rope, w, dev),
+         _is(out, w, "out", z.dt, z.queries, dev),
+         _is(workspace, w, "workspace", torch.uint8, ws, dev), ws,
+         _is(dev_err, w, "dev_err", i32, 1, dev))
+
+
+def fastgen_paged_fork_table_len(params, max_new_tokens: int) -> int:
+    return lib().fastgen_paged_fork_table_len(params, max_new_tokens)
+
+
+def fastgen_paged_fork(params, prefix, max_new_tokens, cache, stream=None) -> PagedInfo:
+    w, torch = "fastgen_paged_fork", _torch()
+    z, dev, info = _of_cache(params, cache, w), cache.dev, PagedInfo()
+    if prefix is None:
+        _refuse(w, "no prefix")
+    _run(w, dev, stream, lib().fastgen_paged_fork, params, _prefix(params, prefix, z, dev, w),
+         max_new_tokens, cache.c, info)
+    return info
+
+
+def fastgen_paged_clear(params, cache, dev_err, stream=None) -> None:
+    w, torch = "fastgen_paged_clear", _torch()
+    _of_cache(params, cache, w)
+    _run(w, cache.dev, stream, lib().fastgen_paged_clear, params, cache.c,
+         _is(dev_err, w, "dev_err", torch.int32, 1, cache.dev))
+
+
+def fastgen_scores_q8(params, cache, scores, colsum, ids, n_new, pos, special_ids, dev_err,
+                      stream=None) -> None:
+    """Scores that the rows of tokens ids [B, m] at pos [B] (None: 0) start with: colsum [G, m]
+    summed over the group (None: 0), +inf for special tokens."""
+    w, torch = "fastgen_scores_q8", _torch()
+    z, dev, i32 = _of_cache(params, cache, w), cache.dev, torch.int32
+    m = ids.numel() // z.B
+    special, n_special = _id_set(special_ids, w, "special_ids", dev)
+    _run(w, dev, stream, lib().fastgen_scores_q8, params, cache.c, _scores(scores, cache, w, dev),
+         None if colsum is None else _is(colsum, w, "colsum", torch.float32, z.G * m, dev),
+         _is(ids, w, "ids", i32, z.B * m, dev), m,
+         None if n_new is None else _is(n_new, w, "n_new", i32, z.B, dev),
+         None if pos is None else _is(pos, w, "pos", i32, z.B, dev), special, n_special,
+         _is(dev_err, w, "dev_err", i32, 1, dev))
+
+
+def fastgen_evict_q8_workspace_bytes(params, budget: int) -> int:
+    return lib().fastgen_evict_q8_workspace_bytes(params, budget)
+
+
+def fastgen_evict_q8(params, cache, scores, budget, recent, pos, workspace, dev_err,
+                     stream=None) -> None:
+    """Cuts segments of more than `budget` rows: the rows of the newest `recent` positions up to
+    pos [B] stay, then those of the largest scores."""
+    w, torch = "fastgen_evict_q8", _torch()
+    z, dev, i32, ws = _of_cache(params, cache, w), cache.dev, torch.int32, workspace.numel()
+    _run(w, dev, stream, lib().fastgen_evict_q8, params, cache.c, _scores(scores, cache, w, dev),
+         budget, recent, _is(pos, w, "pos", i32, z.B, dev),
          _is(workspace, w, "workspace", torch.uint8, ws, dev), ws,
          _is(dev_err, w, "dev_err", i32, 1, dev))

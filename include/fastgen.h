@@ -601,6 +601,87 @@ fg_status fastgen_decode_attn_q8(const fg_params* p, const fg_paged_cache* cache
                                  const fg_rope* rope, void* out, void* workspace,
                                  size_t workspace_bytes, int32_t* dev_err, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Steps of sequences that continue one prompt, and caches within a budget.
+ *
+ * fastgen_decode_attn_q8_ex is fastgen_decode_attn_q8 with two options.
+ *
+ * prefix (NULL: none): caches that every sequence of the batch shares, L * Hkv of them, laid
+ * out and filled for a batch of one sequence (fastgen_paged_plan and fastgen_compact_q8 with
+ * B = 1; p gives their n and r_l).  Query head g of sequence b attends over the rows of cache
+ * (l, h / R) of the prefix and of its own cache together, in one softmax; ring rows of either
+ * count while their position is in (pos[b] - w, pos[b]].  So a step gives what it would give if
+ * each sequence had the prefix's rows in a cache of its own; they are read once for all of them,
+ * and never written.  Of the prefix's fields rows_out, next_page and the work list are not used.
+ *   In the products with the prefix's rows queries and weights have 11 bits in bf16 and 22 in
+ * fp32.  A NaN among the values of a ring row makes the whole outputs of the queries that see the
+ * row NaN; the others are untouched.
+ *
+ * scores (NULL: none) [n_pages, FG_PAGE_ROWS] float: what each row of the never-evicted segments
+ * has received so far.  A row that the step appends starts at 0, or at +inf when its token is
+ * one of special_ids (+inf: never dropped); then every segment row of an active sequence gets the
+ * sum, over the query heads of its group, of the weights that the step's softmax gives it.
+ *   Other rows' entries stay.  32-bit sums in a fixed order.
+ *
+ * Arguments, errors and limits else as fastgen_decode_attn_q8; another workspace size.  A work
+ * list is needed for `cache` alone. */
+size_t fastgen_decode_q8_ex_workspace_bytes(const fg_params* p, const fg_paged_cache* cache,
+                                            const fg_paged_cache* prefix, int32_t scores);
+
+fg_status fastgen_decode_attn_q8_ex(const fg_params* p, const fg_paged_cache* cache,
+                                    const fg_paged_cache* prefix, float* scores, const void* q,
+                                    const void* k_new, const void* v_new, const int32_t* new_ids,
+                                    const int32_t* special_ids, int32_t n_special,
+                                    const int32_t* punct_ids, int32_t n_punct, const int32_t* pos,
+                                    const fg_rope* rope, void* out, void* workspace,
+                                    size_t workspace_bytes, int32_t* dev_err, void* stream);
+
+/* Layout of the sequences' own caches behind a prefix: for each of the B sequences of p a cache
+ * of the policy of every prefix cache, without rows, that may grow by max_new_tokens.  Writes
+ * what fastgen_paged_plan writes; needs table_len >= fastgen_paged_fork_table_len (0: parameters
+ * rejected, or past 2^31 - 1).  Of the prefix only the descriptors are read.  Before the first
+ * step fastgen_paged_clear has to empty the rings.  SYNCHRONOUS on `stream`.
+ * fastgen_paged_clear empties caches whose pages are there: no rows (rows and rows_out), and ring
+ * slots without a position.  Pages that a segment has taken stay with it.  Asynchronous; a ring
+ * page that is missing ORs 4 into *dev_err.
+ * Errors: FG_EINVAL, FG_EDTYPE, FG_EWORKSPACE. */
+int32_t fastgen_paged_fork_table_len(const fg_params* p, int32_t max_new_tokens);
+
+fg_status fastgen_paged_fork(const fg_params* p, const fg_paged_cache* prefix,
+                             int32_t max_new_tokens, fg_paged_cache* cache, fg_paged_info* info,
+                             void* stream);
+
+fg_status fastgen_paged_clear(const fg_params* p, const fg_paged_cache* cache, int32_t* dev_err,
+                              void* stream);
+
+/* Scores that rows start with, for rows that no step appended: those of the prompt, or of tokens
+ * that fastgen_append_q8 appended.  ids [B, m] are the tokens at positions pos[b], pos[b] + 1, ...
+ * (pos NULL: from 0; n_new[b] of them, NULL: m; a sequence with pos[b] < 0 is left out).  A
+ * segment row whose position is among them gets +inf if its token is one of special_ids, else the
+ * sum of colsum [G, m] over its group's query heads (fastgen_profile's output for a prompt), 0 with
+ * colsum NULL.  Asynchronous.  Errors: FG_EINVAL, FG_EDTYPE. */
+fg_status fastgen_scores_q8(const fg_params* p, const fg_paged_cache* cache, float* scores,
+                            const float* colsum, const int32_t* ids, int32_t m,
+                            const int32_t* n_new, const int32_t* pos, const int32_t* special_ids,
+                            int32_t n_special, int32_t* dev_err, void* stream);
+
+/* Cuts never-evicted segments of more than `budget` rows to `budget` rows.  The rows that stay
+ * are the first of this order: rows of positions in (pos[b] - recent, pos[b]]; then by larger score
+ * (+inf first; NaN and negative scores count as 0); ties to the lower row.  Rows that stay and lie
+ * below row `budget` are not moved; the others come, in row order, to the places of the dropped
+ * rows below it, with their positions and scores, and are coded again at the exponents of the
+ * blocks they come to (which grow where they have to).  Nothing else changes: shorter segments,
+ * rings, sequences with pos[b] < 0 (pos [B]: the newest position), pages behind the budget, which
+ * the segment keeps for its next rows.  rows_out gets the counts.  The work list stays valid.
+ * budget: a multiple of FG_BLOCK_ROWS, >= 1; recent: 0 .. budget.  The workspace (256-byte
+ * aligned) holds nothing between calls.  Asynchronous.
+ * Errors: FG_EINVAL, FG_EDTYPE, FG_EWORKSPACE; bad pages as above. */
+size_t fastgen_evict_q8_workspace_bytes(const fg_params* p, int32_t budget);
+
+fg_status fastgen_evict_q8(const fg_params* p, const fg_paged_cache* cache, float* scores,
+                           int32_t budget, int32_t recent, const int32_t* pos, void* workspace,
+                           size_t workspace_bytes, int32_t* dev_err, void* stream);
+
 /* Synchronously reads a device flag written by fastgen_profile,
  * fastgen_profile_with_policy, fastgen_decode_attn or a paged call and maps it to a status
  * (FG_OK, FG_ECAPACITY, FG_EINVAL for an out-of-range saved policy or a bad
