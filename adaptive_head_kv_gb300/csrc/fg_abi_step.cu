@@ -4,38 +4,29 @@
 
 namespace {
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return sms;
-}
-
 // [own partial results: (maximum, sum), outputs][scores of the pool's rows][(maximum, sum) of the
-// heads][partial results of the shared caches: (maximum, sum), outputs]
+// heads][shared caches: tile counts, queries, their factors, partial results]
 struct StepParts {
-  size_t ml, acc, sc, head, pml, pacc, total;
-  int parts;
+  size_t ml, acc, sc, head, px[5], total;
+  fg::PrefixParts prefix;
 };
 StepParts step_parts(const fg_params* p, const fg_paged_cache* c, bool prefix, bool scores) {
   const fg::ProfileDims pd = dims(p);
   const size_t nw = (size_t)c->n_work * pd.R;
   StepParts o;
-  o.parts = prefix ? fg::prefix_parts(pd, sm_count()) : 0;
-  const size_t np = (size_t)pd.HLkv * o.parts * pd.B * pd.R;
-  size_t at = 0;
-  const auto put = [&](size_t floats) {
+  size_t at = 0, bytes[5] = {0, 0, 0, 0, 0};
+  o.prefix = fg::PrefixParts{};
+  if (prefix) o.prefix = fg::prefix_parts(pd, bytes);
+  const auto put = [&](size_t size) {
     const size_t was = at;
-    at += align_up(floats * sizeof(float));
+    at += align_up(size);
     return was;
   };
-  o.ml = put(nw * 2);
-  o.acc = put(nw * pd.d);
-  o.sc = put(scores ? (size_t)c->n_pages * fg::kPageRows * pd.R : 0);
-  o.head = put(scores ? (size_t)pd.G * 2 : 0);
-  o.pml = put(np * 2);
-  o.pacc = put(np * pd.d);
+  o.ml = put(nw * 2 * sizeof(float));
+  o.acc = put(nw * pd.d * sizeof(float));
+  o.sc = put(scores ? (size_t)c->n_pages * fg::kPageRows * pd.R * sizeof(float) : 0);
+  o.head = put(scores ? (size_t)pd.G * 2 * sizeof(float) : 0);
+  for (int i = 0; i < 5; ++i) o.px[i] = put(bytes[i]);
   o.total = at;
   return o;
 }
@@ -104,14 +95,14 @@ fg_status fastgen_decode_attn_q8_ex(const fg_params* p, const fg_paged_cache* ca
   n.row_w = scores;
   n.row_sc = scores ? (float*)(ws + o.sc) : nullptr;
   n.head_ml = scores ? (float*)(ws + o.head) : nullptr;
-  fg::PrefixParts px = {};
+  fg::PrefixParts px = o.prefix;
   fg::PagedArgs pre = {};
   if (prefix) {
-    px.parts = o.parts;
-    px.caches = pd.HLkv;
-    px.nq = pd.B * pd.R;
-    px.ml = (const float*)(ws + o.pml);
-    px.acc = (const float*)(ws + o.pacc);
+    px.cum = (long long*)(ws + o.px[0]);
+    px.q = (uint8_t*)(ws + o.px[1]);
+    px.qf = (float*)(ws + o.px[2]);
+    px.ml = (float*)(ws + o.px[3]);
+    px.acc = (float*)(ws + o.px[4]);
     fg_paged_cache c = *prefix;
     c.sched = nullptr;
     pre = paged_args(p, &c, dev_err);

@@ -426,13 +426,43 @@ struct PagedDecodeArgs {
   float* head_ml;  // [G, 2]: each query's maximum and sum
 };
 
-// What the shared caches of a batch give a step's combine: partial results of every query.
+// The shared caches of a batch (fg_prefix.cu): how the work on them is cut, and what it leaves
+// for a step's combine.
+//
+// The queries of a cache, sequence by sequence with R of each, are cut into tiles of
+// kPrefixTile; a group is the one or two tiles that a thread block takes at once, a unit a group
+// of a cache.  The units' key tiles lie end to end, unit after unit, and are cut into equal
+// ranges for the thread blocks.  Block i leaves partial results of unit u at part i + u, which no
+// other pair has: u does not fall while i grows.
+constexpr int kPrefixTile = 128;
+constexpr int kPrefixMaxCtas = 192;
+constexpr int kPrefixMinTiles = 1;  // of a thread block's range, where there are so many
 struct PrefixParts {
-  int parts;         // of each cache (0: no shared caches)
-  int caches, nq;    // shared caches; queries of each: sequences x group size
-  const float* ml;   // [caches, parts, nq, 2]
-  const float* acc;  // [caches, parts, nq, d]
+  int caches, nq;    // shared caches (0: none); queries of each: sequences x group size
+  int tiles, groups; // of the queries of a cache
+  int pair;          // groups of two tiles (a last one may be alone)
+  int rows;          // rows of a part: queries of a tile
+  int ctas;          // thread blocks
+  // workspace
+  long long* cum;  // [caches + 1] key tiles before each cache
+  uint8_t* q;    // [caches, tiles] tiles of f16 queries, as the tensor cores read them
+  float* qf;     // [caches, tiles x kPrefixTile] what the queries were divided by, times the scale
+  float* ml;     // [kPrefixMaxCtas + units, 2, rows, 2] maximum, sum
+  float* acc;    // [.., d] outputs
 };
+
+// The units' key tiles of thread block i: [first, last) of `total`.
+__host__ __device__ inline int prefix_ctas(long long total, int ctas) {
+  const long long n = (total + kPrefixMinTiles - 1) / kPrefixMinTiles;
+  return (int)(n < 1 ? 1 : n < ctas ? n : ctas);
+}
+__host__ __device__ inline long long prefix_first(long long total, int ctas, int i) {
+  return total * i / ctas;
+}
+// The thread block whose range holds x.
+__host__ __device__ inline int prefix_cta(long long total, int ctas, long long x) {
+  return (int)(((x + 1) * ctas - 1) / total);
+}
 
 struct EvictArgs {
   float* scores;
@@ -473,13 +503,13 @@ cudaError_t launch_append_q8(const ProfileDims& pd, const PagedArgs& a, const Ap
                              cudaStream_t s);
 cudaError_t launch_decode_q8(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
                              cudaStream_t s);
-// One step with shared caches (px.nq > 0; `pre` their pages) and / or weights (n.row_w).
+// One step with shared caches (px.caches > 0; `pre` their pages) and / or weights (n.row_w).
 cudaError_t launch_step_q8(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
                            const PagedArgs& pre, const PrefixParts& px, cudaStream_t s);
 cudaError_t launch_prefix(const ProfileDims& pd, const PagedDecodeArgs& n, const PagedArgs& pre,
                           const PrefixParts& px, cudaStream_t s);
-// Partial results of each shared cache.
-int prefix_parts(const ProfileDims& pd, int sms);
+// How the work of a batch is cut; bytes of cum, q, qf, ml and acc.
+PrefixParts prefix_parts(const ProfileDims& pd, size_t (&bytes)[5]);
 // Policies of B sequences' caches behind shared ones, without rows: cinfo [Gkv].
 cudaError_t launch_fork(const ProfileDims& pd, const fg_paged_desc* prefix, int2* cinfo,
                         cudaStream_t s);

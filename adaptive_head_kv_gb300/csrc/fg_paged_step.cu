@@ -38,8 +38,27 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     if (qi == 0 && lane == 0) a.rows_out[c] = had;
     return;
   }
-  const int total = range.y + px.parts;
-  const size_t pre0 = ((size_t)(c % HLkv) * px.parts) * px.nq + (size_t)b * R + qi;
+  // the shared cache's parts of this query: of every thread block that had tiles of its unit, one,
+  // or two where the block's two streams shared the unit's key tiles
+  int parts = 0, streams = 1;
+  size_t pre0 = 0;  // row of the first part
+  if (px.caches > 0) {
+    const int pc = c % HLkv, j = b * R + qi, tile = j / kPrefixTile;
+    const int grp = px.pair ? tile / 2 : tile;
+    const long long c0 = px.cum[pc], tiles = px.cum[pc + 1] - c0;
+    const long long all = px.cum[px.caches] * px.groups;
+    const bool both = px.pair && 2 * grp + 1 < px.tiles;
+    if (tiles > 0) {
+      const int ctas = prefix_ctas(all, px.ctas);
+      const long long x = c0 * px.groups + grp * tiles;
+      const int i0 = prefix_cta(all, ctas, x), i1 = prefix_cta(all, ctas, x + tiles - 1);
+      streams = both ? 1 : 2;
+      parts = (i1 - i0 + 1) * streams;
+      pre0 = (((size_t)i0 + (size_t)pc * px.groups + grp) * 2 + (both ? tile & 1 : 0)) * px.rows +
+             j % kPrefixTile;
+    }
+  }
+  const int total = range.y + parts;
   float M = kNoScore, L = 0.f, acc[PER];  // of the parts so far: maximum, sum, output
 #pragma unroll
   for (int k = 0; k < PER; ++k) acc[k] = 0.f;
@@ -49,7 +68,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     for (int j = 0; j < kAhead; ++j) {
       const int i = i0 + j;
       const bool own = i < range.y;
-      const size_t slot = own ? ((size_t)range.x + i) * R + qi : pre0 + (size_t)(i - range.y) * px.nq;
+      const size_t slot = own ? ((size_t)range.x + i) * R + qi
+                              : pre0 + (size_t)(i - range.y) * (2 / streams) * px.rows;
       const float2 ml = i < total
                             ? *reinterpret_cast<const float2*>((own ? n.part_ml : px.ml) + 2 * slot)
                             : make_float2(kNoScore, 0.f);
@@ -161,9 +181,14 @@ cudaError_t run_step(const ProfileDims& pd, const PagedArgs& a, const PagedDecod
 }  // namespace
 
 cudaError_t launch_step_q8(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
-                           const PagedArgs& pre, const PrefixParts& px, cudaStream_t s) {
-  if (px.nq > 0) {
-    const cudaError_t e = launch_prefix(pd, n, pre, px, s);
+                           const PagedArgs& pre, const PrefixParts& px0, cudaStream_t s) {
+  PrefixParts px = px0;
+  if (px.caches > 0) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    px.ctas = sms < kPrefixMaxCtas ? sms : kPrefixMaxCtas;
+    if (e == cudaSuccess) e = launch_prefix(pd, n, pre, px, s);
     if (e != cudaSuccess) return e;
   }
   if (pd.dtype == FG_FP32)
