@@ -38,8 +38,8 @@ constexpr int kUnpackWarps = 4, kSoftWarps = 8;
 constexpr int kLoadWarp = kSoftWarps + kUnpackWarps, kMmaWarp = kLoadWarp + 1;
 constexpr int kPrefixThreads = (kMmaWarp + 1) * 32;
 constexpr int kMetas = 4;     // key tiles whose description is there
-constexpr float kSlack = 4.f;
-constexpr float kProdBits = 11.f;  // weights enter the product times 2^11, at most 2^15
+constexpr float kSlack = 8.f;
+constexpr float kProdBits = 7.f;  // weights enter the product times 2^7, at most 2^15
 constexpr int kSmem = 227 * 1024;
 
 // A key tile: two pages of a segment or of a ring.
@@ -88,8 +88,9 @@ constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t s_col(int s) { return s * kTile; }
 __device__ __forceinline__ uint32_t o_col(int s) { return 2 * kTile + s * 128; }
 
-__device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
+// (out of line, like everything that a tile seldom needs: what the warps run for every tile has to
+// stay in the instruction cache together)
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort) {
   const uint64_t t0 = global_timer_ns();
   while (!*abort) {
 #pragma unroll 1
@@ -98,6 +99,9 @@ __device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, vol
     if (global_timer_ns() - t0 > kWaitLimitNs) *abort = 1;
   }
   return false;
+}
+__device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort);
 }
 // The same by a whole warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
@@ -170,20 +174,21 @@ __device__ __forceinline__ int2 key_tiles(const PagedArgs& a, const fg_paged_des
 }
 
 // ------------------------------------------------------------- before the products
-// A CTA a tile of queries: rotated, divided by the power of two that brings the largest value to
-// [2^13, 2^14), as f16 in the tensor cores' layout.  The last CTA counts the caches' key tiles.
+// A warp a query: rotated, divided by the power of two that brings its largest value to
+// [2^13, 2^14), as f16 in the tensor cores' layout.  (Rows of a tile without a query stay as they
+// are: no other row's result depends on them.)  The last CTA counts the caches' key tiles.
 constexpr int kPrepThreads = 256;
 
 template <typename T, int D, int kTerms>
 __global__ void __launch_bounds__(kPrepThreads)
-    prefix_prep_kernel(const PagedArgs a, const PagedDecodeArgs n, const PrefixParts px, int H,
-                       int R, int HL, float sl2) {
+    prefix_prep_kernel(const PagedArgs a, const PagedDecodeArgs n, const PrefixParts px, int G,
+                       int H, int R, int HL, float sl2) {
   constexpr int PER = D / 32;
   __shared__ long long scr[33];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   griddep_wait();
   griddep_launch_dependents();
-  if (blockIdx.x == px.caches * px.tiles) {
+  if (blockIdx.x == gridDim.x - 1) {
     long long sum = 0, tot;
     for (int base = 0; base < px.caches; base += kPrepThreads) {
       const int c = base + threadIdx.x;
@@ -203,53 +208,43 @@ __global__ void __launch_bounds__(kPrepThreads)
     if (threadIdx.x == 0) px.cum[px.caches] = sum;
     return;
   }
-  const int c = blockIdx.x / px.tiles, tile = blockIdx.x % px.tiles;
-  uint8_t* dst = px.q + (size_t)blockIdx.x * kTerms * kTile * D * 2;
-  float* qf = px.qf + (size_t)blockIdx.x * kTile;
-  float2 cs[PER];
-  int cs_of = -1;
-  for (int r = warp; r < kTile; r += kPrepThreads / 32) {
-    const int j = tile * kTile + r, b = j / R;
-    const int t = j < px.nq ? n.pos[b] : -1;
-    float x[PER];
-#pragma unroll
-    for (int k = 0; k < PER; ++k) x[k] = 0.f;
-    float f = 0.f, inv = 0.f;
-    if (t >= 0) {
-      const size_t g = (size_t)b * HL + (size_t)(c / (H / R)) * H + (size_t)(c % (H / R)) * R + j % R;
-      load_row<PER>((const T*)n.q + g * D, x);
-      if (n.rope.rot > 0) {
-        if (cs_of != b)
-          row_angles<PER>(cs, n.rope.rot, n.rope.style, [&](int p) {
-            float2 y;
-            rope_cos_sin((unsigned)t, n.rope.turns[p], y.x, y.y);
-            return y;
-          });
-        cs_of = b;
-        rotate_row<PER>(x, cs, n.rope.rot, n.rope.style);
-      }
-      uint32_t top = 0;
-#pragma unroll
-      for (int k = 0; k < PER; ++k) top = max(top, finite_bits(x[k]));
-      top = __reduce_max_sync(0xffffffffu, top);
-      const int eq = max(-110, (int)(top >> 23) - 127 - 13);
-      inv = pow2f(-eq);
-      f = pow2f(eq) * sl2;
-    }
-    const int e = lane * PER;
-    uint8_t* p = dst + e / 64 * (kTile * 128) + r * 128 + ((((e % 64) / 8) ^ (r & 7)) << 4) + e % 8 * 2;
-#pragma unroll
-    for (int k = 0; k < PER; k += 2) {
-      const float u = x[k] * inv, v = x[k + 1] * inv;
-      const uint32_t hi = pack_f16x2(u, v);
-      *reinterpret_cast<uint32_t*>(p + 2 * k) = hi;
-      if constexpr (kTerms == 2) {  // what f16 loses, down to 2^-38 of the largest value
-        const float2 z = unpack_f16x2(hi);
-        *reinterpret_cast<uint32_t*>(p + 2 * k + kTile * D * 2) = pack_f16x2(u - z.x, v - z.y);
-      }
-    }
-    if (lane == 0) qf[r] = f;
+  const int g = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
+  if (g >= G) return;
+  const int b = g / HL, c = kv_head(g % HL, H, R), j = b * R + g % H % R;
+  const int t = n.pos[b];
+  if (t < 0) return;
+  float x[PER];
+  load_row<PER>((const T*)n.q + (size_t)g * D, x);
+  if (n.rope.rot > 0) {
+    float2 cs[PER];
+    row_angles<PER>(cs, n.rope.rot, n.rope.style, [&](int p) {
+      float2 y;
+      rope_cos_sin((unsigned)t, n.rope.turns[p], y.x, y.y);
+      return y;
+    });
+    rotate_row<PER>(x, cs, n.rope.rot, n.rope.style);
   }
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) top = max(top, finite_bits(x[k]));
+  top = __reduce_max_sync(0xffffffffu, top);
+  const int eq = max(-110, (int)(top >> 23) - 127 - 13);
+  const float inv = pow2f(-eq);
+  const size_t tile = (size_t)c * px.tiles + j / kTile;
+  const int r = j % kTile, e = lane * PER;
+  uint8_t* p = px.q + tile * kTerms * kTile * D * 2 + e / 64 * (kTile * 128) + r * 128 +
+               ((((e % 64) / 8) ^ (r & 7)) << 4) + e % 8 * 2;
+#pragma unroll
+  for (int k = 0; k < PER; k += 2) {
+    const float u = x[k] * inv, v = x[k + 1] * inv;
+    const uint32_t hi = pack_f16x2(u, v);
+    *reinterpret_cast<uint32_t*>(p + 2 * k) = hi;
+    if constexpr (kTerms == 2) {  // what f16 loses, down to 2^-38 of the largest value
+      const float2 z = unpack_f16x2(hi);
+      *reinterpret_cast<uint32_t*>(p + 2 * k + kTile * D * 2) = pack_f16x2(u - z.x, v - z.y);
+    }
+  }
+  if (lane == 0) px.qf[tile * kTile + r] = pow2f(eq) * sl2;
 }
 
 // ------------------------------------------------------------------- the products
@@ -342,18 +337,20 @@ __device__ __forceinline__ void load_pages(Smem<D, kTerms, kPair>& s, const Page
               bulk_load(m.pos + g * kPageRows, a.pos + (size_t)page[g] * kPageRows, kPageRows * 4,
                         &s.meta_full[ms]);
         }
+#pragma unroll 1
         for (int z = 0; z < 2 * kTilePages && !stop; ++z) {
-          const int seq = 2 * kTilePages * k + z, slot = seq % P::kPieces, g = z % kTilePages;
+          const int seq = 2 * kTilePages * k + z, slot = seq % P::kPieces;
+          const int at = z % kTilePages ? page[1] : page[0];
           if (seq >= P::kPieces &&
               !wait_or_stop(&s.raw_empty[slot], (seq / P::kPieces - 1) & 1, abort)) {
             stop = true;
-          } else if (page[g] < 0) {
+          } else if (at < 0) {
             mbar_arrive(&s.raw_full[slot]);
             ++pieces;
           } else {
             ++pieces;
             mbar_expect_tx(&s.raw_full[slot], P::kPiece);
-            bulk_load(s.raw[slot], (z < kTilePages ? a.kp : a.vp) + (size_t)page[g] * P::kPiece,
+            bulk_load(s.raw[slot], (z < kTilePages ? a.kp : a.vp) + (size_t)at * P::kPiece,
                       P::kPiece, &s.raw_full[slot]);
           }
         }
@@ -380,6 +377,11 @@ __device__ __forceinline__ void widen(Smem<D, kTerms, kPair>& s, int uw, int tot
   constexpr int kIter = kBlockRows * (D / 16) / 32;  // 16-byte pieces of a lane
   const int lane = threadIdx.x & 31, lr = lane & 7;
   volatile int* abort = &s.abort;
+  auto row_of = [&](int i) { return lr + (i & 1) * 8; };
+  auto piece_of = [&](int i) {
+    return D == 128 ? ((lane >> 3) + 4 * (i >> 1) + lr) & 7
+                    : (((((lr >> 2) ^ (lr >> 1)) & 1) << 1 | (lr >> 2)) ^ (lane >> 3)) & 3;
+  };
   for (int k = 0; k < total; ++k) {
     const int ms = k % kMetas;
     if (!warp_wait(&s.meta_full[ms], k / kMetas & 1, abort)) return;
@@ -402,6 +404,7 @@ __device__ __forceinline__ void widen(Smem<D, kTerms, kPair>& s, int uw, int tot
         if (!warp_wait(&s.raw_full[seq % P::kPieces], seq / P::kPieces & 1, abort)) return;
         const uint8_t* v = s.raw[seq % P::kPieces] + uw * kBlockRows * D;
         if (m.cnt[g] > 0)
+#pragma unroll 1
           for (int r = 0; r < kBlockRows; r += 8) {
             bool nan = false;
 #pragma unroll
@@ -417,44 +420,54 @@ __device__ __forceinline__ void widen(Smem<D, kTerms, kPair>& s, int uw, int tot
           }
       }
     }
-#pragma unroll
+#pragma unroll 1
     for (int side = 0; side < 2; ++side) {
       const int oseq = 2 * k + side, slot = oseq % P::kOperands;
       if (oseq >= P::kOperands && !warp_wait(&s.op_empty[slot], (oseq / P::kOperands - 1) & 1, abort))
         return;
-#pragma unroll
+#pragma unroll 1
       for (int g = 0; g < kTilePages; ++g) {
+        const uint32_t here = g ? there[1] : there[0], bad_rows = g ? poison[1] : poison[0];
         const int seq = 2 * kTilePages * k + side * kTilePages + g, raw = seq % P::kPieces;
         if (!warp_wait(&s.raw_full[raw], seq / P::kPieces & 1, abort)) return;
         const uint8_t* src = s.raw[raw] + uw * kBlockRows * D;
         uint8_t* dst = s.op[slot] + (g * kPageRows + uw * kBlockRows) * 128;
-#pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-          const int r = lr + (i & 1) * 8;
-          const int c = D == 128 ? ((lane >> 3) + 4 * (i >> 1) + lr) & 7
-                                 : (((((lr >> 2) ^ (lr >> 1)) & 1) << 1 | (lr >> 2)) ^ (lane >> 3)) & 3;
-          uint4 x = *reinterpret_cast<const uint4*>(src + r * D + c * 16);
-          uint32_t y[8];
-          const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            y[2 * z] = decode2(w4[z]);
-            y[2 * z + 1] = decode2(w4[z] >> 16);
-          }
-          if (!(there[g] >> r & 1)) {
-#pragma unroll
-            for (int z = 0; z < 8; ++z) y[z] = 0;
-          } else if (poison[g] >> r & 1) {
-#pragma unroll
-            for (int z = 0; z < 8; ++z) {
-              const uint32_t nan = __vcmpgtu2(y[z] & 0x7fff7fffu, 0x7c007c00u);
-              y[z] = side == 0 ? 0x7fff7fffu : y[z] & ~nan;
-            }
-          }
+        auto put = [&](int r, int c, const uint32_t (&y)[8]) {
           uint8_t* p = dst + c / 4 * P::kHalf + r * 128;
           const int z = c % 4 * 2;
           *reinterpret_cast<uint4*>(p + ((z ^ lr) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
           *reinterpret_cast<uint4*>(p + (((z + 1) ^ lr) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+        };
+        if (here == 0xffffu && bad_rows == 0) {
+          uint4 x[kIter];
+#pragma unroll
+          for (int i = 0; i < kIter; ++i)
+            x[i] = *reinterpret_cast<const uint4*>(src + row_of(i) * D + piece_of(i) * 16);
+#pragma unroll
+          for (int i = 0; i < kIter; ++i) {
+            const uint32_t y[8] = {decode2(x[i].x), decode2(x[i].x >> 16), decode2(x[i].y),
+                                   decode2(x[i].y >> 16), decode2(x[i].z), decode2(x[i].z >> 16),
+                                   decode2(x[i].w), decode2(x[i].w >> 16)};
+            put(row_of(i), piece_of(i), y);
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < kIter; ++i) {
+            const int r = row_of(i), c = piece_of(i);
+            const bool ok = here >> r & 1, bad = bad_rows >> r & 1;
+            const uint4 x = *reinterpret_cast<const uint4*>(src + r * D + c * 16);
+            uint32_t y[8] = {decode2(x.x), decode2(x.x >> 16), decode2(x.y), decode2(x.y >> 16),
+                             decode2(x.z), decode2(x.z >> 16), decode2(x.w), decode2(x.w >> 16)};
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+              if (bad)  // the codes' NaN is f16's 0x7fff
+                y[z] = side == 0 ? 0x7fff7fffu
+                                 : ((y[z] & 0x7fffu) == 0x7fffu ? 0u : y[z] & 0xffffu) |
+                                       ((y[z] & 0x7fff0000u) == 0x7fff0000u ? 0u : y[z] & 0xffff0000u);
+              if (!ok) y[z] = 0;
+            }
+            put(r, c, y);
+          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.raw_empty[raw]);
@@ -473,13 +486,13 @@ __device__ __forceinline__ void issue(Smem<D, kTerms, kPair>& s, const PrefixPar
   constexpr uint32_t kScores = idesc_f16(kTile, kTile, false), kValues = idesc_f16(kTile, D, true);
   volatile int* abort = &s.abort;
   const uint32_t tmem = s.tmem;
-  int base = 0, units = 0;    // key tiles and units done
-  int done[2] = {0, 0};       // P V products issued of each stream
+  int base = 0, units = 0;  // key tiles and units done
+  int done0 = 0, done1 = 0;  // P V products issued of each stream
   bool stop = false;
   for (; wk.more() && !stop; wk.next(), ++units) {
     const int nt = wk.count();
     const bool both = wk.both();
-    const int n[2] = {both ? nt : (nt + 1) / 2, both ? nt : nt / 2};
+    const int n0 = both ? nt : (nt + 1) / 2, n1 = both ? nt : nt / 2;
     // the scores of the unit before are complete (their weights were formed)
     const uint32_t bytes = (both ? 2 : 1) * kTerms * P::kQTerm;
     mbar_expect_tx(&s.q_full, bytes);
@@ -488,70 +501,76 @@ __device__ __forceinline__ void issue(Smem<D, kTerms, kPair>& s, const PrefixPar
       *abort = 1;
       break;
     }
-    int si[2] = {0, 0}, pi[2] = {0, 0};
-    int idle = 0;
-    uint64_t t0 = global_timer_ns();
-    while (pi[0] < n[0] || pi[1] < n[1]) {
+    // tiles of each stream whose scores and whose weighted values have been asked for
+    int si0 = 0, si1 = 0, pi0 = 0, pi1 = 0, idle = 0, st = 0;
+    uint64_t t0 = 0;
+#pragma unroll 1
+    while (pi0 < n0 || pi1 < n1) {
       bool did = false;
+      const int other_s = st ? si0 : si1, other_p = st ? pi0 : pi1;
+      int si = st ? si1 : si0, pi = st ? pi1 : pi0, done = st ? done1 : done0;
+      const uint32_t sc = tmem + s_col(st), oc = tmem + o_col(st);
+      if (pi < si) {  // the weighted values of a tile whose weights are there
+        const int t = both ? pi : 2 * pi + st, oseq = 2 * (base + t) + 1;
+        const int slot = oseq % P::kOperands;
+        // (the first weights of a unit come when O of the unit before has been read)
+        if (test_bar(&s.p_full[st], done & 1) &&
+            test_bar(&s.op_full[slot], oseq / P::kOperands & 1)) {
+          tc_fence_after();
+          const uint64_t v = desc_mn_sw128(smem_addr(s.op[slot]), P::kHalf);
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        if (pi[st] < si[st]) {  // the weighted values of a tile whose weights are there
-          const int t = both ? pi[st] : 2 * pi[st] + st, oseq = 2 * (base + t) + 1;
-          const int slot = oseq % P::kOperands;
-          // (the first weights of a unit come when O of the unit before has been read)
-          if (test_bar(&s.p_full[st], done[st] & 1) &&
-              test_bar(&s.op_full[slot], oseq / P::kOperands & 1)) {
-            tc_fence_after();
-            const uint32_t v = smem_addr(s.op[slot]);
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-#pragma unroll
-              for (int term = 0; term < kTerms; ++term)
-                mma_ts(tmem + o_col(st), tmem + s_col(st) + kk / 2 * 32 + term * 16 + kk % 2 * 8,
-                       desc_mn_sw128(v + kk * 16 * 128, P::kHalf), kValues,
-                       pi[st] > 0 || kk > 0 || term > 0);
-            umma_commit(&s.pv_done[st]);
-            ++pi[st];
-            ++done[st];
-            if (!both || pi[st ^ 1] > t) umma_commit(&s.op_empty[slot]);
-            did = true;
-          }
-        }
-        if (si[st] < n[st] && si[st] == pi[st]) {  // the scores of a tile: P of the one before is read
-          const int t = both ? si[st] : 2 * si[st] + st, oseq = 2 * (base + t);
-          const int slot = oseq % P::kOperands;
-          if ((done[st] == 0 || test_bar(&s.pv_done[st], (done[st] - 1) & 1)) &&
-              test_bar(&s.op_full[slot], oseq / P::kOperands & 1)) {
-            tc_fence_after();
-            const uint32_t q = smem_addr(s.q) + (both ? st * kTerms * P::kQTerm : 0);
-            const uint32_t kt = smem_addr(s.op[slot]);
+          for (int kk = 0; kk < kTile / 16; ++kk)
 #pragma unroll
             for (int term = 0; term < kTerms; ++term)
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = kk / 4 * P::kHalf + kk % 4 * 32;
-                mma_ss(tmem + s_col(st), desc_kmajor_sw128(q + term * P::kQTerm + off),
-                       desc_kmajor_sw128(kt + off), kScores, term > 0 || kk > 0);
-              }
-            umma_commit(&s.s_full[st]);
-            ++si[st];
-            if (!both || si[st ^ 1] > t) umma_commit(&s.op_empty[slot]);
-            did = true;
-          }
+              mma_ts(oc, sc + kk / 2 * 32 + term * 16 + kk % 2 * 8, v + kk * (16 * 128 >> 4), kValues,
+                     pi > 0 || kk > 0 || term > 0);
+          umma_commit(&s.pv_done[st]);
+          if (!both || other_p > t) umma_commit(&s.op_empty[slot]);
+          ++pi;
+          ++done;
+          did = true;
         }
       }
+      // The scores of a tile, when P of the one before has been read.  They follow it at once, so
+      // that the two streams come to run in turns, one's softmax beside the other's products.
+      if (pi == si && si < (st ? n1 : n0)) {
+        const int t = both ? si : 2 * si + st, oseq = 2 * (base + t);
+        const int slot = oseq % P::kOperands;
+        if (test_bar(&s.op_full[slot], oseq / P::kOperands & 1) &&
+            (done == 0 || wait_or_stop(&s.pv_done[st], (done - 1) & 1, abort))) {
+          tc_fence_after();
+          const uint64_t q = desc_kmajor_sw128(smem_addr(s.q) + (both ? st * kTerms * P::kQTerm : 0));
+          const uint64_t kd = desc_kmajor_sw128(smem_addr(s.op[slot]));
+#pragma unroll
+          for (int term = 0; term < kTerms; ++term)
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const int off = kk / 4 * (P::kHalf >> 4) + kk % 4 * 2;
+              mma_ss(sc, q + term * (P::kQTerm >> 4) + off, kd + off, kScores, term > 0 || kk > 0);
+            }
+          umma_commit(&s.s_full[st]);
+          if (!both || other_s > t) umma_commit(&s.op_empty[slot]);
+          ++si;
+          did = true;
+        }
+      }
+      if (st)
+        si1 = si, pi1 = pi, done1 = done;
+      else
+        si0 = si, pi0 = pi, done0 = done;
+      st ^= 1;
       if (did) {
         idle = 0;
-        t0 = global_timer_ns();
         continue;
       }
       if (*abort) {
         stop = true;
         break;
       }
-      if (++idle >= 64) {  // bounded like every other wait
-        idle = 0;
-        if (global_timer_ns() - t0 > kWaitLimitNs) *abort = 1;
+      if ((++idle & 63) == 0) {  // bounded like every other wait
+        const uint64_t now = global_timer_ns();
+        if (idle == 64) t0 = now;
+        if (now - t0 > kWaitLimitNs) *abort = 1;
       }
     }
     base += nt;
@@ -575,7 +594,7 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
     const bool both = wk.both();
     const int tile = wk.tile() + (both ? st : 0), j = tile * kTile + row;
     const int t = j < px.nq ? n.pos[j / R] : -1;
-    const float fq = px.qf[((size_t)wk.c * px.tiles + tile) * kTile + row];
+    const float fq = t < 0 ? 0.f : px.qf[((size_t)wk.c * px.tiles + tile) * kTile + row];
     const bool work = __any_sync(0xffffffffu, t >= 0);  // else no lane's result is asked for
     float ms = kNoScore, mo = kNoScore, l = 0.f;  // reference of the scores; + V's exponent; sum
     int taken = 0;
@@ -592,49 +611,98 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
       if (!warp_wait(&s.s_full[st], mine & 1, abort)) return;
       tc_fence_after();
       if (work) {
-        const bool ring = m.ring, whole = !ring && m.cnt[0] == kPageRows && m.cnt[1] == kPageRows;
         const uint4 e4 = *reinterpret_cast<const uint4*>(m.exps);
-        const uint32_t ew[4] = {e4.x, e4.y, e4.z, e4.w};
-        auto ek = [&](int b) { return (int)(signed char)(ew[b / 2] >> (16 * (b & 1)) & 0xff); };
-        auto ev = [&](int b) { return (float)(signed char)(ew[b / 2] >> (16 * (b & 1) + 8) & 0xff); };
-        // does this query see key x of the tile?
-        auto sees = [&](int x) {
-          bool ok = x % kPageRows < m.cnt[x / kPageRows];
-          if (ring) {
-            const int p = m.pos[x];
-            ok = ok && p >= 0 && (unsigned)t - (unsigned)p < (unsigned)m.w;
+        const int cnt0 = m.cnt[0], cnt1 = m.cnt[1], w = m.w;
+        const bool ring = m.ring;
+        // Which keys are there, as bits of the tile's four columns of 32, and, in a ring, does
+        // every query of the warp see all of those?
+        uint32_t there[4];
+        bool near = true;
+        if (ring) {
+          uint32_t lo = 0xffffffffu, hi = 0;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int p = m.pos[x * 32 + lane];
+            const bool ok = (x & 1) * 32 + lane < (x < 2 ? cnt0 : cnt1) && p >= 0;
+            there[x] = __ballot_sync(0xffffffffu, ok);
+            lo = min(lo, ok ? (uint32_t)p : 0xffffffffu);
+            hi = max(hi, ok ? (uint32_t)p : 0u);
           }
-          return ok;
+          lo = __reduce_min_sync(0xffffffffu, lo);
+          hi = __reduce_max_sync(0xffffffffu, hi);
+          near = __all_sync(0xffffffffu,
+                            t < 0 || (hi <= (uint32_t)t && (uint32_t)t - lo < (uint32_t)w));
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int left = (x < 2 ? cnt0 : cnt1) - (x & 1) * 32;
+            there[x] = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1;
+          }
+        }
+        const bool whole = near && (there[0] & there[1] & there[2] & there[3]) == 0xffffffffu;
+        // factor of a block's scores and the exponent of its values, from the bytes of two blocks
+        auto factor = [&](uint32_t ew, int b) {
+          return fminf(fq * pow2f((int)(signed char)(ew >> (16 * b) & 0xff)), 1.7e38f);
         };
+        auto vexp = [&](uint32_t ew, int b) {
+          return (float)(signed char)(ew >> (16 * b + 8) & 0xff);
+        };
+        // The loops over 32 keys stay loops: unrolled, the warps' code outgrows the instruction
+        // cache (a tile then took two to five times as long).
         float smax = FG_NEG_INF, omax = FG_NEG_INF;
-        uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
-        if (!whole)
-#pragma unroll
+        if (!whole) {  // keys that do not count score -inf
+#pragma unroll 1
           for (int ch = 0; ch < 4; ++ch) {
-            uint32_t bits = 0;
-#pragma unroll 8
-            for (int e = 0; e < 32; ++e) bits |= (sees(ch * 32 + e) ? 1u : 0u) << e;
-            seen[ch] = bits;
+            constexpr uint32_t kNone = 0xff800000u;
+            const uint32_t bits = ch == 0 ? there[0] : ch == 1 ? there[1] : ch == 2 ? there[2] : there[3];
+            uint32_t r[32];
+            tmem_ld32(sc + ch * 32, r);
+            tmem_wait_ld(r);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              if ((bits >> e & 15u) != 15u) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (!(bits >> (e + i) & 1)) r[e + i] = kNone;
+              }
+            if (!near) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const int4 p = *reinterpret_cast<const int4*>(m.pos + ch * 32 + e);
+                const int p4[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (p4[i] > t || (uint32_t)t - (uint32_t)p4[i] >= (uint32_t)w) r[e + i] = kNone;
+              }
+            }
+            tmem_st16(sc + ch * 32, r);
+            tmem_st16(sc + ch * 32 + 16, r + 16);
           }
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          uint32_t r[32];
-          tmem_ld32(sc + ch * 32, r);
-          tmem_wait_ld(r);
-          if (!whole)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(seen[ch] >> e & 1)) r[e] = 0xff800000u;
+          tmem_wait_st();
+        }
+        auto tops = [&](uint32_t ew, const uint32_t (&r)[32]) {
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             float mx = FG_NEG_INF;
 #pragma unroll
             for (int e = 0; e < 16; e += 2)
               mx = max3(mx, __uint_as_float(r[b * 16 + e]), __uint_as_float(r[b * 16 + e + 1]));
-            const float y = mx * fminf(fq * pow2f(ek(ch * 2 + b)), 1.7e38f);
+            const float y = mx * factor(ew, b);
             smax = fmaxf(smax, y);
-            omax = fmaxf(omax, y + ev(ch * 2 + b));
+            omax = fmaxf(omax, y + vexp(ew, b));
           }
+        };
+        // 32 columns are on their way while the 32 before them are worked on
+        uint32_t ra[32], rb[32];
+        tmem_ld32(sc, ra);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          tmem_wait_ld(ra);
+          tmem_ld32(sc + h * 64 + 32, rb);
+          tops(h ? e4.z : e4.x, ra);
+          tmem_wait_ld(rb);
+          if (h == 0) tmem_ld32(sc + 64, ra);
+          tops(h ? e4.w : e4.y, rb);
         }
         if (__any_sync(0xffffffffu, smax > ms + kSlack || omax > mo + kSlack)) {
           const float sn = fmaxf(ms, smax), on = fmaxf(mo, omax), f = ex2(mo - on);
@@ -656,28 +724,19 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
         }
         uint64_t sum2 = 0;  // (0, 0)
         const uint64_t nm2 = pack2(-ms, -ms);
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          uint32_t r[32], hi[16], lo[16];
-          tmem_ld32(sc + ch * 32, r);
-          tmem_wait_ld(r);
+        const float lift = ms - mo + kProdBits;
+        auto form = [&](int ch, uint32_t ew, const uint32_t (&r)[32]) {
+          uint32_t hi[16], lo[16];
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const float f = fminf(fq * pow2f(ek(ch * 2 + b)), 1.7e38f);
-            const float g = ex2(fminf(ev(ch * 2 + b) + ms - mo + kProdBits, 126.f));
+            const float f = factor(ew, b), g = ex2(fminf(vexp(ew, b) + lift, 126.f));
             const uint64_t f2 = pack2(f, f), g2 = pack2(g, g);
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
               const int z = b * 16 + e;
               float x0, x1, p0, p1;
               unpack2(fma2(pack2(__uint_as_float(r[z]), __uint_as_float(r[z + 1])), f2, nm2), x0, x1);
-              x0 = ex2(x0);
-              x1 = ex2(x1);
-              if (!whole) {
-                if (!(seen[ch] >> z & 1)) x0 = 0.f;
-                if (!(seen[ch] >> (z + 1) & 1)) x1 = 0.f;
-              }
-              const uint64_t w2 = pack2(x0, x1);
+              const uint64_t w2 = pack2(ex2(x0), ex2(x1));
               sum2 = add2(sum2, w2);
               unpack2(mul2(w2, g2), p0, p1);
               hi[z / 2] = pack_f16x2(p0, p1);
@@ -689,6 +748,16 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
           }
           tmem_st16(sc + ch * 32, hi);
           if constexpr (kTerms == 2) tmem_st16(sc + ch * 32 + 16, lo);
+        };
+        tmem_ld32(sc, ra);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          tmem_wait_ld(ra);
+          tmem_ld32(sc + h * 64 + 32, rb);
+          form(2 * h, h ? e4.z : e4.x, ra);
+          tmem_wait_ld(rb);
+          if (h == 0) tmem_ld32(sc + 64, ra);
+          form(2 * h + 1, h ? e4.w : e4.y, rb);
         }
         float a, b;
         unpack2(sum2, a, b);
@@ -811,8 +880,8 @@ cudaError_t run_prefix(const ProfileDims& pd, const PagedDecodeArgs& n, const Pa
   static_assert(sizeof(Smem<D, kTerms, kPair>) + 1024 <= kSmem, "shared memory of a block");
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess)
-    e = launch_pdl(prefix_prep_kernel<T, D, kTerms>, px.caches * px.tiles + 1, kPrepThreads, 0, s,
-                   pre, n, px, pd.H, pd.R, pd.HL, pd.sl2);
+    e = launch_pdl(prefix_prep_kernel<T, D, kTerms>, cdiv(pd.G, kPrepThreads / 32) + 1,
+                   kPrepThreads, 0, s, pre, n, px, pd.G, pd.H, pd.R, pd.HL, pd.sl2);
   if (e == cudaSuccess) e = launch_pdl(kernel, px.ctas, kPrefixThreads, smem, s, pre, n, px, pd.R);
   return e;
 }
