@@ -448,7 +448,7 @@ struct PrefixParts {
   uint8_t* q;    // [caches, tiles] tiles of f16 queries, as the tensor cores read them
   float* qf;     // [caches, tiles x kPrefixTile] what the queries were divided by, times the scale
   float* ml;     // [kPrefixMaxCtas + units, 2, rows, 2] maximum, sum
-  float* acc;    // [.., d] outputs
+  float* acc;    // [.., 2, d / 4, rows, 4] outputs
 };
 
 // The units' key tiles of thread block i: [first, last) of `total`.

@@ -40,8 +40,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   }
   // the shared cache's parts of this query: of every thread block that had tiles of its unit, one,
   // or two where the block's two streams shared the unit's key tiles
-  int parts = 0, streams = 1;
-  size_t pre0 = 0;  // row of the first part
+  int parts = 0, streams = 1, row = 0;
+  size_t pre0 = 0;  // the first part
   if (px.caches > 0) {
     const int pc = c % HLkv, j = b * R + qi, tile = j / kPrefixTile;
     const int grp = px.pair ? tile / 2 : tile;
@@ -54,8 +54,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
       const int i0 = prefix_cta(all, ctas, x), i1 = prefix_cta(all, ctas, x + tiles - 1);
       streams = both ? 1 : 2;
       parts = (i1 - i0 + 1) * streams;
-      pre0 = (((size_t)i0 + (size_t)pc * px.groups + grp) * 2 + (both ? tile & 1 : 0)) * px.rows +
-             j % kPrefixTile;
+      pre0 = ((size_t)i0 + (size_t)pc * px.groups + grp) * 2 + (both ? tile & 1 : 0);
+      row = j % kPrefixTile;
     }
   }
   const int total = range.y + parts;
@@ -68,8 +68,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     for (int j = 0; j < kAhead; ++j) {
       const int i = i0 + j;
       const bool own = i < range.y;
-      const size_t slot = own ? ((size_t)range.x + i) * R + qi
-                              : pre0 + (size_t)(i - range.y) * (2 / streams) * px.rows;
+      const size_t part = pre0 + (size_t)(i - range.y) * (2 / streams);
+      const size_t slot = own ? ((size_t)range.x + i) * R + qi : part * px.rows + row;
       const float2 ml = i < total
                             ? *reinterpret_cast<const float2*>((own ? n.part_ml : px.ml) + 2 * slot)
                             : make_float2(kNoScore, 0.f);
@@ -78,8 +78,16 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
       if (l[j] == 0.f) {  // no row: nothing was written
 #pragma unroll
         for (int k = 0; k < PER; ++k) x[j][k] = 0.f;
+      } else if (own) {
+        load_row<PER>(n.part_acc + slot * D, x[j]);
       } else {
-        load_row<PER>((own ? n.part_acc : px.acc) + slot * D, x[j]);
+        const float* p = px.acc + part * px.rows * D + ((size_t)(lane * PER / 4) * px.rows + row) * 4;
+#pragma unroll
+        for (int k = 0; k < PER; k += 2) {
+          const float2 y = *reinterpret_cast<const float2*>(p + lane * PER % 4 + k);
+          x[j][k] = y.x;
+          x[j][k + 1] = y.y;
+        }
       }
     }
     float Mn = M;

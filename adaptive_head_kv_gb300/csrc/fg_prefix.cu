@@ -35,8 +35,8 @@ constexpr int kTile = kPrefixTile;
 constexpr int kTilePages = kTile / kPageRows;
 constexpr int kUnpackWarps = 4, kSoftWarps = 8;
 // warps 0-7 softmax (warp w reads tensor memory lanes 32 (w % 4) ..), 8-11 widen
-constexpr int kLoadWarp = kSoftWarps + kUnpackWarps, kMmaWarp = kLoadWarp + 1;
-constexpr int kPrefixThreads = (kMmaWarp + 1) * 32;
+constexpr int kLoadWarp = kSoftWarps + kUnpackWarps, kMmaWarp = kLoadWarp + 1;  // and the next
+constexpr int kPrefixThreads = (kMmaWarp + 2) * 32;
 constexpr int kMetas = 4;     // key tiles whose description is there
 constexpr float kSlack = 8.f;
 constexpr float kProdBits = 7.f;  // weights enter the product times 2^7, at most 2^15
@@ -59,7 +59,7 @@ struct Plan {
   static constexpr int kQBytes = (kPair ? 2 : 1) * kTerms * kQTerm;   // the queries in shared memory
   static constexpr int kPiece = kPageRows * D;                        // codes of K or of V of a page
   // widened K or V tiles: K of the next tile beside K and V of this one at least
-  static constexpr int kOperands = D == 64 ? 6 : kPair || kTerms == 2 ? 3 : 4;
+  static constexpr int kOperands = 3;
   static constexpr int kRoom =
       (kSmem - 1024 - 3584 - kQBytes - kOperands * kTileBytes) / kPiece;
   static constexpr int kPieces = kRoom > 16 ? 16 : kRoom;
@@ -77,7 +77,7 @@ struct alignas(1024) Smem {
   uint64_t meta_full[kMetas], meta_empty[kMetas];
   uint64_t op_full[P::kOperands], op_empty[P::kOperands];
   uint64_t s_full[2], p_full[2], pv_done[2];
-  uint64_t q_full, drain;
+  uint64_t q_full, q_free, turn, drain[2];
   int abort;
   uint32_t tmem;
   int first_cache;  // of this block's range
@@ -106,17 +106,6 @@ __device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, vol
 // The same by a whole warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, wait_or_stop(bar, parity, abort));
-}
-__device__ __forceinline__ bool test_bar(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -480,103 +469,90 @@ __device__ __forceinline__ void widen(Smem<D, kTerms, kPair>& s, int uw, int tot
   }
 }
 
+// The thread that issues stream st's products.  (The scores of a tile overwrite P of the one before,
+// so they wait until its product is complete: two threads, so that neither stream waits for the
+// other's.)  Each tile's operands are released by both streams, used or not.
 template <int D, int kTerms, bool kPair>
-__device__ __forceinline__ void issue(Smem<D, kTerms, kPair>& s, const PrefixParts& px, Walk wk) {
+__device__ __forceinline__ void issue(Smem<D, kTerms, kPair>& s, const PrefixParts& px, int st,
+                                      Walk wk) {
   using P = Plan<D, kTerms, kPair>;
   constexpr uint32_t kScores = idesc_f16(kTile, kTile, false), kValues = idesc_f16(kTile, D, true);
   volatile int* abort = &s.abort;
-  const uint32_t tmem = s.tmem;
-  int base = 0, units = 0;  // key tiles and units done
-  int done0 = 0, done1 = 0;  // P V products issued of each stream
-  bool stop = false;
-  for (; wk.more() && !stop; wk.next(), ++units) {
+  const uint32_t sc = s.tmem + s_col(st), oc = s.tmem + o_col(st);
+  int base = 0, units = 0, done = 0;  // key tiles, units, products P V of this stream
+  bool asked = false;
+  for (; wk.more(); wk.next(), ++units) {
     const int nt = wk.count();
     const bool both = wk.both();
-    const int n0 = both ? nt : (nt + 1) / 2, n1 = both ? nt : nt / 2;
-    // the scores of the unit before are complete (their weights were formed)
-    const uint32_t bytes = (both ? 2 : 1) * kTerms * P::kQTerm;
-    mbar_expect_tx(&s.q_full, bytes);
-    bulk_load(s.q, px.q + ((size_t)wk.c * px.tiles + wk.tile()) * kTerms * P::kQTerm, bytes, &s.q_full);
-    if (!mbar_wait(&s.q_full, units & 1)) {
-      *abort = 1;
-      break;
+    if (st == 0) {
+      const uint32_t bytes = (both ? 2 : 1) * kTerms * P::kQTerm;
+      if (units > 0 && !wait_or_stop(&s.q_free, (units - 1) & 1, abort)) break;
+      mbar_expect_tx(&s.q_full, bytes);
+      bulk_load(s.q, px.q + ((size_t)wk.c * px.tiles + wk.tile()) * kTerms * P::kQTerm, bytes,
+                &s.q_full);
+      asked = true;
     }
-    // tiles of each stream whose scores and whose weighted values have been asked for
-    int si0 = 0, si1 = 0, pi0 = 0, pi1 = 0, idle = 0, st = 0;
-    uint64_t t0 = 0;
+    if (!wait_or_stop(&s.q_full, units & 1, abort)) break;
+    asked = false;
+    const uint64_t q = desc_kmajor_sw128(smem_addr(s.q) + (both ? st * kTerms * P::kQTerm : 0));
+    // Streams in step would have their products, then their softmaxes at the same time: stream 1
+    // begins a unit when stream 0 has asked for its first weighted values.
+    if (st == 1 && !wait_or_stop(&s.turn, units & 1, abort)) break;
+    bool stop = false;
 #pragma unroll 1
-    while (pi0 < n0 || pi1 < n1) {
-      bool did = false;
-      const int other_s = st ? si0 : si1, other_p = st ? pi0 : pi1;
-      int si = st ? si1 : si0, pi = st ? pi1 : pi0, done = st ? done1 : done0;
-      const uint32_t sc = tmem + s_col(st), oc = tmem + o_col(st);
-      if (pi < si) {  // the weighted values of a tile whose weights are there
-        const int t = both ? pi : 2 * pi + st, oseq = 2 * (base + t) + 1;
-        const int slot = oseq % P::kOperands;
-        // (the first weights of a unit come when O of the unit before has been read)
-        if (test_bar(&s.p_full[st], done & 1) &&
-            test_bar(&s.op_full[slot], oseq / P::kOperands & 1)) {
-          tc_fence_after();
-          const uint64_t v = desc_mn_sw128(smem_addr(s.op[slot]), P::kHalf);
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-#pragma unroll
-            for (int term = 0; term < kTerms; ++term)
-              mma_ts(oc, sc + kk / 2 * 32 + term * 16 + kk % 2 * 8, v + kk * (16 * 128 >> 4), kValues,
-                     pi > 0 || kk > 0 || term > 0);
-          umma_commit(&s.pv_done[st]);
-          if (!both || other_p > t) umma_commit(&s.op_empty[slot]);
-          ++pi;
-          ++done;
-          did = true;
-        }
-      }
-      // The scores of a tile, when P of the one before has been read.  They follow it at once, so
-      // that the two streams come to run in turns, one's softmax beside the other's products.
-      if (pi == si && si < (st ? n1 : n0)) {
-        const int t = both ? si : 2 * si + st, oseq = 2 * (base + t);
-        const int slot = oseq % P::kOperands;
-        if (test_bar(&s.op_full[slot], oseq / P::kOperands & 1) &&
-            (done == 0 || wait_or_stop(&s.pv_done[st], (done - 1) & 1, abort))) {
-          tc_fence_after();
-          const uint64_t q = desc_kmajor_sw128(smem_addr(s.q) + (both ? st * kTerms * P::kQTerm : 0));
-          const uint64_t kd = desc_kmajor_sw128(smem_addr(s.op[slot]));
-#pragma unroll
-          for (int term = 0; term < kTerms; ++term)
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const int off = kk / 4 * (P::kHalf >> 4) + kk % 4 * 2;
-              mma_ss(sc, q + term * (P::kQTerm >> 4) + off, kd + off, kScores, term > 0 || kk > 0);
-            }
-          umma_commit(&s.s_full[st]);
-          if (!both || other_s > t) umma_commit(&s.op_empty[slot]);
-          ++si;
-          did = true;
-        }
-      }
-      if (st)
-        si1 = si, pi1 = pi, done1 = done;
-      else
-        si0 = si, pi0 = pi, done0 = done;
-      st ^= 1;
-      if (did) {
-        idle = 0;
+    for (int i = 0; i < nt; ++i) {
+      const int ks = 2 * (base + i) % P::kOperands, kp = 2 * (base + i) / P::kOperands & 1;
+      const int vs = (2 * (base + i) + 1) % P::kOperands, vp = (2 * (base + i) + 1) / P::kOperands & 1;
+      if (!both && (i & 1) != st) {  // the other stream's tile
+        if (!wait_or_stop(&s.op_full[ks], kp, abort)) stop = true;
+        if (!stop) mbar_arrive(&s.op_empty[ks]);
+        if (!stop && !wait_or_stop(&s.op_full[vs], vp, abort)) stop = true;
+        if (!stop) mbar_arrive(&s.op_empty[vs]);
+        if (stop) break;
         continue;
       }
-      if (*abort) {
+      if ((done > 0 && !wait_or_stop(&s.pv_done[st], (done - 1) & 1, abort)) ||
+          !wait_or_stop(&s.op_full[ks], kp, abort)) {
         stop = true;
         break;
       }
-      if ((++idle & 63) == 0) {  // bounded like every other wait
-        const uint64_t now = global_timer_ns();
-        if (idle == 64) t0 = now;
-        if (now - t0 > kWaitLimitNs) *abort = 1;
+      tc_fence_after();
+      const uint64_t kd = desc_kmajor_sw128(smem_addr(s.op[ks]));
+#pragma unroll
+      for (int term = 0; term < kTerms; ++term)
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const int off = kk / 4 * (P::kHalf >> 4) + kk % 4 * 2;
+          mma_ss(sc, q + term * (P::kQTerm >> 4) + off, kd + off, kScores, term > 0 || kk > 0);
+        }
+      umma_commit(&s.s_full[st]);
+      umma_commit(&s.op_empty[ks]);
+      // (the first weights of a unit come when O of the unit before has been read)
+      if (!wait_or_stop(&s.p_full[st], done & 1, abort) || !wait_or_stop(&s.op_full[vs], vp, abort)) {
+        stop = true;
+        break;
       }
+      tc_fence_after();
+      const uint64_t v = desc_mn_sw128(smem_addr(s.op[vs]), P::kHalf);
+      const bool more = i >= (both ? 1 : 2);
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk)
+#pragma unroll
+        for (int term = 0; term < kTerms; ++term)
+          mma_ts(oc, sc + kk / 2 * 32 + term * 16 + kk % 2 * 8, v + kk * (16 * 128 >> 4), kValues,
+                 more || kk > 0 || term > 0);
+      umma_commit(&s.pv_done[st]);
+      umma_commit(&s.op_empty[vs]);
+      if (st == 0 && i == 0) mbar_arrive(&s.turn);
+      ++done;
     }
+    if (stop) break;
+    mbar_arrive(&s.q_free);  // the weights were there, so the scores are complete
     base += nt;
   }
-  umma_commit(&s.drain);  // every product issued is complete before the block ends
-  mbar_wait(&s.drain, 0);
+  if (asked) mbar_wait(&s.q_full, units & 1);  // (after a stop: nothing stays in flight)
+  umma_commit(&s.drain[st]);  // every product issued is complete before the block ends
+  mbar_wait(&s.drain[st], 0);
 }
 
 // A softmax warpgroup: stream st, a thread a query.
@@ -596,6 +572,9 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
     const int t = j < px.nq ? n.pos[j / R] : -1;
     const float fq = t < 0 ? 0.f : px.qf[((size_t)wk.c * px.tiles + tile) * kTile + row];
     const bool work = __any_sync(0xffffffffu, t >= 0);  // else no lane's result is asked for
+    // the positions of the warp's queries lie from t_lo to t_hi
+    const int t_lo = (int)__reduce_min_sync(0xffffffffu, t < 0 ? 0x7fffffffu : (uint32_t)t);
+    const int t_hi = (int)__reduce_max_sync(0xffffffffu, t < 0 ? 0u : (uint32_t)t);
     float ms = kNoScore, mo = kNoScore, l = 0.f;  // reference of the scores; + V's exponent; sum
     int taken = 0;
     for (int i = 0; i < nt; ++i, ++k) {
@@ -614,24 +593,21 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
         const uint4 e4 = *reinterpret_cast<const uint4*>(m.exps);
         const int cnt0 = m.cnt[0], cnt1 = m.cnt[1], w = m.w;
         const bool ring = m.ring;
-        // Which keys are there, as bits of the tile's four columns of 32, and, in a ring, does
-        // every query of the warp see all of those?
+        // Which keys does any query of the warp see, as bits of the tile's four columns of 32, and
+        // do all of them see those?  (A ring also holds positions that no one sees any more.)
         uint32_t there[4];
         bool near = true;
         if (ring) {
-          uint32_t lo = 0xffffffffu, hi = 0;
+          bool same = true;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int p = m.pos[x * 32 + lane];
             const bool ok = (x & 1) * 32 + lane < (x < 2 ? cnt0 : cnt1) && p >= 0;
-            there[x] = __ballot_sync(0xffffffffu, ok);
-            lo = min(lo, ok ? (uint32_t)p : 0xffffffffu);
-            hi = max(hi, ok ? (uint32_t)p : 0u);
+            const bool any = ok && p <= t_hi && t_lo - p < w;
+            same &= any == (ok && p <= t_lo && t_hi - p < w);
+            there[x] = __ballot_sync(0xffffffffu, any);
           }
-          lo = __reduce_min_sync(0xffffffffu, lo);
-          hi = __reduce_max_sync(0xffffffffu, hi);
-          near = __all_sync(0xffffffffu,
-                            t < 0 || (hi <= (uint32_t)t && (uint32_t)t - lo < (uint32_t)w));
+          near = __all_sync(0xffffffffu, same);
         } else {
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
@@ -655,6 +631,7 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
           for (int ch = 0; ch < 4; ++ch) {
             constexpr uint32_t kNone = 0xff800000u;
             const uint32_t bits = ch == 0 ? there[0] : ch == 1 ? there[1] : ch == 2 ? there[2] : there[3];
+            if (near && bits == 0xffffffffu) continue;
             uint32_t r[32];
             tmem_ld32(sc + ch * 32, r);
             tmem_wait_ld(r);
@@ -784,7 +761,8 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
       if (work) {
         // O is in units of 2^(mo - kProdBits), l of 2^ms
         const float f = l == 0.f ? 0.f : exp2f(mo - ms - kProdBits) / l;
-        float* out = px.acc + (part * px.rows + row) * D;
+        // [d / 4][rows][4]: a warp's lanes write next to one another
+        float4* out = reinterpret_cast<float4*>(px.acc + part * px.rows * D) + row;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t r[32];
@@ -793,7 +771,7 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
           if (write)
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(out + c + e) =
+              out[(size_t)((c + e) / 4) * px.rows] =
                   make_float4(__uint_as_float(r[e]) * f, __uint_as_float(r[e + 1]) * f,
                               __uint_as_float(r[e + 2]) * f, __uint_as_float(r[e + 3]) * f);
         }
@@ -827,15 +805,17 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     }
     for (int i = 0; i < P::kOperands; ++i) {
       mbar_init(&s.op_full[i], kUnpackWarps);
-      mbar_init(&s.op_empty[i], 1);
+      mbar_init(&s.op_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.p_full[i], kSoftWarps / 2);
       mbar_init(&s.pv_done[i], 1);
+      mbar_init(&s.drain[i], 1);
     }
     mbar_init(&s.q_full, 1);
-    mbar_init(&s.drain, 1);
+    mbar_init(&s.q_free, 2);
+    mbar_init(&s.turn, 1);
     fence_barrier_init();
   }
   griddep_wait();
@@ -854,8 +834,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     const Walk wk(px, s.first_cache, x0, x1);
     if (warp == kLoadWarp)
       load_pages<D, kTerms, kPair>(s, a, wk);
-    else if (warp == kMmaWarp) {
-      if (lane == 0) issue<D, kTerms, kPair>(s, px, wk);
+    else if (warp >= kMmaWarp) {
+      if (lane == 0) issue<D, kTerms, kPair>(s, px, warp - kMmaWarp, wk);
     } else if (warp >= kSoftWarps)
       widen<D, kTerms, kPair>(s, warp - kSoftWarps, (int)(x1 - x0));
     else
