@@ -436,7 +436,7 @@ struct PagedDecodeArgs {
 // other pair has: u does not fall while i grows.
 constexpr int kPrefixTile = 128;
 constexpr int kPrefixMaxCtas = 192;
-constexpr int kPrefixMinTiles = 1;  // of a thread block's range, where there are so many
+constexpr int kPrefixMinPages = 2;  // of a thread block's range, where there are so many
 struct PrefixParts {
   int caches, nq;    // shared caches (0: none); queries of each: sequences x group size
   int tiles, groups; // of the queries of a cache
@@ -444,16 +444,16 @@ struct PrefixParts {
   int rows;          // rows of a part: queries of a tile
   int ctas;          // thread blocks
   // workspace
-  long long* cum;  // [caches + 1] key tiles before each cache
+  long long* cum;  // [caches + 1] pages before each cache
   uint8_t* q;    // [caches, tiles] tiles of f16 queries, as the tensor cores read them
   float* qf;     // [caches, tiles x kPrefixTile] what the queries were divided by, times the scale
   float* ml;     // [kPrefixMaxCtas + units, 2, rows, 2] maximum, sum
   float* acc;    // [.., 2, d / 4, rows, 4] outputs
 };
 
-// The units' key tiles of thread block i: [first, last) of `total`.
+// The thread blocks that share `total` pages, and the first page of block i.
 __host__ __device__ inline int prefix_ctas(long long total, int ctas) {
-  const long long n = (total + kPrefixMinTiles - 1) / kPrefixMinTiles;
+  const long long n = (total + kPrefixMinPages - 1) / kPrefixMinPages;
   return (int)(n < 1 ? 1 : n < ctas ? n : ctas);
 }
 __host__ __device__ inline long long prefix_first(long long total, int ctas, int i) {

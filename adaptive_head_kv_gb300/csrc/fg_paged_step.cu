@@ -38,23 +38,22 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     if (qi == 0 && lane == 0) a.rows_out[c] = had;
     return;
   }
-  // the shared cache's parts of this query: of every thread block that had tiles of its unit, one,
-  // or two where the block's two streams shared the unit's key tiles
+  // the shared cache's parts of this query: of every thread block that had pages of its unit, one,
+  // or two where the block's two streams shared the unit's pages
   int parts = 0, streams = 1, row = 0;
   size_t pre0 = 0;  // the first part
   if (px.caches > 0) {
     const int pc = c % HLkv, j = b * R + qi, tile = j / kPrefixTile;
     const int grp = px.pair ? tile / 2 : tile;
-    const long long c0 = px.cum[pc], tiles = px.cum[pc + 1] - c0;
+    const long long c0 = px.cum[pc], pages = px.cum[pc + 1] - c0;
     const long long all = px.cum[px.caches] * px.groups;
-    const bool both = px.pair && 2 * grp + 1 < px.tiles;
-    if (tiles > 0) {
+    if (pages > 0) {
       const int ctas = prefix_ctas(all, px.ctas);
-      const long long x = c0 * px.groups + grp * tiles;
-      const int i0 = prefix_cta(all, ctas, x), i1 = prefix_cta(all, ctas, x + tiles - 1);
-      streams = both ? 1 : 2;
+      const long long x = c0 * px.groups + grp * pages;
+      const int i0 = prefix_cta(all, ctas, x), i1 = prefix_cta(all, ctas, x + pages - 1);
+      streams = px.pair ? 1 : 2;
       parts = (i1 - i0 + 1) * streams;
-      pre0 = ((size_t)i0 + (size_t)pc * px.groups + grp) * 2 + (both ? tile & 1 : 0);
+      pre0 = ((size_t)i0 + (size_t)pc * px.groups + grp) * 2 + (px.pair ? tile & 1 : 0);
       row = j % kPrefixTile;
     }
   }

@@ -31,77 +31,72 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTile = kPrefixTile;
-constexpr int kTilePages = kTile / kPageRows;
+constexpr int kTile = kPrefixTile;  // queries of a tile
 constexpr int kUnpackWarps = 4, kSoftWarps = 8;
 // warps 0-7 softmax (warp w reads tensor memory lanes 32 (w % 4) ..), 8-11 widen
 constexpr int kLoadWarp = kSoftWarps + kUnpackWarps, kMmaWarp = kLoadWarp + 1;  // and the next
 constexpr int kPrefixThreads = (kMmaWarp + 2) * 32;
-constexpr int kMetas = 4;     // key tiles whose description is there
+constexpr int kMetas = 8;  // pages whose description is there
 constexpr float kSlack = 8.f;
 constexpr float kProdBits = 7.f;  // weights enter the product times 2^7, at most 2^15
 constexpr int kSmem = 227 * 1024;
 
-// A key tile: two pages of a segment or of a ring.
-struct TileMeta {
-  uint32_t exps[2 * kTilePages];  // of the pages' blocks: (K, V) bytes
-  int cnt[kTilePages];            // rows of each page (0: no page)
-  int ring;
-  int w;
-  int pos[kTile];                 // of a ring's rows
+// A page of a segment or of a ring.
+struct PageMeta {
+  uint32_t exps[2];     // of the page's blocks: (K, V) bytes
+  int cnt;              // rows (0: no page)
+  int w;                // ring slots, 0: a segment's page
+  int pos[kPageRows];   // of a ring's rows
 };
 
 template <int D, int kTerms, bool kPair>
 struct Plan {
-  static constexpr int kHalf = kTile * 128;  // bytes of 64 dimensions of a tile
-  static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kQTerm = kTileBytes;                           // one term of a tile of queries
+  static constexpr int kQHalf = kTile * 128;  // bytes of 64 dimensions of a tile of queries
+  static constexpr int kQTerm = kTile * D * 2;                        // one term of a tile of queries
   static constexpr int kQBytes = (kPair ? 2 : 1) * kTerms * kQTerm;   // the queries in shared memory
   static constexpr int kPiece = kPageRows * D;                        // codes of K or of V of a page
-  // widened K or V tiles: K of the next tile beside K and V of this one at least
-  static constexpr int kOperands = 3;
-  static constexpr int kRoom =
-      (kSmem - 1024 - 3584 - kQBytes - kOperands * kTileBytes) / kPiece;
+  static constexpr int kHalf = kPageRows * 128;  // bytes of 64 dimensions of an operand
+  static constexpr int kOpBytes = kPageRows * D * 2;
+  // Widened K or V pages in shared memory.  Where the streams take pages in turns, a multiple of
+  // four, so that a place always has the same stream's pages.
+  static constexpr int kOperands = kPair ? 6 : kTerms == 2 && D == 128 ? 4 : 8;
+  static constexpr int kRoom = (kSmem - 1024 - 3584 - kQBytes - kOperands * kOpBytes) / kPiece;
   static constexpr int kPieces = kRoom > 16 ? 16 : kRoom;
-  static_assert(kPieces >= 2 * kTilePages, "a tile's codes are there together");
+  static_assert(kPieces >= 2 && (kPair || kOperands % 4 == 0), "a page's codes are there together");
 };
 
 template <int D, int kTerms, bool kPair>
 struct alignas(1024) Smem {
   using P = Plan<D, kTerms, kPair>;
   uint8_t q[P::kQBytes];
-  uint8_t op[P::kOperands][P::kTileBytes];
+  uint8_t op[P::kOperands][P::kOpBytes];
   alignas(128) uint8_t raw[P::kPieces][P::kPiece];
-  alignas(16) TileMeta meta[kMetas];
+  alignas(16) PageMeta meta[kMetas];
   uint64_t raw_full[P::kPieces], raw_empty[P::kPieces];
   uint64_t meta_full[kMetas], meta_empty[kMetas];
   uint64_t op_full[P::kOperands], op_empty[P::kOperands];
-  uint64_t s_full[2], p_full[2], pv_done[2];
-  uint64_t q_full, q_free, turn, drain[2];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // of a stream's two places of S
+  uint64_t q_full, q_free, drain[2];
   int abort;
   uint32_t tmem;
   int first_cache;  // of this block's range
 };
 
-// tensor memory: S (and P) of the two streams, then O
+// tensor memory: two places of S (and P) of each stream, then O
 constexpr uint32_t kTmemCols = 512;
-__device__ __forceinline__ uint32_t s_col(int s) { return s * kTile; }
-__device__ __forceinline__ uint32_t o_col(int s) { return 2 * kTile + s * 128; }
+__device__ __forceinline__ uint32_t s_col(int st, int b) { return st * 128 + b * kPageRows; }
+__device__ __forceinline__ uint32_t o_col(int st) { return 256 + st * 128; }
 
-// (out of line, like everything that a tile seldom needs: what the warps run for every tile has to
-// stay in the instruction cache together)
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const uint64_t t0 = global_timer_ns();
-  while (!*abort) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (global_timer_ns() - t0 > kWaitLimitNs) *abort = 1;
-  }
-  return false;
-}
+// Waits for at most about a second (2^31 cycles), or until another wait has run out.
 __device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort);
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > (1ll << 31)) *abort = 1;
+    if (*abort) return false;
+  }
+  return true;
 }
 // The same by a whole warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
@@ -148,6 +143,24 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[15])
       : "memory");
 }
+// 16 columns, and the wait for them.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -157,15 +170,15 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// Key tiles of a cache: of its segment, of its ring.
-__device__ __forceinline__ int2 key_tiles(const PagedArgs& a, const fg_paged_desc& hd, int rows) {
-  return make_int2(cdiv(live_rows(hd, rows), kTile), cdiv(ring_slots(hd, a.max_w), kTile));
+// Pages of a cache: of its segment, of its ring.
+__device__ __forceinline__ int2 key_pages(const PagedArgs& a, const fg_paged_desc& hd, int rows) {
+  return make_int2(cdiv(live_rows(hd, rows), kPageRows), cdiv(ring_slots(hd, a.max_w), kPageRows));
 }
 
 // ------------------------------------------------------------- before the products
 // A warp a query: rotated, divided by the power of two that brings its largest value to
 // [2^13, 2^14), as f16 in the tensor cores' layout.  (Rows of a tile without a query stay as they
-// are: no other row's result depends on them.)  The last CTA counts the caches' key tiles.
+// are: no other row's result depends on them.)  The last CTA counts the caches' pages.
 constexpr int kPrepThreads = 256;
 
 template <typename T, int D, int kTerms>
@@ -187,7 +200,7 @@ __global__ void __launch_bounds__(kPrepThreads)
         const int rows = a.rows[c];
         if (live_rows(hd, rows) != rows || ring_slots(hd, a.max_w) != hd.w)
           atomicOr(a.dev_err, kErrInvalid);
-        const int2 k = key_tiles(a, hd, rows);
+        const int2 k = key_pages(a, hd, rows);
         x = (long long)k.x + k.y;
       }
       const long long at = sum + block_exclusive_scan(x, scr, &tot);
@@ -237,21 +250,21 @@ __global__ void __launch_bounds__(kPrepThreads)
 }
 
 // ------------------------------------------------------------------- the products
-// The part of a unit's key tiles that a thread block takes.
+// The parts of units' pages that a thread block takes.
 struct Walk {
   const PrefixParts& px;
   long long x, end;  // of the block's range
   int c, grp;
-  long long c0, tiles;  // of the cache
+  long long c0, pages;  // of the cache
   __device__ Walk(const PrefixParts& p, int first_cache, long long x0, long long x1)
       : px(p), x(x0), end(x1), c(first_cache) {
     c0 = px.cum[c];
-    tiles = px.cum[c + 1] - c0;
-    grp = tiles > 0 ? (int)((x - c0 * px.groups) / tiles) : 0;
+    pages = px.cum[c + 1] - c0;
+    grp = pages > 0 ? (int)((x - c0 * px.groups) / pages) : 0;
   }
   __device__ bool more() const { return x < end; }
-  __device__ int first() const { return (int)(x - c0 * px.groups - grp * tiles); }  // key tile
-  __device__ int count() const { return (int)min(tiles - first(), end - x); }
+  __device__ int first() const { return (int)(x - c0 * px.groups - grp * pages); }  // page
+  __device__ int count() const { return (int)min(pages - first(), end - x); }
   __device__ bool both() const { return px.pair && 2 * grp + 1 < px.tiles; }
   __device__ int tile() const { return px.pair ? 2 * grp : grp; }  // of the queries
   __device__ size_t unit() const { return (size_t)c * px.groups + grp; }
@@ -262,8 +275,8 @@ struct Walk {
     grp = 0;
     do {
       c0 = px.cum[++c];
-      tiles = px.cum[c + 1] - c0;
-    } while (tiles == 0);
+      pages = px.cum[c + 1] - c0;
+    } while (pages == 0);
   }
 };
 
@@ -272,82 +285,70 @@ __device__ __forceinline__ void load_pages(Smem<D, kTerms, kPair>& s, const Page
   using P = Plan<D, kTerms, kPair>;
   const int lane = threadIdx.x & 31;
   volatile int* abort = &s.abort;
-  int k = 0, pieces = 0, metas = 0;  // key tiles of this block; copies asked for so far
+  int k = 0, pieces = 0, metas = 0;  // pages of this block; copies asked for so far
   bool stop = false;
   for (; wk.more() && !stop; wk.next()) {
     const fg_paged_desc hd = a.caches[wk.c];
     const int rows = live_rows(hd, a.rows[wk.c]), w = ring_slots(hd, a.max_w);
-    const int seg = cdiv(rows, kTile), t0 = wk.first(), nt = wk.count();
+    const int seg = cdiv(rows, kPageRows), t0 = wk.first(), nt = wk.count();
     int page_l = -1;
     uint2 exp_l = make_uint2(0, 0);
+#pragma unroll 1
     for (int i = 0; i < nt; ++i, ++k) {
-      if ((i & 15) == 0) {  // pages of the next 16 tiles: lane l holds one and its exponents
-        const int t = t0 + i + lane / 2, e = (t < seg ? t : t - seg) * kTilePages + lane % 2;
+      if ((i & 31) == 0) {  // the next 32 pages: lane l holds one and its exponents
+        const int t = t0 + i + lane;
         page_l = -1;
-        if (i + lane / 2 < nt && e * kPageRows < (t < seg ? rows : w)) {
-          page_l = t < seg ? page_at(a, hd.first_page, hd.max_pages, e)
-                           : page_at(a, hd.ring_page, hd.ring_pages, e);
+        if (i + lane < nt) {
+          page_l = t < seg ? page_at(a, hd.first_page, hd.max_pages, t)
+                           : page_at(a, hd.ring_page, hd.ring_pages, t - seg);
           if (page_l < 0)
             atomicOr(a.dev_err, kErrInvalid);
           else
             exp_l = *reinterpret_cast<const uint2*>(a.exps + (size_t)page_l * kPageBlocks * 2);
         }
       }
-      const int t = t0 + i, ring = t >= seg, row0 = (ring ? t - seg : t) * kTile;
-      const int left = (ring ? w : rows) - row0;
-      int page[kTilePages];
-      uint2 ex[kTilePages];
-#pragma unroll
-      for (int g = 0; g < kTilePages; ++g) {
-        page[g] = __shfl_sync(0xffffffffu, page_l, (i & 15) * 2 + g);
-        ex[g].x = __shfl_sync(0xffffffffu, exp_l.x, (i & 15) * 2 + g);
-        ex[g].y = __shfl_sync(0xffffffffu, exp_l.y, (i & 15) * 2 + g);
-      }
+      const int t = t0 + i;
+      const bool ring = t >= seg;
+      const int page = __shfl_sync(0xffffffffu, page_l, i & 31);
+      uint2 ex;
+      ex.x = __shfl_sync(0xffffffffu, exp_l.x, i & 31);
+      ex.y = __shfl_sync(0xffffffffu, exp_l.y, i & 31);
       if (lane == 0) {
         const int ms = k % kMetas;
         if (k >= kMetas && !wait_or_stop(&s.meta_empty[ms], (k / kMetas - 1) & 1, abort)) stop = true;
-        TileMeta& m = s.meta[ms];
-        uint32_t bytes = 0;
         if (!stop) {
-#pragma unroll
-          for (int g = 0; g < kTilePages; ++g) {
-            m.exps[2 * g] = ex[g].x;
-            m.exps[2 * g + 1] = ex[g].y;
-            m.cnt[g] = page[g] < 0 ? 0 : max(0, min(kPageRows, left - g * kPageRows));
-            if (ring && page[g] >= 0) bytes += kPageRows * 4;
-          }
-          m.ring = ring;
-          m.w = w;
-          mbar_expect_tx(&s.meta_full[ms], bytes);
+          PageMeta& m = s.meta[ms];
+          m.exps[0] = ex.x;
+          m.exps[1] = ex.y;
+          m.cnt = page < 0 ? 0 : min(kPageRows, (ring ? w : rows) - (ring ? t - seg : t) * kPageRows);
+          m.w = ring ? w : 0;
+          const bool copy = ring && page >= 0;
+          mbar_expect_tx(&s.meta_full[ms], copy ? kPageRows * 4 : 0);
           ++metas;
-#pragma unroll
-          for (int g = 0; g < kTilePages; ++g)
-            if (ring && page[g] >= 0)
-              bulk_load(m.pos + g * kPageRows, a.pos + (size_t)page[g] * kPageRows, kPageRows * 4,
-                        &s.meta_full[ms]);
+          if (copy)
+            bulk_load(m.pos, a.pos + (size_t)page * kPageRows, kPageRows * 4, &s.meta_full[ms]);
         }
 #pragma unroll 1
-        for (int z = 0; z < 2 * kTilePages && !stop; ++z) {
-          const int seq = 2 * kTilePages * k + z, slot = seq % P::kPieces;
-          const int at = z % kTilePages ? page[1] : page[0];
+        for (int side = 0; side < 2 && !stop; ++side) {
+          const int seq = 2 * k + side, slot = seq % P::kPieces;
           if (seq >= P::kPieces &&
               !wait_or_stop(&s.raw_empty[slot], (seq / P::kPieces - 1) & 1, abort)) {
             stop = true;
-          } else if (at < 0) {
+            break;
+          }
+          ++pieces;
+          if (page < 0) {
             mbar_arrive(&s.raw_full[slot]);
-            ++pieces;
           } else {
-            ++pieces;
             mbar_expect_tx(&s.raw_full[slot], P::kPiece);
-            bulk_load(s.raw[slot], (z < kTilePages ? a.kp : a.vp) + (size_t)at * P::kPiece,
-                      P::kPiece, &s.raw_full[slot]);
+            bulk_load(s.raw[slot], (side ? a.vp : a.kp) + (size_t)page * P::kPiece, P::kPiece,
+                      &s.raw_full[slot]);
           }
         }
       }
       stop = __shfl_sync(0xffffffffu, stop, 0);
       if (stop) break;
     }
-    if (stop) break;
   }
   if (*abort && lane == 0) {  // what is in flight lands before the block ends
     for (int i = max(0, pieces - P::kPieces); i < pieces; ++i)
@@ -359,7 +360,7 @@ __device__ __forceinline__ void load_pages(Smem<D, kTerms, kPair>& s, const Page
 
 // One of the four warps that widen codes: rows 16 w .. of every page, where an operand row that is
 // not there is zero.  A lane's 16 bytes and the 32 it makes of them are chosen so that the eight
-// lanes of a phase meet eight different banks, in the codes and in the swizzled tile.
+// lanes of a phase meet eight different banks, in the codes and in the swizzled operand.
 template <int D, int kTerms, bool kPair>
 __device__ __forceinline__ void widen(Smem<D, kTerms, kPair>& s, int uw, int total) {
   using P = Plan<D, kTerms, kPair>;
@@ -371,96 +372,92 @@ __device__ __forceinline__ void widen(Smem<D, kTerms, kPair>& s, int uw, int tot
     return D == 128 ? ((lane >> 3) + 4 * (i >> 1) + lr) & 7
                     : (((((lr >> 2) ^ (lr >> 1)) & 1) << 1 | (lr >> 2)) ^ (lane >> 3)) & 3;
   };
+#pragma unroll 1
   for (int k = 0; k < total; ++k) {
     const int ms = k % kMetas;
     if (!warp_wait(&s.meta_full[ms], k / kMetas & 1, abort)) return;
-    const TileMeta& m = s.meta[ms];
-    const int ring = m.ring;
-    uint32_t there[kTilePages], poison[kTilePages] = {};
-#pragma unroll
-    for (int g = 0; g < kTilePages; ++g) {
+    const PageMeta& m = s.meta[ms];
+    const bool ring = m.w > 0;
+    uint32_t here = 0xffffu, poison = 0;
+    if (ring || m.cnt < kPageRows) {
       const int row = uw * kBlockRows + lane;
-      bool ok = lane < kBlockRows && row < m.cnt[g];
-      if (ok && ring) ok = m.pos[g * kPageRows + row] >= 0;
-      there[g] = __ballot_sync(0xffffffffu, ok);
+      bool ok = lane < kBlockRows && row < m.cnt;
+      if (ok && ring) ok = m.pos[row] >= 0;
+      here = __ballot_sync(0xffffffffu, ok);
     }
     if (ring) {
       // A ring's row may be seen by some queries and not by others, and 0 times a NaN value is
       // NaN: its NaN values become zeros, and its key NaN, which only who sees it takes.
-#pragma unroll
-      for (int g = 0; g < kTilePages; ++g) {
-        const int seq = 2 * kTilePages * k + kTilePages + g;
-        if (!warp_wait(&s.raw_full[seq % P::kPieces], seq / P::kPieces & 1, abort)) return;
-        const uint8_t* v = s.raw[seq % P::kPieces] + uw * kBlockRows * D;
-        if (m.cnt[g] > 0)
+      const int seq = 2 * k + 1;
+      if (!warp_wait(&s.raw_full[seq % P::kPieces], seq / P::kPieces & 1, abort)) return;
+      const uint8_t* v = s.raw[seq % P::kPieces] + uw * kBlockRows * D;
 #pragma unroll 1
-          for (int r = 0; r < kBlockRows; r += 8) {
-            bool nan = false;
+      for (int r = 0; r < kBlockRows; r += 8) {
+        bool nan = false;
 #pragma unroll
-            for (int z = 0; z < D / 64; ++z) {
-              const uint4 x = *reinterpret_cast<const uint4*>(v + (r + lane / 4) * D +
-                                                              (lane % 4 * (D / 64) + z) * 16);
-              nan |= (__vcmpeq4(x.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(x.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
-                      __vcmpeq4(x.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(x.w & 0x7f7f7f7fu, 0x7f7f7f7fu)) != 0;
-            }
-            const uint32_t hit = __ballot_sync(0xffffffffu, nan);
-            for (int i = 0; i < 8; ++i)
-              if (hit >> (4 * i) & 15u) poison[g] |= 1u << (r + i);
+        for (int z = 0; z < D / 64; ++z) {
+          const uint4 x = *reinterpret_cast<const uint4*>(v + (r + lane / 4) * D +
+                                                          (lane % 4 * (D / 64) + z) * 16);
+          const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // a code's NaN is 0x7f: the only one that 1 carries into bit 7
+            const uint32_t y = (w4[i] & 0x7f7f7f7fu) + 0x01010101u;
+            nan |= (y & 0x80808080u) != 0;
           }
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, nan);
+        for (int i = 0; i < 8; ++i)
+          if (hit >> (4 * i) & 15u) poison |= 1u << (r + i);
       }
+      poison &= here;
     }
 #pragma unroll 1
     for (int side = 0; side < 2; ++side) {
-      const int oseq = 2 * k + side, slot = oseq % P::kOperands;
-      if (oseq >= P::kOperands && !warp_wait(&s.op_empty[slot], (oseq / P::kOperands - 1) & 1, abort))
+      const int seq = 2 * k + side, slot = seq % P::kOperands, raw = seq % P::kPieces;
+      if (seq >= P::kOperands && !warp_wait(&s.op_empty[slot], (seq / P::kOperands - 1) & 1, abort))
         return;
-#pragma unroll 1
-      for (int g = 0; g < kTilePages; ++g) {
-        const uint32_t here = g ? there[1] : there[0], bad_rows = g ? poison[1] : poison[0];
-        const int seq = 2 * kTilePages * k + side * kTilePages + g, raw = seq % P::kPieces;
-        if (!warp_wait(&s.raw_full[raw], seq / P::kPieces & 1, abort)) return;
-        const uint8_t* src = s.raw[raw] + uw * kBlockRows * D;
-        uint8_t* dst = s.op[slot] + (g * kPageRows + uw * kBlockRows) * 128;
-        auto put = [&](int r, int c, const uint32_t (&y)[8]) {
-          uint8_t* p = dst + c / 4 * P::kHalf + r * 128;
-          const int z = c % 4 * 2;
-          *reinterpret_cast<uint4*>(p + ((z ^ lr) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<uint4*>(p + (((z + 1) ^ lr) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
-        };
-        if (here == 0xffffu && bad_rows == 0) {
-          uint4 x[kIter];
+      if (!warp_wait(&s.raw_full[raw], seq / P::kPieces & 1, abort)) return;
+      const uint8_t* src = s.raw[raw] + uw * kBlockRows * D;
+      uint8_t* dst = s.op[slot] + uw * kBlockRows * 128;
+      auto put = [&](int r, int c, const uint32_t (&y)[8]) {
+        uint8_t* p = dst + c / 4 * P::kHalf + r * 128;
+        const int z = c % 4 * 2;
+        *reinterpret_cast<uint4*>(p + ((z ^ lr) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(p + (((z + 1) ^ lr) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+      };
+      if (here == 0xffffu && poison == 0) {
+        uint4 x[kIter];
 #pragma unroll
-          for (int i = 0; i < kIter; ++i)
-            x[i] = *reinterpret_cast<const uint4*>(src + row_of(i) * D + piece_of(i) * 16);
+        for (int i = 0; i < kIter; ++i)
+          x[i] = *reinterpret_cast<const uint4*>(src + row_of(i) * D + piece_of(i) * 16);
 #pragma unroll
-          for (int i = 0; i < kIter; ++i) {
-            const uint32_t y[8] = {decode2(x[i].x), decode2(x[i].x >> 16), decode2(x[i].y),
-                                   decode2(x[i].y >> 16), decode2(x[i].z), decode2(x[i].z >> 16),
-                                   decode2(x[i].w), decode2(x[i].w >> 16)};
-            put(row_of(i), piece_of(i), y);
-          }
-        } else {
-#pragma unroll 1
-          for (int i = 0; i < kIter; ++i) {
-            const int r = row_of(i), c = piece_of(i);
-            const bool ok = here >> r & 1, bad = bad_rows >> r & 1;
-            const uint4 x = *reinterpret_cast<const uint4*>(src + r * D + c * 16);
-            uint32_t y[8] = {decode2(x.x), decode2(x.x >> 16), decode2(x.y), decode2(x.y >> 16),
-                             decode2(x.z), decode2(x.z >> 16), decode2(x.w), decode2(x.w >> 16)};
-#pragma unroll
-            for (int z = 0; z < 8; ++z) {
-              if (bad)  // the codes' NaN is f16's 0x7fff
-                y[z] = side == 0 ? 0x7fff7fffu
-                                 : ((y[z] & 0x7fffu) == 0x7fffu ? 0u : y[z] & 0xffffu) |
-                                       ((y[z] & 0x7fff0000u) == 0x7fff0000u ? 0u : y[z] & 0xffff0000u);
-              if (!ok) y[z] = 0;
-            }
-            put(r, c, y);
-          }
+        for (int i = 0; i < kIter; ++i) {
+          const uint32_t y[8] = {decode2(x[i].x), decode2(x[i].x >> 16), decode2(x[i].y),
+                                 decode2(x[i].y >> 16), decode2(x[i].z), decode2(x[i].z >> 16),
+                                 decode2(x[i].w), decode2(x[i].w >> 16)};
+          put(row_of(i), piece_of(i), y);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.raw_empty[raw]);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kIter; ++i) {
+          const int r = row_of(i), c = piece_of(i);
+          const bool ok = here >> r & 1, bad = poison >> r & 1;
+          const uint4 x = *reinterpret_cast<const uint4*>(src + r * D + c * 16);
+          uint32_t y[8] = {decode2(x.x), decode2(x.x >> 16), decode2(x.y), decode2(x.y >> 16),
+                           decode2(x.z), decode2(x.z >> 16), decode2(x.w), decode2(x.w >> 16)};
+#pragma unroll
+          for (int z = 0; z < 8; ++z) {
+            if (bad)  // the codes' NaN is f16's 0x7fff
+              y[z] = side == 0 ? 0x7fff7fffu
+                               : ((y[z] & 0x7fffu) == 0x7fffu ? 0u : y[z] & 0xffffu) |
+                                     ((y[z] & 0x7fff0000u) == 0x7fff0000u ? 0u : y[z] & 0xffff0000u);
+            if (!ok) y[z] = 0;
+          }
+          put(r, c, y);
+        }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.raw_empty[raw]);
       fence_async_shared();  // the tensor cores read what the lanes have written
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.op_full[slot]);
@@ -469,19 +466,22 @@ __device__ __forceinline__ void widen(Smem<D, kTerms, kPair>& s, int uw, int tot
   }
 }
 
-// The thread that issues stream st's products.  (The scores of a tile overwrite P of the one before,
-// so they wait until its product is complete: two threads, so that neither stream waits for the
-// other's.)  Each tile's operands are released by both streams, used or not.
+// The thread that issues stream st's products.  A page's scores go to one of two places, when P of
+// the page two before, which lay there, has been used: so the softmax has the next page's scores
+// before it while the tensor cores take its weights.
 template <int D, int kTerms, bool kPair>
 __device__ __forceinline__ void issue(Smem<D, kTerms, kPair>& s, const PrefixParts& px, int st,
                                       Walk wk) {
   using P = Plan<D, kTerms, kPair>;
-  constexpr uint32_t kScores = idesc_f16(kTile, kTile, false), kValues = idesc_f16(kTile, D, true);
+  constexpr uint32_t kScores = idesc_f16(kTile, kPageRows, false);
+  constexpr uint32_t kValues = idesc_f16(kTile, D, true);
+  constexpr int kStep = kPair ? 1 : 2;
   volatile int* abort = &s.abort;
-  const uint32_t sc = s.tmem + s_col(st), oc = s.tmem + o_col(st);
-  int base = 0, units = 0, done = 0;  // key tiles, units, products P V of this stream
-  bool asked = false;
-  for (; wk.more(); wk.next(), ++units) {
+  const uint32_t oc = s.tmem + o_col(st);
+  int base = 0, units = 0;  // pages, units
+  int ns = 0, np = 0;       // this stream's pages whose scores, whose weighted values were asked for
+  bool asked = false, go = true;
+  for (; wk.more() && go; wk.next(), ++units) {
     const int nt = wk.count();
     const bool both = wk.both();
     if (st == 0) {
@@ -494,59 +494,61 @@ __device__ __forceinline__ void issue(Smem<D, kTerms, kPair>& s, const PrefixPar
     }
     if (!wait_or_stop(&s.q_full, units & 1, abort)) break;
     asked = false;
-    const uint64_t q = desc_kmajor_sw128(smem_addr(s.q) + (both ? st * kTerms * P::kQTerm : 0));
-    // Streams in step would have their products, then their softmaxes at the same time: stream 1
-    // begins a unit when stream 0 has asked for its first weighted values.
-    if (st == 1 && !wait_or_stop(&s.turn, units & 1, abort)) break;
-    bool stop = false;
+    if (kPair && st == 1 && !both) {  // no second tile of queries: the pages pass by
 #pragma unroll 1
-    for (int i = 0; i < nt; ++i) {
-      const int ks = 2 * (base + i) % P::kOperands, kp = 2 * (base + i) / P::kOperands & 1;
-      const int vs = (2 * (base + i) + 1) % P::kOperands, vp = (2 * (base + i) + 1) / P::kOperands & 1;
-      if (!both && (i & 1) != st) {  // the other stream's tile
-        if (!wait_or_stop(&s.op_full[ks], kp, abort)) stop = true;
-        if (!stop) mbar_arrive(&s.op_empty[ks]);
-        if (!stop && !wait_or_stop(&s.op_full[vs], vp, abort)) stop = true;
-        if (!stop) mbar_arrive(&s.op_empty[vs]);
-        if (stop) break;
-        continue;
+      for (int seq = 2 * base; seq < 2 * (base + nt) && go; ++seq) {
+        go = wait_or_stop(&s.op_full[seq % P::kOperands], seq / P::kOperands & 1, abort);
+        if (go) mbar_arrive(&s.op_empty[seq % P::kOperands]);
       }
-      if ((done > 0 && !wait_or_stop(&s.pv_done[st], (done - 1) & 1, abort)) ||
-          !wait_or_stop(&s.op_full[ks], kp, abort)) {
-        stop = true;
-        break;
+      if (!go) break;
+      mbar_arrive(&s.q_free);
+      base += nt;
+      continue;
+    }
+    const uint64_t q = desc_kmajor_sw128(smem_addr(s.q) + (both ? st * kTerms * P::kQTerm : 0));
+    const int first = kPair ? 0 : (base ^ st) & 1;  // the unit's first page of this stream
+    const int mine = nt > first ? (nt - first - 1) / kStep + 1 : 0;
+#pragma unroll 1
+    for (int pi = -2; pi < mine; ++pi) {
+      if (pi >= 0) {  // the weighted values of page pi
+        const int b = np & 1, seq = 2 * (base + first + pi * kStep) + 1, slot = seq % P::kOperands;
+        // (the first weights of a unit come when O of the unit before has been read)
+        go = wait_or_stop(&s.p_full[st][b], np >> 1 & 1, abort) &&
+             wait_or_stop(&s.op_full[slot], seq / P::kOperands & 1, abort);
+        if (!go) break;
+        tc_fence_after();
+        const uint64_t v = desc_mn_sw128(smem_addr(s.op[slot]), P::kHalf);
+        const uint32_t w = s.tmem + s_col(st, b);
+#pragma unroll
+        for (int kk = 0; kk < kPageRows / 16; ++kk)
+#pragma unroll
+          for (int term = 0; term < kTerms; ++term)
+            mma_ts(oc, w + kk / 2 * 32 + term * 16 + kk % 2 * 8, v + kk * (16 * 128 >> 4), kValues,
+                   pi > 0 || kk > 0 || term > 0);
+        umma_commit(&s.pv_done[st][b]);
+        umma_commit(&s.op_empty[slot]);
+        ++np;
       }
-      tc_fence_after();
-      const uint64_t kd = desc_kmajor_sw128(smem_addr(s.op[ks]));
-#pragma unroll
-      for (int term = 0; term < kTerms; ++term)
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const int off = kk / 4 * (P::kHalf >> 4) + kk % 4 * 2;
-          mma_ss(sc, q + term * (P::kQTerm >> 4) + off, kd + off, kScores, term > 0 || kk > 0);
-        }
-      umma_commit(&s.s_full[st]);
-      umma_commit(&s.op_empty[ks]);
-      // (the first weights of a unit come when O of the unit before has been read)
-      if (!wait_or_stop(&s.p_full[st], done & 1, abort) || !wait_or_stop(&s.op_full[vs], vp, abort)) {
-        stop = true;
-        break;
-      }
-      tc_fence_after();
-      const uint64_t v = desc_mn_sw128(smem_addr(s.op[vs]), P::kHalf);
-      const bool more = i >= (both ? 1 : 2);
-#pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk)
+      if (pi + 2 < mine) {  // the scores of page pi + 2
+        const int b = ns & 1, seq = 2 * (base + first + (pi + 2) * kStep), slot = seq % P::kOperands;
+        go = wait_or_stop(&s.op_full[slot], seq / P::kOperands & 1, abort) &&
+             (ns < 2 || wait_or_stop(&s.pv_done[st][b], ((ns >> 1) - 1) & 1, abort));
+        if (!go) break;
+        tc_fence_after();
+        const uint64_t kd = desc_kmajor_sw128(smem_addr(s.op[slot]));
+        const uint32_t sc = s.tmem + s_col(st, b);
 #pragma unroll
         for (int term = 0; term < kTerms; ++term)
-          mma_ts(oc, sc + kk / 2 * 32 + term * 16 + kk % 2 * 8, v + kk * (16 * 128 >> 4), kValues,
-                 more || kk > 0 || term > 0);
-      umma_commit(&s.pv_done[st]);
-      umma_commit(&s.op_empty[vs]);
-      if (st == 0 && i == 0) mbar_arrive(&s.turn);
-      ++done;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(sc, q + term * (P::kQTerm >> 4) + kk / 4 * (P::kQHalf >> 4) + kk % 4 * 2,
+                   kd + kk / 4 * (P::kHalf >> 4) + kk % 4 * 2, kScores, term > 0 || kk > 0);
+        umma_commit(&s.s_full[st][b]);
+        umma_commit(&s.op_empty[slot]);
+        ++ns;
+      }
     }
-    if (stop) break;
+    if (!go) break;
     mbar_arrive(&s.q_free);  // the weights were there, so the scores are complete
     base += nt;
   }
@@ -563,12 +565,12 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
   const int st = warp / 4, row = (warp & 3) * 32 + lane;
   volatile int* abort = &s.abort;
   const uint32_t lanes = s.tmem + ((uint32_t)((warp & 3) * 32) << 16);
-  const uint32_t sc = lanes + s_col(st), oc = lanes + o_col(st);
-  int k = 0, mine = 0, cta = blockIdx.x;  // key tiles of the block, those of this stream
+  const uint32_t oc = lanes + o_col(st);
+  int k = 0, mine = 0;  // pages of the block, those of this stream
   for (; wk.more(); wk.next()) {
     const int nt = wk.count();
     const bool both = wk.both();
-    const int tile = wk.tile() + (both ? st : 0), j = tile * kTile + row;
+    const int tile = wk.tile() + (kPair ? st : 0), j = tile * kTile + row;
     const int t = j < px.nq ? n.pos[j / R] : -1;
     const float fq = t < 0 ? 0.f : px.qf[((size_t)wk.c * px.tiles + tile) * kTile + row];
     const bool work = __any_sync(0xffffffffu, t >= 0);  // else no lane's result is asked for
@@ -577,60 +579,44 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
     const int t_hi = (int)__reduce_max_sync(0xffffffffu, t < 0 ? 0u : (uint32_t)t);
     float ms = kNoScore, mo = kNoScore, l = 0.f;  // reference of the scores; + V's exponent; sum
     int taken = 0;
+#pragma unroll 1
     for (int i = 0; i < nt; ++i, ++k) {
       const int slot = k % kMetas;
-      if (!both && (i & 1) != st) {  // the other stream's
-        if (!warp_wait(&s.meta_full[slot], k / kMetas & 1, abort)) return;
-        __syncwarp();
+      if (!warp_wait(&s.meta_full[slot], k / kMetas & 1, abort)) return;
+      if (kPair ? st == 1 && !both : (k & 1) != st) {  // the other stream's
         if (lane == 0) mbar_arrive(&s.meta_empty[slot]);
         continue;
       }
-      if (!warp_wait(&s.meta_full[slot], k / kMetas & 1, abort)) return;
-      const TileMeta& m = s.meta[slot];
-      if (!warp_wait(&s.s_full[st], mine & 1, abort)) return;
+      const PageMeta& m = s.meta[slot];
+      const uint4 head = *reinterpret_cast<const uint4*>(&m);
+      const int b2 = mine & 1;
+      const uint32_t sc = lanes + s_col(st, b2);
+      if (!warp_wait(&s.s_full[st][b2], mine >> 1 & 1, abort)) return;
       tc_fence_after();
       if (work) {
-        const uint4 e4 = *reinterpret_cast<const uint4*>(m.exps);
-        const int cnt0 = m.cnt[0], cnt1 = m.cnt[1], w = m.w;
-        const bool ring = m.ring;
-        // Which keys does any query of the warp see, as bits of the tile's four columns of 32, and
-        // do all of them see those?  (A ring also holds positions that no one sees any more.)
-        uint32_t there[4];
-        bool near = true;
-        if (ring) {
-          bool same = true;
+        const int cnt = (int)head.z, w = (int)head.w;
+        if (cnt < kPageRows || w > 0) {
+          // Which keys does any query of the warp see, as bits of the two columns of 32, and do
+          // all of them see those?  (A ring also holds positions that no one sees any more.)
+          uint32_t there[2];
+          bool near = true;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int p = m.pos[x * 32 + lane];
-            const bool ok = (x & 1) * 32 + lane < (x < 2 ? cnt0 : cnt1) && p >= 0;
-            const bool any = ok && p <= t_hi && t_lo - p < w;
-            same &= any == (ok && p <= t_lo && t_hi - p < w);
+          for (int x = 0; x < 2; ++x) {
+            const bool ok = x * 32 + lane < cnt;
+            bool any = ok;
+            if (w > 0) {
+              const int p = m.pos[x * 32 + lane];
+              any = ok && p >= 0 && p <= t_hi && t_lo - p < w;
+              near &= any == (ok && p >= 0 && p <= t_lo && t_hi - p < w);
+            }
             there[x] = __ballot_sync(0xffffffffu, any);
           }
-          near = __all_sync(0xffffffffu, same);
-        } else {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int left = (x < 2 ? cnt0 : cnt1) - (x & 1) * 32;
-            there[x] = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1;
-          }
-        }
-        const bool whole = near && (there[0] & there[1] & there[2] & there[3]) == 0xffffffffu;
-        // factor of a block's scores and the exponent of its values, from the bytes of two blocks
-        auto factor = [&](uint32_t ew, int b) {
-          return fminf(fq * pow2f((int)(signed char)(ew >> (16 * b) & 0xff)), 1.7e38f);
-        };
-        auto vexp = [&](uint32_t ew, int b) {
-          return (float)(signed char)(ew >> (16 * b + 8) & 0xff);
-        };
-        // The loops over 32 keys stay loops: unrolled, the warps' code outgrows the instruction
-        // cache (a tile then took two to five times as long).
-        float smax = FG_NEG_INF, omax = FG_NEG_INF;
-        if (!whole) {  // keys that do not count score -inf
+          near = __all_sync(0xffffffffu, near);
+          // keys that do not count score -inf
 #pragma unroll 1
-          for (int ch = 0; ch < 4; ++ch) {
+          for (int ch = 0; ch < 2; ++ch) {
             constexpr uint32_t kNone = 0xff800000u;
-            const uint32_t bits = ch == 0 ? there[0] : ch == 1 ? there[1] : ch == 2 ? there[2] : there[3];
+            const uint32_t bits = ch ? there[1] : there[0];
             if (near && bits == 0xffffffffu) continue;
             uint32_t r[32];
             tmem_ld32(sc + ch * 32, r);
@@ -639,8 +625,8 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
             for (int e = 0; e < 32; e += 4)
               if ((bits >> e & 15u) != 15u) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (!(bits >> (e + i) & 1)) r[e + i] = kNone;
+                for (int x = 0; x < 4; ++x)
+                  if (!(bits >> (e + x) & 1)) r[e + x] = kNone;
               }
             if (!near) {
 #pragma unroll
@@ -648,8 +634,8 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
                 const int4 p = *reinterpret_cast<const int4*>(m.pos + ch * 32 + e);
                 const int p4[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (p4[i] > t || (uint32_t)t - (uint32_t)p4[i] >= (uint32_t)w) r[e + i] = kNone;
+                for (int x = 0; x < 4; ++x)
+                  if (p4[x] > t || (uint32_t)t - (uint32_t)p4[x] >= (uint32_t)w) r[e + x] = kNone;
               }
             }
             tmem_st16(sc + ch * 32, r);
@@ -657,62 +643,66 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
           }
           tmem_wait_st();
         }
-        auto tops = [&](uint32_t ew, const uint32_t (&r)[32]) {
+        uint32_t r[2][32];  // the row of S
+        tmem_ld32(sc, r[0]);
+        tmem_ld32(sc + 32, r[1]);
+        // factors of the blocks' scores and the exponents of their values
+        float f[4], ev[4];
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            float mx = FG_NEG_INF;
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t x = (b < 2 ? head.x : head.y) >> (16 * (b & 1));
+          f[b] = fminf(fq * pow2f((int)(signed char)(x & 0xff)), 1.7e38f);
+          ev[b] = (float)(signed char)(x >> 8 & 0xff);
+        }
+        tmem_wait_ld(r[0]);
+        reg_barrier(r[1]);
+        float smax = FG_NEG_INF, omax = FG_NEG_INF;
 #pragma unroll
-            for (int e = 0; e < 16; e += 2)
-              mx = max3(mx, __uint_as_float(r[b * 16 + e]), __uint_as_float(r[b * 16 + e + 1]));
-            const float y = mx * factor(ew, b);
-            smax = fmaxf(smax, y);
-            omax = fmaxf(omax, y + vexp(ew, b));
-          }
-        };
-        // 32 columns are on their way while the 32 before them are worked on
-        uint32_t ra[32], rb[32];
-        tmem_ld32(sc, ra);
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          tmem_wait_ld(ra);
-          tmem_ld32(sc + h * 64 + 32, rb);
-          tops(h ? e4.z : e4.x, ra);
-          tmem_wait_ld(rb);
-          if (h == 0) tmem_ld32(sc + 64, ra);
-          tops(h ? e4.w : e4.y, rb);
+        for (int b = 0; b < 4; ++b) {
+          float mx = FG_NEG_INF;
+#pragma unroll
+          for (int e = 0; e < 16; e += 2)
+            mx = max3(mx, __uint_as_float(r[b / 2][b % 2 * 16 + e]),
+                      __uint_as_float(r[b / 2][b % 2 * 16 + e + 1]));
+          const float y = mx * f[b];
+          smax = fmaxf(smax, y);
+          omax = fmaxf(omax, y + ev[b]);
         }
         if (__any_sync(0xffffffffu, smax > ms + kSlack || omax > mo + kSlack)) {
-          const float sn = fmaxf(ms, smax), on = fmaxf(mo, omax), f = ex2(mo - on);
+          const float sn = fmaxf(ms, smax), on = fmaxf(mo, omax), z = ex2(mo - on);
           l *= ex2(ms - sn);
           ms = sn;
           mo = on;
-          if (taken > 0) {
+          if (taken > 0) {  // O, when the product before is complete
+            if (!warp_wait(&s.pv_done[st][b2 ^ 1], (mine - 1) >> 1 & 1, abort)) return;
+            tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t r[32];
-              tmem_ld32(oc + c, r);
-              tmem_wait_ld(r);
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(oc + c, o);
+              tmem_wait_ld16(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-              tmem_st16(oc + c, r);
-              tmem_st16(oc + c + 16, r + 16);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * z);
+              tmem_st16(oc + c, o);
             }
           }
         }
         uint64_t sum2 = 0;  // (0, 0)
         const uint64_t nm2 = pack2(-ms, -ms);
         const float lift = ms - mo + kProdBits;
-        auto form = [&](int ch, uint32_t ew, const uint32_t (&r)[32]) {
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
           uint32_t hi[16], lo[16];
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const float f = factor(ew, b), g = ex2(fminf(vexp(ew, b) + lift, 126.f));
-            const uint64_t f2 = pack2(f, f), g2 = pack2(g, g);
+            const float g = ex2(fminf(ev[ch * 2 + b] + lift, 126.f));
+            const uint64_t f2 = pack2(f[ch * 2 + b], f[ch * 2 + b]), g2 = pack2(g, g);
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
               const int z = b * 16 + e;
               float x0, x1, p0, p1;
-              unpack2(fma2(pack2(__uint_as_float(r[z]), __uint_as_float(r[z + 1])), f2, nm2), x0, x1);
+              unpack2(fma2(pack2(__uint_as_float(r[ch][z]), __uint_as_float(r[ch][z + 1])), f2, nm2),
+                      x0, x1);
               const uint64_t w2 = pack2(ex2(x0), ex2(x1));
               sum2 = add2(sum2, w2);
               unpack2(mul2(w2, g2), p0, p1);
@@ -725,55 +715,45 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
           }
           tmem_st16(sc + ch * 32, hi);
           if constexpr (kTerms == 2) tmem_st16(sc + ch * 32 + 16, lo);
-        };
-        tmem_ld32(sc, ra);
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          tmem_wait_ld(ra);
-          tmem_ld32(sc + h * 64 + 32, rb);
-          form(2 * h, h ? e4.z : e4.x, ra);
-          tmem_wait_ld(rb);
-          if (h == 0) tmem_ld32(sc + 64, ra);
-          form(2 * h + 1, h ? e4.w : e4.y, rb);
         }
-        float a, b;
-        unpack2(sum2, a, b);
-        l += a + b;
+        float x, y;
+        unpack2(sum2, x, y);
+        l += x + y;
         tmem_wait_st();
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&s.p_full[st]);
+        mbar_arrive(&s.p_full[st][b2]);
         mbar_arrive(&s.meta_empty[slot]);
       }
       ++mine;
       ++taken;
     }
     // the unit's partial result
-    const size_t part = ((size_t)cta + wk.unit()) * 2 + st;
+    const size_t part = ((size_t)blockIdx.x + wk.unit()) * 2 + st;
     const bool write = row < px.rows && t >= 0;
     if (write)
       *reinterpret_cast<float2*>(px.ml + 2 * (part * px.rows + row)) = make_float2(ms, l);
     if (taken > 0) {
-      if (!warp_wait(&s.pv_done[st], (mine - 1) & 1, abort)) return;
+      if (!warp_wait(&s.pv_done[st][(mine - 1) & 1], (mine - 1) >> 1 & 1, abort)) return;
       tc_fence_after();
       if (work) {
         // O is in units of 2^(mo - kProdBits), l of 2^ms
-        const float f = l == 0.f ? 0.f : exp2f(mo - ms - kProdBits) / l;
+        const float z = l == 0.f ? 0.f : exp2f(mo - ms - kProdBits) / l;
         // [d / 4][rows][4]: a warp's lanes write next to one another
         float4* out = reinterpret_cast<float4*>(px.acc + part * px.rows * D) + row;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
-          uint32_t r[32];
-          tmem_ld32(oc + c, r);
-          tmem_wait_ld(r);
+          uint32_t o[32];
+          tmem_ld32(oc + c, o);
+          tmem_wait_ld(o);
           if (write)
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
               out[(size_t)((c + e) / 4) * px.rows] =
-                  make_float4(__uint_as_float(r[e]) * f, __uint_as_float(r[e + 1]) * f,
-                              __uint_as_float(r[e + 2]) * f, __uint_as_float(r[e + 3]) * f);
+                  make_float4(__uint_as_float(o[e]) * z, __uint_as_float(o[e + 1]) * z,
+                              __uint_as_float(o[e + 2]) * z, __uint_as_float(o[e + 3]) * z);
         }
       }
       tc_fence_before();
@@ -805,17 +785,17 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     }
     for (int i = 0; i < P::kOperands; ++i) {
       mbar_init(&s.op_full[i], kUnpackWarps);
-      mbar_init(&s.op_empty[i], 2);
+      mbar_init(&s.op_empty[i], kPair ? 2 : 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.p_full[i], kSoftWarps / 2);
-      mbar_init(&s.pv_done[i], 1);
-      mbar_init(&s.drain[i], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s.s_full[0][0] + i, 1);
+      mbar_init(&s.p_full[0][0] + i, kSoftWarps / 2);
+      mbar_init(&s.pv_done[0][0] + i, 1);
     }
+    mbar_init(&s.drain[0], 1);
+    mbar_init(&s.drain[1], 1);
     mbar_init(&s.q_full, 1);
     mbar_init(&s.q_free, 2);
-    mbar_init(&s.turn, 1);
     fence_barrier_init();
   }
   griddep_wait();
