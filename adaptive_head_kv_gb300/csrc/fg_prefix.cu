@@ -32,9 +32,10 @@ namespace {
 using namespace sm100;
 
 constexpr int kTile = kPrefixTile;  // queries of a tile
-constexpr int kUnpackWarps = 4, kSoftWarps = 8;
 // warps 0-7 softmax (warp w reads tensor memory lanes 32 (w % 4) ..), 8-11 widen
-constexpr int kLoadWarp = kSoftWarps + kUnpackWarps, kMmaWarp = kLoadWarp + 1;  // and the next
+constexpr int kSoftWarps = 8, kUnpackWarps = 4;
+constexpr int kLoadWarp = kSoftWarps + kUnpackWarps, kMetaWarp = kLoadWarp + 1;
+constexpr int kMmaWarp = kMetaWarp + 1;  // and the next
 constexpr int kPrefixThreads = (kMmaWarp + 2) * 32;
 constexpr int kMetas = 8;  // pages whose description is there
 constexpr float kSlack = 8.f;
@@ -60,9 +61,9 @@ struct Plan {
   // Widened K or V pages in shared memory.  Where the streams take pages in turns, a multiple of
   // four, so that a place always has the same stream's pages.
   static constexpr int kOperands = kPair ? 6 : kTerms == 2 && D == 128 ? 4 : 8;
-  static constexpr int kRoom = (kSmem - 1024 - 3584 - kQBytes - kOperands * kOpBytes) / kPiece;
-  static constexpr int kPieces = kRoom > 16 ? 16 : kRoom;
-  static_assert(kPieces >= 2 && (kPair || kOperands % 4 == 0), "a page's codes are there together");
+  static constexpr int kRoom = (kSmem - 1024 - 3584 - kQBytes - kOperands * kOpBytes) / (2 * kPiece);
+  static constexpr int kRaw = kRoom > 8 ? 8 : kRoom;  // pages of codes in shared memory
+  static_assert(kRaw >= 2 && (kPair || kOperands % 4 == 0), "rings of a block");
 };
 
 template <int D, int kTerms, bool kPair>
@@ -70,9 +71,9 @@ struct alignas(1024) Smem {
   using P = Plan<D, kTerms, kPair>;
   uint8_t q[P::kQBytes];
   uint8_t op[P::kOperands][P::kOpBytes];
-  alignas(128) uint8_t raw[P::kPieces][P::kPiece];
+  alignas(128) uint8_t raw[P::kRaw][2 * P::kPiece];  // K, V
   alignas(16) PageMeta meta[kMetas];
-  uint64_t raw_full[P::kPieces], raw_empty[P::kPieces];
+  uint64_t raw_full[P::kRaw], raw_empty[P::kRaw];
   uint64_t meta_full[kMetas], meta_empty[kMetas];
   uint64_t op_full[P::kOperands], op_empty[P::kOperands];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // of a stream's two places of S
@@ -97,6 +98,17 @@ __device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, vol
     if (*abort) return false;
   }
   return true;
+}
+__device__ __forceinline__ bool test_bar(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 // The same by a whole warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
@@ -280,14 +292,13 @@ struct Walk {
   }
 };
 
-template <int D, int kTerms, bool kPair>
-__device__ __forceinline__ void load_pages(Smem<D, kTerms, kPair>& s, const PagedArgs& a, Walk wk) {
-  using P = Plan<D, kTerms, kPair>;
+// Calls page(k, page number or -1, exponents, first row, rows, is it a ring's, ring slots) for every
+// page of the block in order, until that returns false (all lanes; one warp).
+template <typename F>
+__device__ __forceinline__ void each_page(const PagedArgs& a, Walk wk, F&& page) {
   const int lane = threadIdx.x & 31;
-  volatile int* abort = &s.abort;
-  int k = 0, pieces = 0, metas = 0;  // pages of this block; copies asked for so far
-  bool stop = false;
-  for (; wk.more() && !stop; wk.next()) {
+  int k = 0;
+  for (; wk.more(); wk.next()) {
     const fg_paged_desc hd = a.caches[wk.c];
     const int rows = live_rows(hd, a.rows[wk.c]), w = ring_slots(hd, a.max_w);
     const int seg = cdiv(rows, kPageRows), t0 = wk.first(), nt = wk.count();
@@ -295,70 +306,89 @@ __device__ __forceinline__ void load_pages(Smem<D, kTerms, kPair>& s, const Page
     uint2 exp_l = make_uint2(0, 0);
 #pragma unroll 1
     for (int i = 0; i < nt; ++i, ++k) {
+      const int t = t0 + i;
       if ((i & 31) == 0) {  // the next 32 pages: lane l holds one and its exponents
-        const int t = t0 + i + lane;
         page_l = -1;
         if (i + lane < nt) {
-          page_l = t < seg ? page_at(a, hd.first_page, hd.max_pages, t)
-                           : page_at(a, hd.ring_page, hd.ring_pages, t - seg);
+          const int e = t + lane;
+          page_l = e < seg ? page_at(a, hd.first_page, hd.max_pages, e)
+                           : page_at(a, hd.ring_page, hd.ring_pages, e - seg);
           if (page_l < 0)
             atomicOr(a.dev_err, kErrInvalid);
           else
             exp_l = *reinterpret_cast<const uint2*>(a.exps + (size_t)page_l * kPageBlocks * 2);
         }
       }
-      const int t = t0 + i;
       const bool ring = t >= seg;
-      const int page = __shfl_sync(0xffffffffu, page_l, i & 31);
       uint2 ex;
       ex.x = __shfl_sync(0xffffffffu, exp_l.x, i & 31);
       ex.y = __shfl_sync(0xffffffffu, exp_l.y, i & 31);
-      if (lane == 0) {
-        const int ms = k % kMetas;
-        if (k >= kMetas && !wait_or_stop(&s.meta_empty[ms], (k / kMetas - 1) & 1, abort)) stop = true;
-        if (!stop) {
-          PageMeta& m = s.meta[ms];
-          m.exps[0] = ex.x;
-          m.exps[1] = ex.y;
-          m.cnt = page < 0 ? 0 : min(kPageRows, (ring ? w : rows) - (ring ? t - seg : t) * kPageRows);
-          m.w = ring ? w : 0;
-          const bool copy = ring && page >= 0;
-          mbar_expect_tx(&s.meta_full[ms], copy ? kPageRows * 4 : 0);
-          ++metas;
-          if (copy)
-            bulk_load(m.pos, a.pos + (size_t)page * kPageRows, kPageRows * 4, &s.meta_full[ms]);
-        }
-#pragma unroll 1
-        for (int side = 0; side < 2 && !stop; ++side) {
-          const int seq = 2 * k + side, slot = seq % P::kPieces;
-          if (seq >= P::kPieces &&
-              !wait_or_stop(&s.raw_empty[slot], (seq / P::kPieces - 1) & 1, abort)) {
-            stop = true;
-            break;
-          }
-          ++pieces;
-          if (page < 0) {
-            mbar_arrive(&s.raw_full[slot]);
-          } else {
-            mbar_expect_tx(&s.raw_full[slot], P::kPiece);
-            bulk_load(s.raw[slot], (side ? a.vp : a.kp) + (size_t)page * P::kPiece, P::kPiece,
-                      &s.raw_full[slot]);
-          }
-        }
-      }
-      stop = __shfl_sync(0xffffffffu, stop, 0);
-      if (stop) break;
+      if (!page(k, __shfl_sync(0xffffffffu, page_l, i & 31), ex,
+                (ring ? w : rows) - (ring ? t - seg : t) * kPageRows, ring ? w : 0))
+        return;
     }
-  }
-  if (*abort && lane == 0) {  // what is in flight lands before the block ends
-    for (int i = max(0, pieces - P::kPieces); i < pieces; ++i)
-      mbar_wait(&s.raw_full[i % P::kPieces], i / P::kPieces & 1);
-    for (int i = max(0, metas - kMetas); i < metas; ++i)
-      mbar_wait(&s.meta_full[i % kMetas], i / kMetas & 1);
   }
 }
 
-// One of the four warps that widen codes: rows 16 w .. of every page, where an operand row that is
+// The warp that loads the pages' codes.
+template <int D, int kTerms, bool kPair>
+__device__ __forceinline__ void load_pages(Smem<D, kTerms, kPair>& s, const PagedArgs& a, Walk wk) {
+  using P = Plan<D, kTerms, kPair>;
+  volatile int* abort = &s.abort;
+  int pages = 0;  // asked for so far
+  each_page(a, wk, [&](int k, int page, uint2, int, int) {
+    bool go = true;
+    if ((threadIdx.x & 31) == 0) {
+      const int slot = k % P::kRaw;
+      go = k < P::kRaw || wait_or_stop(&s.raw_empty[slot], (k / P::kRaw - 1) & 1, abort);
+      if (go) {
+        ++pages;
+        if (page < 0) {
+          mbar_arrive(&s.raw_full[slot]);
+        } else {
+          mbar_expect_tx(&s.raw_full[slot], 2 * P::kPiece);
+          bulk_load(s.raw[slot], a.kp + (size_t)page * P::kPiece, P::kPiece, &s.raw_full[slot]);
+          bulk_load(s.raw[slot] + P::kPiece, a.vp + (size_t)page * P::kPiece, P::kPiece,
+                    &s.raw_full[slot]);
+        }
+      }
+    }
+    return (bool)__shfl_sync(0xffffffffu, go, 0);
+  });
+  if (*abort && (threadIdx.x & 31) == 0)  // what is in flight lands before the block ends
+    for (int i = max(0, pages - P::kRaw); i < pages; ++i)
+      mbar_wait(&s.raw_full[i % P::kRaw], i / P::kRaw & 1);
+}
+
+// The warp that describes them.
+template <int D, int kTerms, bool kPair>
+__device__ __forceinline__ void load_metas(Smem<D, kTerms, kPair>& s, const PagedArgs& a, Walk wk) {
+  volatile int* abort = &s.abort;
+  int metas = 0;
+  each_page(a, wk, [&](int k, int page, uint2 ex, int left, int w) {
+    bool go = true;
+    if ((threadIdx.x & 31) == 0) {
+      const int slot = k % kMetas;
+      go = k < kMetas || wait_or_stop(&s.meta_empty[slot], (k / kMetas - 1) & 1, abort);
+      if (go) {
+        PageMeta& m = s.meta[slot];
+        *reinterpret_cast<uint4*>(&m) = make_uint4(ex.x, ex.y, page < 0 ? 0 : min(kPageRows, left), w);
+        const bool copy = w > 0 && page >= 0;
+        mbar_expect_tx(&s.meta_full[slot], copy ? kPageRows * 4 : 0);
+        ++metas;
+        if (copy)
+          bulk_load(m.pos, a.pos + (size_t)page * kPageRows, kPageRows * 4, &s.meta_full[slot]);
+      }
+    }
+    return (bool)__shfl_sync(0xffffffffu, go, 0);
+  });
+  if (*abort && (threadIdx.x & 31) == 0)
+    for (int i = max(0, metas - kMetas); i < metas; ++i)
+      mbar_wait(&s.meta_full[i % kMetas], i / kMetas & 1);
+}
+
+// One of the four warps that widen codes: rows 16 w .. of every page (a warp that skipped pages could
+// take a barrier's phase for the one two before it), where an operand row that is
 // not there is zero.  A lane's 16 bytes and the 32 it makes of them are chosen so that the eight
 // lanes of a phase meet eight different banks, in the codes and in the swizzled operand.
 template <int D, int kTerms, bool kPair>
@@ -374,23 +404,25 @@ __device__ __forceinline__ void widen(Smem<D, kTerms, kPair>& s, int uw, int tot
   };
 #pragma unroll 1
   for (int k = 0; k < total; ++k) {
-    const int ms = k % kMetas;
+    const int ms = k % kMetas, raw = k % P::kRaw;
     if (!warp_wait(&s.meta_full[ms], k / kMetas & 1, abort)) return;
     const PageMeta& m = s.meta[ms];
-    const bool ring = m.w > 0;
+    const int cnt = m.cnt, w = m.w;
     uint32_t here = 0xffffu, poison = 0;
-    if (ring || m.cnt < kPageRows) {
+    if (w > 0 || cnt < kPageRows) {
       const int row = uw * kBlockRows + lane;
-      bool ok = lane < kBlockRows && row < m.cnt;
-      if (ok && ring) ok = m.pos[row] >= 0;
+      bool ok = lane < kBlockRows && row < cnt;
+      if (ok && w > 0) ok = m.pos[row] >= 0;
       here = __ballot_sync(0xffffffffu, ok);
     }
-    if (ring) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.meta_empty[ms]);
+    if (!warp_wait(&s.raw_full[raw], k / P::kRaw & 1, abort)) return;
+    const uint8_t* codes = s.raw[raw] + uw * kBlockRows * D;
+    if (w > 0) {
       // A ring's row may be seen by some queries and not by others, and 0 times a NaN value is
       // NaN: its NaN values become zeros, and its key NaN, which only who sees it takes.
-      const int seq = 2 * k + 1;
-      if (!warp_wait(&s.raw_full[seq % P::kPieces], seq / P::kPieces & 1, abort)) return;
-      const uint8_t* v = s.raw[seq % P::kPieces] + uw * kBlockRows * D;
+      const uint8_t* v = codes + P::kPiece;
 #pragma unroll 1
       for (int r = 0; r < kBlockRows; r += 8) {
         bool nan = false;
@@ -411,40 +443,45 @@ __device__ __forceinline__ void widen(Smem<D, kTerms, kPair>& s, int uw, int tot
       }
       poison &= here;
     }
-#pragma unroll 1
-    for (int side = 0; side < 2; ++side) {
-      const int seq = 2 * k + side, slot = seq % P::kOperands, raw = seq % P::kPieces;
-      if (seq >= P::kOperands && !warp_wait(&s.op_empty[slot], (seq / P::kOperands - 1) & 1, abort))
-        return;
-      if (!warp_wait(&s.raw_full[raw], seq / P::kPieces & 1, abort)) return;
-      const uint8_t* src = s.raw[raw] + uw * kBlockRows * D;
-      uint8_t* dst = s.op[slot] + uw * kBlockRows * 128;
-      auto put = [&](int r, int c, const uint32_t (&y)[8]) {
-        uint8_t* p = dst + c / 4 * P::kHalf + r * 128;
-        const int z = c % 4 * 2;
-        *reinterpret_cast<uint4*>(p + ((z ^ lr) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<uint4*>(p + (((z + 1) ^ lr) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
-      };
-      if (here == 0xffffu && poison == 0) {
-        uint4 x[kIter];
+    const bool plain = here == 0xffffu && poison == 0;
+    auto put = [&](uint8_t* dst, int r, int c, const uint32_t (&y)[8]) {
+      uint8_t* p = dst + c / 4 * P::kHalf + r * 128;
+      const int z = c % 4 * 2;
+      *reinterpret_cast<uint4*>(p + ((z ^ lr) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint4*>(p + (((z + 1) ^ lr) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+    };
+    // K and V are read before either is written: one wait for both
+    uint4 x[2][kIter];
+    if (plain) {
+#pragma unroll
+      for (int side = 0; side < 2; ++side)
 #pragma unroll
         for (int i = 0; i < kIter; ++i)
-          x[i] = *reinterpret_cast<const uint4*>(src + row_of(i) * D + piece_of(i) * 16);
+          x[side][i] = *reinterpret_cast<const uint4*>(codes + side * P::kPiece + row_of(i) * D +
+                                                       piece_of(i) * 16);
+    }
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      const int seq = 2 * k + side, slot = seq % P::kOperands;
+      if (seq >= P::kOperands && !warp_wait(&s.op_empty[slot], (seq / P::kOperands - 1) & 1, abort))
+        return;
+      uint8_t* dst = s.op[slot] + uw * kBlockRows * 128;
+      if (plain) {
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
-          const uint32_t y[8] = {decode2(x[i].x), decode2(x[i].x >> 16), decode2(x[i].y),
-                                 decode2(x[i].y >> 16), decode2(x[i].z), decode2(x[i].z >> 16),
-                                 decode2(x[i].w), decode2(x[i].w >> 16)};
-          put(row_of(i), piece_of(i), y);
+          const uint4 z = x[side][i];
+          const uint32_t y[8] = {decode2(z.x), decode2(z.x >> 16), decode2(z.y), decode2(z.y >> 16),
+                                 decode2(z.z), decode2(z.z >> 16), decode2(z.w), decode2(z.w >> 16)};
+          put(dst, row_of(i), piece_of(i), y);
         }
       } else {
 #pragma unroll 1
         for (int i = 0; i < kIter; ++i) {
           const int r = row_of(i), c = piece_of(i);
           const bool ok = here >> r & 1, bad = poison >> r & 1;
-          const uint4 x = *reinterpret_cast<const uint4*>(src + r * D + c * 16);
-          uint32_t y[8] = {decode2(x.x), decode2(x.x >> 16), decode2(x.y), decode2(x.y >> 16),
-                           decode2(x.z), decode2(x.z >> 16), decode2(x.w), decode2(x.w >> 16)};
+          const uint4 z4 = *reinterpret_cast<const uint4*>(codes + side * P::kPiece + r * D + c * 16);
+          uint32_t y[8] = {decode2(z4.x), decode2(z4.x >> 16), decode2(z4.y), decode2(z4.y >> 16),
+                           decode2(z4.z), decode2(z4.z >> 16), decode2(z4.w), decode2(z4.w >> 16)};
 #pragma unroll
           for (int z = 0; z < 8; ++z) {
             if (bad)  // the codes' NaN is f16's 0x7fff
@@ -453,16 +490,16 @@ __device__ __forceinline__ void widen(Smem<D, kTerms, kPair>& s, int uw, int tot
                                      ((y[z] & 0x7fff0000u) == 0x7fff0000u ? 0u : y[z] & 0xffff0000u);
             if (!ok) y[z] = 0;
           }
-          put(r, c, y);
+          put(dst, r, c, y);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.raw_empty[raw]);
       fence_async_shared();  // the tensor cores read what the lanes have written
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s.op_full[slot]);
+      if (lane == 0) {
+        mbar_arrive(&s.op_full[slot]);
+        if (side == 1) mbar_arrive(&s.raw_empty[raw]);
+      }
     }
-    if (lane == 0) mbar_arrive(&s.meta_empty[ms]);
   }
 }
 
@@ -508,44 +545,63 @@ __device__ __forceinline__ void issue(Smem<D, kTerms, kPair>& s, const PrefixPar
     const uint64_t q = desc_kmajor_sw128(smem_addr(s.q) + (both ? st * kTerms * P::kQTerm : 0));
     const int first = kPair ? 0 : (base ^ st) & 1;  // the unit's first page of this stream
     const int mine = nt > first ? (nt - first - 1) / kStep + 1 : 0;
+    // What is ready goes first, weighted values before scores: a page's operands come in order, so
+    // waiting for a key page while weights are there would hold up the pages before it.
+    int si = 0, pi = 0;
+    long long since = 0;
 #pragma unroll 1
-    for (int pi = -2; pi < mine; ++pi) {
-      if (pi >= 0) {  // the weighted values of page pi
+    while (pi < mine) {
+      bool did = false;
+      if (pi < si) {  // the weighted values of page pi
         const int b = np & 1, seq = 2 * (base + first + pi * kStep) + 1, slot = seq % P::kOperands;
         // (the first weights of a unit come when O of the unit before has been read)
-        go = wait_or_stop(&s.p_full[st][b], np >> 1 & 1, abort) &&
-             wait_or_stop(&s.op_full[slot], seq / P::kOperands & 1, abort);
-        if (!go) break;
-        tc_fence_after();
-        const uint64_t v = desc_mn_sw128(smem_addr(s.op[slot]), P::kHalf);
-        const uint32_t w = s.tmem + s_col(st, b);
+        if (test_bar(&s.p_full[st][b], np >> 1 & 1) &&
+            test_bar(&s.op_full[slot], seq / P::kOperands & 1)) {
+          tc_fence_after();
+          const uint64_t v = desc_mn_sw128(smem_addr(s.op[slot]), P::kHalf);
+          const uint32_t w = s.tmem + s_col(st, b);
 #pragma unroll
-        for (int kk = 0; kk < kPageRows / 16; ++kk)
+          for (int kk = 0; kk < kPageRows / 16; ++kk)
+#pragma unroll
+            for (int term = 0; term < kTerms; ++term)
+              mma_ts(oc, w + kk / 2 * 32 + term * 16 + kk % 2 * 8, v + kk * (16 * 128 >> 4), kValues,
+                     pi > 0 || kk > 0 || term > 0);
+          umma_commit(&s.pv_done[st][b]);
+          umma_commit(&s.op_empty[slot]);
+          ++np;
+          ++pi;
+          did = true;
+        }
+      }
+      if (si < mine && si < pi + 2) {  // the scores of page si
+        const int b = ns & 1, seq = 2 * (base + first + si * kStep), slot = seq % P::kOperands;
+        if (test_bar(&s.op_full[slot], seq / P::kOperands & 1) &&
+            (ns < 2 || test_bar(&s.pv_done[st][b], ((ns >> 1) - 1) & 1))) {
+          tc_fence_after();
+          const uint64_t kd = desc_kmajor_sw128(smem_addr(s.op[slot]));
+          const uint32_t sc = s.tmem + s_col(st, b);
 #pragma unroll
           for (int term = 0; term < kTerms; ++term)
-            mma_ts(oc, w + kk / 2 * 32 + term * 16 + kk % 2 * 8, v + kk * (16 * 128 >> 4), kValues,
-                   pi > 0 || kk > 0 || term > 0);
-        umma_commit(&s.pv_done[st][b]);
-        umma_commit(&s.op_empty[slot]);
-        ++np;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ss(sc, q + term * (P::kQTerm >> 4) + kk / 4 * (P::kQHalf >> 4) + kk % 4 * 2,
+                     kd + kk / 4 * (P::kHalf >> 4) + kk % 4 * 2, kScores, term > 0 || kk > 0);
+          umma_commit(&s.s_full[st][b]);
+          umma_commit(&s.op_empty[slot]);
+          ++ns;
+          ++si;
+          did = true;
+        }
       }
-      if (pi + 2 < mine) {  // the scores of page pi + 2
-        const int b = ns & 1, seq = 2 * (base + first + (pi + 2) * kStep), slot = seq % P::kOperands;
-        go = wait_or_stop(&s.op_full[slot], seq / P::kOperands & 1, abort) &&
-             (ns < 2 || wait_or_stop(&s.pv_done[st][b], ((ns >> 1) - 1) & 1, abort));
-        if (!go) break;
-        tc_fence_after();
-        const uint64_t kd = desc_kmajor_sw128(smem_addr(s.op[slot]));
-        const uint32_t sc = s.tmem + s_col(st, b);
-#pragma unroll
-        for (int term = 0; term < kTerms; ++term)
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(sc, q + term * (P::kQTerm >> 4) + kk / 4 * (P::kQHalf >> 4) + kk % 4 * 2,
-                   kd + kk / 4 * (P::kHalf >> 4) + kk % 4 * 2, kScores, term > 0 || kk > 0);
-        umma_commit(&s.s_full[st][b]);
-        umma_commit(&s.op_empty[slot]);
-        ++ns;
+      if (did) {
+        since = 0;
+      } else {  // bounded like every other wait
+        if (since == 0) since = clock64();
+        if (clock64() - since > (1ll << 31)) *abort = 1;
+        if (*abort) {
+          go = false;
+          break;
+        }
       }
     }
     if (!go) break;
@@ -775,7 +831,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   }
   if (threadIdx.x == kLoadWarp * 32) {
     s.abort = 0;
-    for (int i = 0; i < P::kPieces; ++i) {
+    for (int i = 0; i < P::kRaw; ++i) {
       mbar_init(&s.raw_full[i], 1);
       mbar_init(&s.raw_empty[i], kUnpackWarps);
     }
@@ -812,14 +868,16 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   tc_fence_after();
   if (x0 < x1) {
     const Walk wk(px, s.first_cache, x0, x1);
-    if (warp == kLoadWarp)
-      load_pages<D, kTerms, kPair>(s, a, wk);
-    else if (warp >= kMmaWarp) {
-      if (lane == 0) issue<D, kTerms, kPair>(s, px, warp - kMmaWarp, wk);
-    } else if (warp >= kSoftWarps)
-      widen<D, kTerms, kPair>(s, warp - kSoftWarps, (int)(x1 - x0));
-    else
+    if (warp < kSoftWarps)
       weights<D, kTerms, kPair>(s, n, px, R, wk);
+    else if (warp < kLoadWarp)
+      widen<D, kTerms, kPair>(s, warp - kSoftWarps, (int)(x1 - x0));
+    else if (warp == kLoadWarp)
+      load_pages<D, kTerms, kPair>(s, a, wk);
+    else if (warp == kMetaWarp)
+      load_metas<D, kTerms, kPair>(s, a, wk);
+    else if (lane == 0)
+      issue<D, kTerms, kPair>(s, px, warp - kMmaWarp, wk);
   }
   __syncwarp();
   tc_fence_before();
