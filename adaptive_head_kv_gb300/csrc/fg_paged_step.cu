@@ -284,11 +284,351 @@ __global__ void __launch_bounds__(kWeighThreads)
   }
 }
 
+// Many small caches: a warp an item.  The split kernel's streaming warp opens one item after the
+// other, a chain of dependent loads each, which its pages hide only where there are enough of them:
+// 16384 caches of some 30 rows took 4.5 us an item of a block.  Here an SM's warps open a dozen
+// items at a time and read each lane's operands where they lie; the arithmetic is the split kernel's,
+// with keys and values in their own order.  Pages of a ring without a row that counts (rings behind
+// a shared prompt begin empty) are passed over.
+constexpr int kSmallWarps = 4;
+
+template <typename T, int D, bool kFold, int kMode>
+__global__ void __launch_bounds__(kSmallWarps * 32, 4)
+    q8_small_kernel(const PagedArgs a, const PagedDecodeArgs n, int Gkv, int H, int R, int HLkv,
+                    float sl2) {
+  constexpr bool kWide = wide<T>(kFold, kMode), kTwo = kFold || kWide;
+  constexpr int NQ = kFold ? 1 : 2;  // queries of a lane
+  constexpr int PER = D / 32, KI = D / 64, PW = D / 32, MT = D / 16;
+  constexpr int kQNext = (kFold ? 2 : 1) * D, kQTerm = (kFold ? 1 : kMaxR) * D;  // in f16
+  constexpr int kQueries = kFold ? kMaxR / 2 : kMaxR;
+  __shared__ __align__(16) uint16_t sm_q[kSmallWarps][kMaxR * D + (kWide ? kQTerm : 0)];
+  __shared__ float sm_e[kSmallWarps][kMaxR];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const int q0 = NQ * t4;  // the lane's first query
+  const int wi = blockIdx.x * kSmallWarps + warp;
+  const bool have = wi < a.n_work;
+  const PagedItem it = a.items[have ? wi : 0];
+  const bool listed = same_list(a);
+  griddep_wait();
+  griddep_launch_dependents();
+  if (!listed) {
+    if (threadIdx.x == 0) atomicOr(a.dev_err, kErrInvalid);
+    return;
+  }
+  if (!have) return;
+  const int c = it.cache, b = c / HLkv;
+  if ((unsigned)c >= (unsigned)Gkv) {
+    if (lane == 0) atomicOr(a.dev_err, kErrInvalid);
+    return;
+  }
+  const int t = n.pos[b], had = a.rows[c], tau = n.k_new ? n.ids[b] : 0;
+  const fg_paged_desc hd = a.caches[c];
+  const size_t g0 = (size_t)(c / (H / R)) * H + (size_t)(c % (H / R)) * R;
+  if (t < 0) return;  // the sequence takes no part
+  const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
+  const int w = ring_slots(hd, a.max_w), old = live_rows(hd, had);
+  if ((old != had || w != hd.w) && it.last && lane == 0) atomicOr(a.dev_err, kErrInvalid);
+  // the queries: rotated, divided by the power of two that brings the largest value to
+  // [2^13, 2^14), as f16 (two terms: and what f16 loses, times 2^11)
+  {
+    float x[kQueries][PER];
+#pragma unroll
+    for (int qi = 0; qi < kQueries; ++qi)
+      if (qi < R) load_row<PER>((const T*)n.q + (g0 + qi) * D, x[qi]);
+    float2 cs[PER];
+    if (n.rope.rot > 0)
+      row_angles<PER>(cs, n.rope.rot, n.rope.style, [&](int p) {
+        float2 y;
+        rope_cos_sin<kTwo>((unsigned)t, n.rope.turns[p], y.x, y.y);
+        return y;
+      });
+#pragma unroll
+    for (int qi = 0; qi < kQueries; ++qi) {
+      if (qi >= R) break;
+      if (n.rope.rot > 0) rotate_row<PER>(x[qi], cs, n.rope.rot, n.rope.style);
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) top = max(top, finite_bits(x[qi][k]));
+      top = __reduce_max_sync(0xffffffffu, top);
+      const int eq = max(-110, (int)(top >> 23) - 127 - 13);
+      const float inv = pow2f(-eq);
+#pragma unroll
+      for (int k = 0; k < PER; k += 2) {
+        const float u = x[qi][k] * inv, v = x[qi][k + 1] * inv;
+        const uint32_t hi = pack_f16x2(u, v);
+        uint16_t* q = sm_q[warp] + qi * kQNext + lane * PER + k;
+        *reinterpret_cast<uint32_t*>(q) = hi;
+        if constexpr (kTwo) {
+          const float2 f = unpack_f16x2(hi);
+          *reinterpret_cast<uint32_t*>(q + kQTerm) =
+              pack_f16x2((u - f.x) * 2048.f, (v - f.y) * 2048.f);
+        }
+      }
+      if (lane == 0) sm_e[warp][qi] = pow2f(eq) * sl2;
+    }
+  }
+  const Put put = item_put(n, it, hd, special, punct, w, old, t, tau);
+  int seg_end = it.last ? old : (int)min((long long)old, (long long)it.seg1 * kPageRows);
+  if (put.at >= 0) {
+    put_token<T, D, kMode>(a, n, c, hd, put, t, kMode == kScores && special.has(tau));
+    if (!put.ring && page_at(a, hd.first_page, hd.max_pages, put.at / kPageRows) >= 0)
+      seg_end = put.at + 1;
+  }
+  __syncwarp();  // the queries and the new row are there
+  uint32_t qa[4 * KI][kWide ? 4 : 2];  // (kWide: the second terms behind the first)
+  float fq[NQ];
+#pragma unroll
+  for (int i = 0; i < KI; ++i)
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      uint2 x = make_uint2(0, 0), y = make_uint2(0, 0);
+      if (g < (kFold ? 2 * R : R)) {
+        const uint16_t* q = sm_q[warp] + g * D + 64 * i + 16 * t4 + 4 * z;
+        x = *reinterpret_cast<const uint2*>(q);
+        if constexpr (kWide) y = *reinterpret_cast<const uint2*>(q + kQTerm);
+      }
+      qa[4 * i + z][0] = x.x;
+      qa[4 * i + z][1] = x.y;
+      if constexpr (kWide) {
+        qa[4 * i + z][2] = y.x;
+        qa[4 * i + z][3] = y.y;
+      }
+    }
+  float m[NQ], ms[NQ], l[NQ];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    fq[q] = q0 + q < R ? sm_e[warp][q0 + q] : 0.f;
+    m[q] = ms[q] = q0 + q < R ? kNoScore : 1e30f;
+    l[q] = 0.f;
+  }
+  float o[MT][4];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+
+  const int ring_end = (int)min((long long)w, (long long)it.ring1 * kPageRows);
+  const int n_seg = max(0, cdiv(seg_end - it.seg0 * kPageRows, kPageRows));
+  const int n_ring =
+      it.ring1 > it.ring0 ? max(0, cdiv(ring_end - it.ring0 * kPageRows, kPageRows)) : 0;
+  // a page's number, exponents and which of its rows count, asked for a page ahead
+  int page = -1, page_next = -1;
+  uint2 ex = make_uint2(0, 0), ex_next = make_uint2(0, 0);
+  int2 p_next = make_int2(-1, -1);
+  auto ask = [&](int j) {
+    page_next = -1;
+    p_next = make_int2(-1, -1);
+    if (j >= n_seg + n_ring) return;
+    page_next = j < n_seg ? page_at(a, hd.first_page, hd.max_pages, it.seg0 + j)
+                          : page_at(a, hd.ring_page, hd.ring_pages, it.ring0 + j - n_seg);
+    if (page_next < 0) {
+      if (lane == 0) atomicOr(a.dev_err, kErrInvalid);
+      return;
+    }
+    ex_next = __ldcg(reinterpret_cast<const uint2*>(a.exps + (size_t)page_next * kPageBlocks * 2));
+    if (j >= n_seg) {
+      const int32_t* p = a.pos + (size_t)page_next * kPageRows + lane;
+      p_next = make_int2(__ldcg(p), __ldcg(p + 32));
+    }
+  };
+  ask(0);
+#pragma unroll 1
+  for (int j = 0; j < n_seg + n_ring; ++j) {
+    page = page_next;
+    ex = ex_next;
+    const bool ring = j >= n_seg;
+    uint32_t live0, live1;  // rows 0-31 and 32-63 that count
+    if (ring) {
+      const int left = ring_end - (it.ring0 + j - n_seg) * kPageRows;
+      const int2 p = p_next;
+      live0 = __ballot_sync(0xffffffffu, lane < left && p.x >= 0 && (unsigned)t - (unsigned)p.x < (unsigned)w);
+      live1 = __ballot_sync(0xffffffffu, lane + 32 < left && p.y >= 0 && (unsigned)t - (unsigned)p.y < (unsigned)w);
+    } else {
+      const int left = seg_end - (it.seg0 + j) * kPageRows;
+      live0 = left >= 32 ? 0xffffffffu : (1u << max(left, 0)) - 1;
+      live1 = left >= 64 ? 0xffffffffu : left > 32 ? (1u << (left - 32)) - 1 : 0u;
+    }
+    ask(j + 1);
+    if (page < 0) continue;
+#pragma unroll 1
+    for (int blk = 0; blk < kPageBlocks; ++blk) {
+      const uint32_t live = (blk < 2 ? live0 : live1) >> (16 * (blk & 1)) & 0xffffu;
+      if (live == 0) continue;
+      const size_t row = (size_t)page * kPageRows + blk * kBlockRows;
+      const uint8_t *kb = a.kp + row * D, *vb = a.vp + row * D;
+      uint4 k0[KI], k1[KI];
+#pragma unroll
+      for (int i = 0; i < KI; ++i) {
+        k0[i] = __ldcg(reinterpret_cast<const uint4*>(kb + g * D + (t4 + 4 * i) * 16));
+        k1[i] = __ldcg(reinterpret_cast<const uint4*>(kb + (g + 8) * D + (t4 + 4 * i) * 16));
+      }
+      uint32_t v[4][PW];  // keys 2 t4, 2 t4 + 1 and those + 8
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const uint8_t* p = vb + (2 * t4 + (z & 1) + (z >> 1) * 8) * D + g * (D / 8);
+        if constexpr (D == 128) {
+          const uint4 y = __ldcg(reinterpret_cast<const uint4*>(p));
+          v[z][0] = y.x, v[z][1] = y.y, v[z][2] = y.z, v[z][3] = y.w;
+        } else {
+          const uint2 y = __ldcg(reinterpret_cast<const uint2*>(p));
+          v[z][0] = y.x, v[z][1] = y.y;
+        }
+      }
+      const uint32_t e2 = (blk < 2 ? ex.x : ex.y) >> (16 * (blk & 1));
+      const int ek = (int)(signed char)(e2 & 0xff), ev = (int)(signed char)(e2 >> 8 & 0xff);
+      // columns 2 t4 and 2 t4 + 1 of key g ([0], [1]) and of key g + 8 ([2], [3])
+      float x[4] = {0.f, 0.f, 0.f, 0.f}, xl[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < KI; ++i)
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const uint32_t y0 = word4(k0[i], z), y1 = word4(k1[i], z);
+          const uint32_t(&q)[kWide ? 4 : 2] = qa[4 * i + z];
+          const uint32_t f0 = decode2(y0), f1 = decode2(y1), f2 = decode2(y0 >> 16),
+                         f3 = decode2(y1 >> 16);
+          mma_f16_16816(x, f0, f1, f2, f3, q[0], q[1]);
+          if constexpr (kWide) mma_f16_16816(xl, f0, f1, f2, f3, q[2], q[3]);
+        }
+      const float fv = (float)ev, fk = pow2f(ek);
+      float sc[NQ][2];
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const float kf = fminf(fk * fq[q], 1.7e38f);  // (a score of 0 stays 0)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float y = kFold   ? fmaf(x[2 * h + 1], 1.f / 2048.f, x[2 * h])
+                          : kWide ? fmaf(xl[2 * h + q], 1.f / 2048.f, x[2 * h + q])
+                                  : x[2 * h + q];
+          sc[q][h] = live >> (g + 8 * h) & 1 ? y * kf : FG_NEG_INF;
+        }
+      }
+      if (live != 0xffffu) {  // such a row may hold anything, also NaN
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          if (!(live >> (2 * t4 + (z & 1) + (z >> 1) * 8) & 1))
+#pragma unroll
+            for (int k = 0; k < PW; ++k) v[z][k] = 0;
+      }
+      if constexpr (kMode == kScores) {
+        if (!ring && q0 < R) {
+          float* p = n.row_sc + row * R + q0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if constexpr (NQ == 2)  // R = 8
+              *reinterpret_cast<float2*>(p + (g + 8 * h) * R) = make_float2(sc[0][h], sc[1][h]);
+            else
+              p[(g + 8 * h) * R] = sc[0][h];
+          }
+        }
+      }
+      float top[NQ];
+      bool rises = false;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        top[q] = fmaxf(sc[q][0], sc[q][1]);
+        rises |= top[q] > ms[q] || top[q] + fv > m[q];
+      }
+      if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1)
+            top[q] = fmaxf(top[q], __shfl_xor_sync(0xffffffffu, top[q], d));
+          const float mn = fmaxf(m[q], top[q] + fv), sn = fmaxf(ms[q], top[q]);
+          const float corr = ex2(m[q] - mn);
+          l[q] *= ex2(ms[q] - sn);
+          m[q] = mn;
+          ms[q] = sn;
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (kFold || (k & 1) == q) o[i][k] *= corr;
+        }
+      }
+      float p[NQ][2];
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const float up = fv - m[q] + kPBits;
+        p[q][0] = ex2(sc[q][0] + up);
+        p[q][1] = ex2(sc[q][1] + up);
+        l[q] += ex2(sc[q][0] - ms[q]) + ex2(sc[q][1] - ms[q]);
+      }
+      uint32_t p01, p23, r01 = 0, r23 = 0;  // of keys g and g + 8; r: second terms
+      if constexpr (kFold) {
+        const float2 f = unpack_f16x2(pack_f16x2(p[0][0], p[0][1]));
+        p01 = transpose8x8(pack_f16x2(f.x, p[0][0] - f.x));
+        p23 = transpose8x8(pack_f16x2(f.y, p[0][1] - f.y));
+      } else {
+        const uint32_t lo = pack_f16x2(p[0][0], p[NQ - 1][0]), hi = pack_f16x2(p[0][1], p[NQ - 1][1]);
+        p01 = transpose8x8(lo);
+        p23 = transpose8x8(hi);
+        if constexpr (kWide) {
+          const float2 f01 = unpack_f16x2(lo), f23 = unpack_f16x2(hi);
+          r01 = transpose8x8(pack_f16x2(p[0][0] - f01.x, p[NQ - 1][0] - f01.y));
+          r23 = transpose8x8(pack_f16x2(p[0][1] - f23.x, p[NQ - 1][1] - f23.y));
+        }
+      }
+#pragma unroll
+      for (int z = 0; z < PW; ++z) {
+        // byte pairs (key, next key) of dimensions 4 z, 4 z + 1 and 4 z + 2, 4 z + 3
+        const uint32_t lo01 = __byte_perm(v[0][z], v[1][z], 0x5140),
+                       hi01 = __byte_perm(v[0][z], v[1][z], 0x7362),
+                       lo23 = __byte_perm(v[2][z], v[3][z], 0x5140),
+                       hi23 = __byte_perm(v[2][z], v[3][z], 0x7362);
+        const uint32_t f0 = decode2(lo01), f1 = decode2(lo01 >> 16), f2 = decode2(lo23),
+                       f3 = decode2(lo23 >> 16);
+        const uint32_t h0 = decode2(hi01), h1 = decode2(hi01 >> 16), h2 = decode2(hi23),
+                       h3 = decode2(hi23 >> 16);
+        mma_f16_16816(o[2 * z], f0, f1, f2, f3, p01, p23);
+        mma_f16_16816(o[2 * z + 1], h0, h1, h2, h3, p01, p23);
+        if constexpr (kWide) {
+          mma_f16_16816(o[2 * z], f0, f1, f2, f3, r01, r23);
+          mma_f16_16816(o[2 * z + 1], h0, h1, h2, h3, r01, r23);
+        }
+      }
+    }
+  }
+  // O^T: rows 16 j + g, + 8 are dimensions (D / 8) g + 2 j, + 1; the columns as the queries'
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) l[q] += __shfl_xor_sync(0xffffffffu, l[q], d);
+    const int qi = q0 + q;
+    if (qi >= R) continue;
+    // the sums are in units of 2^(m - kPBits), l in 2^ms
+    const float f = l[q] == 0.f ? 0.f : exp2f(m[q] - ms[q] - kPBits) / l[q];
+    float* out = n.part_acc + ((size_t)wi * R + qi) * D + (D / 8) * g;
+#pragma unroll
+    for (int j = 0; j < MT; j += 2) {
+      float4 y;
+      if constexpr (kFold)
+        y = make_float4((o[j][0] + o[j][1]) * f, (o[j][2] + o[j][3]) * f,
+                        (o[j + 1][0] + o[j + 1][1]) * f, (o[j + 1][2] + o[j + 1][3]) * f);
+      else
+        y = make_float4(o[j][q] * f, o[j][q + 2] * f, o[j + 1][q] * f, o[j + 1][q + 2] * f);
+      *reinterpret_cast<float4*>(out + 2 * j) = y;
+    }
+    if (g == 0)
+      *reinterpret_cast<float2*>(n.part_ml + 2 * ((size_t)wi * R + qi)) = make_float2(ms[q], l[q]);
+  }
+}
+
+// A list whose thread blocks have this many items each has small ones: a block's length is at most
+// 192 pages' worth, of which an item takes 3 to 7 beside its pages.
+constexpr int kSmallItems = 4;
+
+template <typename T, int D, bool kFold, int kMode>
+cudaError_t run_items(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
+                      cudaStream_t s) {
+  if (a.n_work < kSmallItems * a.n_ctas) return launch_split<T, D, kFold, kMode>(pd, a, n, s);
+  return launch_pdl(q8_small_kernel<T, D, kFold, kMode>, cdiv(a.n_work, kSmallWarps),
+                    kSmallWarps * 32, 0, s, a, n, pd.Gkv, pd.H, pd.R, pd.HLkv, pd.sl2);
+}
+
 template <typename T, int D, bool kFold>
 cudaError_t run_split(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
                       cudaStream_t s) {
-  return n.row_w ? launch_split<T, D, kFold, kScores>(pd, a, n, s)
-                 : launch_split<T, D, kFold, kParts>(pd, a, n, s);
+  return n.row_w ? run_items<T, D, kFold, kScores>(pd, a, n, s)
+                 : run_items<T, D, kFold, kParts>(pd, a, n, s);
 }
 
 template <typename T, int D>
