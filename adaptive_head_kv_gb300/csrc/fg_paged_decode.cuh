@@ -219,22 +219,16 @@ __device__ __forceinline__ uint32_t word4(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// Codes the new token's row of an item into its page (all lanes call).
-template <typename T, int D, int kMode>
-__device__ __forceinline__ void put_token(const PagedArgs& a, const PagedDecodeArgs& n, int c,
-                                          const fg_paged_desc& hd, const Put& put, int t,
-                                          bool pinned) {
-  constexpr int PER = D / 32;
-  const int lane = threadIdx.x & 31;
+// The page of an item's new row, taken if it is the segment's first there (all lanes call); -1 and a
+// flag if there is none.
+__device__ __forceinline__ int put_page(const PagedArgs& a, const fg_paged_desc& hd,
+                                        const Put& put) {
   const int first = put.ring ? hd.ring_page : hd.first_page;
   const int entries = put.ring ? hd.ring_pages : hd.max_pages;
-  float xk[PER], xv[PER];
-  load_row<PER>((const T*)n.k_new + (size_t)c * D, xk);
-  load_row<PER>((const T*)n.v_new + (size_t)c * D, xv);
   const int i = put.at / kPageRows;
   int page = page_at(a, first, entries, i);
   if (page < 0) {
-    if (lane == 0) {
+    if ((threadIdx.x & 31) == 0) {
       int err = kErrInvalid;
       if (!put.ring && i >= entries) {
         err = kErrCapacity;
@@ -252,6 +246,44 @@ __device__ __forceinline__ void put_token(const PagedArgs& a, const PagedDecodeA
     }
     page = __shfl_sync(0xffffffffu, page, 0);
   }
+  return page;
+}
+
+// Codes the new row, K rotated, into that page; had_k, had_v: its block's exponents.  Returns the
+// powers of two that K and V were multiplied by.
+template <int D, int kMode>
+__device__ __forceinline__ float2 put_row(const PagedArgs& a, const PagedDecodeArgs& n, const Put& put,
+                                          int page, int t, bool pinned, int had_k, int had_v,
+                                          const float (&xk)[D / 32], const float (&xv)[D / 32]) {
+  constexpr int PER = D / 32;
+  const int r = put.at % kPageRows, blk = r / kBlockRows;
+  const size_t row = (size_t)page * kPageRows + blk * kBlockRows;
+  int8_t* ex = a.exps + ((size_t)page * kPageBlocks + blk) * 2;
+  const bool fresh = !put.ring && r % kBlockRows == 0;
+  uint8_t *kb = a.kp + row * D, *vb = a.vp + row * D;
+  float2 f;
+  f.x = open_block<D>(top_bits<PER>(xk), fresh ? -128 : had_k, kb, ex);
+  code_row<PER>(xk, f.x, kb + r % kBlockRows * D);
+  f.y = open_block<D>(top_bits<PER>(xv), fresh ? -128 : had_v, vb, ex + 1);
+  code_row<PER>(xv, f.y, vb + r % kBlockRows * D);
+  if ((threadIdx.x & 31) == 0) {
+    a.pos[(size_t)page * kPageRows + r] = t;
+    if constexpr (kMode == kScores)  // nothing received yet; a special token's row is pinned
+      if (!put.ring) n.row_w[(size_t)page * kPageRows + r] = pinned ? -FG_NEG_INF : 0.f;
+  }
+  return f;
+}
+
+// Codes the new token's row of an item into its page (all lanes call).
+template <typename T, int D, int kMode>
+__device__ __forceinline__ void put_token(const PagedArgs& a, const PagedDecodeArgs& n, int c,
+                                          const fg_paged_desc& hd, const Put& put, int t,
+                                          bool pinned) {
+  constexpr int PER = D / 32;
+  float xk[PER], xv[PER];
+  load_row<PER>((const T*)n.k_new + (size_t)c * D, xk);
+  load_row<PER>((const T*)n.v_new + (size_t)c * D, xv);
+  const int page = put_page(a, hd, put);
   if (page < 0) return;
   if (n.rope.rot > 0) {
     float2 cs[PER];
@@ -262,19 +294,9 @@ __device__ __forceinline__ void put_token(const PagedArgs& a, const PagedDecodeA
     });
     rotate_row<PER>(xk, cs, n.rope.rot, n.rope.style);
   }
-  const int r = put.at % kPageRows, blk = r / kBlockRows;
-  const size_t row = (size_t)page * kPageRows + blk * kBlockRows;
-  int8_t* ex = a.exps + ((size_t)page * kPageBlocks + blk) * 2;
-  const bool fresh = !put.ring && r % kBlockRows == 0;
-  const int had_k = fresh ? -128 : ex[0], had_v = fresh ? -128 : ex[1];
-  uint8_t *kb = a.kp + row * D, *vb = a.vp + row * D;
-  code_row<PER>(xk, open_block<D>(top_bits<PER>(xk), had_k, kb, ex), kb + r % kBlockRows * D);
-  code_row<PER>(xv, open_block<D>(top_bits<PER>(xv), had_v, vb, ex + 1), vb + r % kBlockRows * D);
-  if (lane == 0) {
-    a.pos[(size_t)page * kPageRows + r] = t;
-    if constexpr (kMode == kScores)  // nothing received yet; a special token's row is pinned
-      if (!put.ring) n.row_w[(size_t)page * kPageRows + r] = pinned ? -FG_NEG_INF : 0.f;
-  }
+  const int8_t* ex =
+      a.exps + ((size_t)page * kPageBlocks + put.at % kPageRows / kBlockRows) * 2;
+  put_row<D, kMode>(a, n, put, page, t, pinned, ex[0], ex[1], xk, xv);
 }
 
 // The streaming warp.

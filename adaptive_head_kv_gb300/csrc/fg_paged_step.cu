@@ -290,10 +290,10 @@ __global__ void __launch_bounds__(kWeighThreads)
 // items at a time and read each lane's operands where they lie; the arithmetic is the split kernel's,
 // with keys and values in their own order.  Pages of a ring without a row that counts (rings behind
 // a shared prompt begin empty) are passed over.
-constexpr int kSmallWarps = 4;
+constexpr int kSmallWarps = 1;  // (a block of four waits for its longest: 194 us, with one 181)
 
 template <typename T, int D, bool kFold, int kMode>
-__global__ void __launch_bounds__(kSmallWarps * 32, 4)
+__global__ void __launch_bounds__(kSmallWarps * 32, 16)
     q8_small_kernel(const PagedArgs a, const PagedDecodeArgs n, int Gkv, int H, int R, int HLkv,
                     float sl2) {
   constexpr bool kWide = wide<T>(kFold, kMode), kTwo = kFold || kWide;
@@ -321,27 +321,78 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 4)
     if (lane == 0) atomicOr(a.dev_err, kErrInvalid);
     return;
   }
+  // what opens an item is asked for together: the sequence, the cache, the queries, the new row
   const int t = n.pos[b], had = a.rows[c], tau = n.k_new ? n.ids[b] : 0;
   const fg_paged_desc hd = a.caches[c];
   const size_t g0 = (size_t)(c / (H / R)) * H + (size_t)(c % (H / R)) * R;
-  if (t < 0) return;  // the sequence takes no part
+  float x[kQueries][PER], xk[PER], xv[PER];
+#pragma unroll
+  for (int qi = 0; qi < kQueries; ++qi)
+    if (qi < R) load_row<PER>((const T*)n.q + (g0 + qi) * D, x[qi]);
+#pragma unroll
+  for (int k = 0; k < PER; ++k) xk[k] = xv[k] = 0.f;
+  if (n.k_new) {
+    load_row<PER>((const T*)n.k_new + (size_t)c * D, xk);
+    load_row<PER>((const T*)n.v_new + (size_t)c * D, xv);
+  }
   const LaneSet special(n.special, n.ns), punct(n.punct, n.np);
+  if (t < 0) return;  // the sequence takes no part
   const int w = ring_slots(hd, a.max_w), old = live_rows(hd, had);
   if ((old != had || w != hd.w) && it.last && lane == 0) atomicOr(a.dev_err, kErrInvalid);
+  const Put put = item_put(n, it, hd, special, punct, w, old, t, tau);
+  int seg_end = it.last ? old : (int)min((long long)old, (long long)it.seg1 * kPageRows);
+  const int ring_end = (int)min((long long)w, (long long)it.ring1 * kPageRows);
+  // a page's number, exponents and which of its rows count, asked for a page ahead
+  int page_next = -1;
+  uint2 ex_next = make_uint2(0, 0);
+  int2 p_next = make_int2(-1, -1);
+  int n_seg = max(0, cdiv(seg_end - it.seg0 * kPageRows, kPageRows));
+  const int n_ring =
+      it.ring1 > it.ring0 ? max(0, cdiv(ring_end - it.ring0 * kPageRows, kPageRows)) : 0;
+  auto ask = [&](int j) {
+    page_next = -1;
+    p_next = make_int2(-1, -1);
+    if (j >= n_seg + n_ring) return;
+    page_next = j < n_seg ? page_at(a, hd.first_page, hd.max_pages, it.seg0 + j)
+                          : page_at(a, hd.ring_page, hd.ring_pages, it.ring0 + j - n_seg);
+    if (page_next < 0) {
+      if (lane == 0) atomicOr(a.dev_err, kErrInvalid);
+      return;
+    }
+    ex_next = __ldcg(reinterpret_cast<const uint2*>(a.exps + (size_t)page_next * kPageBlocks * 2));
+    if (j >= n_seg) {
+      const int32_t* p = a.pos + (size_t)page_next * kPageRows + lane;
+      p_next = make_int2(__ldcg(p), __ldcg(p + 32));
+    }
+  };
+  int new_page = -1, new_k = 0, new_v = 0;
+  if (put.at >= 0) {
+    new_page = put_page(a, hd, put);
+    __syncwarp();  // its entry is there
+    if (new_page >= 0) {
+      const int8_t* ex =
+          a.exps + ((size_t)new_page * kPageBlocks + put.at % kPageRows / kBlockRows) * 2;
+      new_k = ex[0];
+      new_v = ex[1];
+      if (!put.ring) {
+        seg_end = put.at + 1;
+        n_seg = max(0, cdiv(seg_end - it.seg0 * kPageRows, kPageRows));
+      }
+    }
+  }
+  ask(0);
   // the queries: rotated, divided by the power of two that brings the largest value to
   // [2^13, 2^14), as f16 (two terms: and what f16 loses, times 2^11)
   {
-    float x[kQueries][PER];
-#pragma unroll
-    for (int qi = 0; qi < kQueries; ++qi)
-      if (qi < R) load_row<PER>((const T*)n.q + (g0 + qi) * D, x[qi]);
     float2 cs[PER];
-    if (n.rope.rot > 0)
+    if (n.rope.rot > 0) {
       row_angles<PER>(cs, n.rope.rot, n.rope.style, [&](int p) {
         float2 y;
-        rope_cos_sin<kTwo>((unsigned)t, n.rope.turns[p], y.x, y.y);
+        rope_cos_sin((unsigned)t, n.rope.turns[p], y.x, y.y);
         return y;
       });
+      if (put.at >= 0) rotate_row<PER>(xk, cs, n.rope.rot, n.rope.style);
+    }
 #pragma unroll
     for (int qi = 0; qi < kQueries; ++qi) {
       if (qi >= R) break;
@@ -367,12 +418,11 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 4)
       if (lane == 0) sm_e[warp][qi] = pow2f(eq) * sl2;
     }
   }
-  const Put put = item_put(n, it, hd, special, punct, w, old, t, tau);
-  int seg_end = it.last ? old : (int)min((long long)old, (long long)it.seg1 * kPageRows);
-  if (put.at >= 0) {
-    put_token<T, D, kMode>(a, n, c, hd, put, t, kMode == kScores && special.has(tau));
-    if (!put.ring && page_at(a, hd.first_page, hd.max_pages, put.at / kPageRows) >= 0)
-      seg_end = put.at + 1;
+  if (new_page >= 0) {
+    const float2 f = put_row<D, kMode>(a, n, put, new_page, t, kMode == kScores && special.has(tau),
+                                       new_k, new_v, xk, xv);
+    new_k = 127 - (int)(__float_as_uint(f.x) >> 23);  // the exponents now
+    new_v = 127 - (int)(__float_as_uint(f.y) >> 23);
   }
   __syncwarp();  // the queries and the new row are there
   uint32_t qa[4 * KI][kWide ? 4 : 2];  // (kWide: the second terms behind the first)
@@ -405,46 +455,33 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 4)
 #pragma unroll
   for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
-  const int ring_end = (int)min((long long)w, (long long)it.ring1 * kPageRows);
-  const int n_seg = max(0, cdiv(seg_end - it.seg0 * kPageRows, kPageRows));
-  const int n_ring =
-      it.ring1 > it.ring0 ? max(0, cdiv(ring_end - it.ring0 * kPageRows, kPageRows)) : 0;
-  // a page's number, exponents and which of its rows count, asked for a page ahead
-  int page = -1, page_next = -1;
-  uint2 ex = make_uint2(0, 0), ex_next = make_uint2(0, 0);
-  int2 p_next = make_int2(-1, -1);
-  auto ask = [&](int j) {
-    page_next = -1;
-    p_next = make_int2(-1, -1);
-    if (j >= n_seg + n_ring) return;
-    page_next = j < n_seg ? page_at(a, hd.first_page, hd.max_pages, it.seg0 + j)
-                          : page_at(a, hd.ring_page, hd.ring_pages, it.ring0 + j - n_seg);
-    if (page_next < 0) {
-      if (lane == 0) atomicOr(a.dev_err, kErrInvalid);
-      return;
-    }
-    ex_next = __ldcg(reinterpret_cast<const uint2*>(a.exps + (size_t)page_next * kPageBlocks * 2));
-    if (j >= n_seg) {
-      const int32_t* p = a.pos + (size_t)page_next * kPageRows + lane;
-      p_next = make_int2(__ldcg(p), __ldcg(p + 32));
-    }
-  };
-  ask(0);
 #pragma unroll 1
   for (int j = 0; j < n_seg + n_ring; ++j) {
-    page = page_next;
-    ex = ex_next;
+    const int page = page_next;
+    uint2 ex = ex_next;
+    const int2 p = p_next;
     const bool ring = j >= n_seg;
+    // (what this step put may have been asked for before)
+    const bool fresh_page = page >= 0 && page == new_page;
+    if (fresh_page) {
+      const int blk = put.at % kPageRows / kBlockRows, shift = 16 * (blk & 1);
+      const uint32_t e = (uint32_t)(new_k & 0xff) | (uint32_t)(new_v & 0xff) << 8;
+      uint32_t& word = blk < 2 ? ex.x : ex.y;
+      word = (word & ~(0xffffu << shift)) | e << shift;
+    }
     uint32_t live0, live1;  // rows 0-31 and 32-63 that count
     if (ring) {
       const int left = ring_end - (it.ring0 + j - n_seg) * kPageRows;
-      const int2 p = p_next;
       live0 = __ballot_sync(0xffffffffu, lane < left && p.x >= 0 && (unsigned)t - (unsigned)p.x < (unsigned)w);
       live1 = __ballot_sync(0xffffffffu, lane + 32 < left && p.y >= 0 && (unsigned)t - (unsigned)p.y < (unsigned)w);
     } else {
       const int left = seg_end - (it.seg0 + j) * kPageRows;
       live0 = left >= 32 ? 0xffffffffu : (1u << max(left, 0)) - 1;
       live1 = left >= 64 ? 0xffffffffu : left > 32 ? (1u << (left - 32)) - 1 : 0u;
+    }
+    if (ring && fresh_page) {
+      const int slot = put.at % kPageRows;
+      (slot < 32 ? live0 : live1) |= 1u << (slot & 31);
     }
     ask(j + 1);
     if (page < 0) continue;
