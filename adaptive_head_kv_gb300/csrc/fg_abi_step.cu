@@ -171,6 +171,7 @@ fg_status fastgen_evict_q8(const fg_params* p, const fg_paged_cache* cache, floa
   n.pos = pos;
   n.budget = budget;
   n.recent = recent;
+  n.caches = kv_count(p);
   n.moves = (int32_t*)workspace;
   n.src = (int32_t*)((char*)workspace + align_up((size_t)kv_count(p) * sizeof(int32_t)));
   return cuda_status(fg::launch_evict_q8(dims(p), paged_args(p, cache, dev_err), n,

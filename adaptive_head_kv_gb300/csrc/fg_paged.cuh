@@ -467,7 +467,7 @@ __host__ __device__ inline int prefix_cta(long long total, int ctas, long long x
 struct EvictArgs {
   float* scores;
   const int32_t* pos;  // [B]
-  int budget, recent;
+  int budget, recent, caches;
   // workspace
   int32_t* moves;  // [Gkv] rows that move
   int32_t* src;    // [Gkv, budget] the row that comes to this place, -1: none

@@ -1,5 +1,7 @@
 // Caches that stay within a budget: the weights their rows start with, the cut
 // to the budget, and empty caches behind a shared prompt.
+#include <type_traits>
+
 #include "fg_paged.cuh"
 
 namespace fg {
@@ -66,25 +68,36 @@ __global__ void __launch_bounds__(256) scores_kernel(const PagedArgs a, const Sc
 }
 
 // ------------------------------------------------------------------- the cut
+__device__ __forceinline__ float2 half2_values(uint32_t w) {
+  float2 f;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(w));
+  return f;
+}
+
 // Order of the rows that stay: recent ones, then by weight; ties to the lower row.
 __device__ __forceinline__ uint32_t row_key(float score, int p, int t, int recent) {
   if (p <= t && (long long)p > (long long)t - recent) return 0xffffffffu;
   return score > 0.f ? __float_as_uint(score) : 0u;
 }
 
-constexpr int kSelectThreads = 1024;
-
 // One CTA per cache: which rows stay, and which of those behind the budget come to which place
-// below it.
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const PagedArgs a,
-                                                                      const EvictArgs n, int HLkv) {
-  __shared__ int hist[256];
+// below it.  The keys are read once, into shared memory where they fit (kKeys); the budget-th
+// largest is found eleven bits at a time.  A chain of loads, scans and barriers bounds it: 1024 caches
+// of 1280 rows about 10 us, 16 of 32768 rows 25 us (with clusters of eight blocks a cache, whose
+// barriers cost as much as the shorter runs save, 30 us).
+template <int kThreads, int kKeys>
+__global__ void __launch_bounds__(kThreads)
+    evict_select_kernel(const PagedArgs a, const EvictArgs n, int HLkv) {
+  constexpr int kBins = 2048, kPerThread = kBins / kThreads, kPasses = 3;
+  extern __shared__ uint32_t keys[];  // [kKeys]
+  __shared__ int hist[kBins];
   __shared__ int scr[33];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
+  __shared__ int s_bin, s_need;
   griddep_wait();
   griddep_launch_dependents();
-  const int c = blockIdx.x, tid = threadIdx.x;
+  const int c = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const fg_paged_desc hd = a.caches[c];
   const int t = n.pos[c / HLkv], had = a.rows[c], rows = live_rows(hd, had);
   __syncthreads();  // every thread has read the count
@@ -94,8 +107,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Page
     n.moves[c] = 0;
   }
   if (t < 0 || rows <= n.budget) return;
-  auto key_of = [&](int r) {
-    const int page = page_at(a, hd.first_page, hd.max_pages, r / kPageRows);
+  auto key_of = [&](int r, int page) {
     if (page < 0) {  // a row that is not there
       atomicOr(a.dev_err, kErrInvalid);
       return 0u;
@@ -103,37 +115,67 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Page
     const size_t at = (size_t)page * kPageRows + r % kPageRows;
     return row_key(n.scores[at], a.pos[at], t, n.recent);
   };
-  // the budget-th largest key, eight bits at a time
+  const bool kept_here = rows <= kKeys;
+  auto key = [&](int r) {
+    return kept_here ? keys[r] : key_of(r, page_at(a, hd.first_page, hd.max_pages, r / kPageRows));
+  };
+  for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+  if (kept_here) {
+    // a warp takes pages in turns, each lane two rows; four pages under way
+    constexpr int kAhead = 4, kWarps = kThreads / 32;
+    for (int p0 = warp; p0 * kPageRows < rows; p0 += kAhead * kWarps) {
+      int page[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        page[u] = page_at(a, hd.first_page, hd.max_pages, p0 + u * kWarps);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = (p0 + u * kWarps) * kPageRows + h * 32 + lane;
+          if (r < rows) keys[r] = key_of(r, page[u]);
+        }
+    }
+  }
+  __syncthreads();
   uint32_t prefix = 0;
   int need = n.budget;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int r = tid; r < rows; r += kSelectThreads) {
-      const uint32_t k = key_of(r);
-      if (shift == 24 || k >> (shift + 8) == prefix >> (shift + 8))
-        atomicAdd(&hist[k >> shift & 255], 1);
+#pragma unroll 1
+  for (int pass = 0; pass < kPasses; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t bins = pass == 2 ? 1024 : 2048;
+    for (int r = tid; r < rows; r += kThreads) {
+      const uint32_t k = key(r);
+      if (pass == 0 || k >> (pass == 1 ? 21 : 10) == prefix >> (pass == 1 ? 21 : 10))
+        atomicAdd(&hist[k >> shift & (bins - 1)], 1);
     }
     __syncthreads();
-    if (tid == 0) {
-      int bin = 255;
-      for (; bin > 0 && hist[bin] < need; --bin) need -= hist[bin];
-      s_prefix = prefix | (uint32_t)bin << shift;
-      s_need = need;
+    // thread i counts the bins below 2048 - kPerThread i; the scan gives how many keys lie above
+    int own[kPerThread], sum = 0, total;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) sum += own[i] = hist[kBins - 1 - tid * kPerThread - i];
+    const int above = block_exclusive_scan(sum, scr, &total);
+    if (above < need && need <= above + sum) {
+      int left = need - above, i = 0;
+      while (i < kPerThread - 1 && own[i] < left) left -= own[i++];
+      s_bin = kBins - 1 - tid * kPerThread - i;
+      s_need = left;
     }
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) hist[kBins - 1 - tid * kPerThread - i] = 0;
     __syncthreads();
-    prefix = s_prefix;
+    prefix |= (uint32_t)s_bin << shift;
     need = s_need;
   }
-  // rows a thread, in order: how many tie, then who stays
-  const int per = cdiv(rows, kSelectThreads), r0 = min(tid * per, rows), r1 = min(r0 + per, rows);
+  // rows a thread, in order: how many tie, then who stays (an odd number, for the banks)
+  const int per = cdiv(rows, kThreads) | 1, r0 = min(tid * per, rows), r1 = min(r0 + per, rows);
   int ties = 0, total;
-  for (int r = r0; r < r1; ++r) ties += key_of(r) == prefix;
+  for (int r = r0; r < r1; ++r) ties += key(r) == prefix;
   const int before = block_exclusive_scan(ties, scr, &total);
   auto each = [&](auto hole, auto mover) {
     int tie = before;
     for (int r = r0; r < r1; ++r) {
-      const uint32_t k = key_of(r);
+      const uint32_t k = key(r);
       const bool stays = k > prefix || (k == prefix && tie++ < need);
       if (r < n.budget ? !stays : stays) {
         if (r < n.budget) hole(r);
@@ -145,73 +187,102 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Page
   each([&](int) { ++holes; }, [&](int) { ++movers; });
   int h0 = block_exclusive_scan(holes, scr, &total);
   int m0 = block_exclusive_scan(movers, scr, &total);
-  // src[i] first lists the movers in order, then is read by who fills hole i
-  int32_t* list = n.src + (size_t)gridDim.x * n.budget + (size_t)c * n.budget;
+  // the movers in order, then who fills which hole
+  int32_t* list = n.src + (size_t)n.caches * n.budget + (size_t)c * n.budget;
   int32_t* src = n.src + (size_t)c * n.budget;
-  for (int r = tid; r < n.budget; r += kSelectThreads) src[r] = -1;
+  for (int r = tid; r < n.budget; r += kThreads) src[r] = -1;
   each([](int) {}, [&](int r) { list[m0++] = r; });
   __syncthreads();
   each([&](int r) { src[r] = list[h0++]; }, [](int) {});
   if (tid == 0) n.moves[c] = total;
 }
 
-// One warp per block of 16 places below the budget.
+// A warp takes kMoveBlocks blocks of 16 places below the budget in turn.  The codes of K and of V of
+// all rows that come to a block are asked for before any is used.
+constexpr int kMoveWarps = 4, kMoveBlocks = 4;
+
 template <int D>
-__global__ void __launch_bounds__(128) evict_move_kernel(const PagedArgs a, const EvictArgs n,
-                                                         int blocks) {
+__global__ void __launch_bounds__(kMoveWarps * 32)
+    evict_move_kernel(const PagedArgs a, const EvictArgs n, int blocks) {
   constexpr int PER = D / 32;
-  const int quads = cdiv(blocks, 4);
-  const int c = blockIdx.x / quads, lane = threadIdx.x & 31;
-  const int blk = blockIdx.x % quads * 4 + (threadIdx.x >> 5);
+  using Word = typename std::conditional<PER == 4, uint32_t, uint16_t>::type;  // a lane's codes of a row
+  const int warps = cdiv(blocks, kMoveBlocks), lane = threadIdx.x & 31;
+  const long long wi = (long long)blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
   griddep_wait();
   griddep_launch_dependents();
-  if (blk >= blocks || n.moves[c] == 0) return;
-  const int src = lane < kBlockRows ? n.src[(size_t)c * n.budget + blk * kBlockRows + lane] : -1;
-  const uint32_t mask = __ballot_sync(0xffffffffu, src >= 0);
-  if (mask == 0) return;
+  const int c = (int)(wi / warps), blk0 = (int)(wi % warps) * kMoveBlocks;
+  if (c >= n.caches || n.moves[c] == 0) return;
   const fg_paged_desc hd = a.caches[c];
-  const int row0 = blk * kBlockRows;
-  const int page = page_at(a, hd.first_page, hd.max_pages, row0 / kPageRows);
-  const int from = src >= 0 ? page_at(a, hd.first_page, hd.max_pages, src / kPageRows) : -1;
-  const bool ok = page >= 0 && from >= 0;
-  if (src >= 0 && !ok) atomicOr(a.dev_err, kErrInvalid);
-  const uint32_t todo = __ballot_sync(0xffffffffu, ok);
-  if (todo == 0) return;
-  const size_t to = (size_t)page * kPageRows + row0 % kPageRows;
-  const int b0 = row0 % kPageRows / kBlockRows;
-  const long long at = ok ? (long long)from * kPageRows + src % kPageRows : 0;
-  if (ok) {
-    a.pos[to + lane] = a.pos[at];
-    n.scores[to + lane] = n.scores[at];
+  int src_l[kMoveBlocks / 2];  // of two blocks
+#pragma unroll
+  for (int i = 0; i < kMoveBlocks / 2; ++i) {
+    const int place = (blk0 + 2 * i) * kBlockRows + lane;
+    src_l[i] = place < n.budget ? n.src[(size_t)c * n.budget + place] : -1;
   }
-  for (int side = 0; side < 2; ++side) {
-    uint8_t* codes = (side ? a.vp : a.kp);
-    int8_t* ex = a.exps + ((size_t)page * kPageBlocks + b0) * 2 + side;
-    float x[kBlockRows][PER];
-    uint32_t top = 0;
+#pragma unroll 1
+  for (int i = 0; i < kMoveBlocks; ++i) {
+    int src = i < 2 ? src_l[0] : src_l[kMoveBlocks / 2 - 1];
+    src = __shfl_sync(0xffffffffu, src, (lane & 15) + 16 * (i & 1));
+    if (lane >= kBlockRows) src = -1;
+    if (__ballot_sync(0xffffffffu, src >= 0) == 0) continue;
+    const int row0 = (blk0 + i) * kBlockRows, b0 = row0 % kPageRows / kBlockRows;
+    const int page = page_at(a, hd.first_page, hd.max_pages, row0 / kPageRows);
+    const int from = src >= 0 ? page_at(a, hd.first_page, hd.max_pages, src / kPageRows) : -1;
+    const bool ok = page >= 0 && from >= 0;
+    if (src >= 0 && !ok) atomicOr(a.dev_err, kErrInvalid);
+    const uint32_t todo = __ballot_sync(0xffffffffu, ok);
+    if (todo == 0) continue;
+    const size_t to = (size_t)page * kPageRows + row0 % kPageRows;
+    const long long at = ok ? (long long)from * kPageRows + src % kPageRows : 0;
+    Word x[2][kBlockRows];
 #pragma unroll
-    for (int i = 0; i < kBlockRows; ++i) {
-      const long long z = __shfl_sync(0xffffffffu, at, i);
-#pragma unroll
-      for (int k = 0; k < PER; ++k) x[i][k] = 0.f;
-      if (!(todo >> i & 1)) continue;
-      const float f = pow2f(a.exps[z / kBlockRows * 2 + side]);
-#pragma unroll
-      for (int k = 0; k < PER; k += 2) {
-        const uint16_t w = *reinterpret_cast<const uint16_t*>(codes + z * D + lane * PER + k);
-        const uint32_t h = decode2(w);
-        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-            : "=f"(x[i][k]), "=f"(x[i][k + 1])
-            : "r"(h));
-        x[i][k] *= f;
-        x[i][k + 1] *= f;
+    for (int r = 0; r < kBlockRows; ++r) {
+      const long long z = __shfl_sync(0xffffffffu, at, r);
+      x[0][r] = x[1][r] = 0;
+      if (todo >> r & 1) {
+        x[0][r] = __ldcg(reinterpret_cast<const Word*>(a.kp + z * D) + lane);
+        x[1][r] = __ldcg(reinterpret_cast<const Word*>(a.vp + z * D) + lane);
       }
-      top = max(top, top_bits<PER>(x[i]));
     }
-    const float inv = open_block<D>(top, ex[0], codes + to * D, ex);
+    int e_k = 0, e_v = 0;
+    if (ok) {
+      const int8_t* e = a.exps + at / kBlockRows * 2;
+      e_k = e[0];
+      e_v = e[1];
+      a.pos[to + lane] = a.pos[at];
+      n.scores[to + lane] = n.scores[at];
+    }
+    int8_t* ex = a.exps + ((size_t)page * kPageBlocks + b0) * 2;
+    const int had_k = ex[0], had_v = ex[1];
 #pragma unroll
-    for (int i = 0; i < kBlockRows; ++i)
-      if (todo >> i & 1) code_row<PER>(x[i], inv, codes + (to + i) * D);
+    for (int side = 0; side < 2; ++side) {
+      uint8_t* codes = side ? a.vp : a.kp;
+      auto values = [&](int r, float (&y)[PER]) {
+        const float f = pow2f(__shfl_sync(0xffffffffu, side ? e_v : e_k, r));
+#pragma unroll
+        for (int k = 0; k < PER; k += 2) {
+          const float2 z = half2_values(decode2((uint32_t)x[side][r] >> (8 * k)));
+          y[k] = z.x * f;
+          y[k + 1] = z.y * f;
+        }
+      };
+      uint32_t top = 0;
+#pragma unroll
+      for (int r = 0; r < kBlockRows; ++r) {
+        if (!(todo >> r & 1)) continue;
+        float y[PER];
+        values(r, y);
+        top = max(top, top_bits<PER>(y));
+      }
+      const float inv = open_block<D>(top, side ? had_v : had_k, codes + to * D, ex + side);
+#pragma unroll
+      for (int r = 0; r < kBlockRows; ++r) {
+        if (!(todo >> r & 1)) continue;
+        float y[PER];
+        values(r, y);
+        code_row<PER>(y, inv, codes + (to + r) * D);
+      }
+    }
   }
 }
 
@@ -234,15 +305,28 @@ cudaError_t launch_scores_q8(const ProfileDims& pd, const PagedArgs& a, const Sc
   return launch_pdl(scores_kernel, pd.Gkv, 256, 0, s, a, n, pd.H, pd.R, pd.HLkv);
 }
 
+template <int kThreads, int kKeys>
+static cudaError_t run_select(const ProfileDims& pd, const PagedArgs& a, const EvictArgs& n,
+                              cudaStream_t s) {
+  const auto k = evict_select_kernel<kThreads, kKeys>;
+  const int smem = kKeys * (int)sizeof(uint32_t);
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  return e == cudaSuccess ? launch_pdl(k, pd.Gkv, kThreads, smem, s, a, n, pd.HLkv) : e;
+}
+
 cudaError_t launch_evict_q8(const ProfileDims& pd, const PagedArgs& a, const EvictArgs& n,
                             cudaStream_t s) {
-  cudaError_t e = launch_pdl(evict_select_kernel, pd.Gkv, kSelectThreads, 0, s, a, n, pd.HLkv);
+  // by the rows that the table gives a cache on average
+  const long long room = (long long)a.table_len * kPageRows / pd.Gkv;
+  const cudaError_t e =
+      room <= 4096 ? run_select<256, 4096>(pd, a, n, s) : run_select<1024, 49152>(pd, a, n, s);
   if (e != cudaSuccess) return e;
   const int blocks = n.budget / kBlockRows;
-  const long long grid = (long long)cdiv(blocks, 4) * pd.Gkv;
+  const long long warps = (long long)cdiv(blocks, kMoveBlocks) * pd.Gkv;
+  const long long grid = (warps + kMoveWarps - 1) / kMoveWarps;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   return launch_pdl(pd.d == 64 ? evict_move_kernel<64> : evict_move_kernel<128>, (unsigned)grid,
-                    128, 0, s, a, n, blocks);
+                    kMoveWarps * 32, 0, s, a, n, blocks);
 }
 
 }  // namespace fg
