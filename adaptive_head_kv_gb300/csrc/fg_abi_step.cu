@@ -69,7 +69,7 @@ fg_status fastgen_decode_attn_q8_ex(const fg_params* p, const fg_paged_cache* ca
   if (!q || !pos || !out || !workspace || !dev_err || (k_new == nullptr) != (v_new == nullptr))
     return FG_EINVAL;
   if (k_new && (!new_ids || !cache->next_page || !aligned(cache->next_page, 4))) return FG_EINVAL;
-  if (!aligned(cache->rows_out, 4) || !aligned(scores, 4) || !aligned(q, 16) ||
+  if (!aligned(cache->rows_out, 4) || !aligned(scores, 8) || !aligned(q, 16) ||
       !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(out, 16) || !aligned(new_ids, 4) ||
       !aligned(pos, 4) || !aligned(workspace, kAlign) || !aligned(dev_err, 4))
     return FG_EINVAL;

@@ -149,6 +149,14 @@ __host__ __device__ constexpr bool wide(bool fold, int mode) {
   return !fold && (sizeof(T) == 4 || mode == kScores);
 }
 
+// The merge of an item's warps takes the queries of a group of eight in two halves where the
+// scores' second terms fill the stages, so that three blocks still fit an SM (192 caches of 8192
+// positions: two blocks 99 us, three TIME_THREE).
+template <bool kFold, int kMode>
+__host__ __device__ constexpr int kHalves() {
+  return kMode == kScores && !kFold ? 2 : 1;
+}
+
 // A stage: a page's K and V codes, its rows' positions, StageInfo, and, in an
 // item's first stage, the group's queries: f16 terms and the power of
 // two each query was divided by.  Row r's 16-byte piece c sits at piece c ^ swizzle(r).
@@ -527,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
   extern __shared__ __align__(128) uint8_t ring_smem[];
   __shared__ float sm_ml[2][3][kWarps][kMaxR];
   __shared__ Bars bars;
-  float* sums = reinterpret_cast<float*>(ring_smem + RG::kBytes);  // [kWarps][R][D]
+  float* sums = reinterpret_cast<float*>(ring_smem + RG::kBytes);  // [kWarps][R / kHalves][D]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
@@ -830,45 +838,51 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
     }
     sync_warps();
     // O^T: rows 16 j + g, + 8 are dimensions (D / 8) g + 2 j, + 1; the columns as the queries'
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      const int qi = q0 + q;
-      if (qi < R) {
-        float M = kNoScore;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][qi]);
-        const float f = exp2f(m[q] - M);
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-          *reinterpret_cast<float2*>(&sums[(warp * R + qi) * D + (D / 8) * g + 2 * j]) =
-              kFold ? make_float2((o[j][0] + o[j][1]) * f, (o[j][2] + o[j][3]) * f)
-                    : make_float2(o[j][q] * f, o[j][q + 2] * f);
-      }
-    }
-    sync_warps();
     const size_t g0 = (size_t)(cache / (H / R)) * H + (size_t)(cache % (H / R)) * R;
-    for (int x = warp * 32 + lane; x < R * D; x += kWarps * 32) {
-      const int qi = x / D;
-      float A = 0.f;
+    const int RH = R / kHalves<kFold, kMode>();
+#pragma unroll 1
+    for (int half_r = 0; half_r < R; half_r += RH) {
+      if (half_r > 0) sync_warps();  // the half before has been read
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) A += sums[w * R * D + x];
-      float M = kNoScore, S = kNoScore, L = 0.f;
+      for (int q = 0; q < NQ; ++q) {
+        const int qi = q0 + q;
+        if (qi >= half_r && qi < half_r + RH) {
+          float M = kNoScore;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        M = fmaxf(M, sm_m[w][qi]);
-        S = fmaxf(S, sm_s[w][qi]);
+          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][qi]);
+          const float f = exp2f(m[q] - M);
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+            *reinterpret_cast<float2*>(
+                &sums[(warp * RH + qi - half_r) * D + (D / 8) * g + 2 * j]) =
+                kFold ? make_float2((o[j][0] + o[j][1]) * f, (o[j][2] + o[j][3]) * f)
+                      : make_float2(o[j][q] * f, o[j][q + 2] * f);
+        }
       }
+      sync_warps();
+      for (int x = warp * 32 + lane; x < RH * D; x += kWarps * 32) {
+        const int qi = half_r + x / D;
+        float A = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) L += sm_l[w][qi] * exp2f(sm_s[w][qi] - S);
-      // the item's own output: the sums are in units of 2^(M - kPBits), L in 2^S
-      const float y = L == 0.f ? 0.f : A / L * exp2f(M - S - kPBits);
-      if (alone) {
-        store_out((T*)n.out + g0 * D + x, y);
-      } else {
-        n.part_acc[(size_t)item * R * D + x] = y;
-        if (x % D == 0) {
-          n.part_ml[2 * ((size_t)item * R + qi)] = S;
-          n.part_ml[2 * ((size_t)item * R + qi) + 1] = L;
+        for (int w = 0; w < kWarps; ++w) A += sums[w * RH * D + x];
+        float M = kNoScore, S = kNoScore, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          M = fmaxf(M, sm_m[w][qi]);
+          S = fmaxf(S, sm_s[w][qi]);
+        }
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) L += sm_l[w][qi] * exp2f(sm_s[w][qi] - S);
+        // the item's own output: the sums are in units of 2^(M - kPBits), L in 2^S
+        const float y = L == 0.f ? 0.f : A / L * exp2f(M - S - kPBits);
+        if (alone) {
+          store_out((T*)n.out + (g0 + half_r) * D + x, y);
+        } else {
+          n.part_acc[((size_t)item * R + half_r) * D + x] = y;
+          if (x % D == 0) {
+            n.part_ml[2 * ((size_t)item * R + qi)] = S;
+            n.part_ml[2 * ((size_t)item * R + qi) + 1] = L;
+          }
         }
       }
     }
@@ -879,7 +893,8 @@ constexpr int kFoldR = 4;  // queries whose two terms fill the MMA's eight colum
 
 template <typename T, int D, bool kFold, int kMode>
 int split_smem(int R) {
-  return Ring<D, kFold, wide<T>(kFold, kMode)>::kBytes + kWarps * R * D * (int)sizeof(float);
+  return Ring<D, kFold, wide<T>(kFold, kMode)>::kBytes +
+         kWarps * (R / kHalves<kFold, kMode>()) * D * (int)sizeof(float);
 }
 
 template <typename T, int D, bool kFold, int kMode>

@@ -249,23 +249,23 @@ cudaError_t run_join(const ProfileDims& pd, const PagedArgs& a, const PagedDecod
                     pd.H, pd.R, pd.HL);
 }
 
-// Adds the step's weights to the rows of a work item's part of the segment, a thread a row.
-constexpr int kWeighThreads = 256;
+// Adds the step's weights to the rows of a work item's part of the segment: a warp takes pages in
+// turns, a lane two rows of each.
+constexpr int kWeighWarps = 8;
 
 template <int R>
-__global__ void __launch_bounds__(kWeighThreads)
+__global__ void __launch_bounds__(kWeighWarps * 32)
     weigh_kernel(const PagedArgs a, const PagedDecodeArgs n, int Gkv, int H, int HLkv) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PagedItem it = a.items[blockIdx.x];
   const bool listed = same_list(a);
   griddep_wait();
   griddep_launch_dependents();
   const int c = it.cache;
   if (!listed || (unsigned)c >= (unsigned)Gkv) return;
-  if (n.pos[c / HLkv] < 0) return;
-  const fg_paged_desc hd = a.caches[c];
-  const int rows = live_rows(hd, a.rows_out[c]);
-  const int end = it.last ? rows : (int)min((long long)rows, (long long)it.seg1 * kPageRows);
   const size_t g0 = (size_t)(c / (H / R)) * H + (size_t)(c % (H / R)) * R;
+  const int t = n.pos[c / HLkv], now = a.rows_out[c];
+  const fg_paged_desc hd = a.caches[c];
   float M[R], r[R];
 #pragma unroll
   for (int q = 0; q < R; ++q) {
@@ -273,14 +273,52 @@ __global__ void __launch_bounds__(kWeighThreads)
     M[q] = ml.x;
     r[q] = ml.y == 0.f ? 0.f : 1.f / ml.y;
   }
-  for (int row = it.seg0 * kPageRows + threadIdx.x; row < end; row += kWeighThreads) {
-    const int page = page_at(a, hd.first_page, hd.max_pages, row / kPageRows);
-    if (page < 0) continue;  // flagged by the split kernel
-    const size_t at = (size_t)page * kPageRows + row % kPageRows;
-    float w = 0.f;
+  if (t < 0) return;
+  const int rows = live_rows(hd, now);
+  const int end = it.last ? rows : (int)min((long long)rows, (long long)it.seg1 * kPageRows);
+  constexpr int kAhead = R > 2 ? 1 : 2;
+  for (int j = it.seg0 + warp; j * kPageRows < end; j += kAhead * kWeighWarps) {
+    float s[kAhead][2][R];
+    float2 w[kAhead];
+    long long at[kAhead];
 #pragma unroll
-    for (int q = 0; q < R; ++q) w = fmaf(ex2(n.row_sc[at * R + q] - M[q]), r[q], w);
-    n.row_w[at] += w;
+    for (int u = 0; u < kAhead; ++u) {
+      const int p = j + u * kWeighWarps, row = p * kPageRows + 2 * lane;
+      const int page = row < end ? page_at(a, hd.first_page, hd.max_pages, p) : -1;
+      at[u] = page < 0 ? -1 : (long long)page * kPageRows + 2 * lane;  // (flagged by the split kernel)
+      if (at[u] < 0) continue;
+      w[u] = *reinterpret_cast<const float2*>(n.row_w + at[u]);
+      // two rows' scores lie side by side
+      const float* x = n.row_sc + at[u] * R;
+      if constexpr (R == 1) {
+        const float2 y = *reinterpret_cast<const float2*>(x);
+        s[u][0][0] = y.x;
+        s[u][1][0] = y.y;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2 * R; k += 4) {
+          const float4 y = *reinterpret_cast<const float4*>(x + k);
+          s[u][k / R][k % R] = y.x;
+          s[u][(k + 1) / R][(k + 1) % R] = y.y;
+          s[u][(k + 2) / R][(k + 2) % R] = y.z;
+          s[u][(k + 3) / R][(k + 3) % R] = y.w;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (at[u] < 0) continue;
+      float y[2] = {0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < R; ++q) y[h] = fmaf(ex2(s[u][h][q] - M[q]), r[q], y[h]);
+      const int row = (j + u * kWeighWarps) * kPageRows + 2 * lane;
+      if (row + 1 < end)
+        *reinterpret_cast<float2*>(n.row_w + at[u]) = make_float2(w[u].x + y[0], w[u].y + y[1]);
+      else
+        n.row_w[at[u]] = w[u].x + y[0];
+    }
   }
 }
 
@@ -688,7 +726,7 @@ cudaError_t run_step(const ProfileDims& pd, const PagedArgs& a, const PagedDecod
                      : pd.R == 2 ? weigh_kernel<2>
                      : pd.R == 4 ? weigh_kernel<4>
                                  : weigh_kernel<8>;
-  return launch_pdl(weigh, a.n_work, kWeighThreads, 0, s, a, n, pd.Gkv, pd.H, pd.HLkv);
+  return launch_pdl(weigh, a.n_work, kWeighWarps * 32, 0, s, a, n, pd.Gkv, pd.H, pd.HLkv);
 }
 
 }  // namespace
