@@ -95,6 +95,7 @@ fg_status fastgen_decode_attn_q8_ex(const fg_params* p, const fg_paged_cache* ca
   n.row_w = scores;
   n.row_sc = scores ? (float*)(ws + o.sc) : nullptr;
   n.head_ml = scores ? (float*)(ws + o.head) : nullptr;
+  n.beside = prefix ? 1 : 0;
   fg::PrefixParts px = o.prefix;
   fg::PagedArgs pre = {};
   if (prefix) {

@@ -424,7 +424,18 @@ struct PagedDecodeArgs {
   float* row_sc;
   float* row_w;
   float* head_ml;  // [G, 2]: each query's maximum and sum
+  int beside;      // behind fg_prefix.cu's kernels, whose results this one does not need
 };
+
+// The start of a kernel that may run beside the one before it (launched with one more block).  That
+// one waited for all before it, so nothing else is to be waited for; the last block waits until it
+// has ended, so that who waits for this kernel has both.  False: nothing else to do.
+__device__ __forceinline__ bool start_beside() {
+  griddep_launch_dependents();
+  if (blockIdx.x < gridDim.x - 1) return true;
+  griddep_wait();
+  return false;
+}
 
 // The shared caches of a batch (fg_prefix.cu): how the work on them is cut, and what it leaves
 // for a step's combine.

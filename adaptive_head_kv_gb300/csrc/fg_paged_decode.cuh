@@ -540,6 +540,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
   const int q0 = NQ * t4;  // the lane's first query
+  const bool beside = kMode != kDecode && n.beside;
+  if (beside && !start_beside()) return;
   // a list of another cache may say anything: its items are bounded here, its
   // caches where they are used
   const int wi0 = max(0, min(a.cta_first[blockIdx.x], a.n_work - 1));
@@ -563,8 +565,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
   const int own_items = a.ranges[own_c].y;
   const bool listed = same_list(a);
   __syncthreads();
-  griddep_wait();
-  griddep_launch_dependents();
+  if (!beside) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
   const fg_paged_desc own_cache = a.caches[own_c];
   if (!listed) {
     if (threadIdx.x == 0) atomicOr(a.dev_err, kErrInvalid);
@@ -911,7 +915,7 @@ cudaError_t launch_split(const ProfileDims& pd, const PagedArgs& a, const PagedD
     e = cudaFuncSetAttribute(split, cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared);
   if (e == cudaSuccess)
-    e = launch_pdl(split, a.n_ctas, kThreads, smem, s, a, n, pd.G, pd.H, pd.R, pd.HLkv, pd.sl2);
+    e = launch_pdl(split, a.n_ctas + n.beside, kThreads, smem, s, a, n, pd.G, pd.H, pd.R, pd.HLkv, pd.sl2);
   return e;
 }
 

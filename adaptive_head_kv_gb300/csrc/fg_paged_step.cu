@@ -347,8 +347,12 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 16)
   const bool have = wi < a.n_work;
   const PagedItem it = a.items[have ? wi : 0];
   const bool listed = same_list(a);
-  griddep_wait();
-  griddep_launch_dependents();
+  if (n.beside) {
+    if (!start_beside()) return;
+  } else {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
   if (!listed) {
     if (threadIdx.x == 0) atomicOr(a.dev_err, kErrInvalid);
     return;
@@ -695,7 +699,7 @@ template <typename T, int D, bool kFold, int kMode>
 cudaError_t run_items(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
                       cudaStream_t s) {
   if (a.n_work < kSmallItems * a.n_ctas) return launch_split<T, D, kFold, kMode>(pd, a, n, s);
-  return launch_pdl(q8_small_kernel<T, D, kFold, kMode>, cdiv(a.n_work, kSmallWarps),
+  return launch_pdl(q8_small_kernel<T, D, kFold, kMode>, cdiv(a.n_work, kSmallWarps) + n.beside,
                     kSmallWarps * 32, 0, s, a, n, pd.Gkv, pd.H, pd.R, pd.HLkv, pd.sl2);
 }
 
@@ -731,6 +735,8 @@ cudaError_t run_step(const ProfileDims& pd, const PagedArgs& a, const PagedDecod
 
 }  // namespace
 
+constexpr int kFewPages = 8;  // an SM's, of the shared caches
+
 cudaError_t launch_step_q8(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
                            const PagedArgs& pre, const PrefixParts& px0, cudaStream_t s) {
   PrefixParts px = px0;
@@ -738,6 +744,11 @@ cudaError_t launch_step_q8(const ProfileDims& pd, const PagedArgs& a, const Page
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    // Few pages: half of the SMs take them as fast, and the others have the sequences' own caches
+    // meanwhile (8 caches of 8192 positions, 64 queries each: 31 -> 25 us, with 40 of 152 SMs
+    // 29; 60 pages an SM: 129 -> 160).
+    const long long pages = (long long)(pre.table_len < pre.n_pages ? pre.table_len : pre.n_pages);
+    if (pages * px.groups < (long long)kFewPages * sms) sms = (sms + 1) / 2;
     px.ctas = sms < kPrefixMaxCtas ? sms : kPrefixMaxCtas;
     if (e == cudaSuccess) e = launch_prefix(pd, n, pre, px, s);
     if (e != cudaSuccess) return e;
