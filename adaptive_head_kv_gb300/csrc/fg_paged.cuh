@@ -453,7 +453,7 @@ struct PrefixParts {
   int tiles, groups; // of the queries of a cache
   int pair;          // groups of two tiles (a last one may be alone)
   int rows;          // rows of a part: queries of a tile
-  int ctas;          // thread blocks
+  int ctas, sms;     // thread blocks; of the device
   // workspace
   long long* cum;  // [caches + 1] pages before each cache
   uint8_t* q;    // [caches, tiles] tiles of f16 queries, as the tensor cores read them

@@ -106,19 +106,22 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
 }
 
 // With shared caches: their parts hold the queries of a tile side by side, so a lane takes a query
-// and a warp four dimensions of 32 of them.  kSplit warps share the parts of these (where few caches
-// leave many parts to each), eight warps a block.
+// and a warp 4 kFours dimensions of 32 of them.  kSplit warps share the parts of these (where few
+// caches leave many parts to each), eight warps a block.  What a warp asks for before the values (the
+// sequence, its list's items, the parts) is a chain of loads: it takes more dimensions where there are
+// warps enough.
 constexpr int kJoinWarps = 8;
 
-template <typename T, int D, int kSplit>
+template <typename T, int D, int kSplit, int kFours>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     step_join_kernel(const PagedArgs a, const PagedDecodeArgs n, const PrefixParts px, int H, int R,
                      int HL) {
-  constexpr int kAhead = 4, kQuads = kJoinWarps / kSplit, kSlices = D / 4 / kQuads;
-  __shared__ float sm[kSplit > 1 ? kSplit - 1 : 1][kQuads][6][32];
+  constexpr int kAhead = 4, kQuads = kJoinWarps / kSplit, kPer = 4 * kFours;
+  constexpr int kSlices = D / kPer / kQuads;
+  __shared__ float sm[kSplit > 1 ? kSplit - 1 : 1][kQuads][kPer + 2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int split = warp / kQuads, dq = warp % kQuads;
-  const int d4 = blockIdx.x % kSlices * kQuads + dq;
+  const int d4 = (blockIdx.x % kSlices * kQuads + dq) * kFours;
   const int quads = cdiv(px.rows, 32);  // of 32 queries, of a tile
   const int rest = blockIdx.x / kSlices, quad = rest % quads, unit = rest / quads;
   const int pc = unit / px.tiles, tile = unit % px.tiles;
@@ -149,12 +152,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     parts = (i1 - i0 + 1) * streams;
     part = ((size_t)i0 + (size_t)pc * px.groups + grp) * 2 + (px.pair ? tile & 1 : 0);
   }
-  Joined<kAhead, 4> o;
+  Joined<kAhead, kPer> o;
   const int most = parts + __reduce_max_sync(0xffffffffu, t >= 0 ? range.y : 0);
   for (int i0 = split; i0 < most; i0 += kAhead * kSplit) {
-    float m[kAhead], l[kAhead], x[kAhead][4];
+    float m[kAhead], l[kAhead], x[kAhead][kPer];
     float2 ml[kAhead];
-    float4 v[kAhead];
+    float4 v[kAhead][kFours];
 #pragma unroll
     for (int z = 0; z < kAhead; ++z) {
       const int i = i0 + z * kSplit;
@@ -163,65 +166,74 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       const size_t slot = shared ? p * px.rows + row : ((size_t)range.x + i - parts) * R + qi;
       ml[z] = ok ? *reinterpret_cast<const float2*>((shared ? px.ml : n.part_ml) + 2 * slot)
                  : make_float2(kNoScore, 0.f);
-      v[z] = ok ? *reinterpret_cast<const float4*>(
-                      shared ? px.acc + (p * (D / 4) + d4) * px.rows * 4 + (size_t)row * 4
-                             : n.part_acc + slot * D + d4 * 4)
-                : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int f = 0; f < kFours; ++f)
+        v[z][f] = ok ? *reinterpret_cast<const float4*>(
+                           shared ? px.acc + ((p * (D / 4) + d4 + f) * px.rows + row) * 4
+                                  : n.part_acc + slot * D + (d4 + f) * 4)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
     for (int z = 0; z < kAhead; ++z) {
       m[z] = ml[z].x;
       l[z] = ml[z].y;
       const bool some = l[z] != 0.f;  // (a part without a row has no values)
-      x[z][0] = some ? v[z].x : 0.f;
-      x[z][1] = some ? v[z].y : 0.f;
-      x[z][2] = some ? v[z].z : 0.f;
-      x[z][3] = some ? v[z].w : 0.f;
+#pragma unroll
+      for (int f = 0; f < kFours; ++f) {
+        x[z][4 * f] = some ? v[z][f].x : 0.f;
+        x[z][4 * f + 1] = some ? v[z][f].y : 0.f;
+        x[z][4 * f + 2] = some ? v[z][f].z : 0.f;
+        x[z][4 * f + 3] = some ? v[z][f].w : 0.f;
+      }
     }
     o.add(m, l, x);
   }
   if constexpr (kSplit > 1) {
     if (split > 0) {
-      float(&s)[6][32] = sm[split - 1][dq];
+      float(&s)[kPer + 2][32] = sm[split - 1][dq];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s[k][lane] = o.acc[k];
-      s[4][lane] = o.M;
-      s[5][lane] = o.L;
+      for (int k = 0; k < kPer; ++k) s[k][lane] = o.acc[k];
+      s[kPer][lane] = o.M;
+      s[kPer + 1][lane] = o.L;
     }
     __syncthreads();
-    Joined<kSplit - 1, 4> all;
+    Joined<kSplit - 1, kPer> all;
     all.M = o.M;
     all.L = o.L;
-    float m[kSplit - 1], l[kSplit - 1], x[kSplit - 1][4];
+    float m[kSplit - 1], l[kSplit - 1], x[kSplit - 1][kPer];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) all.acc[k] = o.acc[k];
+    for (int k = 0; k < kPer; ++k) all.acc[k] = o.acc[k];
 #pragma unroll
     for (int z = 0; z < kSplit - 1; ++z) {
-      float(&s)[6][32] = sm[z][dq];
+      float(&s)[kPer + 2][32] = sm[z][dq];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[z][k] = s[k][lane];
-      m[z] = s[4][lane];
-      l[z] = s[5][lane];
+      for (int k = 0; k < kPer; ++k) x[z][k] = s[k][lane];
+      m[z] = s[kPer][lane];
+      l[z] = s[kPer + 1][lane];
     }
     all.add(m, l, x);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) o.acc[k] = all.acc[k];
+    for (int k = 0; k < kPer; ++k) o.acc[k] = all.acc[k];
     o.M = all.M;
     o.L = all.L;
   }
-  // a query's dimensions of this block side by side in memory: the lanes of a warp take kQuads of
-  // the block's fours of each of 32 / kQuads queries
-  __shared__ float4 sm_out[32][kQuads + 1];
+  // a query's dimensions of this block side by side in memory: the lanes of a warp take fours of
+  // the block's dimensions of the same queries
+  constexpr int kOut = kQuads * kFours;
+  __shared__ float4 sm_out[32][kOut + 1];
   __shared__ long long sm_at[32];
   if (split == 0) {
-    sm_out[lane][dq] = make_float4(o.acc[0], o.acc[1], o.acc[2], o.acc[3]);
+#pragma unroll
+    for (int f = 0; f < kFours; ++f)
+      sm_out[lane][dq * kFours + f] =
+          make_float4(o.acc[4 * f], o.acc[4 * f + 1], o.acc[4 * f + 2], o.acc[4 * f + 3]);
     if (dq == 0) sm_at[lane] = t >= 0 ? (long long)g : -1;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 32 * kQuads; i += kJoinWarps * 32) {
-    const float4 v = sm_out[i / kQuads][i % kQuads];
-    const long long at = sm_at[i / kQuads];
-    T* out = (T*)n.out + at * D + (blockIdx.x % kSlices * kQuads + i % kQuads) * 4;
+  for (int i = threadIdx.x; i < 32 * kOut; i += kJoinWarps * 32) {
+    const float4 v = sm_out[i / kOut][i % kOut];
+    const long long at = sm_at[i / kOut];
+    T* out = (T*)n.out + at * D + (blockIdx.x % kSlices * kOut + i % kOut) * 4;
     if (at < 0) continue;
     if constexpr (sizeof(T) == 4)
       *reinterpret_cast<float4*>(out) = v;
@@ -239,13 +251,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   }
 }
 
-template <typename T, int D, int kSplit>
+template <typename T, int D, int kSplit, int kFours>
 cudaError_t run_join(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
                      const PrefixParts& px, cudaStream_t s) {
   const long long grid =
-      (long long)px.caches * px.tiles * cdiv(px.rows, 32) * (D / 4 / (kJoinWarps / kSplit));
+      (long long)px.caches * px.tiles * cdiv(px.rows, 32) * (D / 4 / kFours / (kJoinWarps / kSplit));
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_pdl(step_join_kernel<T, D, kSplit>, (unsigned)grid, kJoinWarps * 32, 0, s, a, n, px,
+  return launch_pdl(step_join_kernel<T, D, kSplit, kFours>, (unsigned)grid, kJoinWarps * 32, 0, s, a, n, px,
                     pd.H, pd.R, pd.HL);
 }
 
@@ -320,6 +332,10 @@ __global__ void __launch_bounds__(kWeighWarps * 32)
         n.row_w[at[u]] = w[u].x + y[0];
     }
   }
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 // Many small caches: a warp an item.  The split kernel's streaming warp opens one item after the
@@ -402,7 +418,13 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 16)
       return;
     }
     ex_next = __ldcg(reinterpret_cast<const uint2*>(a.exps + (size_t)page_next * kPageBlocks * 2));
-    if (j >= n_seg) {
+    if (j < n_seg) {  // its rows, on their way while what opens the item is looked up
+      const int bytes = min(kPageRows, seg_end - (it.seg0 + j) * kPageRows) * D;
+      for (int i = lane * 128; i < bytes; i += 32 * 128) {
+        prefetch_l2(a.kp + (size_t)page_next * kPageRows * D + i);
+        prefetch_l2(a.vp + (size_t)page_next * kPageRows * D + i);
+      }
+    } else {
       const int32_t* p = a.pos + (size_t)page_next * kPageRows + lane;
       p_next = make_int2(__ldcg(p), __ldcg(p + 32));
     }
@@ -723,7 +745,8 @@ cudaError_t run_step(const ProfileDims& pd, const PagedArgs& a, const PagedDecod
     // by a warp a query, 33 with a lane a query, 9 shared); many: each part has work enough for all
     // SMs (32 caches, 512 queries each: 25, shared 58)
     const long long blocks = (long long)px.caches * px.tiles * cdiv(px.rows, 32) * (D / 4 / kJoinWarps);
-    e = blocks <= 2 * px.ctas ? run_join<T, D, 4>(pd, a, n, px, s) : run_join<T, D, 1>(pd, a, n, px, s);
+    e = blocks <= 2 * px.sms ? run_join<T, D, 4, 1>(pd, a, n, px, s)
+                             : run_join<T, D, 1, 2>(pd, a, n, px, s);
   }
   if (e != cudaSuccess || !n.row_w) return e;
   const auto weigh = pd.R == 1   ? weigh_kernel<1>
@@ -747,6 +770,7 @@ cudaError_t launch_step_q8(const ProfileDims& pd, const PagedArgs& a, const Page
     // Few pages: half of the SMs take them as fast, and the others have the sequences' own caches
     // meanwhile (8 caches of 8192 positions, 64 queries each: 31 -> 25 us, with 40 of 152 SMs
     // 29; 60 pages an SM: 129 -> 160).
+    px.sms = sms;
     const long long pages = (long long)(pre.table_len < pre.n_pages ? pre.table_len : pre.n_pages);
     if (pages * px.groups < (long long)kFewPages * sms) sms = (sms + 1) / 2;
     px.ctas = sms < kPrefixMaxCtas ? sms : kPrefixMaxCtas;
