@@ -267,8 +267,6 @@ fg_status fastgen_decode_attn_q8(const fg_params* p, const fg_paged_cache* cache
   n.np = n_punct;
   n.out = out;
   char* ws = (char*)workspace;
-  n.row_sc = n.row_w = n.head_ml = nullptr;
-  n.beside = 0;
   n.part_ml = (float*)ws;
   n.part_acc = (float*)(ws + align_up((size_t)cache->n_work * pd.R * 2 * sizeof(float)));
   return cuda_status(fg::launch_decode_q8(pd, paged_args(p, cache, dev_err), n,

@@ -74,7 +74,7 @@ fg_status fastgen_decode_attn_q8_ex(const fg_params* p, const fg_paged_cache* ca
       !aligned(pos, 4) || !aligned(workspace, kAlign) || !aligned(dev_err, 4))
     return FG_EINVAL;
   if (!has_list(p, cache)) return FG_EINVAL;
-  fg::PagedDecodeArgs n;
+  fg::StepArgs n;
   if ((st = check_rope(rope, p->d, &n.rope)) != FG_OK) return st;
   const fg::ProfileDims pd = dims(p);
   const StepParts o = step_parts(p, cache, prefix != nullptr, scores != nullptr);

@@ -141,6 +141,8 @@ enum { kSeg, kRing, kNone, kKind = 3, kLast = 4 };
 // combine joins them with what lies outside the cache).  kScores: also every
 // segment row's scores are written, for the rows' weights.
 enum Mode { kDecode, kParts, kScores };
+template <int kMode>
+using ModeArgs = typename std::conditional<kMode == kDecode, PagedDecodeArgs, StepArgs>::type;
 
 // Second MMAs for the queries' and weights' second terms?  Weights that add up over a
 // generation are formed from 22-bit queries in bf16 groups of eight too.
@@ -257,22 +259,26 @@ __device__ __forceinline__ int put_page(const PagedArgs& a, const fg_paged_desc&
   return page;
 }
 
-// Codes the new row, K rotated, into that page; had_k, had_v: its block's exponents.  Returns the
-// powers of two that K and V were multiplied by.
+// Is the new row the first of a block, which then starts afresh?
+__device__ __forceinline__ bool put_opens(const Put& put) {
+  return !put.ring && put.at % kBlockRows == 0;
+}
+
+// Codes the new row, K rotated, into that page; had_k, had_v: its block's exponents, -128 if it
+// opens the block.  Returns the powers of two that K and V were multiplied by.
 template <int D, int kMode>
-__device__ __forceinline__ float2 put_row(const PagedArgs& a, const PagedDecodeArgs& n, const Put& put,
-                                          int page, int t, bool pinned, int had_k, int had_v,
+__device__ __forceinline__ float2 put_row(const PagedArgs& a, const ModeArgs<kMode>& n,
+                                          const Put& put, int page, int t, bool pinned, int had_k, int had_v,
                                           const float (&xk)[D / 32], const float (&xv)[D / 32]) {
   constexpr int PER = D / 32;
   const int r = put.at % kPageRows, blk = r / kBlockRows;
   const size_t row = (size_t)page * kPageRows + blk * kBlockRows;
   int8_t* ex = a.exps + ((size_t)page * kPageBlocks + blk) * 2;
-  const bool fresh = !put.ring && r % kBlockRows == 0;
   uint8_t *kb = a.kp + row * D, *vb = a.vp + row * D;
   float2 f;
-  f.x = open_block<D>(top_bits<PER>(xk), fresh ? -128 : had_k, kb, ex);
+  f.x = open_block<D>(top_bits<PER>(xk), had_k, kb, ex);
   code_row<PER>(xk, f.x, kb + r % kBlockRows * D);
-  f.y = open_block<D>(top_bits<PER>(xv), fresh ? -128 : had_v, vb, ex + 1);
+  f.y = open_block<D>(top_bits<PER>(xv), had_v, vb, ex + 1);
   code_row<PER>(xv, f.y, vb + r % kBlockRows * D);
   if ((threadIdx.x & 31) == 0) {
     a.pos[(size_t)page * kPageRows + r] = t;
@@ -284,7 +290,7 @@ __device__ __forceinline__ float2 put_row(const PagedArgs& a, const PagedDecodeA
 
 // Codes the new token's row of an item into its page (all lanes call).
 template <typename T, int D, int kMode>
-__device__ __forceinline__ void put_token(const PagedArgs& a, const PagedDecodeArgs& n, int c,
+__device__ __forceinline__ void put_token(const PagedArgs& a, const ModeArgs<kMode>& n, int c,
                                           const fg_paged_desc& hd, const Put& put, int t,
                                           bool pinned) {
   constexpr int PER = D / 32;
@@ -304,12 +310,13 @@ __device__ __forceinline__ void put_token(const PagedArgs& a, const PagedDecodeA
   }
   const int8_t* ex =
       a.exps + ((size_t)page * kPageBlocks + put.at % kPageRows / kBlockRows) * 2;
-  put_row<D, kMode>(a, n, put, page, t, pinned, ex[0], ex[1], xk, xv);
+  const bool opens = put_opens(put);
+  put_row<D, kMode>(a, n, put, page, t, pinned, opens ? -128 : ex[0], opens ? -128 : ex[1], xk, xv);
 }
 
 // The streaming warp.
 template <typename T, int D, bool kFold, int kMode>
-__device__ __forceinline__ void stream_items(const PagedArgs& a, const PagedDecodeArgs& n, int Gkv,
+__device__ __forceinline__ void stream_items(const PagedArgs& a, const ModeArgs<kMode>& n, int Gkv,
                                              int H, int R, int HLkv, uint8_t* ring_smem, Bars* bars,
                                              int wi, int wi_end, PagedItem it, fg_paged_desc hd,
                                              int items, const LaneSet& special,
@@ -524,7 +531,7 @@ __device__ __forceinline__ bool same_list(const PagedArgs& a) {
 // its two columns, that query's two terms; else two queries (2 t4, 2 t4 + 1).
 template <typename T, int D, bool kFold, int kMode>
 __global__ void __launch_bounds__(kThreads, kBlocks(D))
-    q8_split_kernel(const PagedArgs a, const PagedDecodeArgs n, int G, int H, int R, int HLkv,
+    q8_split_kernel(const PagedArgs a, const ModeArgs<kMode> n, int G, int H, int R, int HLkv,
                     float sl2) {
   constexpr bool kWide = wide<T>(kFold, kMode);
   using RG = Ring<D, kFold, kWide>;
@@ -540,8 +547,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
   const int q0 = NQ * t4;  // the lane's first query
-  const bool beside = kMode != kDecode && n.beside;
-  if (beside && !start_beside()) return;
+  bool beside = false;
+  if constexpr (kMode != kDecode) {
+    beside = n.beside;
+    if (beside && !start_beside()) return;
+  }
   // a list of another cache may say anything: its items are bounded here, its
   // caches where they are used
   const int wi0 = max(0, min(a.cta_first[blockIdx.x], a.n_work - 1));
@@ -842,15 +852,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
     }
     sync_warps();
     // O^T: rows 16 j + g, + 8 are dimensions (D / 8) g + 2 j, + 1; the columns as the queries'
-    const size_t g0 = (size_t)(cache / (H / R)) * H + (size_t)(cache % (H / R)) * R;
-    const int RH = R / kHalves<kFold, kMode>();
-#pragma unroll 1
-    for (int half_r = 0; half_r < R; half_r += RH) {
-      if (half_r > 0) sync_warps();  // the half before has been read
+    constexpr int kMerges = kHalves<kFold, kMode>();
+    const int RH = R / kMerges;
+#pragma unroll
+    for (int z = 0; z < kMerges; ++z) {
+      const int r0 = z * RH;    // its first query
+      if (z > 0) sync_warps();  // the half before has been read
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
         const int qi = q0 + q;
-        if (qi >= half_r && qi < half_r + RH) {
+        if (kMerges == 1 ? qi < R : qi >= r0 && qi < r0 + RH) {
           float M = kNoScore;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][qi]);
@@ -858,14 +869,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
 #pragma unroll
           for (int j = 0; j < MT; ++j)
             *reinterpret_cast<float2*>(
-                &sums[(warp * RH + qi - half_r) * D + (D / 8) * g + 2 * j]) =
+                &sums[(warp * RH + qi - r0) * D + (D / 8) * g + 2 * j]) =
                 kFold ? make_float2((o[j][0] + o[j][1]) * f, (o[j][2] + o[j][3]) * f)
                       : make_float2(o[j][q] * f, o[j][q + 2] * f);
         }
       }
       sync_warps();
+      const size_t g0 = (size_t)(cache / (H / R)) * H + (size_t)(cache % (H / R)) * R + r0;
       for (int x = warp * 32 + lane; x < RH * D; x += kWarps * 32) {
-        const int qi = half_r + x / D;
+        const int qi = r0 + x / D;
         float A = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) A += sums[w * RH * D + x];
@@ -880,9 +892,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks(D))
         // the item's own output: the sums are in units of 2^(M - kPBits), L in 2^S
         const float y = L == 0.f ? 0.f : A / L * exp2f(M - S - kPBits);
         if (alone) {
-          store_out((T*)n.out + (g0 + half_r) * D + x, y);
+          store_out((T*)n.out + g0 * D + x, y);
         } else {
-          n.part_acc[((size_t)item * R + half_r) * D + x] = y;
+          n.part_acc[((size_t)item * R + r0) * D + x] = y;
           if (x % D == 0) {
             n.part_ml[2 * ((size_t)item * R + qi)] = S;
             n.part_ml[2 * ((size_t)item * R + qi) + 1] = L;
@@ -902,7 +914,7 @@ int split_smem(int R) {
 }
 
 template <typename T, int D, bool kFold, int kMode>
-cudaError_t launch_split(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
+cudaError_t launch_split(const ProfileDims& pd, const PagedArgs& a, const ModeArgs<kMode>& n,
                          cudaStream_t s) {
   const auto split = q8_split_kernel<T, D, kFold, kMode>;
   const int smem = split_smem<T, D, kFold, kMode>(pd.R);
@@ -914,8 +926,10 @@ cudaError_t launch_split(const ProfileDims& pd, const PagedArgs& a, const PagedD
   if (D == 64 && e == cudaSuccess)
     e = cudaFuncSetAttribute(split, cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared);
+  int grid = a.n_ctas;
+  if constexpr (kMode != kDecode) grid += n.beside;
   if (e == cudaSuccess)
-    e = launch_pdl(split, a.n_ctas + n.beside, kThreads, smem, s, a, n, pd.G, pd.H, pd.R, pd.HLkv, pd.sl2);
+    e = launch_pdl(split, grid, kThreads, smem, s, a, n, pd.G, pd.H, pd.R, pd.HLkv, pd.sl2);
   return e;
 }
 

@@ -45,7 +45,7 @@ struct Joined {
 };
 
 // The count of a cache's rows after the step (all lanes of a warp call, with the same cache).
-__device__ __forceinline__ int rows_after(const PagedArgs& a, const PagedDecodeArgs& n,
+__device__ __forceinline__ int rows_after(const PagedArgs& a, const StepArgs& n,
                                           const fg_paged_desc& hd, int had, bool special,
                                           bool punct) {
   const bool stored = n.k_new && joins_static(hd.policy, special, special || punct) && had >= 0 &&
@@ -58,7 +58,7 @@ constexpr int kCombineWarps = 4;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kCombineWarps * 32)
-    step_combine_kernel(const PagedArgs a, const PagedDecodeArgs n, int G, int H, int R, int HLkv) {
+    step_combine_kernel(const PagedArgs a, const StepArgs n, int G, int H, int R, int HLkv) {
   constexpr int PER = D / 32, kAhead = 4;
   const int gq = blockIdx.x * kCombineWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const bool in = gq < G;
@@ -114,7 +114,7 @@ constexpr int kJoinWarps = 8;
 
 template <typename T, int D, int kSplit, int kFours>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-    step_join_kernel(const PagedArgs a, const PagedDecodeArgs n, const PrefixParts px, int H, int R,
+    step_join_kernel(const PagedArgs a, const StepArgs n, const PrefixParts px, int H, int R,
                      int HL) {
   constexpr int kAhead = 4, kQuads = kJoinWarps / kSplit, kPer = 4 * kFours;
   constexpr int kSlices = D / kPer / kQuads;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 }
 
 template <typename T, int D, int kSplit, int kFours>
-cudaError_t run_join(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
+cudaError_t run_join(const ProfileDims& pd, const PagedArgs& a, const StepArgs& n,
                      const PrefixParts& px, cudaStream_t s) {
   const long long grid =
       (long long)px.caches * px.tiles * cdiv(px.rows, 32) * (D / 4 / kFours / (kJoinWarps / kSplit));
@@ -267,7 +267,7 @@ constexpr int kWeighWarps = 8;
 
 template <int R>
 __global__ void __launch_bounds__(kWeighWarps * 32)
-    weigh_kernel(const PagedArgs a, const PagedDecodeArgs n, int Gkv, int H, int HLkv) {
+    weigh_kernel(const PagedArgs a, const StepArgs n, int Gkv, int H, int HLkv) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PagedItem it = a.items[blockIdx.x];
   const bool listed = same_list(a);
@@ -348,7 +348,7 @@ constexpr int kSmallWarps = 1;  // (a block of four waits for its longest: 194 u
 
 template <typename T, int D, bool kFold, int kMode>
 __global__ void __launch_bounds__(kSmallWarps * 32, 16)
-    q8_small_kernel(const PagedArgs a, const PagedDecodeArgs n, int Gkv, int H, int R, int HLkv,
+    q8_small_kernel(const PagedArgs a, const StepArgs n, int Gkv, int H, int R, int HLkv,
                     float sl2) {
   constexpr bool kWide = wide<T>(kFold, kMode), kTwo = kFold || kWide;
   constexpr int NQ = kFold ? 1 : 2;  // queries of a lane
@@ -484,7 +484,8 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 16)
   }
   if (new_page >= 0) {
     const float2 f = put_row<D, kMode>(a, n, put, new_page, t, kMode == kScores && special.has(tau),
-                                       new_k, new_v, xk, xv);
+                                       put_opens(put) ? -128 : new_k, put_opens(put) ? -128 : new_v,
+                                       xk, xv);
     new_k = 127 - (int)(__float_as_uint(f.x) >> 23);  // the exponents now
     new_v = 127 - (int)(__float_as_uint(f.y) >> 23);
   }
@@ -718,7 +719,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 16)
 constexpr int kSmallItems = 4;
 
 template <typename T, int D, bool kFold, int kMode>
-cudaError_t run_items(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
+cudaError_t run_items(const ProfileDims& pd, const PagedArgs& a, const StepArgs& n,
                       cudaStream_t s) {
   if (a.n_work < kSmallItems * a.n_ctas) return launch_split<T, D, kFold, kMode>(pd, a, n, s);
   return launch_pdl(q8_small_kernel<T, D, kFold, kMode>, cdiv(a.n_work, kSmallWarps) + n.beside,
@@ -726,14 +727,14 @@ cudaError_t run_items(const ProfileDims& pd, const PagedArgs& a, const PagedDeco
 }
 
 template <typename T, int D, bool kFold>
-cudaError_t run_split(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
+cudaError_t run_split(const ProfileDims& pd, const PagedArgs& a, const StepArgs& n,
                       cudaStream_t s) {
   return n.row_w ? run_items<T, D, kFold, kScores>(pd, a, n, s)
                  : run_items<T, D, kFold, kParts>(pd, a, n, s);
 }
 
 template <typename T, int D>
-cudaError_t run_step(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
+cudaError_t run_step(const ProfileDims& pd, const PagedArgs& a, const StepArgs& n,
                      const PrefixParts& px, cudaStream_t s) {
   cudaError_t e = pd.R <= kFoldR ? run_split<T, D, true>(pd, a, n, s)
                                  : run_split<T, D, false>(pd, a, n, s);
@@ -760,7 +761,7 @@ cudaError_t run_step(const ProfileDims& pd, const PagedArgs& a, const PagedDecod
 
 constexpr int kFewPages = 8;  // an SM's, of the shared caches
 
-cudaError_t launch_step_q8(const ProfileDims& pd, const PagedArgs& a, const PagedDecodeArgs& n,
+cudaError_t launch_step_q8(const ProfileDims& pd, const PagedArgs& a, const StepArgs& n,
                            const PagedArgs& pre, const PrefixParts& px0, cudaStream_t s) {
   PrefixParts px = px0;
   if (px.caches > 0) {
