@@ -268,7 +268,8 @@ __device__ __forceinline__ bool put_opens(const Put& put) {
 // opens the block.  Returns the powers of two that K and V were multiplied by.
 template <int D, int kMode>
 __device__ __forceinline__ float2 put_row(const PagedArgs& a, const ModeArgs<kMode>& n,
-                                          const Put& put, int page, int t, bool pinned, int had_k, int had_v,
+                                          const Put& put, int page, int t, bool pinned, int had_k,
+                                          int had_v,
                                           const float (&xk)[D / 32], const float (&xv)[D / 32]) {
   constexpr int PER = D / 32;
   const int r = put.at % kPageRows, blk = r / kBlockRows;

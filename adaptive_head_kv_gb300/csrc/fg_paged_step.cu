@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
 // With shared caches: their parts hold the queries of a tile side by side, so a lane takes a query
 // and a warp 4 kFours dimensions of 32 of them.  kSplit warps share the parts of these (where few
 // caches leave many parts to each), eight warps a block.  What a warp asks for before the values (the
-// sequence, its list's items, the parts) is a chain of loads: it takes more dimensions where there are
-// warps enough.
+// sequence, its list's items, the parts) is a chain of loads, which bounds it (16384 queries of 4
+// parts, 37 MB, 18 us): it takes more dimensions where there are warps enough (20 us with four).
 constexpr int kJoinWarps = 8;
 
 template <typename T, int D, int kSplit, int kFours>
@@ -257,12 +257,14 @@ cudaError_t run_join(const ProfileDims& pd, const PagedArgs& a, const StepArgs& 
   const long long grid =
       (long long)px.caches * px.tiles * cdiv(px.rows, 32) * (D / 4 / kFours / (kJoinWarps / kSplit));
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_pdl(step_join_kernel<T, D, kSplit, kFours>, (unsigned)grid, kJoinWarps * 32, 0, s, a, n, px,
-                    pd.H, pd.R, pd.HL);
+  return launch_pdl(step_join_kernel<T, D, kSplit, kFours>, (unsigned)grid, kJoinWarps * 32, 0, s, a,
+                    n, px, pd.H, pd.R, pd.HL);
 }
 
 // Adds the step's weights to the rows of a work item's part of the segment: a warp takes pages in
-// turns, a lane two rows of each.
+// turns, a lane two rows of each.  It reads R scores of a row and reads and writes its weight so far,
+// 4 R + 8 bytes beside the 2 d of its codes: 11 of 68 us (192 caches of 8192 positions, groups of
+// 8), which the chain item, table, row bounds more than their bytes (26 MB, 4 us at HBM's rate).
 constexpr int kWeighWarps = 8;
 
 template <int R>
@@ -343,7 +345,9 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
 // 16384 caches of some 30 rows took 4.5 us an item of a block.  Here an SM's warps open a dozen
 // items at a time and read each lane's operands where they lie; the arithmetic is the split kernel's,
 // with keys and values in their own order.  Pages of a ring without a row that counts (rings behind
-// a shared prompt begin empty) are passed over.
+// a shared prompt begin empty) are passed over.  Those caches take 80 us: 1600 instructions an item, at
+// a third of the schedulers' rate with the four warps each that registers leave room for.  (Warps that
+// take over blocks not yet started: 85 us.)
 constexpr int kSmallWarps = 1;  // (a block of four waits for its longest: 194 us, with one 181)
 
 template <typename T, int D, bool kFold, int kMode>
@@ -537,8 +541,11 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 16)
     uint32_t live0, live1;  // rows 0-31 and 32-63 that count
     if (ring) {
       const int left = ring_end - (it.ring0 + j - n_seg) * kPageRows;
-      live0 = __ballot_sync(0xffffffffu, lane < left && p.x >= 0 && (unsigned)t - (unsigned)p.x < (unsigned)w);
-      live1 = __ballot_sync(0xffffffffu, lane + 32 < left && p.y >= 0 && (unsigned)t - (unsigned)p.y < (unsigned)w);
+      auto counts = [&](int row, int pos) {
+        return row < left && pos >= 0 && (unsigned)t - (unsigned)pos < (unsigned)w;
+      };
+      live0 = __ballot_sync(0xffffffffu, counts(lane, p.x));
+      live1 = __ballot_sync(0xffffffffu, counts(lane + 32, p.y));
     } else {
       const int left = seg_end - (it.seg0 + j) * kPageRows;
       live0 = left >= 32 ? 0xffffffffu : (1u << max(left, 0)) - 1;
@@ -745,7 +752,8 @@ cudaError_t run_step(const ProfileDims& pd, const PagedArgs& a, const StepArgs& 
     // few queries: warps share a query's parts (8 caches of 8192 positions, 64 queries each: 71 us
     // by a warp a query, 33 with a lane a query, 9 shared); many: each part has work enough for all
     // SMs (32 caches, 512 queries each: 25, shared 58)
-    const long long blocks = (long long)px.caches * px.tiles * cdiv(px.rows, 32) * (D / 4 / kJoinWarps);
+    const long long blocks =
+        (long long)px.caches * px.tiles * cdiv(px.rows, 32) * (D / 4 / kJoinWarps);
     e = blocks <= 2 * px.sms ? run_join<T, D, 4, 1>(pd, a, n, px, s)
                              : run_join<T, D, 1, 2>(pd, a, n, px, s);
   }

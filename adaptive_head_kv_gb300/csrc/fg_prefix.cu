@@ -3,8 +3,8 @@
 // read once for all sequences.
 //
 // With B sequences and groups of R a cache meets B R queries, so both products
-// are matrix products of the tensor cores:
-//   S [128 queries x 128 keys] = Q K^T,  O [128 x d] += P V,
+// are matrix products of the tensor cores, a page of 64 keys at a time:
+//   S [128 queries x 64 keys] = Q K^T,  O [128 x d] += P V,
 // accumulators and P in tensor memory, operands in shared memory.  The codes of
 // a page are widened to f16, which holds them exactly, on their way; the
 // exponents of a block of 16 keys are two numbers for 16 columns of S: K's
@@ -12,18 +12,30 @@
 // Queries are f16 after the division by a power of two (11 bits; fp32 inputs two
 // terms, 22 bits: Q = Qh + Ql along the product's depth, P = Ph + Pl likewise).
 //
-// A thread block per SM: a warp that loads pages (bulk copies of codes, 2 KB to
-// 8 KB each), four that widen them into the swizzled layout the tensor cores
-// read, one that issues the products, and two warpgroups of softmax, a thread a
-// query.  The two work on separate streams with S and O of their own: two tiles
-// of queries over the same key tiles, or, where there is one tile of queries,
-// the even and the odd key tiles.  One stream's softmax runs while the tensor
-// cores have the other's products.  P takes S's place in tensor memory.
+// A thread block per SM: a warp that loads the pages' codes (bulk copies of 4 or
+// 8 KB), one that describes the pages, four that widen codes into the swizzled
+// layout the tensor cores read, two threads that issue products, and two
+// warpgroups of softmax, a thread a query.  The two work on separate streams
+// with S and O of their own: two tiles of queries over the same pages (each
+// widened once for both), or, where there is one tile of queries, the even and
+// the odd pages.  A stream has two places of S, so that the next page's scores
+// are there before the softmax asks; P takes S's place in tensor memory.
 //
 // The softmax is one pass over the rows: sums and products are kept relative
 // to reference maxima that follow the true ones when those get 2^kSlack ahead
 // (then O is rescaled in tensor memory).  The sum's maximum is that of the
 // scores, the product's that of score + V's exponent, as in the split kernel.
+//
+// What bounds it: 32 caches of 16384 positions (about 4800 pages), 512 queries each, take 81 us, 63
+// pages of two tiles an SM, 2400 cycles each.  Of those the products have 1270 (S of 64 keys is
+// bound by shared memory: 405 cycles where 260 would be the tensor cores'), exponentials 510, the
+// warps' instructions 1130 of each scheduler's; what is left is waiting of one role for another.
+// Without the softmax it takes 20 us less, without the products 10, without both 32, with pages from
+// L2 alone 1.  So rows cost 6 to 8 times their share of HBM's rate, and few queries do not change
+// that: below some 60 queries a cache the products compute rows of a tile that no query fills.
+//   The kernel's code has to fit the instruction cache: with the roles' loops unrolled it was 78 KB,
+// and the same case took 342 us.  Taken and dropped: key tiles of 128 with one place of S (197), S
+// in registers with a register split of the warps (198), eight warps that widen (180 -> 179).
 #include "fg_paged_decode.cuh"
 
 namespace fg {
@@ -31,7 +43,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTile = kPrefixTile;  // queries of a tile
+constexpr int kTile = kPrefixTile;  // queries of a tile (rows of tensor memory)
 // warps 0-7 softmax (warp w reads tensor memory lanes 32 (w % 4) ..), 8-11 widen
 constexpr int kSoftWarps = 8, kUnpackWarps = 4;
 constexpr int kLoadWarp = kSoftWarps + kUnpackWarps, kMetaWarp = kLoadWarp + 1;

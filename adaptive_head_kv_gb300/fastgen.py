@@ -24,11 +24,12 @@ FG_KEEP_DROP, FG_KEEP_STATIC, FG_KEEP_WINDOW = 0, 1, 2
 FG_ROPE_INTERLEAVED, FG_ROPE_HALF = 0, 1
 FG_PAGE_ROWS, FG_BLOCK_ROWS = 64, 16
 
-# kernels launched by one call of each entry point (counted in the bench)
+# kernels launched by one call of each entry point (counted in the bench); decode_q8_ex: with both
+# options (4 without scores, 3 without a prefix)
 LAUNCHES = {"profile": 4, "profile_attn": 5, "profile_with_policy": 5, "plan": 3, "compact": 1,
             "decode": 2, "decode_acc": 3, "refresh": 1, "refresh_init": 1, "rope": 1, "paged_plan": 5,
             "paged_schedule": 2, "compact_q8": 1, "append_q8": 2, "decode_q8": 2,
-            "decode_q8_ex": 4, "paged_fork": 5, "paged_clear": 1, "scores_q8": 1, "evict_q8": 2}
+            "decode_q8_ex": 5, "paged_fork": 5, "paged_clear": 1, "scores_q8": 1, "evict_q8": 2}
 
 EXPORTS = (
     "fastgen_status_string", "fastgen_version", "fastgen_profile_workspace_bytes",
