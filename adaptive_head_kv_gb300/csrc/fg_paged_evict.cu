@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // A warp takes kMoveBlocks blocks of 16 places below the budget in turn.  The codes of K and of V of
-// all rows that come to a block are asked for before any is used; rows lie far apart, so their
-// latency bounds it (1024 caches, 200 of 1024 places filled in each: 10 us for 50 MB).
+// all rows that come to a block are asked for before any is used; they lie far apart, and the chain
+// list, page, row, exponent bounds it (1024 caches of 1280 rows cut to 1024: 10 us, 20 MB).
 constexpr int kMoveWarps = 4, kMoveBlocks = 4;
 
 template <int D>

@@ -31,8 +31,8 @@
 // bound by shared memory: 405 cycles where 260 would be the tensor cores'), exponentials 510, the
 // warps' instructions 1130 of each scheduler's; what is left is waiting of one role for another.
 // Without the softmax it takes 20 us less, without the products 10, without both 32, with pages from
-// L2 alone 1.  So rows cost 6 to 8 times their share of HBM's rate, and few queries do not change
-// that: below some 60 queries a cache the products compute rows of a tile that no query fills.
+// L2 alone 1.  With one tile of 64 queries (256 caches of 4096, 133 MB) 65 us, 3.3 times HBM's: rows
+// of a tile that no query fills are computed all the same.
 //   The kernel's code has to fit the instruction cache: with the roles' loops unrolled it was 78 KB,
 // and the same case took 342 us.  Taken and dropped: key tiles of 128 with one place of S (197), S
 // in registers with a register split of the warps (198), eight warps that widen (180 -> 179).
