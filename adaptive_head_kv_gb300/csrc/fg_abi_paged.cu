@@ -135,7 +135,8 @@ fg_status fastgen_paged_fork(const fg_params* p, const fg_paged_cache* prefix,
   if (!prefix || !prefix->caches || !aligned(prefix->caches, 8) || !info || max_new_tokens < 0)
     return FG_EINVAL;
   if ((st = check_layout(cache)) != FG_OK) return st;
-  if (!cache->next_page || !aligned(cache->next_page, 4)) return FG_EINVAL;
+  if (!cache->next_page || !aligned(cache->next_page, 4) || cache->caches == prefix->caches)
+    return FG_EINVAL;
   const int32_t need = fastgen_paged_fork_table_len(p, max_new_tokens);
   if (need == 0) return FG_EINVAL;
   if (cache->table_len < need) return FG_EWORKSPACE;

@@ -31,8 +31,10 @@ StepParts step_parts(const fg_params* p, const fg_paged_cache* c, bool prefix, b
   return o;
 }
 
-// The shared caches: those of one sequence, read only.
-fg_status check_prefix(const fg_paged_cache* c) {
+// The shared caches: those of one sequence, read only, so not the ones that the step appends to.
+fg_status check_prefix(const fg_paged_cache* c, const fg_paged_cache* own) {
+  if (c->caches == own->caches || c->rows == own->rows || c->page_table == own->page_table)
+    return FG_EINVAL;
   if (!c->page_table || !c->caches || !c->rows || c->table_len < 1) return FG_EINVAL;
   if (!c->k_pages || !c->v_pages || !c->exps || !c->pos || c->n_pages < 1) return FG_EINVAL;
   if (!aligned(c->page_table, 4) || !aligned(c->caches, 8) || !aligned(c->rows, 4) ||
@@ -63,7 +65,7 @@ fg_status fastgen_decode_attn_q8_ex(const fg_params* p, const fg_paged_cache* ca
   if (st != FG_OK) return st;
   if ((st = check_pages(cache)) != FG_OK) return st;
   if ((st = check_sched(p, cache)) != FG_OK) return st;
-  if (prefix && (st = check_prefix(prefix)) != FG_OK) return st;
+  if (prefix && (st = check_prefix(prefix, cache)) != FG_OK) return st;
   if ((st = check_ids(special_ids, n_special)) != FG_OK) return st;
   if ((st = check_ids(punct_ids, n_punct)) != FG_OK) return st;
   if (!q || !pos || !out || !workspace || !dev_err || (k_new == nullptr) != (v_new == nullptr))

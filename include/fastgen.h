@@ -612,7 +612,8 @@ fg_status fastgen_decode_attn_q8(const fg_params* p, const fg_paged_cache* cache
  * (l, h / R) of the prefix and of its own cache together, in one softmax; ring rows of either
  * count while their position is in (pos[b] - w, pos[b]].  So a step gives what it would give if
  * each sequence had the prefix's rows in a cache of its own; they are read once for all of them,
- * and never written.  Of the prefix's fields rows_out, next_page and the work list are not used.
+ * and never written: they must not be `cache` itself.  Of the prefix's fields rows_out, next_page
+ * and the work list are not used.
  *   In the products with the prefix's rows queries and weights have 11 bits in bf16 and 22 in
  * fp32: off by at most 2^-11 or 2^-22 of each, or by 2^-38 of the query's largest value and 2^-32
  * of the largest weight (times its value exponent) where that is more.  A NaN among the values

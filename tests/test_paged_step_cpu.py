@@ -9,6 +9,8 @@ from adaptive_head_kv_gb300.session import PagedSession, make_params
 from test_paged_cpu import FAKE, LAYOUT, P, PAGES, built, cache, rope  # noqa: F401
 
 al = lambda x: (x + 255) // 256 * 256
+OTHER = FAKE + 4096
+PREFIX = dict(caches=OTHER, rows=OTHER, page_table=OTHER)  # not the ones that a step appends to
 
 
 def test_fork_table_len():
@@ -62,16 +64,19 @@ def test_step_rejects_on_host():
 
     def call(p=p, q=FAKE, k=FAKE, v=FAKE, ids=FAKE, ns=1, at=FAKE, r=None, out=FAKE, ws=FAKE,
              ws_bytes=need, err=FAKE, scores=FAKE, prefix=None, **kw):
-        return L.fastgen_decode_attn_q8_ex(p, cache(P(), **kw), cache(P(B=1), **(prefix or {})),
+        return L.fastgen_decode_attn_q8_ex(p, cache(P(), **kw), cache(P(B=1), **{**PREFIX, **(prefix or {})}),
                                            scores, q, k, v, ids, FAKE, ns, FAKE, 1, at, r or rope(),
                                            out, ws, ws_bytes, err, None)
 
+    assert call(ws_bytes=0) == fg.FG_EWORKSPACE  # nothing else is wrong
     for kw in LAYOUT + PAGES + [dict(prefix=x) for x in LAYOUT + PAGES] + [
             dict(sched=None), dict(sched=FAKE + 32), dict(n_work=0), dict(n_work=7),
             dict(n_work=1 << 20), dict(n_ctas=0), dict(n_ctas=41), dict(next_page=None),
             dict(q=None), dict(q=FAKE + 8), dict(k=None), dict(v=None), dict(v=FAKE + 8),
             dict(ids=None), dict(ns=9999), dict(at=None), dict(at=FAKE + 2), dict(out=None),
             dict(out=FAKE + 4), dict(ws=None), dict(ws=FAKE + 16), dict(err=None),
+            dict(prefix=dict(caches=FAKE)), dict(prefix=dict(rows=FAKE)),
+            dict(prefix=dict(page_table=FAKE)),
             dict(scores=FAKE + 4), dict(r=rope(rot_dim=256)), dict(rows_out=FAKE + 3)]:
         assert call(**kw) == fg.FG_EINVAL, kw
     assert call(ws_bytes=need - 1) == fg.FG_EWORKSPACE
@@ -89,12 +94,12 @@ def test_fork_and_clear_reject_on_host():
     L, p, info = fg.lib(), P(), fg.PagedInfo()
 
     def fork(p=p, new=64, out=info, prefix=None, **kw):
-        return L.fastgen_paged_fork(p, cache(P(B=1), **(prefix or {})), new, cache(P(), **kw), out,
-                                    None)
+        return L.fastgen_paged_fork(p, cache(P(B=1), **{**PREFIX, **(prefix or {})}), new,
+                                    cache(P(), **kw), out, None)
 
     for kw in LAYOUT + [dict(next_page=None), dict(next_page=FAKE + 2), dict(sched=None),
                         dict(sched=FAKE + 64), dict(new=-1), dict(out=None), dict(p=P(T=0.0)),
-                        dict(prefix=dict(caches=None)), dict(prefix=dict(caches=FAKE + 4))]:
+                        dict(prefix=dict(caches=FAKE)), dict(prefix=dict(caches=None)), dict(prefix=dict(caches=FAKE + 4))]:
         assert fork(**kw) == fg.FG_EINVAL, kw
     assert fork(table_len=15) == fg.FG_EWORKSPACE
     assert fork(sched_bytes=5) == fg.FG_EWORKSPACE
