@@ -49,7 +49,9 @@ __global__ void __launch_bounds__(256) scores_kernel(const PagedArgs a, const Sc
   const int count = n.n_new ? min(n.n_new[b], n.m) : n.m;
   if (first < 0) return;
   const fg_paged_desc hd = a.caches[c];
-  const int rows = live_rows(hd, a.rows[c]);
+  const int had = a.rows[c], rows = live_rows(hd, had);
+  if (threadIdx.x == 0 && (rows != had || ring_slots(hd, a.max_w) != hd.w))
+    atomicOr(a.dev_err, kErrInvalid);
   const size_t g0 = (size_t)(c / (H / R)) * H + (size_t)(c % (H / R)) * R;
   for (int r = threadIdx.x; r < rows; r += 256) {
     const int page = page_at(a, hd.first_page, hd.max_pages, r / kPageRows);
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(kThreads)
   const int t = n.pos[c / HLkv], had = a.rows[c], rows = live_rows(hd, had);
   __syncthreads();  // every thread has read the count
   if (tid == 0) {
-    if (rows != had) atomicOr(a.dev_err, kErrInvalid);
+    if (rows != had || ring_slots(hd, a.max_w) != hd.w) atomicOr(a.dev_err, kErrInvalid);
     a.rows_out[c] = t >= 0 && rows > n.budget ? n.budget : had;
     n.moves[c] = 0;
   }

@@ -282,6 +282,9 @@ class PagedSession(FastGenSession):
     def _prompt_buffers(self, G, n):
         if self.prefix is None:
             super()._prompt_buffers(G, n)
+        else:  # a fork has no prompt of its own
+            self.policy = self.mass = self.cost = self.colsum = self.keep = self.kept = None
+            self.ws = self.plan = None
 
     def _new_cache(self):
         Gkv, E, i32 = self.Gkv, self._empty, torch.int32
@@ -374,6 +377,8 @@ class PagedSession(FastGenSession):
         return out
 
     def _ready(self, Q, K):
+        if self.prefix is not None:
+            raise ValueError("a fork continues its prompt: prefill the session it was made from")
         if self.rope is None:
             return Q, K
         return self.rotate(Q, K, out=(Q, K) if self.in_place else None)

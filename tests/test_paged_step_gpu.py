@@ -571,6 +571,7 @@ def test_cut_bad_pages_are_flagged_not_followed():
     first = int(s.cache.caches[2, 2])
     plants = [(s.cache.page_table, first + i, bad) for i in (0, 1, 4) for bad in (1 << 30, -5)]
     plants += [(s.cache.caches[2:3, j], 0, bad) for j, bad in ((2, -1), (2, 1 << 30), (3, 0))]
+    plants += [(s.cache.caches[2:3, 1], 0, bad) for bad in (1 << 20, -1)]  # ring slots
     plants += [(s.cache.rows, 2, bad) for bad in (1 << 30, -9)]
     for x, i, bad in plants:
         x[i] = bad
@@ -707,6 +708,61 @@ def test_the_step_leaves_its_guards_alone():
     assert (out[[0, -1]] == 3.5).all() and (sc[[0, -1]] == 0.25).all()
 
 
+def lift(s, by):
+    """The same caches in the last pages of a pool that is `by` pages larger."""
+    c, n = s.cache, s.cache.c.n_pages
+    old = [x.clone() for x in (c.k_pages, c.v_pages, c.exps, c.pos)]
+    s.set_pages(n + by)
+    for x, y in zip((c.k_pages, c.v_pages, c.exps, c.pos), old):
+        x[by:] = y
+    t = c.page_table
+    t.copy_(torch.where(t >= 0, t + by, t))
+    c.next_page += by
+
+
+def same_rows(x, y):
+    """Pages, positions and scores of two pools by their tables."""
+    tx, ty = x.cache.page_table.long(), y.cache.page_table.long()
+    tx, ty = tx[tx >= 0], ty[ty >= 0]
+    assert torch.equal(x.cache.rows, y.cache.rows) and len(tx) == len(ty)
+    for name in ("k_pages", "v_pages", "exps", "pos"):
+        assert torch.equal(getattr(x.cache, name)[tx], getattr(y.cache, name)[ty]), name
+    assert torch.equal(x.scores[tx], y.scores[ty])
+
+
+def test_pages_past_four_gigabytes():
+    """Codes and scores that lie past 2^32 bytes of their buffers give what they give before."""
+    by = 540000  # pages of 64 x 128 codes: 4.4e9 bytes; a step's scores of groups of 8: 1.1e9
+    pair = [fork(45, 9, L=1, H=16, Hkv=2, n=200, policies=[4, 3]) for _ in range(2)]
+    lift(pair[1], by)
+    lift(pair[1].prefix, by)
+    for f in pair:
+        f.scores = torch.zeros(f.cache.c.n_pages, 64, device="cuda")
+    for st in range(3):
+        ids, k, v = pair[0].tokens(st, 1)
+        q = torch.randn(pair[0].G, 128, generator=gen(st)).to(torch.bfloat16)
+        outs = [f.decode(q, ids, k, v, [200 + st] * 9) for f in pair]
+        assert torch.equal(*outs) and float(outs[0].abs().max()) > 0
+    same_rows(*pair)
+    assert int(pair[1].cache.next_page.item()) > by and int(pair[1].err.item()) == 0
+    del f, pair
+    pair = [Step(46, L=1, H=8, Hkv=1, n=150, policies=[4]) for _ in range(2)]
+    for s in pair:
+        s.compact()
+    lift(pair[1], by)
+    ws = torch.empty(fg.fastgen_evict_q8_workspace_bytes(s.p, 64), dtype=torch.uint8, device="cuda")
+    ids, k, v = s.tokens(1, 1)
+    q = torch.randn(s.G, 128, generator=gen(1)).to(torch.bfloat16)
+    outs = []
+    for s in pair:
+        s.scores = torch.zeros(s.cache.c.n_pages, 64, device="cuda")
+        outs.append(s.decode(q, ids, k, v, [150]))
+        fg.fastgen_evict_q8(s.p, s.cache, s.scores, 64, 8, dev([150], torch.int32), ws, s.err)
+        assert int(s.err.item()) == 0 and s.cache.rows.tolist() == [64]
+    assert torch.equal(*outs)
+    same_rows(*pair)
+
+
 # ------------------------------------------------------------ the whole path
 @pytest.mark.parametrize("dtype,H,Hkv,d", [("bf16", 8, 2, 128), ("fp32", 4, 4, 64)])
 @pytest.mark.parametrize("own_stream", [False, True])
@@ -734,7 +790,8 @@ def test_session_forks_a_prompt_and_keeps_a_budget(dtype, H, Hkv, d, own_stream)
     torch.cuda.synchronize()
     pre.prefill_with_policy(*given, saved)
     s = pre.fork(B, max_new, budget=32, recent=8, guard=True)
-    for bad in (lambda: s.fork(2, 4), lambda: s.compact(given[1], given[2]), lambda: pre.evict(n)):
+    for bad in (lambda: s.fork(2, 4), lambda: s.compact(given[1], given[2]), lambda: pre.evict(n),
+                lambda: s.prefill(*given), lambda: s.prefill_with_policy(*given, saved)):
         with pytest.raises(ValueError):
             bad()
     torch.cuda.synchronize()
@@ -857,3 +914,55 @@ def test_session_scores_start_with_the_column_sums():
     out = s.decode(q, k, v, ids[:, 5].contiguous(), n)
     assert torch.isfinite(out).all() and (s.cache.rows == 33).all()
     assert fg.fastgen_read_error(s.dev_err) == fg.FG_OK and s.check_guards() == 0
+
+
+def test_a_captured_cut_of_a_pool_that_was_replaced_does_nothing_and_says_so():
+    """A later prompt wants more pages: step and cut captured before leave the new caches, the new
+    scores and what the old pool's memory holds now alone; forks of the prompt before see no rows of
+    it, and say so."""
+    from adaptive_head_kv_gb300.session import PagedSession, make_params
+
+    L, H, n, d = 1, 4, 200, 64
+    p = make_params(1, L, H, n, d, "bf16", 0.9, 0.3, 0.3)
+    g = gen(6)
+    Q, K, V = (dev(torch.randn(4, n, d, generator=g).to(torch.bfloat16)) for _ in range(3))
+    ids = dev(torch.randint(100, 300, (1, n), generator=g, dtype=torch.int32))
+    s = PagedSession(p, SPECIAL, PUNCT, 60, budget=16, recent=4)
+    s.prefill_with_policy(Q, K, V, ids, torch.tensor([3, 0, 0, 3], dtype=torch.int8))
+    f = s.fork(2, 8)
+    pos = dev([n], torch.int32)
+    step = [dev(torch.randn(4, d, generator=g).to(torch.bfloat16)) for _ in range(3)]
+    tok = dev([5], torch.int32)
+    s.decode(*step, tok, pos)
+    s.evict(pos)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    out = torch.full((4, d), 3.5, dtype=torch.bfloat16, device="cuda")
+    with torch.cuda.graph(graph):
+        s.decode(*step, tok, pos, out=out)
+        s.evict(pos)
+    graph.replay()
+    assert fg.fastgen_read_error(s.dev_err) == fg.FG_OK
+    old = s.cache
+    s.prefill_with_policy(Q, K, V, ids, torch.full((4,), 4, dtype=torch.int8))
+    assert s.cache is not old and (s.cache.rows == n).all()
+    before = [x.clone() for x in (s.cache.k_pages, s.cache.rows, s.cache.page_table, s.scores)]
+    graph.replay()
+    assert fg.fastgen_read_error(s.dev_err) == fg.FG_EINVAL
+    s.dev_err.zero_()
+    s.ews.zero_()
+    fg.fastgen_evict_q8(s.p, old_view(old, s), s.scores, 16, 4, pos, s.ews, s.dev_err)
+    assert fg.fastgen_read_error(s.dev_err) == fg.FG_EINVAL
+    for x, y in zip(before, (s.cache.k_pages, s.cache.rows, s.cache.page_table, s.scores)):
+        assert torch.equal(x, y)
+    q2 = dev(torch.randn(8, d, generator=g).to(torch.bfloat16))
+    kv = [dev(torch.randn(8, d, generator=g).to(torch.bfloat16)) for _ in range(2)]
+    got = f.decode(q2, *kv, dev([5, 6], torch.int32), n)
+    assert fg.fastgen_read_error(f.dev_err) == fg.FG_EINVAL and torch.isfinite(got).all()
+
+
+def old_view(old, s):
+    """The retired cache's descriptors and counts with the new cache's pages."""
+    c = s.cache
+    return fg.PagedCache(s.p, c.k_pages, c.v_pages, c.exps, c.pos, old.page_table, old.caches,
+                         old.rows, c.next_page)
