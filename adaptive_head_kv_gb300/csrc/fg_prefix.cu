@@ -417,7 +417,34 @@ __device__ __forceinline__ void widen(Smem<D, kTerms, kPair>& s, int uw, int tot
 #pragma unroll 1
   for (int k = 0; k < total; ++k) {
     const int ms = k % kMetas, raw = k % P::kRaw;
-    if (!warp_wait(&s.meta_full[ms], k / kMetas & 1, abort)) return;
+    const int seq[2] = {2 * k, 2 * k + 1}, slot[2] = {seq[0] % P::kOperands, seq[1] % P::kOperands};
+    auto has_room = [&](int side) {
+      return seq[side] < P::kOperands ||
+             test_bar(&s.op_empty[slot[side]], (seq[side] / P::kOperands - 1) & 1);
+    };
+    auto wait_room = [&](int side) {
+      return seq[side] < P::kOperands ||
+             warp_wait(&s.op_empty[slot[side]], (seq[side] / P::kOperands - 1) & 1, abort);
+    };
+    // What the page needs is asked for at once: one after the other the answers took 1000 of a page's
+    // 1650 cycles.
+    const bool ready = test_bar(&s.meta_full[ms], k / kMetas & 1) &
+                       test_bar(&s.raw_full[raw], k / P::kRaw & 1) & has_room(0);
+    const bool room = __all_sync(0xffffffffu, has_room(1));
+    if (!__all_sync(0xffffffffu, ready)) {
+      if (!warp_wait(&s.meta_full[ms], k / kMetas & 1, abort)) return;
+      if (!warp_wait(&s.raw_full[raw], k / P::kRaw & 1, abort)) return;
+      if (!wait_room(0)) return;
+    }
+    const uint8_t* codes = s.raw[raw] + uw * kBlockRows * D;
+    // K and V are read before either is written: one wait for both
+    uint4 x[2][kIter];
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+#pragma unroll
+      for (int i = 0; i < kIter; ++i)
+        x[side][i] = *reinterpret_cast<const uint4*>(codes + side * P::kPiece + row_of(i) * D +
+                                                     piece_of(i) * 16);
     const PageMeta& m = s.meta[ms];
     const int cnt = m.cnt, w = m.w;
     uint32_t here = 0xffffu, poison = 0;
@@ -427,10 +454,6 @@ __device__ __forceinline__ void widen(Smem<D, kTerms, kPair>& s, int uw, int tot
       if (ok && w > 0) ok = m.pos[row] >= 0;
       here = __ballot_sync(0xffffffffu, ok);
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s.meta_empty[ms]);
-    if (!warp_wait(&s.raw_full[raw], k / P::kRaw & 1, abort)) return;
-    const uint8_t* codes = s.raw[raw] + uw * kBlockRows * D;
     if (w > 0) {
       // A ring's row may be seen by some queries and not by others, and 0 times a NaN value is
       // NaN: its NaN values become zeros, and its key NaN, which only who sees it takes.
@@ -462,22 +485,10 @@ __device__ __forceinline__ void widen(Smem<D, kTerms, kPair>& s, int uw, int tot
       *reinterpret_cast<uint4*>(p + ((z ^ lr) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
       *reinterpret_cast<uint4*>(p + (((z + 1) ^ lr) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
     };
-    // K and V are read before either is written: one wait for both
-    uint4 x[2][kIter];
-    if (plain) {
-#pragma unroll
-      for (int side = 0; side < 2; ++side)
-#pragma unroll
-        for (int i = 0; i < kIter; ++i)
-          x[side][i] = *reinterpret_cast<const uint4*>(codes + side * P::kPiece + row_of(i) * D +
-                                                       piece_of(i) * 16);
-    }
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
-      const int seq = 2 * k + side, slot = seq % P::kOperands;
-      if (seq >= P::kOperands && !warp_wait(&s.op_empty[slot], (seq / P::kOperands - 1) & 1, abort))
-        return;
-      uint8_t* dst = s.op[slot] + uw * kBlockRows * 128;
+      if (side == 1 && !room && !wait_room(1)) return;
+      uint8_t* dst = s.op[slot[side]] + uw * kBlockRows * 128;
       if (plain) {
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
@@ -508,8 +519,8 @@ __device__ __forceinline__ void widen(Smem<D, kTerms, kPair>& s, int uw, int tot
       fence_async_shared();  // the tensor cores read what the lanes have written
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&s.op_full[slot]);
-        if (side == 1) mbar_arrive(&s.raw_empty[raw]);
+        mbar_arrive(&s.op_full[slot[side]]);
+        mbar_arrive(side == 0 ? &s.meta_empty[ms] : &s.raw_empty[raw]);
       }
     }
   }
