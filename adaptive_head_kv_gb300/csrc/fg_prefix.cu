@@ -27,12 +27,14 @@
 // scores, the product's that of score + V's exponent, as in the split kernel.
 //
 // What bounds it: 32 caches of 16384 positions (about 4800 pages), 512 queries each, take 81 us, 63
-// pages of two tiles an SM, 2400 cycles each.  Of those the products have 1270 (S of 64 keys is
-// bound by shared memory: 405 cycles where 260 would be the tensor cores'), exponentials 510, the
-// warps' instructions 1130 of each scheduler's; what is left is waiting of one role for another.
-// Without the softmax it takes 20 us less, without the products 10, without both 32, with pages from
-// L2 alone 1.  With one tile of 64 queries (256 caches of 4096, 133 MB) 65 us, 3.3 times HBM's: rows
-// of a tile that no query fills are computed all the same.
+// pages of two tiles an SM, 2350 cycles each, in which the threads that issue products wait for the
+// tensor cores and these for shared memory: it moves 192 KB a page, 1540 cycles (for each tile
+// S reads 32 KB of queries and 16 of keys, the product with V 16; codes come in, are read and
+// written widened, 64).  S of 64 keys alone takes 405 cycles where 260 would be the tensor cores'.
+// Exponentials have 510 cycles, the warps' instructions 1130 of each scheduler's.  Without the softmax
+// it takes 20 us less, without the products 10, without both 32, with pages from L2 alone 1.
+// With one tile of 64 queries (256 caches of 4096, 133 MB) 60 us, 3 times HBM's: widening a page
+// takes its warps 1300 cycles, and rows of a tile that no query fills are computed all the same.
 //   The kernel's code has to fit the instruction cache: with the roles' loops unrolled it was 78 KB,
 // and the same case took 342 us.  Taken and dropped: key tiles of 128 with one place of S (197), S
 // in registers with a register split of the warps (198), eight warps that widen (180 -> 179).
