@@ -64,9 +64,10 @@ def test_step_rejects_on_host():
 
     def call(p=p, q=FAKE, k=FAKE, v=FAKE, ids=FAKE, ns=1, at=FAKE, r=None, out=FAKE, ws=FAKE,
              ws_bytes=need, err=FAKE, scores=FAKE, prefix=None, **kw):
-        return L.fastgen_decode_attn_q8_ex(p, cache(P(), **kw), cache(P(B=1), **{**PREFIX, **(prefix or {})}),
-                                           scores, q, k, v, ids, FAKE, ns, FAKE, 1, at, r or rope(),
-                                           out, ws, ws_bytes, err, None)
+        shared = cache(P(B=1), **{**PREFIX, **(prefix or {})})
+        return L.fastgen_decode_attn_q8_ex(p, cache(P(), **kw), shared, scores, q, k, v, ids, FAKE,
+                                           ns, FAKE, 1, at, r or rope(), out, ws, ws_bytes, err,
+                                           None)
 
     assert call(ws_bytes=0) == fg.FG_EWORKSPACE  # nothing else is wrong
     for kw in LAYOUT + PAGES + [dict(prefix=x) for x in LAYOUT + PAGES] + [
