@@ -654,6 +654,11 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
     const int tile = wk.tile() + (kPair ? st : 0), j = tile * kTile + row;
     const int t = j < px.nq ? n.pos[j / R] : -1;
     const float fq = t < 0 ? 0.f : px.qf[((size_t)wk.c * px.tiles + tile) * kTile + row];
+    // A key that does not count scores -inf, which its block's factor must leave alone: the exponent
+    // of a block without a row may be any byte, and a query of zeros times a block of zeros has a
+    // factor below what a float holds.  So no factor is below the least normal number: scores that
+    // are that small (2^-96 at most) are as good as 0.  (Without a query: 0, whatever lies in S.)
+    const float least = t < 0 ? 0.f : 1.17549435e-38f;
     const bool work = __any_sync(0xffffffffu, t >= 0);  // else no lane's result is asked for
     // the positions of the warp's queries lie from t_lo to t_hi
     const int t_lo = (int)__reduce_min_sync(0xffffffffu, t < 0 ? 0x7fffffffu : (uint32_t)t);
@@ -732,7 +737,7 @@ __device__ __forceinline__ void weights(Smem<D, kTerms, kPair>& s, const PagedDe
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const uint32_t x = (b < 2 ? head.x : head.y) >> (16 * (b & 1));
-          f[b] = fminf(fq * pow2f((int)(signed char)(x & 0xff)), 1.7e38f);
+          f[b] = fminf(fmaxf(fq * pow2f((int)(signed char)(x & 0xff)), least), 1.7e38f);
           ev[b] = (float)(signed char)(x >> 8 & 0xff);
         }
         tmem_wait_ld(r[0]);
