@@ -268,11 +268,16 @@ class PagedSession(FastGenSession):
                  budget=0, recent=0, _prefix=None):
         if budget % fg.FG_BLOCK_ROWS or not 0 <= recent <= budget:
             raise ValueError(f"budget must be a multiple of {fg.FG_BLOCK_ROWS}, recent at most budget")
-        self.prefix = _prefix
-        super().__init__(params, special_ids, punct_ids, max_new_tokens, device, stream, guard)
+        self.prefix, self.device, self.stream = _prefix, torch.device(device), stream
+        made_on = torch.cuda.current_stream(self.device)
+        with self._on_stream():
+            # the buffers are the session's stream's, behind what the current stream has in hand: the
+            # id sets may come from there
+            torch.cuda.current_stream(self.device).wait_stream(made_on)
+            super().__init__(params, special_ids, punct_ids, max_new_tokens, device, stream, guard)
+            self.cache = self._new_cache()
         self.rope, self.pages, self.in_place = rope, pages, in_place
         self.budget, self.recent, self.scores = int(budget), int(recent), None
-        self.cache = self._new_cache()
         self.aws = self.ews = None
         self._held = []  # what captured calls may still use
         self._rotated = None
