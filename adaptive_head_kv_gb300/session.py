@@ -89,11 +89,19 @@ class FastGenSession:
         head, host or device): keep codes of each head's saved entry on this
         prompt; only heads whose entry contains C_frequent are scored."""
         self._ids, self._scored = token_ids, False
-        self.policy.copy_(torch.as_tensor(policy_map, dtype=torch.int8).reshape(-1),
-                          non_blocking=True)
+        with self._on_stream():
+            self.policy.copy_(torch.as_tensor(policy_map, dtype=torch.int8).reshape(-1),
+                              non_blocking=True)
         fg.fastgen_profile_with_policy(self.p, Q, K, token_ids, self.special, self.punct,
                                        self.policy, self.colsum, self.keep, self.kept, self.ws,
                                        self.dev_err, self.stream)
+
+    def _on_stream(self):
+        """Context in which torch works on the session's device and stream."""
+        s = self.stream
+        if isinstance(s, int):
+            s = torch.cuda.ExternalStream(s, self.device)
+        return torch.cuda.stream(torch.cuda.current_stream(self.device) if s is None else s)
 
     def prefill_with_policy(self, Q, K, V, token_ids, policy_map):
         Q, K = self._ready(Q, K)
@@ -335,13 +343,6 @@ class PagedSession(FastGenSession):
                 self.scores.zero_()
         fg.fastgen_paged_clear(self.p, self.cache, self.dev_err, self.stream)
         self._size_decode_workspace()
-
-    def _on_stream(self):
-        """Context in which torch works on the session's device and stream."""
-        s = self.stream
-        if isinstance(s, int):
-            s = torch.cuda.ExternalStream(s, self.device)
-        return torch.cuda.stream(torch.cuda.current_stream(self.device) if s is None else s)
 
     def _hold(self, ws):
         """Keeps the workspace, the cache and the scores of a call that is being captured."""

@@ -60,3 +60,17 @@ def test_a_fork_made_while_the_current_stream_is_busy(as_address):
         outs.append(torch.stack(out))
     assert torch.equal(*outs) and float(outs[0].abs().max()) > 0
     assert rows(forks[0]) == rows(forks[1])
+
+
+def test_a_saved_policy_map_while_the_current_stream_is_busy():
+    got = []
+    for stream in (None, torch.cuda.Stream()):
+        s, given, policies = prompt(stream)
+        if stream is not None:
+            torch.cuda._sleep(BUSY)
+        s.prefill_with_policy(*given, policies)
+        torch.cuda.synchronize()
+        assert s.policy.tolist() == policies.tolist()
+        assert fg.fastgen_read_error(s.dev_err) == fg.FG_OK
+        got.append(rows(s))
+    assert got[0] == got[1]
