@@ -259,10 +259,12 @@ class PagedSession(FastGenSession):
     as FG_ECAPACITY by fastgen_read_error(dev_err).
 
     budget (a multiple of 16; 0: none): evict cuts never-evicted segments that have outgrown it to
-    that many rows: the rows of the newest `recent` positions, then those that have received most
-    attention so far.  The session then keeps scores [pages, 64]: a prompt's rows start with their
-    column sums (with 0 after prefill_with_policy, which does not form them), appended rows with 0,
-    special tokens' rows are pinned, and every decode adds its weights.
+    that many rows: the rows of the newest `recent` positions, then those of special tokens, then
+    those that have received most attention so far.  Leave room for the special tokens: where they
+    and the recent rows pass the budget, the later ones of them go.  The session then keeps scores
+    [pages, 64]: a prompt's rows start with their column sums (with 0 after prefill_with_policy,
+    which does not form them), appended rows with 0, special tokens' rows with +inf, and every
+    decode adds its weights.
 
     fork makes a session of many sequences that continue this one's prompt.
 

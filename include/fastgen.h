@@ -622,8 +622,9 @@ fg_status fastgen_decode_attn_q8(const fg_params* p, const fg_paged_cache* cache
  *
  * scores (NULL: none) [n_pages, FG_PAGE_ROWS] float: what each row of the never-evicted segments
  * has received so far.  A row that the step appends starts at 0, or at +inf when its token is
- * one of special_ids (+inf: never dropped); then every segment row of an active sequence gets the
- * sum, over the query heads of its group, of the weights that the step's softmax gives it.
+ * one of special_ids (a pinned row: fastgen_evict_q8 drops it only where recent and pinned rows
+ * alone pass the budget); then every segment row of an active sequence gets the sum, over the query
+ * heads of its group, of the weights that the step's softmax gives it.
  *   Other rows' entries stay (a prefix's rows have none).  32-bit sums in a fixed order.  Aligned
  * to 8 bytes.
  *
@@ -671,7 +672,8 @@ fg_status fastgen_scores_q8(const fg_params* p, const fg_paged_cache* cache, flo
 
 /* Cuts never-evicted segments of more than `budget` rows to `budget` rows.  The rows that stay
  * are the first of this order: rows of positions in (pos[b] - recent, pos[b]]; then by larger score
- * (+inf first; NaN and negative scores count as 0); ties to the lower row.  Rows that stay and lie
+ * (+inf first; NaN and negative scores count as 0); ties to the lower row.  So a row with +inf stays
+ * as long as recent rows and rows with +inf together are at most `budget`.  Rows that stay and lie
  * below row `budget` are not moved; the others come, in row order, to the places of the dropped
  * rows below it, with their positions and scores, and are coded again at the exponents of the
  * blocks they come to (which grow where they have to).  Nothing else changes: shorter segments,
