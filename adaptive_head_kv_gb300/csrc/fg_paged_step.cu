@@ -328,10 +328,13 @@ __global__ void __launch_bounds__(kWeighWarps * 32)
 #pragma unroll
         for (int q = 0; q < R; ++q) y[h] = fmaf(ex2(s[u][h][q] - M[q]), r[q], y[h]);
       const int row = (j + u * kWeighWarps) * kPageRows + 2 * lane;
+      // a pinned row stays pinned, also where a weight is NaN
+      const float w0 = w[u].x == -FG_NEG_INF ? w[u].x : w[u].x + y[0];
+      const float w1 = w[u].y == -FG_NEG_INF ? w[u].y : w[u].y + y[1];
       if (row + 1 < end)
-        *reinterpret_cast<float2*>(n.row_w + at[u]) = make_float2(w[u].x + y[0], w[u].y + y[1]);
+        *reinterpret_cast<float2*>(n.row_w + at[u]) = make_float2(w0, w1);
       else
-        n.row_w[at[u]] = w[u].x + y[0];
+        n.row_w[at[u]] = w0;
     }
   }
 }

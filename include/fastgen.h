@@ -625,8 +625,8 @@ fg_status fastgen_decode_attn_q8(const fg_params* p, const fg_paged_cache* cache
  * one of special_ids (a pinned row: fastgen_evict_q8 drops it only where recent and pinned rows
  * alone pass the budget); then every segment row of an active sequence gets the sum, over the query
  * heads of its group, of the weights that the step's softmax gives it.
- *   Other rows' entries stay (a prefix's rows have none).  32-bit sums in a fixed order.  Aligned
- * to 8 bytes.
+ *   +inf stays +inf, whatever is added (a weight may be NaN).  Other rows' entries stay (a prefix's
+ * rows have none).  32-bit sums in a fixed order.  Aligned to 8 bytes.
  *
  * Arguments, errors and limits else as fastgen_decode_attn_q8; another workspace size.  A work
  * list is needed for `cache` alone. */

@@ -38,3 +38,22 @@ def test_pinned_rows_rank_behind_recent_ones_alone(budget, recent):
         w = weights[torch.as_tensor(gpu.pages(c, False).repeat(64)[:n]), torch.arange(n) % 64]
         want |= set(sorted(rest, key=lambda r: (-float(w[r]), r))[: max(0, left - len(pinned))])
         assert stay == want
+
+
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (8, 1)])
+def test_a_step_with_nan_leaves_pinned_rows_pinned(H, Hkv):
+    """Weights that are NaN make the rows' scores NaN, which count as 0 from then on, but not those
+    of special tokens."""
+    s = Step(62, L=1, H=H, Hkv=Hkv, n=150, policies=[4]).with_scores(2)
+    s.compact()
+    before = s.scores.clone()
+    q = torch.randn(s.G, s.d, generator=gen(1))
+    q[1] = float("nan")
+    s.decode(q.to(torch.bfloat16), None, None, None, [150])
+    gpu, sick = P.GpuPages(s.cache), 1 // s.R
+    for c in range(s.gk):
+        at = torch.as_tensor(gpu.pages(c, False)[:3])
+        was, now = (x[at.cuda()].reshape(-1)[:150] for x in (before, s.scores))
+        pinned = torch.isinf(was)
+        assert pinned.any() and torch.equal(torch.isinf(now), pinned)
+        assert bool(torch.isnan(now[~pinned]).all()) == (c == sick)
