@@ -261,10 +261,11 @@ class PagedSession(FastGenSession):
     budget (a multiple of 16; 0: none): evict cuts never-evicted segments that have outgrown it to
     that many rows: the rows of the newest `recent` positions, then those of special tokens, then
     those that have received most attention so far.  Leave room for the special tokens: where they
-    and the recent rows pass the budget, the later ones of them go.  The session then keeps scores
-    [pages, 64]: a prompt's rows start with their column sums (with 0 after prefill_with_policy,
-    which does not form them), appended rows with 0, special tokens' rows with +inf, and every
-    decode adds its weights.
+    and the recent rows pass the budget, the later ones of them go.  max_new_tokens, and with it the
+    worst case of the page pool, need then be no more than budget plus the tokens between two cuts,
+    however long the generation.  The session then keeps scores [pages, 64]: a prompt's rows start
+    with their column sums (with 0 after prefill_with_policy, which does not form them), appended
+    rows with 0, special tokens' rows with +inf, and every decode adds its weights.
 
     fork makes a session of many sequences that continue this one's prompt.
 
@@ -494,9 +495,9 @@ class PagedSession(FastGenSession):
 
     def evict(self, pos):
         """Cuts segments that have outgrown the budget; pos [B] (or an int): the newest position
-        of each sequence (< 0: left out).  Worth a call every few dozen steps: 1024 caches cost 20
-        us, segments within the budget next to nothing.  The list of a later reschedule
-        follows."""
+        of each sequence (< 0: left out).  Worth a call every few dozen steps: 1024 caches take 20
+        us where 307 are cut from 1280 rows to 1024, 8 where none is.  The list of a later
+        reschedule follows."""
         if not self.budget:
             raise ValueError("the session has no budget")
         self.ews = self._grown(self.ews, fg.fastgen_evict_q8_workspace_bytes(self.p, self.budget))

@@ -1,10 +1,12 @@
-"""What the cut to a budget promises: which rows a pinned one gives way to."""
+"""What the cut to a budget promises: which rows a pinned one gives way to, what becomes of it in a
+step of NaN, and the pages that a long generation needs."""
 import pytest
 import torch
 
 import paged_ref as P
 from adaptive_head_kv_gb300 import fastgen as fg
-from test_paged_gpu import dev, gen
+from adaptive_head_kv_gb300.session import PagedSession, make_params
+from test_paged_gpu import PUNCT, SPECIAL, dev, gen
 from test_paged_step_gpu import Step
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +59,42 @@ def test_a_step_with_nan_leaves_pinned_rows_pinned(H, Hkv):
         pinned = torch.isinf(was)
         assert pinned.any() and torch.equal(torch.isinf(now), pinned)
         assert bool(torch.isnan(now[~pinned]).all()) == (c == sick)
+
+
+@pytest.mark.parametrize("forked", [False, True])
+def test_a_long_generation_within_the_pages_of_a_budget(forked):
+    """Room for budget + 16 new rows a cache and a cut every 16 steps: any number of steps, with the
+    results that room for all of them gives; without cuts that room ends, and a step says so."""
+    L, H, n, d, budget, every, steps = 1, 4, 150, 64, 48, 16, 120
+    B = 2 if forked else 1
+    p = make_params(1, L, H, n, d, "bf16", 0.9, 0.3, 0.3)
+    g = gen(63)
+    Q, K, V = (dev(torch.randn(H, n, d, generator=g).to(torch.bfloat16)) for _ in range(3))
+    ids = dev(torch.randint(100, 300, (1, n), generator=g, dtype=torch.int32))
+    q = dev(torch.randn(steps, 3, B * H, d, generator=g).to(torch.bfloat16))
+    new = dev(torch.randint(100, 300, (steps, B), generator=g, dtype=torch.int32))
+    full = torch.full((H,), 4, dtype=torch.int8)
+
+    def generate(room, cuts):
+        s = PagedSession(p, SPECIAL, PUNCT, 1 if forked else room, budget=0 if forked else budget,
+                         recent=0 if forked else 8)
+        s.prefill_with_policy(Q, K, V, ids, full)
+        if forked:
+            s = s.fork(B, room, budget=budget, recent=8)
+        elif cuts:
+            s.evict(n - 1)
+        outs, held = [], s.cache.c.n_pages
+        for st in range(steps):
+            outs.append(s.decode(*q[st], new[st], n + st).clone())
+            if cuts and st % every == every - 1:
+                s.evict(n + st)
+        return s, torch.stack(outs), held, fg.fastgen_read_error(s.dev_err)
+
+    s, outs, held, err = generate(budget + every, True)
+    assert err == fg.FG_OK and (s.cache.rows <= budget + every).all()
+    # a fork's caches begin empty, a prompt's with all of its rows
+    assert held == s.Gkv * -(-(budget + every + (0 if forked else n)) // 64)
+    wide, want, more, err = generate(steps, True)
+    assert err == fg.FG_OK and more > held and torch.equal(outs, want)
+    assert torch.equal(s.cache.rows, wide.cache.rows)
+    assert generate(budget + every, False)[3] == fg.FG_ECAPACITY
