@@ -85,8 +85,8 @@ __device__ __forceinline__ uint32_t row_key(float score, int p, int t, int recen
 }
 
 // One CTA per cache: which rows stay, and which of those behind the budget come to which place
-// below it.  The keys are read once, into shared memory where they fit (kKeys); the budget-th
-// largest is found eleven bits at a time.  A chain of loads, scans and barriers bounds it: 1024 caches
+// below it.  The keys are read once, into shared memory (of a cache with more than kKeys rows they
+// are read seven times); the budget-th largest is found eleven bits at a time.  A chain of loads, scans and barriers bounds it: 1024 caches
 // of 1280 rows about 10 us, 16 of 32768 rows 25 us (with clusters of eight blocks a cache, whose
 // barriers cost as much as the shorter runs save, 30 us).
 template <int kThreads, int kKeys>
@@ -319,10 +319,17 @@ static cudaError_t run_select(const ProfileDims& pd, const PagedArgs& a, const E
 
 cudaError_t launch_evict_q8(const ProfileDims& pd, const PagedArgs& a, const EvictArgs& n,
                             cudaStream_t s) {
-  // by the rows that the table gives a cache on average
+  // Rows that do not fit cost the small form dear: 77 of 256 caches cut from 7801 rows 167 us, the
+  // large form 19; 307 of 1024 from 7001 (d = 64) 331 and 70.  Where all fit it has more caches on
+  // an SM: 4096 cut from 2001 rows 190 us and 285 (32 of them 23 and 16).  What is known here is the
+  // room that the table gives a cache on average, and the prompt's length: of a prompt longer than
+  // what fits some head may keep every row, unless the caches are those of sequences behind it, with
+  // room for their own tokens alone (a mix of all policies has room for 0.4 of the prompt).
+  constexpr int kFits = 4096;
   const long long room = (long long)a.table_len * kPageRows / pd.Gkv;
+  const bool longer = room > kFits || (pd.n > kFits && room > pd.n / 8);
   const cudaError_t e =
-      room <= 4096 ? run_select<256, 4096>(pd, a, n, s) : run_select<1024, 49152>(pd, a, n, s);
+      longer ? run_select<1024, 49152>(pd, a, n, s) : run_select<256, kFits>(pd, a, n, s);
   if (e != cudaSuccess) return e;
   const int blocks = n.budget / kBlockRows;
   const long long warps = (long long)cdiv(blocks, kMoveBlocks) * pd.Gkv;

@@ -7,7 +7,7 @@ import paged_ref as P
 from adaptive_head_kv_gb300 import fastgen as fg
 from adaptive_head_kv_gb300.session import PagedSession, make_params
 from test_paged_gpu import PUNCT, SPECIAL, dev, gen
-from test_paged_step_gpu import Step
+from test_paged_step_gpu import Step, check_cut
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +98,18 @@ def test_a_long_generation_within_the_pages_of_a_budget(forked):
     assert err == fg.FG_OK and more > held and torch.equal(outs, want)
     assert torch.equal(s.cache.rows, wide.cache.rows)
     assert generate(budget + every, False)[3] == fg.FG_ECAPACITY
+
+
+@pytest.mark.parametrize("n,policies,recent", [
+    (4500, [4, 2, 1, 3, 0, 1], 100),  # long caches among short ones: room for 0.3 of the prompt
+    (4500, [4] + [0] * 31, 0),        # one of 32: room for less than an eighth
+    (4090, [4, 0, 3], 4000),
+])
+def test_cut_of_caches_of_many_lengths(n, policies, recent):
+    """Some caches hold more rows than the small form has places for, the others few."""
+    s = Step(64, L=1, H=len(policies), n=n, d=64, policies=policies, max_new=4).with_scores(5)
+    s.compact()
+    assert check_cut(s, 4000, recent, [n - 1]) > 0
+    assert sorted(set(s.cache.rows.tolist()))[-1] == 4000 < n
+    s.check()
+    assert int(s.err.item()) == 0
