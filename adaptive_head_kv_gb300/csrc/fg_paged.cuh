@@ -7,7 +7,8 @@
 // scaling itself never rounds) and let a block's exponent grow when a larger
 // row arrives: e4m3 keeps its fraction bits, only codes that fall among the
 // subnormals are rounded again (an error of 2^-10 in units of the new exponent,
-// 2^-17.8 of the block's largest value at most, each time it grows).
+// 2^-17.8 of the block's largest value at most, each time it grows).  The exponents of a block
+// without a row are nobody's: any byte.
 #pragma once
 
 #include "fg_common.cuh"

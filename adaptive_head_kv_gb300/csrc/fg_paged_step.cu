@@ -781,7 +781,11 @@ cudaError_t launch_step_q8(const ProfileDims& pd, const PagedArgs& a, const Step
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     // Few pages: half of the SMs take them as fast, and the others have the sequences' own caches
     // meanwhile (8 caches of 8192 positions, 64 queries each: 31 -> 25 us, with 40 of 152 SMs
-    // 29; 60 pages an SM: 129 -> 160).
+    // 29).  8 caches, 64 queries each, all SMs and half: 2.3 pages an SM 28.3 and 23.2 us, 4.7 31.3
+    // and 28.7, 7.0 32.8 and 32.2, 9.3 35.2 and 40.0, 28 57 and 76; 256 queries each 7.0 53.5 and
+    // 53.8, 9.3 55.7 and 63.1; 4 queries a cache 2.3 24.2 and 24.8, 6.4 27.4 and 31.1.  Pages are
+    // counted by the room of the prompt's table, which the host knows: with eight times the room
+    // the first case takes all SMs.
     px.sms = sms;
     const long long pages = (long long)(pre.table_len < pre.n_pages ? pre.table_len : pre.n_pages);
     if (pages * px.groups < (long long)kFewPages * sms) sms = (sms + 1) / 2;

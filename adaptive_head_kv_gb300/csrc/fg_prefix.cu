@@ -11,6 +11,12 @@
 // scales the scores, V's goes into the weights that enter the product.
 // Queries are f16 after the division by a power of two (11 bits; fp32 inputs two
 // terms, 22 bits: Q = Qh + Ql along the product's depth, P = Ph + Pl likewise).
+// One term in bf16 also where the split kernel takes two (groups of up to four): the
+// outputs' distance from the definition is then 0.00149 to 0.00172 of their size, with
+// two terms 0.00144 to 0.00164, nearly all of it their own rounding, and two terms
+// cost a step 10 to 55 % (4 queries a cache 23.0 -> 25.5 us, 64 in groups of 4 25.0 ->
+// 29.5, 64 in groups of 1 161 -> 189, 512 127 -> 197: a block then has room for one
+// tile of queries).
 //
 // A thread block per SM: a warp that loads the pages' codes (bulk copies of 4 or
 // 8 KB), one that describes the pages, four that widen codes into the swizzled

@@ -611,12 +611,15 @@ fg_status fastgen_decode_attn_q8(const fg_params* p, const fg_paged_cache* cache
  * B = 1; p gives their n and r_l).  Query head g of sequence b attends over the rows of cache
  * (l, h / R) of the prefix and of its own cache together, in one softmax; ring rows of either
  * count while their position is in (pos[b] - w, pos[b]].  So a step gives what it would give if
- * each sequence had the prefix's rows in a cache of its own; they are read once for all of them,
- * and never written: they must not be `cache` itself.  Of the prefix's fields rows_out, next_page
- * and the work list are not used.
- *   In the products with the prefix's rows queries and weights have 11 bits in bf16 and 22 in
- * fp32: off by at most 2^-11 or 2^-22 of each, or by 2^-38 of the query's largest value and 2^-32
- * of the largest weight (times its value exponent) where that is more.  A NaN among the values
+ * each sequence had the prefix's rows in a cache of its own, but for the rounding named next; they
+ * are read once for all of them, and never written: they must not be `cache` itself.  Of the
+ * prefix's fields rows_out, next_page and the work list are not used.
+ *   In the products with the prefix's rows queries, after rotation, and weights have 11 bits in
+ * bf16 (fewer than the 22 that groups of 1, 2 and 4 have in fastgen_decode_attn_q8, as many as
+ * groups of 8) and 22 in fp32: off by at most 2^-11 or 2^-22 of each, or by 2^-38 of the query's
+ * largest value and 2^-32 of the largest weight (times its value exponent) where that is more.
+ * Beside the rounding of bf16 outputs that is little: measured, 0.0015 to 0.0018 of their size from
+ * the definition in all, of which 0.0014 to 0.0017 is the rounding.  A NaN among the values
  * of a ring row makes the whole outputs of the queries that see the row NaN; the others are
  * untouched.
  *
